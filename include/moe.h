@@ -67,7 +67,11 @@ typedef struct CUstream_st* moe_stream_t; /* same type as cudaStream_t */
 #define MOE_ERR_TIMEOUT (-6)      /* a bounded device wait ran out              */
 #define MOE_ERR_DEVICE_CHECK (-7) /* a device-side input check failed          */
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
+typedef enum {
+  MOE_F32 = 0,
+  MOE_BF16 = 1,
+  MOE_E4M3 = 2 /* moe_attn_config.cache_dtype only */
+} moe_dtype;
 
 typedef enum {
   /* g = softmax over the k kept scores ("Mixture of experts and speculative
@@ -554,6 +558,178 @@ MOE_API int moe_layer_backward(const moe_config* cfg, const void* x, const void*
                     const void* dy, float alpha, float aux_grad, float* dx,
                     float* dw_router, float* dw_gate, float* dw_up, float* dw_down,
                     void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * ---- The decode step around the layer --------------------------------------
+ *
+ * Serving one or a few new tokens per sequence: rotary positions and the
+ * paged key-value cache (moe_rope_append), attention of the new tokens over
+ * the cache (moe_paged_attention), and, where a draft model proposed the new
+ * tokens, their verification (moe_verify_drafts; "Mixture of experts and
+ * speculative decoding", the draft-and-verify sections). The pages name
+ * attention and speculative decoding next to the MoE layer and give no
+ * layouts; those below are the library's.
+ *
+ * One description of the batch serves all three calls (int32, [device]):
+ *  cu_new [B+1]  exclusive prefix sum of the sequences' new tokens; sequence
+ *                b's new tokens are rows cu_new[b] .. cu_new[b+1]-1 of every
+ *                [T][...] array; cu_new[0] = 0, cu_new[B] = T, at most
+ *                max_new a sequence (0 for an idle one).
+ *  kv_len [B]    tokens of the sequence in the cache, the new ones included:
+ *                with n new tokens, new token j is at position
+ *                kv_len[b] - n + j.
+ *  block_table [B][max_pages]  page of the cache holding positions
+ *                i*page_size .. of sequence b (entries past the sequence's
+ *                last page are not read).
+ *
+ * Cache: k_cache and v_cache [n_pages][page_size][n_kv_heads][head_dim] of
+ * cache_dtype, or any other order through the strides. E4M3 caches have one
+ * fp32 scale per token and head, [n_pages][n_kv_heads][page_size], formed as
+ * moe_quantize_fp8 forms a row's.
+ *
+ * What the lists hold is checked on the device and recorded in the status
+ * word (moe_stream_status) as MOE_ERR_DEVICE_CHECK: cu_new not ascending
+ * from 0 to T by at most max_new, kv_len below 0 or over
+ * max_pages*page_size, a page outside [0, n_pages) that is in use. No
+ * address is formed from such a value; the outputs it reaches are undefined.
+ */
+typedef struct moe_attn_config {
+  int32_t n_seqs;     /* B, sequences, >= 0                                  */
+  int32_t n_tokens;   /* T, new tokens of all of them, 0..B*max_new          */
+  int32_t max_new;    /* most new tokens of one sequence, 1..4096            */
+  int32_t n_heads;    /* query heads Hq, a multiple of n_kv_heads            */
+  int32_t n_kv_heads; /* key-value heads Hk: head h reads h / (Hq / Hk)      */
+  int32_t head_dim;   /* D, 8..256, a multiple of 8 (E4M3 cache: of 16)      */
+  int32_t page_size;  /* tokens a page, >= 1                                 */
+  int32_t n_pages;    /* pages of the cache                                  */
+  int32_t max_pages;  /* columns of block_table; max_pages*page_size < 2^30  */
+  int32_t dtype;      /* moe_dtype of q, k, v, q_out and out: fp32 or bf16   */
+  int32_t cache_dtype; /* dtype, or MOE_E4M3 with bf16                       */
+  int32_t window;     /* w > 0: a token sees its own position and the w - 1
+                       * before it; 0: all of them                           */
+  int32_t rot_dim;    /* leading elements of a head that are rotated: even,
+                       * <= D; 0: none                                       */
+  int32_t rot_interleaved; /* 0: pair i is elements (i, i + rot_dim/2);
+                            * 1: (2i, 2i + 1)                                */
+  int32_t rot_sections[3]; /* pairs that turn with axis 0, 1 and 2 (time,
+                            * height, width), in order; their sum is
+                            * rot_dim/2. All 0: every pair, axis 0           */
+  float rope_base;    /* pair i turns by position * base^(-2i/rot_dim);
+                       * finite, >= 1 (0: 10000)                             */
+  float scale;        /* factor of the scores, finite; 0: 1/sqrt(D)          */
+  int64_t q_stride, k_stride, v_stride; /* elements from one token's heads to
+                       * the next's, >= heads*D; 0: packed                   */
+  int64_t page_stride, token_stride, head_stride; /* elements between pages,
+                       * tokens of a page and heads of both caches, each
+                       * >= D and such that no two rows share an element;
+                       * all 0: the order above, packed                      */
+} moe_attn_config;
+
+/* Host-only validation; touches no GPU. MOE_ERR_UNSUPPORTED where a stride or
+ * a row is not a multiple of 16 bytes, or a limit above is passed. */
+MOE_API int moe_check_attn_config(const moe_attn_config* cfg);
+
+/* Workspace bytes (0 if cfg is invalid); contents as for the layer's. */
+MOE_API size_t moe_append_workspace_size(const moe_attn_config* cfg);
+MOE_API size_t moe_attention_workspace_size(const moe_attn_config* cfg);
+
+/*
+ * Rotary positions and the cache write, one launch. With p_a the token's
+ * position on axis a and theta = p_a * base^(-2i/rot_dim), pair (x, y) of
+ * every head of q and k becomes
+ *   (x cos theta - y sin theta, y cos theta + x sin theta),
+ * computed in fp32 from an angle reduced exactly (64-bit fixed point, so far
+ * positions lose nothing) and rounded once. The rotated k and v as it is go
+ * into the sequence's slots of the cache.
+ *
+ *  q, k, v   [device] [T][heads][D] cfg->dtype, token strides of cfg (so they
+ *            may be slices of one projection's output).
+ *  positions [device] [3][T] int32 (any sign), or NULL: the position in the
+ *            sequence on every axis. Only axes with a section are read.
+ *  q_out     [device] [T][Hq][D] cfg->dtype out, packed; may be q if q is
+ *            packed. NULL (with q NULL): only the cache is written.
+ *  k_cache, v_cache, k_scale, v_scale: as above; scales NULL unless E4M3.
+ *  A token whose position is below 0 (kv_len below the new tokens) has no
+ *  slot: MOE_ERR_DEVICE_CHECK. Two sequences must not be given one slot.
+ *  ws        [device] moe_append_workspace_size(cfg) bytes.
+ */
+MOE_API int moe_rope_append(const moe_attn_config* cfg, const void* q, const void* k,
+                    const void* v, const int32_t* positions, const int32_t* cu_new,
+                    const int32_t* kv_len, const int32_t* block_table, void* q_out,
+                    void* k_cache, void* v_cache, float* k_scale, float* v_scale, void* ws,
+                    size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Attention of the new tokens over their sequences' pages. The token at
+ * position a sees the positions max(0, a - w + 1) .. a that are below kv_len
+ * (w = window, or without end): with s_i = scale * q.k_i over those,
+ *   out = sum_i exp(s_i) v_i / sum_i exp(s_i),  lse = log sum_i exp(s_i).
+ * A token that sees nothing (a < 0) gets out = 0 and lse = -inf. What the
+ * cache holds elsewhere, NaN included, reaches no output.
+ * Scores, running maxima and sums are fp32; the weights are rounded to the
+ * type they are multiplied in (see the kernels) and out once.
+ *
+ *  q       [device] [T][Hq][D] cfg->dtype, q_stride between tokens.
+ *  cu_new, kv_len, block_table, caches, scales: as above.
+ *  out     [device] [T][Hq][D] cfg->dtype out, packed.
+ *  lse     [device] [T][Hq] fp32 out, or NULL.
+ *  ws      [device] moe_attention_workspace_size(cfg) bytes.
+ * The cut of a sequence into splits depends on cfg and kv_len alone, so
+ * equal calls give equal bits.
+ */
+MOE_API int moe_paged_attention(const moe_attn_config* cfg, const void* q,
+                    const int32_t* cu_new, const int32_t* kv_len, const int32_t* block_table,
+                    const void* k_cache, const void* v_cache, const float* k_scale,
+                    const float* v_scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                    moe_stream_t stream);
+
+/*
+ * Verification of drafted tokens. Row j of sequence b's n new tokens holds
+ * the token that was fed at that place: row 0 the last one decided before,
+ * rows 1 .. n-1 the drafts. p row j is the target model's distribution after
+ * it, q row j the draft model's (from which the token of row j + 1 was
+ * drawn; the last row of q is not read).
+ *  - Draft j + 1, token x, is accepted while u_accept[j] * q_j(x) < p_j(x)
+ *    (compared exactly): the first a drafts are.
+ *  - The token after them is drawn from r = max(p_a - q_a, 0) if a < n - 1,
+ *    else from r = p_a (also if p_a - q_a has no positive entry): the least
+ *    i with r_0 + .. + r_i > u_sample[b] * (r_0 + .. + r_{V-1}). Entries are
+ *    held as 60-bit fractions and summed as integers: exact up to their
+ *    truncation, in any order.
+ * So the tokens follow the target's distribution ("Mixture of experts and
+ * speculative decoding": accept with min(1, p/q), else resample from the
+ * difference).
+ *
+ *  p, q       [device] [T][V] fp32 or bf16 (cfg->dtype), row strides of cfg;
+ *             rows of probabilities: entries outside [0, 1] are clamped, NaN
+ *             counts as 0. q NULL: a draft chosen without chance (q_j(x) = 1
+ *             at the draft, else 0).
+ *  tokens     [device] [T] int32. A draft outside [0, V) is rejected and sets
+ *             MOE_ERR_DEVICE_CHECK.
+ *  u_accept   [device] [T] fp32, u_sample [device] [B] fp32, in [0, 1).
+ *  cu_new     [device] [B+1] as above; kv_len [device] [B] or NULL.
+ *  out_tokens [device] [T] int32 out: row j of a sequence its a accepted
+ *             drafts, then the drawn token (-1 if p_a is all zero), then -1.
+ *  n_accepted [device] [B] int32 out: a (0 for an idle sequence).
+ *  kv_next    [device] [B] int32 out, or NULL (needs kv_len): kv_len less the
+ *             rejected drafts, the cache's length for the next step.
+ *  ws         [device] moe_verify_workspace_size(cfg) bytes.
+ */
+typedef struct moe_verify_config {
+  int32_t n_seqs;   /* B >= 0                                                */
+  int32_t n_tokens; /* T, 0..B*max_new                                       */
+  int32_t max_new;  /* 1..4096                                               */
+  int32_t vocab;    /* V, 1..2^24                                            */
+  int32_t dtype;    /* of p and q: fp32 or bf16                              */
+  int64_t p_stride, q_stride; /* elements between rows, >= V; 0: packed      */
+} moe_verify_config;
+MOE_API int moe_check_verify_config(const moe_verify_config* cfg);
+MOE_API size_t moe_verify_workspace_size(const moe_verify_config* cfg);
+MOE_API int moe_verify_drafts(const moe_verify_config* cfg, const void* p, const void* q,
+                    const int32_t* tokens, const float* u_accept, const float* u_sample,
+                    const int32_t* cu_new, const int32_t* kv_len, int32_t* out_tokens,
+                    int32_t* n_accepted, int32_t* kv_next, void* ws, size_t ws_bytes,
+                    moe_stream_t stream);
 
 /* Synchronises `stream`, then returns the device-side status recorded in the
  * workspace `ws` by the last call that used it (MOE_OK, MOE_ERR_TIMEOUT or

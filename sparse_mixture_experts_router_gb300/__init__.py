@@ -26,7 +26,7 @@ MOE_ERR_CUDA = -5
 MOE_ERR_TIMEOUT = -6
 MOE_ERR_DEVICE_CHECK = -7
 
-MOE_F32, MOE_BF16 = 0, 1
+MOE_F32, MOE_BF16, MOE_E4M3 = 0, 1, 2
 MOE_GATE_TOPK_SOFTMAX, MOE_GATE_ALL_SOFTMAX_RENORM = 0, 1
 MOE_TILES_AUTO, MOE_TILES_CTA, MOE_TILES_PAIR, MOE_TILES_WEIGHT_PAIR = 0, 1, 2, 3
 MOE_GATHER_AUTO, MOE_GATHER_KERNEL, MOE_GATHER_FUSED = 0, 1, 2
@@ -64,10 +64,48 @@ def capacity_for(factor: float, T: int, top_k: int, n_experts: int) -> int:
     return max(1, math.ceil(factor * T * top_k / n_experts))
 
 
+class moe_attn_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("n_seqs", "n_tokens", "max_new", "n_heads", "n_kv_heads", "head_dim", "page_size",
+                 "n_pages", "max_pages", "dtype", "cache_dtype", "window", "rot_dim",
+                 "rot_interleaved")] + [
+        ("rot_sections", ctypes.c_int32 * 3), ("rope_base", ctypes.c_float),
+        ("scale", ctypes.c_float)] + [
+        (n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "page_stride",
+                                      "token_stride", "head_stride")]
+
+
+class moe_verify_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_seqs", "n_tokens", "max_new", "vocab", "dtype")] + [
+        ("p_stride", ctypes.c_int64), ("q_stride", ctypes.c_int64)]
+
+
+def attn_config(n_seqs, n_tokens, n_heads, n_kv_heads, head_dim, page_size, n_pages, max_pages,
+                max_new=1, dtype=MOE_BF16, cache_dtype=None, window=0, rot_dim=0,
+                rot_interleaved=False, rot_sections=(0, 0, 0), rope_base=0.0, scale=0.0, q_stride=0,
+                k_stride=0, v_stride=0, page_stride=0, token_stride=0,
+                head_stride=0) -> moe_attn_config:
+    """The batch and cache of one decode step (``moe_rope_append`` and
+    ``moe_paged_attention``). cache_dtype None: dtype."""
+    return moe_attn_config(n_seqs, n_tokens, max_new, n_heads, n_kv_heads, head_dim, page_size,
+                           n_pages, max_pages, dtype, dtype if cache_dtype is None else cache_dtype,
+                           window, rot_dim, int(rot_interleaved),
+                           (ctypes.c_int32 * 3)(*rot_sections), rope_base, scale, q_stride, k_stride,
+                           v_stride, page_stride, token_stride, head_stride)
+
+
+def verify_config(n_seqs, n_tokens, vocab, max_new=1, dtype=MOE_F32, p_stride=0,
+                  q_stride=0) -> moe_verify_config:
+    """The batch of ``moe_verify_drafts``."""
+    return moe_verify_config(n_seqs, n_tokens, max_new, vocab, dtype, p_stride, q_stride)
+
+
 _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _I = ctypes.c_int
 _CFG = ctypes.POINTER(moe_config)
+_ACFG = ctypes.POINTER(moe_attn_config)
+_VCFG = ctypes.POINTER(moe_verify_config)
 _SIGS = {
     "moe_version": (_I, []),
     "moe_status_string": (ctypes.c_char_p, [_I]),
@@ -97,6 +135,14 @@ _SIGS = {
     "moe_workspace_size_backward": (_SZ, [_CFG]),
     "moe_layer_backward": (_I, [_CFG] + [_P] * 8 + [ctypes.c_float, ctypes.c_float] + [_P] * 5
                            + [_P, _SZ, _P]),
+    "moe_check_attn_config": (_I, [_ACFG]),
+    "moe_append_workspace_size": (_SZ, [_ACFG]),
+    "moe_attention_workspace_size": (_SZ, [_ACFG]),
+    "moe_rope_append": (_I, [_ACFG] + [_P] * 12 + [_P, _SZ, _P]),
+    "moe_paged_attention": (_I, [_ACFG] + [_P] * 10 + [_P, _SZ, _P]),
+    "moe_check_verify_config": (_I, [_VCFG]),
+    "moe_verify_workspace_size": (_SZ, [_VCFG]),
+    "moe_verify_drafts": (_I, [_VCFG] + [_P] * 10 + [_P, _SZ, _P]),
     "moe_stream_status": (_I, [_P, _P]),
     "moe_set_decode_barrier_test": (None, [ctypes.c_int32, ctypes.c_uint64]),
     "moe_profile_enable": (None, [_I]),
@@ -156,19 +202,24 @@ def status_string(rc: int) -> str:
     return lib().moe_status_string(rc).decode()
 
 
-def check_config(cfg: moe_config) -> int:
-    return lib().moe_check_config(ctypes.byref(cfg))
+def check_config(cfg) -> int:
+    """The status of a moe_config, moe_attn_config or moe_verify_config."""
+    fn = {moe_attn_config: "moe_check_attn_config",
+          moe_verify_config: "moe_check_verify_config"}.get(type(cfg), "moe_check_config")
+    return getattr(lib(), fn)(ctypes.byref(cfg))
 
 
-def workspace_size(cfg: moe_config, kind: str = "layer") -> int:
+def workspace_size(cfg, kind: str = "layer") -> int:
     fn = {"layer": "moe_workspace_size", "router": "moe_router_workspace_size",
           "permute": "moe_permute_workspace_size", "grouped": "moe_grouped_workspace_size",
           "layer_fp8": "moe_workspace_size_fp8", "layer_nvfp4": "moe_workspace_size_nvfp4",
-          "backward": "moe_workspace_size_backward", "reroute": "moe_reroute_workspace_size"}[kind]
+          "backward": "moe_workspace_size_backward", "reroute": "moe_reroute_workspace_size",
+          "append": "moe_append_workspace_size", "attention": "moe_attention_workspace_size",
+          "verify": "moe_verify_workspace_size"}[kind]
     return int(getattr(lib(), fn)(ctypes.byref(cfg)))
 
 
-def workspace(cfg: moe_config, kind: str = "layer", device="cuda"):
+def workspace(cfg, kind: str = "layer", device="cuda"):
     """A caller-owned workspace tensor of the size the library asks for."""
     import torch
     n = workspace_size(cfg, kind)
@@ -282,6 +333,30 @@ def moe_layer_backward(cfg, x, w_router, logit_bias, sel_bias, w_gate, w_up, w_d
         _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(dy), ctypes.c_float(alpha),
         ctypes.c_float(aux_grad), _ptr(dx), _ptr(dw_router), _ptr(dw_gate), _ptr(dw_up),
         _ptr(dw_down), _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)))
+
+
+def moe_rope_append(cfg, q, k, v, positions, cu_new, kv_len, block_table, q_out, k_cache, v_cache,
+                    k_scale, v_scale, ws, stream=None):
+    _check("moe_rope_append", lib().moe_rope_append(
+        ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(positions), _ptr(cu_new), _ptr(kv_len),
+        _ptr(block_table), _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+        _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)))
+
+
+def moe_paged_attention(cfg, q, cu_new, kv_len, block_table, k_cache, v_cache, k_scale, v_scale, out,
+                        lse, ws, stream=None):
+    _check("moe_paged_attention", lib().moe_paged_attention(
+        ctypes.byref(cfg), _ptr(q), _ptr(cu_new), _ptr(kv_len), _ptr(block_table), _ptr(k_cache),
+        _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(out), _ptr(lse), _ptr(ws),
+        ws.numel() if ws is not None else 0, _stream(stream)))
+
+
+def moe_verify_drafts(cfg, p, q, tokens, u_accept, u_sample, cu_new, kv_len, out_tokens, n_accepted,
+                      kv_next, ws, stream=None):
+    _check("moe_verify_drafts", lib().moe_verify_drafts(
+        ctypes.byref(cfg), _ptr(p), _ptr(q), _ptr(tokens), _ptr(u_accept), _ptr(u_sample),
+        _ptr(cu_new), _ptr(kv_len), _ptr(out_tokens), _ptr(n_accepted), _ptr(kv_next), _ptr(ws),
+        ws.numel() if ws is not None else 0, _stream(stream)))
 
 
 def moe_balance_stats(n_experts, T, top_k, counts, prob_sum, alpha, f, P, aux, stream=None):

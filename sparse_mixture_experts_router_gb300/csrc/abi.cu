@@ -4,6 +4,7 @@
 // other translation units; nothing here touches tensor data on the host.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <mutex>
 #include <utility>
 #include <vector>
@@ -251,8 +252,7 @@ LayerNvf4Ws carve_layer_nvf4(Carver& cv, const moe_config& c) {
   return w;
 }
 
-int check_ws(const moe_config& c, void* ws, size_t ws_bytes, size_t need) {
-  (void)c;
+int check_ws(void* ws, size_t ws_bytes, size_t need) {
   if (!ws) return MOE_ERR_INVALID_ARG;
   if (!aligned(ws, 256)) return MOE_ERR_MISALIGNED;
   if (ws_bytes < need) return MOE_ERR_WORKSPACE;
@@ -271,15 +271,44 @@ int reset_status(int* status, cudaStream_t s) {
   return e == cudaSuccess ? MOE_OK : fail_cuda(e);
 }
 
-// The bf16 path is built for sm_103a only.
-int check_device(const moe_config& c) {
-  if (c.dtype != MOE_BF16) return MOE_OK;
+// The library's code for one device: sm_103a.
+int check_sm103() {
   int dev = 0, major = 0, minor = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
   if (e != cudaSuccess) return fail_cuda(e);
   return (major == 10 && minor == 3) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+// The bf16 path is built for sm_103a only.
+int check_device(const moe_config& c) { return c.dtype == MOE_BF16 ? check_sm103() : MOE_OK; }
+
+// A checked moe_attn_config with its defaults filled in.
+moe_attn_config attn_defaults(moe_attn_config c) {
+  const int64_t D = c.head_dim;
+  if (c.q_stride == 0) c.q_stride = D * c.n_heads;
+  if (c.k_stride == 0) c.k_stride = D * c.n_kv_heads;
+  if (c.v_stride == 0) c.v_stride = D * c.n_kv_heads;
+  if (c.page_stride == 0) {
+    c.head_stride = D;
+    c.token_stride = D * c.n_kv_heads;
+    c.page_stride = c.token_stride * c.page_size;
+  }
+  if (c.rot_sections[0] + c.rot_sections[1] + c.rot_sections[2] == 0)
+    c.rot_sections[0] = c.rot_dim / 2;
+  if (c.rope_base == 0.f) c.rope_base = 10000.f;
+  if (c.scale == 0.f) c.scale = (float)(1.0 / std::sqrt((double)c.head_dim));
+  return c;
+}
+// The lists of a batch that has sequences; the table where it has columns.
+bool attn_lists(const moe_attn_config& c, const int32_t* cu, const int32_t* len,
+                const int32_t* table) {
+  return c.n_seqs == 0 || (cu && len && (table || c.max_pages == 0));
+}
+// E4M3 caches have scales, the others none.
+bool attn_scales(const moe_attn_config& c, const float* ks, const float* vs) {
+  if (c.cache_dtype != MOE_E4M3) return !ks && !vs;
+  return c.n_tokens == 0 || (ks && vs);
 }
 
 int seg_tile(const moe_config& c) { return c.dtype == MOE_BF16 ? seg_tile_m(c) : kTileM; }
@@ -313,7 +342,8 @@ const char* kKernelNames[K_NUM] = {"reset_status",  "router_topk",    "permute_h
                                    "bwd_gate",      "bwd_score",      "bwd_dh_swiglu",
                                    "bwd_da",        "bwd_dx",         "bwd_router",
                                    "bwd_wgrad",     "decode_fused",   "reroute",
-                                   "decode_front"};
+                                   "decode_front",  "rope_append",    "paged_attention",
+                                   "verify_drafts"};
 struct Prof {
   std::mutex mu;
   uint32_t mask = 0;
@@ -463,7 +493,7 @@ int moe_router_topk(const moe_config* cfg, const void* x, const void* w_router,
   if (!all_aligned({x, w_router, logit_bias, sel_bias, logits_in, logits_out, topk_idx, topk_w,
                     counts, prob_sum}))
     return MOE_ERR_MISALIGNED;
-  if ((rc = check_ws(c, ws, ws_bytes, moe_router_workspace_size(cfg))) != MOE_OK) return rc;
+  if ((rc = check_ws(ws, ws_bytes, moe_router_workspace_size(cfg))) != MOE_OK) return rc;
   Carver cv(ws);
   RouterWs w = carve_router(cv, c);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -484,7 +514,7 @@ int moe_permute(const moe_config* cfg, const void* x, const int32_t* topk_idx,
     return MOE_ERR_INVALID_ARG;
   if (!all_aligned({x, topk_idx, expert_offsets, sorted_pair, inv_pos, x_perm}))
     return MOE_ERR_MISALIGNED;
-  if ((rc = check_ws(c, ws, ws_bytes, moe_permute_workspace_size(cfg))) != MOE_OK) return rc;
+  if ((rc = check_ws(ws, ws_bytes, moe_permute_workspace_size(cfg))) != MOE_OK) return rc;
   Carver cv(ws);
   PermuteWs w = carve_permute(cv, c);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -510,7 +540,7 @@ int moe_grouped_swiglu(const moe_config* cfg, const void* x_perm, const void* x,
   }
   if (!all_aligned({x_perm, x, expert_offsets, sorted_pair, topk_w, w_gate, w_up, w_down, y_perm}))
     return MOE_ERR_MISALIGNED;
-  if ((rc = check_ws(c, ws, ws_bytes, moe_grouped_workspace_size(cfg))) != MOE_OK) return rc;
+  if ((rc = check_ws(ws, ws_bytes, moe_grouped_workspace_size(cfg))) != MOE_OK) return rc;
   if ((rc = check_device(c)) != MOE_OK) return rc;
   Carver cv(ws);
   GroupedWs w = carve_grouped(cv, c);
@@ -546,7 +576,7 @@ int moe_reroute(const moe_config* cfg, const float* logits, const float* sel_bia
   const moe_config& c = *cfg;
   if (c.T > 0 && (!logits || !topk_idx || !assign)) return MOE_ERR_INVALID_ARG;
   if (!all_aligned({logits, sel_bias, topk_idx, assign, rounds})) return MOE_ERR_MISALIGNED;
-  if ((rc = check_ws(c, ws, ws_bytes, moe_reroute_workspace_size(cfg))) != MOE_OK) return rc;
+  if ((rc = check_ws(ws, ws_bytes, moe_reroute_workspace_size(cfg))) != MOE_OK) return rc;
   Carver cv(ws);
   RerouteWs w = carve_reroute(cv, c);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -567,7 +597,7 @@ int moe_layer_forward(const moe_config* cfg, const void* x, const void* w_router
   if (!all_aligned({x, w_router, logit_bias, sel_bias, w_gate, w_up, w_down, y, topk_idx, topk_w,
                     counts, prob_sum}))
     return MOE_ERR_MISALIGNED;
-  if ((rc = check_ws(c, ws, ws_bytes, moe_workspace_size(cfg))) != MOE_OK) return rc;
+  if ((rc = check_ws(ws, ws_bytes, moe_workspace_size(cfg))) != MOE_OK) return rc;
   if ((rc = check_device(c)) != MOE_OK) return rc;
   Carver cv(ws);
   LayerWs w = carve_layer(cv, c);
@@ -703,7 +733,7 @@ int moe_layer_backward(const moe_config* cfg, const void* x, const void* w_route
   if (!all_aligned({x, w_router, logit_bias, sel_bias, w_gate, w_up, w_down, dy, dx, dw_router,
                     dw_gate, dw_up, dw_down}))
     return MOE_ERR_MISALIGNED;
-  if ((rc = check_ws(c, ws, ws_bytes, moe_workspace_size_backward(cfg))) != MOE_OK) return rc;
+  if ((rc = check_ws(ws, ws_bytes, moe_workspace_size_backward(cfg))) != MOE_OK) return rc;
   if ((rc = check_device(c)) != MOE_OK) return rc;
   Carver cv(ws);
   BwdWs w = carve_bwd(cv, c);
@@ -800,7 +830,7 @@ int moe_layer_forward_fp8(const moe_config* cfg, const void* x, const void* w_ro
   if (!all_aligned({x, w_router, logit_bias, sel_bias, wg_q, wg_scale, wu_q, wu_scale, wd_q,
                     wd_scale, y, topk_idx, topk_w, counts, prob_sum}))
     return MOE_ERR_MISALIGNED;
-  if ((rc = check_ws(c, ws, ws_bytes, moe_workspace_size_fp8(cfg))) != MOE_OK) return rc;
+  if ((rc = check_ws(ws, ws_bytes, moe_workspace_size_fp8(cfg))) != MOE_OK) return rc;
   if ((rc = check_device(c)) != MOE_OK) return rc;
   Carver cv(ws);
   LayerFp8Ws w8 = carve_layer_fp8(cv, c);
@@ -903,7 +933,7 @@ int moe_layer_forward_nvfp4(const moe_config* cfg, const void* x, const void* w_
   if (!all_aligned({x, w_router, logit_bias, sel_bias, wg_q, wg_sf, wg_scale, wu_q, wu_sf,
                     wu_scale, wd_q, wd_sf, wd_scale, y, topk_idx, topk_w, counts, prob_sum}))
     return MOE_ERR_MISALIGNED;
-  if ((rc = check_ws(c, ws, ws_bytes, moe_workspace_size_nvfp4(cfg))) != MOE_OK) return rc;
+  if ((rc = check_ws(ws, ws_bytes, moe_workspace_size_nvfp4(cfg))) != MOE_OK) return rc;
   if ((rc = check_device(c)) != MOE_OK) return rc;
   Carver cv(ws);
   LayerNvf4Ws w4 = carve_layer_nvf4(cv, c);
@@ -971,6 +1001,181 @@ int moe_balance_stats(int32_t n_experts, int32_t T, int32_t top_k, const int32_t
   if (!all_aligned({counts, prob_sum, f, P}) || ((uintptr_t)aux % 4)) return MOE_ERR_MISALIGNED;
   cudaError_t e = launch_balance_stats(n_experts, T, top_k, counts, prob_sum, alpha, f, P, aux,
                                        reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : fail_cuda(e);
+}
+
+int moe_check_attn_config(const moe_attn_config* c) {
+  if (!c) return MOE_ERR_INVALID_ARG;
+  if (c->n_seqs < 0 || c->n_tokens < 0 || c->max_new < 1 || c->n_heads < 1 || c->n_kv_heads < 1 ||
+      c->head_dim < 1 || c->page_size < 1 || c->n_pages < 0 || c->max_pages < 0 || c->window < 0)
+    return MOE_ERR_INVALID_ARG;
+  if (c->n_heads % c->n_kv_heads != 0) return MOE_ERR_INVALID_ARG;
+  if (c->n_tokens > (long long)c->n_seqs * c->max_new) return MOE_ERR_INVALID_ARG;
+  if (c->dtype != MOE_F32 && c->dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (c->cache_dtype != c->dtype && !(c->cache_dtype == MOE_E4M3 && c->dtype == MOE_BF16))
+    return MOE_ERR_INVALID_ARG;
+  if (c->rot_dim < 0 || c->rot_dim % 2 != 0 || c->rot_dim > c->head_dim ||
+      (c->rot_interleaved != 0 && c->rot_interleaved != 1))
+    return MOE_ERR_INVALID_ARG;
+  long long pairs = 0;
+  for (int32_t n : c->rot_sections) {
+    if (n < 0) return MOE_ERR_INVALID_ARG;
+    pairs += n;
+  }
+  if (pairs != 0 && pairs != c->rot_dim / 2) return MOE_ERR_INVALID_ARG;
+  // written so that a NaN fails
+  if (c->rope_base != 0.f && !(c->rope_base >= 1.f && c->rope_base <= 3.4e38f))
+    return MOE_ERR_INVALID_ARG;
+  if (!(c->scale >= -3.4e38f && c->scale <= 3.4e38f)) return MOE_ERR_INVALID_ARG;
+  const int64_t D = c->head_dim, rows[3] = {c->q_stride, c->k_stride, c->v_stride};
+  for (int i = 0; i < 3; ++i)
+    if (rows[i] != 0 && rows[i] < D * (i == 0 ? c->n_heads : c->n_kv_heads))
+      return MOE_ERR_INVALID_ARG;
+  const int64_t cache[3] = {c->page_stride, c->token_stride, c->head_stride};
+  if (cache[0] != 0 || cache[1] != 0 || cache[2] != 0)
+    for (int64_t n : cache)
+      if (n < D) return MOE_ERR_INVALID_ARG;
+  if (c->head_dim > kAttnMaxDim || c->max_new > kMaxNew || c->n_heads > kAttnMaxHeads ||
+      c->n_seqs > kMaxSeqs)
+    return MOE_ERR_UNSUPPORTED;
+  if ((long long)c->max_pages * c->page_size >= (1LL << 30) ||
+      (long long)c->n_tokens * c->n_heads >= (1LL << 30) ||
+      (long long)c->n_pages * c->page_size * c->n_kv_heads >= (1LL << 40))
+    return MOE_ERR_UNSUPPORTED;
+  const int64_t e = (int64_t)elem_bytes(c->dtype);
+  const int64_t ce = c->cache_dtype == MOE_E4M3 ? 1 : e;
+  if (D % 8 != 0 || D * ce % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  for (int64_t n : rows)
+    if (n * e % 16 != 0 || n > (1LL << 40)) return MOE_ERR_UNSUPPORTED;
+  for (int64_t n : cache)
+    if (n * ce % 16 != 0 || n > (1LL << 40)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+size_t moe_append_workspace_size(const moe_attn_config* c) {
+  return moe_check_attn_config(c) == MOE_OK ? 256 : 0;
+}
+size_t moe_attention_workspace_size(const moe_attn_config* c) {
+  return moe_check_attn_config(c) == MOE_OK ? 256 : 0;
+}
+
+int moe_rope_append(const moe_attn_config* cfg, const void* q, const void* k, const void* v,
+                    const int32_t* positions, const int32_t* cu_new, const int32_t* kv_len,
+                    const int32_t* block_table, void* q_out, void* k_cache, void* v_cache,
+                    float* k_scale, float* v_scale, void* ws, size_t ws_bytes,
+                    moe_stream_t stream) {
+  int rc = moe_check_attn_config(cfg);
+  if (rc != MOE_OK) return rc;
+  AttnArgs a = {};
+  a.c = attn_defaults(*cfg);
+  if (!attn_lists(a.c, cu_new, kv_len, block_table)) return MOE_ERR_INVALID_ARG;
+  if (a.c.n_tokens > 0 &&
+      (!k || !v || !k_cache || !v_cache || (q == nullptr) != (q_out == nullptr)))
+    return MOE_ERR_INVALID_ARG;
+  if (!attn_scales(a.c, k_scale, v_scale)) return MOE_ERR_INVALID_ARG;
+  // in place only where a token's heads are written where they were read
+  if (q && q == q_out && a.c.q_stride != (int64_t)a.c.n_heads * a.c.head_dim)
+    return MOE_ERR_INVALID_ARG;
+  if (!all_aligned({q, k, v, positions, cu_new, kv_len, block_table, q_out, k_cache, v_cache,
+                    k_scale, v_scale}))
+    return MOE_ERR_MISALIGNED;
+  if ((rc = check_ws(ws, ws_bytes, moe_append_workspace_size(cfg))) != MOE_OK) return rc;
+  if ((rc = check_sm103()) != MOE_OK) return rc;
+  a.cu_new = cu_new;
+  a.kv_len = kv_len;
+  a.table = block_table;
+  a.q = q;
+  a.out = q_out;
+  a.k = k;
+  a.v = v;
+  a.positions = positions;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.status = static_cast<int*>(ws);
+  cudaError_t e = launch_rope_append(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : fail_cuda(e);
+}
+
+int moe_paged_attention(const moe_attn_config* cfg, const void* q, const int32_t* cu_new,
+                        const int32_t* kv_len, const int32_t* block_table, const void* k_cache,
+                        const void* v_cache, const float* k_scale, const float* v_scale, void* out,
+                        float* lse, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  int rc = moe_check_attn_config(cfg);
+  if (rc != MOE_OK) return rc;
+  AttnArgs a = {};
+  a.c = attn_defaults(*cfg);
+  if (!attn_lists(a.c, cu_new, kv_len, block_table)) return MOE_ERR_INVALID_ARG;
+  if (a.c.n_tokens > 0 && (!q || !out || !k_cache || !v_cache)) return MOE_ERR_INVALID_ARG;
+  if (!attn_scales(a.c, k_scale, v_scale)) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned({q, cu_new, kv_len, block_table, k_cache, v_cache, k_scale, v_scale, out, lse}))
+    return MOE_ERR_MISALIGNED;
+  if ((rc = check_ws(ws, ws_bytes, moe_attention_workspace_size(cfg))) != MOE_OK) return rc;
+  if ((rc = check_sm103()) != MOE_OK) return rc;
+  a.cu_new = cu_new;
+  a.kv_len = kv_len;
+  a.table = block_table;
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.k_cache = const_cast<void*>(k_cache);
+  a.v_cache = const_cast<void*>(v_cache);
+  a.k_scale = const_cast<float*>(k_scale);
+  a.v_scale = const_cast<float*>(v_scale);
+  a.status = static_cast<int*>(ws);
+  cudaError_t e = launch_paged_attention(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : fail_cuda(e);
+}
+
+int moe_check_verify_config(const moe_verify_config* c) {
+  if (!c) return MOE_ERR_INVALID_ARG;
+  if (c->n_seqs < 0 || c->n_tokens < 0 || c->max_new < 1 || c->vocab < 1) return MOE_ERR_INVALID_ARG;
+  if (c->n_tokens > (long long)c->n_seqs * c->max_new) return MOE_ERR_INVALID_ARG;
+  if (c->dtype != MOE_F32 && c->dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if ((c->p_stride != 0 && c->p_stride < c->vocab) || (c->q_stride != 0 && c->q_stride < c->vocab))
+    return MOE_ERR_INVALID_ARG;
+  if (c->max_new > kMaxNew || c->n_seqs > kMaxSeqs || c->vocab > (1 << 24) ||
+      c->p_stride > (1LL << 40) || c->q_stride > (1LL << 40))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+size_t moe_verify_workspace_size(const moe_verify_config* c) {
+  return moe_check_verify_config(c) == MOE_OK ? 256 : 0;
+}
+
+int moe_verify_drafts(const moe_verify_config* cfg, const void* p, const void* q,
+                      const int32_t* tokens, const float* u_accept, const float* u_sample,
+                      const int32_t* cu_new, const int32_t* kv_len, int32_t* out_tokens,
+                      int32_t* n_accepted, int32_t* kv_next, void* ws, size_t ws_bytes,
+                      moe_stream_t stream) {
+  int rc = moe_check_verify_config(cfg);
+  if (rc != MOE_OK) return rc;
+  VerifyArgs a = {};
+  a.c = *cfg;
+  if (a.c.p_stride == 0) a.c.p_stride = a.c.vocab;
+  if (a.c.q_stride == 0) a.c.q_stride = a.c.vocab;
+  if (a.c.n_seqs > 0 && (!cu_new || !n_accepted || !u_sample)) return MOE_ERR_INVALID_ARG;
+  if (a.c.n_tokens > 0 && (!p || !tokens || !u_accept || !out_tokens)) return MOE_ERR_INVALID_ARG;
+  if (kv_next && !kv_len) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned({p, q, tokens, u_accept, u_sample, cu_new, kv_len, out_tokens, n_accepted,
+                    kv_next}))
+    return MOE_ERR_MISALIGNED;
+  if ((rc = check_ws(ws, ws_bytes, moe_verify_workspace_size(cfg))) != MOE_OK) return rc;
+  if ((rc = check_sm103()) != MOE_OK) return rc;
+  a.p = p;
+  a.q = q;
+  a.tokens = tokens;
+  a.u_accept = u_accept;
+  a.u_sample = u_sample;
+  a.cu_new = cu_new;
+  a.kv_len = kv_len;
+  a.out_tokens = out_tokens;
+  a.n_accepted = n_accepted;
+  a.kv_next = kv_next;
+  a.status = static_cast<int*>(ws);
+  cudaError_t e = launch_verify_drafts(a, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MOE_OK : fail_cuda(e);
 }
 

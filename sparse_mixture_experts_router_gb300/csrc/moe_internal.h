@@ -18,6 +18,12 @@ constexpr int kMaxExperts = 256;     // router keeps a [tokens x N] score tile i
 constexpr int kMaxTopK = 8;
 constexpr int kMaxShared = 4;
 
+// Limits of the decode-step calls (attention, append, verification).
+constexpr int kAttnMaxDim = 256;    // a head's output stays in one warp's registers
+constexpr int kAttnMaxHeads = 1024;
+constexpr int kMaxNew = 4096;       // new tokens of one sequence
+constexpr int kMaxSeqs = 65535;
+
 // Permutation chunk: pairs handled by one block (8 warps x 8 rounds x 32).
 constexpr int kPermuteChunk = 2048;
 
@@ -294,6 +300,47 @@ cudaError_t launch_bwd_wgrad(const moe_config& c, const int32_t* seg, const void
                              float* dw_gate, float* dw_up, float* dw_down, long long xp_rows,
                              long long r_rows, int* status, cudaStream_t s);
 
+// ---- the decode step around the layer (rope_append.cu, paged_attention.cu,
+// verify_drafts.cu) ----------------------------------------------------------
+// The batch and cache description with the defaults of moe_attn_config filled
+// in (strides, base, scale). The kernels form no address from cu_new, kv_len
+// or block_table entries that fail the checks of serve_util.cuh.
+struct AttnArgs {
+  moe_attn_config c;
+  const int32_t* cu_new;
+  const int32_t* kv_len;
+  const int32_t* table;
+  const void* q;
+  void* out;  // q_out of the append
+  float* lse;
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  // append only
+  const void* k;
+  const void* v;
+  const int32_t* positions;
+  int* status;
+};
+cudaError_t launch_rope_append(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t s);
+struct VerifyArgs {
+  moe_verify_config c;
+  const void* p;
+  const void* q;
+  const int32_t* tokens;
+  const float* u_accept;
+  const float* u_sample;
+  const int32_t* cu_new;
+  const int32_t* kv_len;
+  int32_t* out_tokens;
+  int32_t* n_accepted;
+  int32_t* kv_next;
+  int* status;
+};
+cudaError_t launch_verify_drafts(const VerifyArgs& a, cudaStream_t s);
+
 // ---- profiling hooks (abi.cu) ----------------------------------------------
 enum KernelId {
   K_RESET = 0,
@@ -321,6 +368,9 @@ enum KernelId {
   K_DECODE_FUSED,
   K_REROUTE,
   K_DECODE_FRONT,
+  K_ROPE_APPEND,
+  K_ATTENTION,
+  K_VERIFY,
   K_NUM
 };
 void prof_begin(int id, cudaStream_t s);
