@@ -1042,6 +1042,9 @@ int moe_check_attn_config(const moe_attn_config* c) {
       (long long)c->n_tokens * c->n_heads >= (1LL << 30) ||
       (long long)c->n_pages * c->page_size * c->n_kv_heads >= (1LL << 40))
     return MOE_ERR_UNSUPPORTED;
+  // the attention's blocks: at most 16 for 8 query rows of a (sequence, head)
+  const long long row_tiles = (c->n_heads / c->n_kv_heads * (long long)c->max_new + 7) / 8;
+  if (row_tiles * c->n_kv_heads * c->n_seqs >= (1LL << 27)) return MOE_ERR_UNSUPPORTED;
   const int64_t e = (int64_t)elem_bytes(c->dtype);
   const int64_t ce = c->cache_dtype == MOE_E4M3 ? 1 : e;
   if (D % 8 != 0 || D * ce % 16 != 0) return MOE_ERR_UNSUPPORTED;

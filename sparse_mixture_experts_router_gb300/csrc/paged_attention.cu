@@ -4,11 +4,13 @@
 // in one pass over them with the running maximum m, sum l and weighted sum o
 // of a softmax (all fp32): a key that raises m scales l and o by
 // exp(m_old - m_new). Partial (m, l, o) of disjoint key ranges join the same
-// way, so a row's keys are split over the warps of a block.
+// way, so a row's keys are split over warps, and over the blocks of a cluster.
 //
-// Simple form: one block per (new token, query head), one key a warp and
-// step, the head's elements spread over the lanes.
-#include "serve_util.cuh"
+// bf16 and E4M3 caches run on the matrix kernel of paged_attention_mma.cuh.
+// fp32 caches run on the kernel below, on the CUDA cores: one block per (new
+// token, query head), one key a warp and step, the head's elements spread
+// over the lanes.
+#include "paged_attention_mma.cuh"
 
 namespace moe {
 namespace {
@@ -16,20 +18,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kPerLane = kAttnMaxDim / 32;
 
-__device__ __forceinline__ float cache_value(const float* p, int64_t i) { return p[i]; }
-__device__ __forceinline__ float cache_value(const __nv_bfloat16* p, int64_t i) {
-  return __bfloat162float(p[i]);
-}
-__device__ __forceinline__ float cache_value(const uint8_t* p, int64_t i) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)p[i]));
-  float f;
-  asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.f32.f16 %0, l;}" : "=f"(f) : "r"(h));
-  return f;
-}
-
-template <typename T, typename C>
-__global__ void __launch_bounds__(kWarps * 32) paged_attention_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32) f32_kernel(const AttnArgs a) {
   __shared__ float sm[kWarps], sl[kWarps], so[kWarps][kAttnMaxDim];
   const moe_attn_config& c = a.c;
   const int j = blockIdx.x, b = blockIdx.y, h = blockIdx.z;
@@ -42,11 +31,11 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attention_kernel(const Attn
   const int t = r.row0 + j, pos = r.len - r.n + j, kh = h / (c.n_heads / c.n_kv_heads);
   const int first = c.window ? max(0, pos - c.window + 1) : 0;
   float q[kPerLane], o[kPerLane] = {}, m = -INFINITY, l = 0.f;
-  const T* qp = static_cast<const T*>(a.q) + (int64_t)t * c.q_stride + h * c.head_dim;
+  const float* qp = static_cast<const float*>(a.q) + (int64_t)t * c.q_stride + h * c.head_dim;
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
     const int e = lane + 32 * i;
-    q[i] = e < c.head_dim ? to_f32(qp[e]) * c.scale : 0.f;
+    q[i] = e < c.head_dim ? qp[e] * c.scale : 0.f;
   }
   for (int key = first + warp; key <= pos; key += kWarps) {
     const int page = page_of(a, b, key), at = key % c.page_size;
@@ -56,19 +45,13 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attention_kernel(const Attn
     }
     const int64_t off =
         (int64_t)page * c.page_stride + (int64_t)at * c.token_stride + kh * c.head_stride;
-    float ks = 1.f, vs = 1.f;
-    if (a.k_scale) {
-      const int64_t si = ((int64_t)page * c.n_kv_heads + kh) * c.page_size + at;
-      ks = a.k_scale[si];
-      vs = a.v_scale[si];
-    }
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
       const int e = lane + 32 * i;
-      if (e < c.head_dim) s += q[i] * cache_value(static_cast<const C*>(a.k_cache), off + e);
+      if (e < c.head_dim) s += q[i] * static_cast<const float*>(a.k_cache)[off + e];
     }
-    s = warp_sum(s) * ks;
+    s = warp_sum(s);
     const float top = fmaxf(m, s), f = m == -INFINITY ? 0.f : __expf(m - top);
     const float w = s == -INFINITY ? 0.f : __expf(s - top);
     if (top == -INFINITY) continue;
@@ -78,7 +61,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attention_kernel(const Attn
     for (int i = 0; i < kPerLane; ++i) {
       const int e = lane + 32 * i;
       if (e < c.head_dim)
-        o[i] = o[i] * f + w * vs * cache_value(static_cast<const C*>(a.v_cache), off + e);
+        o[i] = o[i] * f + w * static_cast<const float*>(a.v_cache)[off + e];
     }
   }
   if (lane == 0) sm[warp] = m, sl[warp] = l;
@@ -93,8 +76,8 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attention_kernel(const Attn
     float v = 0.f;
     for (int w = 0; w < kWarps; ++w)
       if (sm[w] != -INFINITY) v += so[w][e] * __expf(sm[w] - top);
-    static_cast<T*>(a.out)[((int64_t)t * c.n_heads + h) * c.head_dim + e] =
-        from_f32<T>(total > 0.f ? v / total : 0.f);
+    static_cast<float*>(a.out)[((int64_t)t * c.n_heads + h) * c.head_dim + e] =
+        total > 0.f ? v / total : 0.f;
   }
   if (a.lse && threadIdx.x == 0)
     a.lse[(int64_t)t * c.n_heads + h] = total > 0.f ? top + logf(total) : -INFINITY;
@@ -102,17 +85,40 @@ __global__ void __launch_bounds__(kWarps * 32) paged_attention_kernel(const Attn
 
 }  // namespace
 
+namespace attn {
+cudaError_t launch_bf16(const Params& p, int dim, int nt, unsigned blocks, cudaStream_t s);
+cudaError_t launch_e4m3(const Params& p, int dim, int nt, unsigned blocks, cudaStream_t s);
+}  // namespace attn
+
 cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t s) {
+  const moe_attn_config& c = a.c;
   cudaError_t e = launch_reset_status(a.status, s);
-  if (e != cudaSuccess || a.c.n_tokens == 0) return e;
+  if (e != cudaSuccess || c.n_tokens == 0) return e;
   ProfScope p(K_ATTENTION, s);
-  const dim3 grid((unsigned)a.c.max_new, (unsigned)a.c.n_seqs, (unsigned)a.c.n_heads);
-  const dim3 block(kWarps * 32);
-  if (a.c.dtype == MOE_F32)
-    return launch_pdl(paged_attention_kernel<float, float>, grid, block, 0, s, 1, a);
-  if (a.c.cache_dtype == MOE_E4M3)
-    return launch_pdl(paged_attention_kernel<__nv_bfloat16, uint8_t>, grid, block, 0, s, 1, a);
-  return launch_pdl(paged_attention_kernel<__nv_bfloat16, __nv_bfloat16>, grid, block, 0, s, 1, a);
+  if (c.cache_dtype == MOE_F32) {
+    const dim3 grid((unsigned)c.max_new, (unsigned)c.n_seqs, (unsigned)c.n_heads);
+    return launch_pdl(f32_kernel, grid, dim3(kWarps * 32), 0, s, 1, a);
+  }
+  // Query rows of a (sequence, head) in blocks of 8 nt.
+  const bool f8 = c.cache_dtype == MOE_E4M3;
+  const int most = c.head_dim <= 128 ? 4 : 2;
+  const int tiles = ceil_div((long long)c.n_heads / c.n_kv_heads * c.max_new, 8);
+  attn::Params prm = {};
+  prm.a = a;
+  prm.page_div = attn::fast_div((uint32_t)c.page_size);
+  prm.row_blocks = ceil_div(tiles, most);
+  const int nt = ceil_div(tiles, prm.row_blocks);
+  const long long items = (long long)c.n_seqs * c.n_kv_heads * prm.row_blocks;
+  long long keys = (long long)c.max_pages * c.page_size;
+  if (c.window) keys = keys < c.window + c.max_new ? keys : c.window + c.max_new;
+  const int key_tiles = ceil_div(keys, f8 ? 32 : 16);
+  prm.parts = 1;
+  while (prm.parts < 16 && items * prm.parts < 4LL * 2 * num_sms() &&
+         key_tiles >= 2 * attn::kWarps * prm.parts)
+    prm.parts *= 2;
+  const unsigned blocks = (unsigned)(items * prm.parts);
+  return f8 ? attn::launch_e4m3(prm, c.head_dim, nt, blocks, s)
+            : attn::launch_bf16(prm, c.head_dim, nt, blocks, s);
 }
 
 }  // namespace moe
