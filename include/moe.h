@@ -694,8 +694,8 @@ MOE_API int moe_paged_attention(const moe_attn_config* cfg, const void* q,
  *  - The token after them is drawn from r = max(p_a - q_a, 0) if a < n - 1,
  *    else from r = p_a (also if p_a - q_a has no positive entry): the least
  *    i with r_0 + .. + r_i > u_sample[b] * (r_0 + .. + r_{V-1}). Entries are
- *    held as 60-bit fractions and summed as integers: exact up to their
- *    truncation, in any order.
+ *    rounded to 2^-60 and summed as integers: the sums do not depend on how
+ *    a row is split (a row's p - q must sum to less than 8).
  * So the tokens follow the target's distribution ("Mixture of experts and
  * speculative decoding": accept with min(1, p/q), else resample from the
  * difference).

@@ -22,7 +22,7 @@ constexpr int kMaxShared = 4;
 constexpr int kAttnMaxDim = 256;    // a head's output stays in one warp's registers
 constexpr int kAttnMaxHeads = 1024;
 constexpr int kMaxNew = 4096;       // new tokens of one sequence
-constexpr int kMaxSeqs = 65535;
+constexpr int kMaxSeqs = 65534;
 
 // Permutation chunk: pairs handled by one block (8 warps x 8 rounds x 32).
 constexpr int kPermuteChunk = 2048;

@@ -21,12 +21,15 @@ constexpr int kPerLane = kAttnMaxDim / 32;
 __global__ void __launch_bounds__(kWarps * 32) f32_kernel(const AttnArgs a) {
   __shared__ float sm[kWarps], sl[kWarps], so[kWarps][kAttnMaxDim];
   const moe_attn_config& c = a.c;
-  const int j = blockIdx.x, b = blockIdx.y, h = blockIdx.z;
+  const int j = blockIdx.x, b = (int)blockIdx.y - 1, h = blockIdx.z;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   pdl_wait();
   pdl_trigger();
+  if (b < 0) {
+    if (j == 0 && h == 0) check_lists<kWarps * 32>(a, attn::FirstKey{c.window});
+    return;
+  }
   const SeqRange r = seq_range(a, b);
-  if (!r.ok && threadIdx.x == 0) set_status(a.status, status_check());
   if (j >= r.n) return;
   const int t = r.row0 + j, pos = r.len - r.n + j, kh = h / (c.n_heads / c.n_kv_heads);
   const int first = c.window ? max(0, pos - c.window + 1) : 0;
@@ -39,10 +42,7 @@ __global__ void __launch_bounds__(kWarps * 32) f32_kernel(const AttnArgs a) {
   }
   for (int key = first + warp; key <= pos; key += kWarps) {
     const int page = page_of(a, b, key), at = key % c.page_size;
-    if (page < 0) {
-      if (lane == 0) set_status(a.status, status_check());
-      continue;
-    }
+    if (page < 0) continue;
     const int64_t off =
         (int64_t)page * c.page_stride + (int64_t)at * c.token_stride + kh * c.head_stride;
     float s = 0.f;
@@ -92,11 +92,10 @@ cudaError_t launch_e4m3(const Params& p, int dim, int nt, unsigned blocks, cudaS
 
 cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t s) {
   const moe_attn_config& c = a.c;
-  cudaError_t e = launch_reset_status(a.status, s);
-  if (e != cudaSuccess || c.n_tokens == 0) return e;
+  if (c.n_tokens == 0) return launch_reset_status(a.status, s);
   ProfScope p(K_ATTENTION, s);
   if (c.cache_dtype == MOE_F32) {
-    const dim3 grid((unsigned)c.max_new, (unsigned)c.n_seqs, (unsigned)c.n_heads);
+    const dim3 grid((unsigned)c.max_new, (unsigned)c.n_seqs + 1, (unsigned)c.n_heads);
     return launch_pdl(f32_kernel, grid, dim3(kWarps * 32), 0, s, 1, a);
   }
   // Query rows of a (sequence, head) in blocks of 8 nt.
@@ -116,7 +115,7 @@ cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t s) {
   while (prm.parts < 16 && items * prm.parts < 4LL * 2 * num_sms() &&
          key_tiles >= 2 * attn::kWarps * prm.parts)
     prm.parts *= 2;
-  const unsigned blocks = (unsigned)(items * prm.parts);
+  const unsigned blocks = (unsigned)((items + 1) * prm.parts);
   return f8 ? attn::launch_e4m3(prm, c.head_dim, nt, blocks, s)
             : attn::launch_bf16(prm, c.head_dim, nt, blocks, s);
 }

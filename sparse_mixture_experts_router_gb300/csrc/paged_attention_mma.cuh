@@ -76,6 +76,14 @@ constexpr int smem_bytes() {
          (2 * kWarps + 2) * 8 * kNT * 4;
 }
 
+// The first position that a sequence's new tokens see.
+struct FirstKey {
+  int window;
+  __device__ int operator()(const SeqRange& r) const {
+    return window ? max(0, r.len - r.n - window + 1) : 0;
+  }
+};
+
 struct Params {
   AttnArgs a;
   FastDiv page_div;
@@ -95,7 +103,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 
 template <int kDim, int kNT, bool kF8>
-__global__ void __launch_bounds__(kThreads) kernel(const __grid_constant__ Params prm) {
+__global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ Params prm) {
   using T = Tile<kDim, kF8>;
   constexpr int kS = T::kStages, kMT = T::kKeys / 16, kDT = kDim / 16, kRows = 8 * kNT;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -108,12 +116,15 @@ __global__ void __launch_bounds__(kThreads) kernel(const __grid_constant__ Param
   pdl_wait();
   pdl_trigger();
   const int part = (int)(blockIdx.x % prm.parts);
-  int item = (int)(blockIdx.x / prm.parts);
+  int item = (int)(blockIdx.x / prm.parts) - 1;
+  if (item < 0) {  // the first cluster
+    if (part == 0) check_lists<kThreads>(a, FirstKey{c.window});
+    return;
+  }
   const int rb = item % prm.row_blocks;
   item /= prm.row_blocks;
   const int kh = item % c.n_kv_heads, b = item / c.n_kv_heads;
   const SeqRange sq = seq_range(a, b);
-  if (!sq.ok && threadIdx.x == 0) set_status(a.status, status_check());
   const int G = c.n_heads / c.n_kv_heads, R = G * sq.n, row0 = rb * kRows;
   if (row0 >= R) return;  // the same for the whole cluster
 
@@ -136,8 +147,8 @@ __global__ void __launch_bounds__(kThreads) kernel(const __grid_constant__ Param
   const int esz = kF8 ? 1 : 2;
   const bool chunk_in = (lane % T::kChunks) * 16 < c.head_dim * esz;
   auto tile_key = [&](int i) { return base + (t0 + warp + kWarps * i) * T::kKeys; };
-  // This lane's key of tile i: its page as the table has it (-1: not a key any
-  // row sees) and its place in the page.
+  // This lane's key of tile i: its page (negative: not a key any row sees, or
+  // no page of the cache) and its place in the page.
   int page = -1, place = 0;
   auto look_up = [&](int i) {
     const int key = tile_key(i) + lane % T::kKeys;
@@ -146,12 +157,11 @@ __global__ void __launch_bounds__(kThreads) kernel(const __grid_constant__ Param
       const int n = div(prm.page_div, key);
       place = key - n * c.page_size;
       page = __ldg(a.table + (int64_t)b * c.max_pages + n);
-      if (page < 0 || page >= c.n_pages) page = -2;
+      if (page >= c.n_pages) page = -1;
     }
   };
   auto load = [&](int i) {  // tile i, the lane's page of it at hand
     if (i < mine) {
-      if (page == -2) set_status(a.status, status_check());
       int64_t off = -1;
       if (page >= 0)
         off = ((int64_t)page * c.page_stride + (int64_t)place * c.token_stride +
@@ -585,15 +595,15 @@ cudaError_t launch(const Params& p, unsigned blocks, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (device != dev) {
-    e = cudaFuncSetAttribute(kernel<kDim, kNT, kF8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(mma_kernel<kDim, kNT, kF8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(kernel<kDim, kNT, kF8>,
+      e = cudaFuncSetAttribute(mma_kernel<kDim, kNT, kF8>,
                                cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     device = dev;
   }
-  return launch_pdl(kernel<kDim, kNT, kF8>, dim3(blocks), dim3(kThreads), (size_t)smem, s, p.parts,
+  return launch_pdl(mma_kernel<kDim, kNT, kF8>, dim3(blocks), dim3(kThreads), (size_t)smem, s, p.parts,
                     p);
 }
 

@@ -15,8 +15,9 @@
 // reduction inside the group, and both halves of every pair are read by the
 // lanes that need them (the second read hits L1) with no staging. The
 // token's sines and cosines are computed once, by the block, for all heads.
+// One block more checks the lists and writes the status.
 // Bound by memory; what it costs beyond that is the latency of one block's
-// chain (sequence of the token, its page, the stores).
+// chain (sequence of the token, its page, the sines, the stores).
 #include <cfloat>
 #include <cmath>
 
@@ -65,6 +66,7 @@ template <typename T, bool kE4M3>
 __global__ void __launch_bounds__(kThreads)
     rope_append_kernel(const AttnArgs a, const __grid_constant__ RopeTable rope, int lane_bits) {
   __shared__ float2 turn[kMaxPairs];  // (cos, sin) of this token's pairs
+  __shared__ int s_at, s_page;
   const moe_attn_config& c = a.c;
   const int t = blockIdx.x, lanes = 1 << lane_bits, groups = kThreads >> lane_bits;
   const int group = threadIdx.x >> lane_bits, gl = threadIdx.x & (lanes - 1);
@@ -111,32 +113,27 @@ __global__ void __launch_bounds__(kThreads)
 
   pdl_wait();
   pdl_trigger();
+  if (t == c.n_tokens) {
+    // a token before the first position has no slot
+    check_lists<kThreads>(a, [](const SeqRange& r) { return r.len - r.n; });
+    return;
+  }
   load(group);  // in flight while the token's place is looked up
 
-  // The token's sequence (the first whose rows end after t) and slot.
-  int lo = 0, hi = c.n_seqs;
-  while (lo < hi) {
-    const int m = (lo + hi) >> 1;
-    if (a.cu_new[m + 1] > t)
-      hi = m;
-    else
-      lo = m + 1;
+  // The token's sequence is found by one comparison a thread (a search would
+  // be a chain of reads), and its thread goes on to the page.
+  if (threadIdx.x == 0) s_page = -1, s_at = 0;
+  __syncthreads();
+  for (int b = threadIdx.x; b < c.n_seqs; b += kThreads) {
+    const SeqRange r = seq_range(a, b);
+    const int j = t - r.row0, p = r.len - r.n + j;
+    if (!r.ok || j < 0 || j >= r.n) continue;
+    s_at = p;
+    if (p >= 0) s_page = page_of(a, b, p);
   }
-  bool ok = lo < c.n_seqs;
-  int at = 0;  // position in the sequence
-  if (ok) {
-    const SeqRange r = seq_range(a, lo);
-    const int j = t - r.row0;
-    ok = r.ok && j >= 0 && j < r.n;
-    at = r.len - r.n + j;
-    ok = ok && at >= 0;
-  }
-  int page = -1;
-  if (ok) {
-    page = page_of(a, lo, at);
-    ok = page >= 0;
-  }
-  if (!ok && threadIdx.x == 0) set_status(a.status, status_check());
+  __syncthreads();
+  const int at = s_at, page = s_page;
+  const bool ok = page >= 0 && at >= 0;
   for (int i = threadIdx.x; i < pairs; i += kThreads) {
     const int axis = (i >= c.rot_sections[0]) + (i >= c.rot_sections[0] + c.rot_sections[1]);
     const int64_t pos = a.positions ? a.positions[(int64_t)axis * c.n_tokens + t] : at;
@@ -146,6 +143,20 @@ __global__ void __launch_bounds__(kThreads)
     turn[i] = cs;
   }
   __syncthreads();
+  // This lane's elements are the same of every head: factors of the element
+  // and of its partner, kept in registers.
+  float own[8], other[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = e0 + i;
+    own[i] = 1.f, other[i] = 0.f;
+    if (e < c.rot_dim) {
+      const bool first = c.rot_interleaved ? i % 2 == 0 : e < pairs;
+      const float2 cs = turn[c.rot_interleaved ? e / 2 : first ? e : e - pairs];
+      own[i] = cs.x;
+      other[i] = first ? -cs.y : cs.y;
+    }
+  }
 
   const int place = at % c.page_size;
   const int64_t row = (int64_t)page * c.page_stride + (int64_t)place * c.token_stride;
@@ -156,16 +167,10 @@ __global__ void __launch_bounds__(kThreads)
     for (int k = 0; k < kUnits; ++k) {
       const int u = u0 + k * groups;
       float o[8];
+      const bool turned = u < nq + c.n_kv_heads;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int e = e0 + i;
-        o[i] = x[k][i];
-        if (u < nq + c.n_kv_heads && e < c.rot_dim) {
-          const bool first = c.rot_interleaved ? i % 2 == 0 : e < pairs;
-          const float2 cs = turn[c.rot_interleaved ? e / 2 : first ? e : e - pairs];
-          o[i] = x[k][i] * cs.x + (first ? -y[k][i] : y[k][i]) * cs.y;
-        }
-      }
+      for (int i = 0; i < 8; ++i)
+        o[i] = turned ? x[k][i] * own[i] + y[k][i] * other[i] : x[k][i];
       float amax = 0.f;
       if (kE4M3) {
 #pragma unroll
@@ -203,8 +208,7 @@ __global__ void __launch_bounds__(kThreads)
 }  // namespace
 
 cudaError_t launch_rope_append(const AttnArgs& a, cudaStream_t s) {
-  cudaError_t e = launch_reset_status(a.status, s);
-  if (e != cudaSuccess || a.c.n_tokens == 0) return e;
+  if (a.c.n_tokens == 0) return launch_reset_status(a.status, s);
   RopeTable rope = {};
   const double ratio = a.c.rot_dim ? std::pow((double)a.c.rope_base, -2.0 / a.c.rot_dim) : 0.0;
   double f = 18446744073709551616.0 / 6.283185307179586476925;  // one radian, 2^64 a turn
@@ -212,7 +216,7 @@ cudaError_t launch_rope_append(const AttnArgs& a, cudaStream_t s) {
   int lane_bits = 0;
   while ((8 << lane_bits) < a.c.head_dim) ++lane_bits;
   ProfScope p(K_ROPE_APPEND, s);
-  const dim3 grid((unsigned)a.c.n_tokens), block(kThreads);
+  const dim3 grid((unsigned)a.c.n_tokens + 1), block(kThreads);
   if (a.c.dtype == MOE_F32)
     return launch_pdl(rope_append_kernel<float, false>, grid, block, 0, s, 1, a, rope, lane_bits);
   if (a.c.cache_dtype == MOE_E4M3)

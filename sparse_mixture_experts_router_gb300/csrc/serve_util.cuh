@@ -45,6 +45,33 @@ __host__ __device__ __forceinline__ int page_of(const AttnArgs& a, int b, int at
   return page >= 0 && page < a.c.n_pages ? page : -1;
 }
 
+// The lists' check, by one block of kThreads: a few threads a sequence look
+// at its rows, its length and the pages from position first(range) on, and
+// the status word is written. The other blocks of the launch only leave out
+// what the clamps above leave out, so no launch to clear the word comes first.
+template <int kThreads, typename First>
+__device__ void check_lists(const AttnArgs& a, First first) {
+  const moe_attn_config& c = a.c;
+  const int per = max(1, kThreads / c.n_seqs), sub = threadIdx.x % per;
+  bool bad = false;
+  for (int b = threadIdx.x / per; b < c.n_seqs; b += kThreads / per) {
+    const SeqRange r = seq_range(a, b);
+    bad = bad || !r.ok;
+    if (r.n == 0 || r.len == 0) continue;
+    const int at = first(r);
+    bad = bad || at < 0;
+    const int last = (r.len - 1) / c.page_size;
+    const int32_t* table = a.table + (int64_t)b * c.max_pages;
+#pragma unroll 4
+    for (int i = max(at, 0) / c.page_size + sub; i <= last; i += per) {
+      const int page = __ldg(table + i);
+      bad |= page < 0 || page >= c.n_pages;
+    }
+  }
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) *a.status = bad ? status_check() : MOE_OK;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);

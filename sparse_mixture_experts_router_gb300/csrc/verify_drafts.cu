@@ -7,46 +7,146 @@
 // draft. The token drawn from r = max(p - q, 0) is the least i whose running
 // sum passes u R. Running sums in floating point depend on the order they
 // are taken in, which a split over many threads changes; so every entry is
-// held as an integer of 2^-60 units and the sums are exact, whatever the
-// split: two passes over the row, one for the sums of segments and one for
-// the place inside the segment that holds u R.
+// held as an integer of 2^-60 units (rounded to nearest) and the sums are
+// exact, whatever the split: one pass over the row for the sums of segments (one a warp), and a
+// second over the one segment that holds u R.
 //
-// Bound by memory for a batch (one or two rows a sequence) and by latency
-// for a single sequence.
+// A sequence is a cluster of up to 16 blocks, so that a single row of the
+// vocabulary spreads over 16 SMs; the blocks' sums meet in distributed shared
+// memory. Every block finds the accepted drafts by itself: that takes the
+// same time as being told. One block more checks the lists and writes the
+// status, so the call is one launch. Bound by memory for a batch (one or two
+// rows a sequence) and by latency for a single sequence: five dependent
+// reads (rows, draft, its probabilities, the row, the segment) and one
+// exchange between the blocks.
 #include "serve_util.cuh"
+#include "sm103_ptx.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxParts = 16;
 
-// A probability: clamped to [0, 1], NaN as 0; and in 2^-60 units.
-__device__ __forceinline__ float prob(float x) { return fminf(fmaxf(x, 0.f), 1.f); }
-__device__ __forceinline__ uint64_t fixed60(float x) { return __float2ull_rz(prob(x) * 0x1p60f); }
-__device__ __forceinline__ uint64_t warp_sum_u64(uint64_t v) {
+// A probability: clamped to [0, 1], NaN as 0.
+__device__ __forceinline__ float prob(float x) { return __saturatef(x); }
+
+// Sums of max(p - q, 0) in 2^-60 units. A conversion of fp32 to a 64-bit
+// integer runs at the FP64 units' rate, 1/64 of fp32's here, and would take
+// five times as long as reading the row. Adding a constant whose last bit
+// weighs 2^-22 rounds p to such units and leaves them in the sum's own bit
+// pattern; what was rounded off is exact, and goes the same way in units of
+// 2^-44 and 2^-60. So an element costs seven fp32 additions, and the three
+// digits are summed as 32-bit integers, the constants' patterns cancelling
+// between p and q.
+struct Digits {
+  int a = 0, b = 0, c = 0;  // units 2^-22, 2^-44, 2^-60
+  template <int kSign>
+  __device__ __forceinline__ void add(float x) {
+    constexpr float k1 = 2.f, k2 = 0x1.8p-21f, k3 = 0x1.8p-37f;
+    const float y1 = __fadd_rn(x, k1), r1 = __fsub_rn(x, __fsub_rn(y1, k1));
+    const float y2 = __fadd_rn(r1, k2), r2 = __fsub_rn(r1, __fsub_rn(y2, k2));
+    const float y3 = __fadd_rn(r2, k3);
+    a += kSign * __float_as_int(y1);
+    b += kSign * __float_as_int(y2);
+    c += kSign * __float_as_int(y3);
+  }
+  __device__ __forceinline__ void add(float p, float q) {
+    const float x = prob(p), y = prob(q);
+    const bool over = x > y;
+    add<1>(over ? x : 0.f);
+    add<-1>(over ? y : 0.f);
+  }
+  // At most 256 elements fit the digits.
+  __device__ __forceinline__ uint64_t value() const {
+    return (uint64_t)(((int64_t)a << 38) + ((int64_t)b << 16) + c);
+  }
+};
+
+// 16 bytes of a row as fp32: 4 fp32 or 8 bf16 elements.
+__device__ __forceinline__ void unpack(uint4 v, float (&x)[4]) {
+  x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y);
+  x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ void unpack(uint4 v, float (&x)[8]) {
+  bf16x2_to_f32(v.x, x[0], x[1]);
+  bf16x2_to_f32(v.y, x[2], x[3]);
+  bf16x2_to_f32(v.z, x[4], x[5]);
+  bf16x2_to_f32(v.w, x[6], x[7]);
+}
+
+// r = max(p - q, 0) of a row in vectors of kE elements on p's 16-byte grid:
+// vector v holds elements v kE - shift ... (those outside the row are 0).
+template <typename T>
+struct Residual {
+  static constexpr int kE = 16 / (int)sizeof(T);
+  const T* p;
+  const T* q;  // null: none, or all of it at `hot`
+  int hot, vocab, shift;
+  bool q_grid;  // q's 16-byte grid is p's
+  __device__ Residual(const T* p_, const T* q_, int hot_, int vocab_)
+      : p(p_), q(q_), hot(hot_), vocab(vocab_) {
+    shift = (int)((uintptr_t)p % 16) / (int)sizeof(T);
+    q_grid = (uintptr_t)p % 16 == (uintptr_t)q % 16;
+  }
+  __device__ int vectors() const { return (vocab + shift + kE - 1) / kE; }
+  __device__ __forceinline__ void row(const T* src, bool grid, int e, float (&x)[kE]) const {
+    if (grid && e >= 0 && e + kE <= vocab) {
+      unpack(__ldg(reinterpret_cast<const uint4*>(src + e)), x);
+    } else {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
+      for (int i = 0; i < kE; ++i) x[i] = e + i >= 0 && e + i < vocab ? to_f32(src[e + i]) : 0.f;
+    }
+  }
+  __device__ __forceinline__ void load(int v, float (&x)[kE], float (&y)[kE]) const {
+    const int e = v * kE - shift;
+    row(p, true, e, x);
+    if (q) {
+      row(q, q_grid, e, y);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kE; ++i) y[i] = e + i == hot ? 1.f : 0.f;
+    }
+  }
+};
 
-template <typename T>
-__device__ __forceinline__ uint64_t residual(const T* p, const T* q, int hot, int i) {
-  const uint64_t v = fixed60(to_f32(p[i]));
-  const uint64_t w = q ? fixed60(to_f32(q[i])) : i == hot ? 1ull << 60 : 0ull;
-  return v > w ? v - w : 0ull;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
-  __shared__ uint64_t part[kWarps];
-  __shared__ int s_accepted;
+// The lists' check: one block, a few threads a sequence.
+__device__ void check_lists(const VerifyArgs& a) {
   const moe_verify_config& c = a.c;
-  const int b = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int per = max(1, kThreads / c.n_seqs), sub = threadIdx.x % per;
+  bool bad = false;
+  for (int b = threadIdx.x / per; b < c.n_seqs; b += kThreads / per) {
+    const SeqRange r = seq_rows(a.cu_new, b, c.n_seqs, c.n_tokens, c.max_new);
+    bad = bad || !r.ok;
+    for (int j = 1 + sub; j < r.n; j += per) {
+      const int x = a.tokens[r.row0 + j];
+      bad = bad || x < 0 || x >= c.vocab;
+    }
+  }
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) *a.status = bad ? status_check() : MOE_OK;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a, int parts) {
+  __shared__ uint64_t warp_part[kWarps];
+  __shared__ uint64_t block_part[2][kMaxParts];  // every block's sum, of each pass
+  __shared__ int s_accepted;
+  constexpr int kE = Residual<T>::kE;
+  const moe_verify_config& c = a.c;
+  const int part = (int)(blockIdx.x % parts), b = (int)(blockIdx.x / parts);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  ptx::cluster_arrive();  // the cluster's blocks have started before any is written to
   pdl_wait();
   pdl_trigger();
+  if (b == c.n_seqs) {
+    if (part == 0) check_lists(a);
+    __syncwarp();
+    ptx::cluster_wait();
+    return;
+  }
   const SeqRange r = seq_rows(a.cu_new, b, c.n_seqs, c.n_tokens, c.max_new);
-  if (!r.ok && threadIdx.x == 0) set_status(a.status, status_check());
   const T* p = static_cast<const T*>(a.p);
   const T* q = static_cast<const T*>(a.q);
   const int drafts = max(r.n - 1, 0);
@@ -59,7 +159,6 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
       if (j < drafts) {
         const int x = a.tokens[r.row0 + j + 1];
         take = x >= 0 && x < c.vocab;
-        if (!take) set_status(a.status, status_check());
         if (take) {
           const int64_t row = r.row0 + j;
           const double px = prob(to_f32(p[row * c.p_stride + x]));
@@ -75,67 +174,133 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
   }
   __syncthreads();
   const int acc = s_accepted;
-  if (threadIdx.x == 0) {
-    a.n_accepted[b] = acc;
-    if (a.kv_next) a.kv_next[b] = a.kv_len[b] - (drafts - acc);
+  if (part == 0) {
+    if (threadIdx.x == 0) {
+      a.n_accepted[b] = acc;
+      if (a.kv_next) a.kv_next[b] = a.kv_len[b] - (drafts - acc);
+    }
+    for (int j = threadIdx.x; j < r.n; j += kThreads)
+      if (j != acc) a.out_tokens[r.row0 + j] = j < acc ? a.tokens[r.row0 + j + 1] : -1;
   }
+  __syncwarp();
+  ptx::cluster_wait();
   if (r.n == 0) return;
-  for (int j = threadIdx.x; j < r.n; j += kThreads)
-    if (j != acc) a.out_tokens[r.row0 + j] = j < acc ? a.tokens[r.row0 + j + 1] : -1;
 
   const int64_t row = r.row0 + acc;
-  const T* pr = p + row * c.p_stride;
   const bool rejected = acc < drafts;
-  const T* qr = rejected && q ? q + row * c.q_stride : nullptr;
-  int hot = rejected && !q ? a.tokens[row + 1] : -1;
-  const int per = (c.vocab + kWarps - 1) / kWarps, i0 = warp * per, i1 = min(i0 + per, c.vocab);
-  uint64_t total = 0;
+  Residual<T> res(p + row * c.p_stride, rejected && q ? q + row * c.q_stride : nullptr,
+                  rejected && !q ? a.tokens[row + 1] : -1, c.vocab);
+  const float u = fminf(fmaxf(a.u_sample[b], 0.f), 0x1.fffffep-1f);
+  // This warp's segment of the row's vectors.
+  const int nv = res.vectors(), segs = parts * kWarps, seg = part * kWarps + warp;
+  const int v0 = (int)((long long)nv * seg / segs), v1 = (int)((long long)nv * (seg + 1) / segs);
+  uint64_t total = 0, before = 0, mine = 0;
   for (int pass = 0; pass < 2; ++pass) {
     uint64_t sum = 0;
-    for (int i = i0 + lane; i < i1; i += 32) sum += residual(pr, qr, hot, i);
-    sum = warp_sum_u64(sum);
-    if (lane == 0) part[warp] = sum;
+    constexpr int kU = 16 / kE;  // 16 elements a thread in flight
+    for (int v = v0 + lane; v < v1; v += 32 * kU) {
+      float x[kU][kE], y[kU][kE];
+#pragma unroll
+      for (int k = 0; k < kU; ++k) res.load(v + 32 * k < v1 ? v + 32 * k : v, x[k], y[k]);
+      Digits d;
+#pragma unroll
+      for (int k = 0; k < kU; ++k)
+        if (v + 32 * k < v1) {
+#pragma unroll
+          for (int i = 0; i < kE; ++i) d.add(x[k][i], y[k][i]);
+        }
+      sum += d.value();
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) warp_part[warp] = sum;
     __syncthreads();
-    for (int w = 0; w < kWarps; ++w) total += part[w];
+    if (warp == 0) {
+      uint64_t s = lane < kWarps ? warp_part[lane] : 0ull;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (lane < parts)
+        ptx::st_cluster_u64(ptx::mapa_shared(ptx::smem_addr(&block_part[pass][part]), lane), s);
+    }
+    ptx::cluster_sync();
+    total = before = 0;
+    for (int i = 0; i < parts; ++i) {
+      const uint64_t s = block_part[pass][i];
+      total += s;
+      if (i < part) before += s;
+    }
+    for (int w = 0; w < warp; ++w) before += warp_part[w];
+    mine = warp_part[warp];
     if (total > 0 || !rejected) break;
-    qr = nullptr;  // nowhere above the draft model: the target itself
-    hot = -1;
+    // nowhere above the draft model: the target itself
+    res = Residual<T>(p + row * c.p_stride, nullptr, -1, c.vocab);
     __syncthreads();
   }
   if (total == 0) {
-    if (threadIdx.x == 0) a.out_tokens[row] = -1;
+    if (part == 0 && threadIdx.x == 0) a.out_tokens[row] = -1;
     return;
   }
-  const float u = fminf(fmaxf(a.u_sample[b], 0.f), 0x1.fffffep-1f);
   const uint64_t mark = __umul64hi(__float2ull_rz(u * 0x1p64f), total);
-  uint64_t before = 0;
-  for (int w = 0; w < warp; ++w) before += part[w];
-  if (mark < before || mark >= before + part[warp]) return;
-  for (int i = i0; i < i1; i += 32) {
-    uint64_t v = i + lane < i1 ? residual(pr, qr, hot, i + lane) : 0ull;
+  if (mark < before || mark - before >= mine) return;
+  for (int v = v0; v < v1; v += 32) {
+    float x[kE], y[kE];
+    uint64_t s[kE], sum = 0;
+    res.load(min(v + lane, v1 - 1), x, y);
+#pragma unroll
+    for (int i = 0; i < kE; ++i) {
+      Digits d;
+      d.add(x[i], y[i]);
+      if (v + lane < v1) sum += d.value();
+      s[i] = sum;
+    }
+    uint64_t upto = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t w = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += w;
+      const uint64_t w = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += w;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, before + v > mark);
+    const unsigned hit = __ballot_sync(0xffffffffu, before + upto > mark);
     if (hit) {
-      if (lane == 0) a.out_tokens[row] = i + __ffs(hit) - 1;
+      if (lane == __ffs(hit) - 1) {
+        int e = 0;
+#pragma unroll
+        for (int i = 0; i < kE - 1; ++i) e += before + (upto - sum) + s[i] <= mark;
+        a.out_tokens[row] = (v + lane) * kE - res.shift + e;
+      }
       return;
     }
-    before += __shfl_sync(0xffffffffu, v, 31);
+    before += __shfl_sync(0xffffffffu, upto, 31);
   }
+}
+
+template <typename T>
+cudaError_t launch(const VerifyArgs& a, int parts, cudaStream_t s) {
+  static thread_local int device = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (device != dev) {
+    e = cudaFuncSetAttribute(verify_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    device = dev;
+  }
+  const unsigned blocks = (unsigned)(a.c.n_seqs + 1) * (unsigned)parts;
+  return launch_pdl(verify_kernel<T>, dim3(blocks), dim3(kThreads), 0, s, parts, a, parts);
 }
 
 }  // namespace
 
 cudaError_t launch_verify_drafts(const VerifyArgs& a, cudaStream_t s) {
-  cudaError_t e = launch_reset_status(a.status, s);
-  if (e != cudaSuccess || a.c.n_seqs == 0) return e;
+  if (a.c.n_seqs == 0) return launch_reset_status(a.status, s);
+  // Blocks a sequence: while they all still run at once (4 an SM) and half
+  // their threads have a vector.
+  int parts = 1;
+  const long long vectors = (long long)a.c.vocab * (a.c.dtype == MOE_F32 ? 4 : 2) / 16;
+  while (parts < kMaxParts && 2LL * parts * a.c.n_seqs <= 4LL * num_sms() &&
+         vectors >= (long long)parts * kThreads)
+    parts *= 2;
   ProfScope p(K_VERIFY, s);
-  const dim3 grid((unsigned)a.c.n_seqs), block(kThreads);
-  if (a.c.dtype == MOE_F32) return launch_pdl(verify_kernel<float>, grid, block, 0, s, 1, a);
-  return launch_pdl(verify_kernel<__nv_bfloat16>, grid, block, 0, s, 1, a);
+  return a.c.dtype == MOE_F32 ? launch<float>(a, parts, s) : launch<__nv_bfloat16>(a, parts, s);
 }
 
 }  // namespace moe

@@ -48,7 +48,7 @@ OK, INV, UNS = moe.MOE_OK, moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_UNSUPPORTED
     ({"q_stride": 1028}, UNS), ({"q_stride": 1536}, OK), ({"k_stride": 255}, INV),
     ({"page_stride": 4096}, INV), ({"page_stride": 4096, "token_stride": 256, "head_stride": 128}, OK),
     ({"page_stride": 4096, "token_stride": 256, "head_stride": 132}, UNS),
-    ({"n_seqs": 65536}, UNS),
+    ({"n_seqs": 65535}, UNS),
 ])
 def test_check_attn_config(lib, kw, rc):
     c = attn(**kw)
