@@ -343,7 +343,7 @@ const char* kKernelNames[K_NUM] = {"reset_status",  "router_topk",    "permute_h
                                    "bwd_da",        "bwd_dx",         "bwd_router",
                                    "bwd_wgrad",     "decode_fused",   "reroute",
                                    "decode_front",  "rope_append",    "paged_attention",
-                                   "verify_drafts"};
+                                   "attention_join", "verify_drafts"};
 struct Prof {
   std::mutex mu;
   uint32_t mask = 0;
@@ -1059,7 +1059,8 @@ size_t moe_append_workspace_size(const moe_attn_config* c) {
   return moe_check_attn_config(c) == MOE_OK ? 256 : 0;
 }
 size_t moe_attention_workspace_size(const moe_attn_config* c) {
-  return moe_check_attn_config(c) == MOE_OK ? 256 : 0;
+  if (moe_check_attn_config(c) != MOE_OK) return 0;
+  return 256 + align_up(attention_scratch_bytes(*c), 256);
 }
 
 int moe_rope_append(const moe_attn_config* cfg, const void* q, const void* k, const void* v,
@@ -1127,7 +1128,8 @@ int moe_paged_attention(const moe_attn_config* cfg, const void* q, const int32_t
   a.k_scale = const_cast<float*>(k_scale);
   a.v_scale = const_cast<float*>(v_scale);
   a.status = static_cast<int*>(ws);
-  cudaError_t e = launch_paged_attention(a, reinterpret_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_paged_attention(a, static_cast<char*>(ws) + 256,
+                                         reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MOE_OK : fail_cuda(e);
 }
 

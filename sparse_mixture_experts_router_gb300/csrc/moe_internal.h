@@ -324,7 +324,9 @@ struct AttnArgs {
   int* status;
 };
 cudaError_t launch_rope_append(const AttnArgs& a, cudaStream_t s);
-cudaError_t launch_paged_attention(const AttnArgs& a, cudaStream_t s);
+// scratch: attention_scratch_bytes(a.c) bytes, 256-byte aligned.
+size_t attention_scratch_bytes(const moe_attn_config& c);
+cudaError_t launch_paged_attention(const AttnArgs& a, void* scratch, cudaStream_t s);
 struct VerifyArgs {
   moe_verify_config c;
   const void* p;
@@ -370,6 +372,7 @@ enum KernelId {
   K_DECODE_FRONT,
   K_ROPE_APPEND,
   K_ATTENTION,
+  K_ATTENTION_JOIN,
   K_VERIFY,
   K_NUM
 };

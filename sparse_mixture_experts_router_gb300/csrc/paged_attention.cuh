@@ -1,0 +1,246 @@
+// What the paged attention kernels share: the cut of the work into items and
+// parts, the lookup of keys in the pages, and the join of the parts.
+//
+// An item is one (sequence, key-value head, block of query rows): row r of a
+// head group is query head r % G of new token r / G, G heads a key-value
+// head. An item's keys are cut into splits x parts ranges, a thread block
+// each. The parts of a split are a cluster and join through its distributed
+// shared memory; the splits, where there are several (an item or two of very
+// many keys), leave unnormalised rows in the workspace that a second kernel
+// joins.
+#pragma once
+#include "serve_util.cuh"
+#include "sm103_ptx.cuh"
+
+namespace moe {
+namespace attn {
+
+constexpr int kMaxParts = 16;   // the largest cluster
+constexpr int kMaxSplits = 32;
+constexpr int kPlanSms = 152;   // the plan does not ask the device, so that the workspace's size is a constant of cfg
+constexpr int kMaxRows = 32;    // query rows of an item
+
+// n / d for 0 <= n < 2^30 and 1 <= d < 2^30 as a multiplication.
+struct FastDiv {
+  uint64_t mul;
+  int shift;
+};
+inline FastDiv fast_div(uint32_t d) {
+  int bits = 0;
+  while ((1u << bits) < d) ++bits;
+  const int shift = 30 + bits;
+  return {((1ull << shift) + d - 1) / d, shift};
+}
+__device__ __forceinline__ int div(const FastDiv& f, int n) {
+  return (int)(((uint64_t)n * f.mul) >> f.shift);
+}
+
+struct Params {
+  AttnArgs a;
+  FastDiv page_div;
+  int parts, splits;
+  int row_blocks;  // of one (sequence, key-value head)
+  // splits > 1: O [item][split][kMaxRows][head_dim] relative to its maximum,
+  // and (maximum in log2 units, sum) [item][split][kMaxRows]
+  float* split_o;
+  float2* split_ml;
+};
+
+// The first position that a sequence's new tokens see.
+struct FirstKey {
+  int window;
+  __device__ int operator()(const SeqRange& r) const {
+    return window ? max(0, r.len - r.n - window + 1) : 0;
+  }
+};
+
+struct Item {
+  SeqRange sq;
+  int index, split, part;  // of this thread block
+  int b, kh, G;
+  int row0, rows;          // its query rows: row0 .. row0 + rows - 1 of the head group
+  int window;
+  __device__ __forceinline__ int clip(int r) const { return row0 + min(r, rows - 1); }
+  // Position of row r's token and the first it sees. Rows past the last one
+  // repeat it and are not written.
+  __device__ __forceinline__ int pos(int r) const { return sq.len - sq.n + clip(r) / G; }
+  __device__ __forceinline__ int first(int at) const {
+    return window ? max(0, at - window + 1) : 0;
+  }
+  // Elements from q's start to row r.
+  __device__ __forceinline__ int64_t q_at(const moe_attn_config& c, int r) const {
+    const int g = clip(r);
+    return (int64_t)(sq.row0 + g / G) * c.q_stride + (int64_t)(kh * G + g % G) * c.head_dim;
+  }
+};
+// This block's item, false where it has none (the first cluster checks the
+// lists; the whole cluster returns alike).
+template <int kThreads>
+__device__ __forceinline__ bool item_of(const Params& p, int block_rows, Item& it) {
+  const moe_attn_config& c = p.a.c;
+  it.part = (int)(blockIdx.x % p.parts);
+  int i = (int)(blockIdx.x / p.parts) - 1;
+  if (i < 0) {
+    if (it.part == 0) check_lists<kThreads>(p.a, FirstKey{c.window});
+    return false;
+  }
+  it.split = i % p.splits;
+  it.index = i /= p.splits;
+  const int rb = i % p.row_blocks;
+  i /= p.row_blocks;
+  it.kh = i % c.n_kv_heads;
+  it.b = i / c.n_kv_heads;
+  it.sq = seq_range(p.a, it.b);
+  it.G = c.n_heads / c.n_kv_heads;
+  it.row0 = rb * block_rows;
+  it.rows = min(block_rows, it.G * it.sq.n - it.row0);
+  it.window = c.window;
+  return it.rows > 0;
+}
+
+// The keys an item's rows see, in tiles of kKeys from `base` on; this block's
+// are t0 .. t1-1.
+struct Range {
+  int hi_min, hi_max;  // last position of the first and of the last row
+  int lo_min, lo_max;  // first position of the same
+  int base, t0, t1;
+};
+__device__ __forceinline__ Range range_of(const Params& p, const Item& it, int block_rows,
+                                          int keys) {
+  Range r;
+  r.hi_min = it.pos(0);
+  r.hi_max = it.pos(block_rows - 1);
+  r.lo_min = it.first(r.hi_min);
+  r.lo_max = it.first(r.hi_max);
+  r.base = r.lo_min / keys * keys;
+  const long long tiles = r.hi_max < 0 ? 0 : (r.hi_max - r.base) / keys + 1;
+  const int at = it.split * p.parts + it.part, of = p.splits * p.parts;
+  r.t0 = (int)(tiles * at / of);
+  r.t1 = (int)(tiles * (at + 1) / of);
+  return r;
+}
+
+// A key's place in the cache: its page (negative: a key no row sees, or no
+// page of the cache) and its place in the page.
+struct Slot {
+  int page, place;
+  __device__ __forceinline__ int64_t at(const moe_attn_config& c, int kh) const {
+    return (int64_t)page * c.page_stride + (int64_t)place * c.token_stride +
+           (int64_t)kh * c.head_stride;
+  }
+  __device__ __forceinline__ int64_t scale_at(const moe_attn_config& c, int kh) const {
+    return ((int64_t)page * c.n_kv_heads + kh) * c.page_size + place;
+  }
+};
+__device__ __forceinline__ Slot slot_of(const Params& p, const Item& it, const Range& r, int key) {
+  Slot s = {-1, 0};
+  if (key >= r.lo_min && key <= r.hi_max) {
+    const int n = div(p.page_div, key);
+    s.place = key - n * p.a.c.page_size;
+    s.page = __ldg(p.a.table + (int64_t)it.b * p.a.c.max_pages + n);
+    if (s.page >= p.a.c.n_pages) s.page = -1;
+  }
+  return s;
+}
+
+// ---- the join ----------------------------------------------------------------
+__device__ __forceinline__ void store4(float* out, int64_t at, float4 x) {
+  reinterpret_cast<float4*>(out)[at] = x;
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* out, int64_t at, float4 x) {
+  reinterpret_cast<uint2*>(out)[at] =
+      make_uint2(f32x2_to_bf16x2(x.x, x.y), f32x2_to_bf16x2(x.z, x.w));
+}
+// Four elements (v) of row r from their sum relative to 2^top and the sum of
+// weights: the output, or the split's part of it.
+template <typename Elem>
+__device__ __forceinline__ void write_row(const Params& p, const Item& it, int r, int v, float4 x,
+                                          float top, float sum) {
+  const moe_attn_config& c = p.a.c;
+  const int vecs = c.head_dim / 4;
+  if (p.splits > 1) {
+    const int64_t row = ((int64_t)it.index * p.splits + it.split) * kMaxRows + r;
+    reinterpret_cast<float4*>(p.split_o)[row * vecs + v] = x;
+    if (v == 0) p.split_ml[row] = make_float2(top, sum);
+    return;
+  }
+  const float f = 1.f / sum;  // a NaN stays one
+  x = sum == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                 : make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+  const int g = it.row0 + r;
+  const int64_t at = (int64_t)(it.sq.row0 + g / it.G) * c.n_heads + it.kh * it.G + g % it.G;
+  store4(static_cast<Elem*>(p.a.out), at * vecs + v, x);
+  if (v == 0 && p.a.lse)
+    p.a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+// Joins a block's kWarps partial O (row r at o + w * stride + r * ld floats,
+// all relative to the block's maximum joined[r]; joined[kRows + r] its sum of
+// weights) and then the cluster's blocks, and writes the rows.
+template <int kRows, int kWarps, int kThreads, typename Elem>
+__device__ __forceinline__ void finish(const Params& p, const Item& it, float* o, int stride, int ld,
+                                       const float* joined) {
+  const int vecs = p.a.c.head_dim / 4;
+  auto block_sum = [&](int r, int v) {
+    float4 x = *reinterpret_cast<const float4*>(o + r * ld + 4 * v);
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) {
+      const float4 y = *reinterpret_cast<const float4*>(o + w * stride + r * ld + 4 * v);
+      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+    }
+    return x;
+  };
+  if (p.parts == 1) {
+    for (int i = threadIdx.x; i < it.rows * vecs; i += kThreads) {
+      const int r = i / vecs, v = i - r * vecs;
+      write_row<Elem>(p, it, r, v, block_sum(r, v), joined[r], joined[kRows + r]);
+    }
+    return;
+  }
+  if (kWarps > 1)  // the block's O, in the first warp's place
+    for (int i = threadIdx.x; i < it.rows * vecs; i += kThreads) {
+      const int r = i / vecs, v = i - r * vecs;
+      *reinterpret_cast<float4*>(o + r * ld + 4 * v) = block_sum(r, v);
+    }
+  __syncwarp();
+  ptx::cluster_sync();
+  const uint32_t o_at = ptx::smem_addr(o), joined_at = ptx::smem_addr(joined);
+  for (int i = it.part * kThreads + threadIdx.x; i < it.rows * vecs; i += p.parts * kThreads) {
+    const int r = i / vecs, v = i - r * vecs;
+    float top = -INFINITY, sum = 0.f;
+    for (int b = 0; b < p.parts; ++b)
+      top = fmaxf(top, ptx::ld_cluster_f32(ptx::mapa_shared(joined_at + r * 4, b)));
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int b = 0; b < p.parts; ++b) {
+      const uint32_t jb = ptx::mapa_shared(joined_at + r * 4, b);
+      const float f = ptx::ex2(ptx::ld_cluster_f32(jb) - top);
+      const float4 y = ptx::ld_cluster_v4(ptx::mapa_shared(o_at + (r * ld + 4 * v) * 4, b));
+      sum += ptx::ld_cluster_f32(jb + kRows * 4) * f;
+      x.x += y.x * f, x.y += y.y * f, x.z += y.z * f, x.w += y.w * f;
+    }
+    write_row<Elem>(p, it, r, v, x, top, sum);
+  }
+  __syncwarp();
+  ptx::cluster_sync();  // no block leaves while another reads its memory
+}
+
+// Sets a kernel's shared memory and cluster attributes (once a thread and
+// device) and launches it.
+template <typename Kernel>
+cudaError_t launch(Kernel kernel, int* configured, const Params& p, unsigned blocks, int threads,
+                   int smem, cudaStream_t s) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (*configured != dev) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    *configured = dev;
+  }
+  return launch_pdl(kernel, dim3(blocks), dim3((unsigned)threads), (size_t)smem, s, p.parts, p);
+}
+
+}  // namespace attn
+}  // namespace moe

@@ -29,8 +29,7 @@
 // each query row scaled by a power of two, and the scales of keys multiply
 // scores, those of values multiply weights.
 #pragma once
-#include "serve_util.cuh"
-#include "sm103_ptx.cuh"
+#include "paged_attention.cuh"
 
 namespace moe {
 namespace attn {
@@ -38,30 +37,18 @@ namespace attn {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 
-// n / d for 0 <= n < 2^30 and 1 <= d < 2^30 as a multiplication.
-struct FastDiv {
-  uint64_t mul;
-  int shift;
-};
-inline FastDiv fast_div(uint32_t d) {
-  int bits = 0;
-  while ((1u << bits) < d) ++bits;
-  const int shift = 30 + bits;
-  return {((1ull << shift) + d - 1) / d, shift};
-}
-__device__ __forceinline__ int div(const FastDiv& f, int n) {
-  return (int)(((uint64_t)n * f.mul) >> f.shift);
-}
-
-template <int kDim, bool kF8>
+template <int kDim, int kNT, bool kF8>
 struct Tile {
   static constexpr int kKeys = kF8 ? 32 : 16;
   static constexpr int kRow = kDim * (kF8 ? 1 : 2);  // bytes of a key in shared memory
   static constexpr int kChunks = kRow / 16;
   static constexpr int kBytes = kKeys * kRow;        // one of K, V
   static constexpr int kStage = 2 * kBytes + (kF8 ? 2 * kKeys * 4 : 0);
-  // Stages a warp: about 24 KB in flight, at least 3.
-  static constexpr int kStages = kStage >= 16384 ? 3 : kStage >= 8192 ? 3 : 6;
+  // Stages a warp. Two where that lets three blocks share an SM and not two:
+  // more warps hide more than more bytes in flight do (the batch of 64 uneven
+  // sequences 175 -> 173 us, 256 short ones in E4M3 130 -> 116 us; four
+  // stages, one block an SM: 268 and 221 us).
+  static constexpr int kStages = kStage >= 16384 || kNT == 4 ? 3 : kStage >= 8192 ? 2 : 4;
   // Byte offset of 16-byte chunk c of key k: the chunks of 8 consecutive keys
   // fall into different banks.
   static __device__ __forceinline__ uint32_t at(int k, int c) {
@@ -72,23 +59,9 @@ struct Tile {
 
 template <int kDim, int kNT, bool kF8>
 constexpr int smem_bytes() {
-  return kWarps * Tile<kDim, kF8>::kStages * Tile<kDim, kF8>::kStage +
+  return kWarps * Tile<kDim, kNT, kF8>::kStages * Tile<kDim, kNT, kF8>::kStage +
          (2 * kWarps + 2) * 8 * kNT * 4;
 }
-
-// The first position that a sequence's new tokens see.
-struct FirstKey {
-  int window;
-  __device__ int operator()(const SeqRange& r) const {
-    return window ? max(0, r.len - r.n - window + 1) : 0;
-  }
-};
-
-struct Params {
-  AttnArgs a;
-  FastDiv page_div;
-  int parts, row_blocks;  // C, blocks of 8 NT query rows a (sequence, head)
-};
 
 // Two E4M3 codes (the low 16 bits of v) as fp16.
 __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t v) {
@@ -104,7 +77,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 
 template <int kDim, int kNT, bool kF8>
 __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ Params prm) {
-  using T = Tile<kDim, kF8>;
+  using T = Tile<kDim, kNT, kF8>;
   constexpr int kS = T::kStages, kMT = T::kKeys / 16, kDT = kDim / 16, kRows = 8 * kNT;
   extern __shared__ __align__(1024) uint8_t smem[];
   const AttnArgs& a = prm.a;
@@ -115,30 +88,10 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
 
   pdl_wait();
   pdl_trigger();
-  const int part = (int)(blockIdx.x % prm.parts);
-  int item = (int)(blockIdx.x / prm.parts) - 1;
-  if (item < 0) {  // the first cluster
-    if (part == 0) check_lists<kThreads>(a, FirstKey{c.window});
-    return;
-  }
-  const int rb = item % prm.row_blocks;
-  item /= prm.row_blocks;
-  const int kh = item % c.n_kv_heads, b = item / c.n_kv_heads;
-  const SeqRange sq = seq_range(a, b);
-  const int G = c.n_heads / c.n_kv_heads, R = G * sq.n, row0 = rb * kRows;
-  if (row0 >= R) return;  // the same for the whole cluster
-
-  // Rows past the last one repeat it and are not written.
-  auto row_pos = [&](int r) { return sq.len - sq.n + min(row0 + r, R - 1) / G; };
-  auto row_first = [&](int pos) { return c.window ? max(0, pos - c.window + 1) : 0; };
-  const int hi_min = row_pos(0), hi_max = row_pos(kRows - 1);
-  const int lo_min = row_first(hi_min), lo_max = row_first(hi_max);
-  const bool one_range = hi_min == hi_max;  // every row sees the same keys
-  const int base = lo_min / T::kKeys * T::kKeys;
-  const int tiles = hi_max < 0 ? 0 : (hi_max - base) / T::kKeys + 1;
-  const int t0 = (int)((long long)tiles * part / prm.parts);
-  const int t1 = (int)((long long)tiles * (part + 1) / prm.parts);
-  const int mine = t1 - t0 > warp ? (t1 - t0 - warp - 1) / kWarps + 1 : 0;
+  Item it;
+  if (!item_of<kThreads>(prm, kRows, it)) return;
+  const Range rg = range_of(prm, it, kRows, T::kKeys);
+  const int mine = rg.t1 - rg.t0 > warp ? (rg.t1 - rg.t0 - warp - 1) / kWarps + 1 : 0;
 
   // ---- the stream of tiles ----
   const uint32_t ring = ptx::smem_addr(smem) + warp * kS * T::kStage;
@@ -146,26 +99,15 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
   const uint8_t* vc = static_cast<const uint8_t*>(a.v_cache);
   const int esz = kF8 ? 1 : 2;
   const bool chunk_in = (lane % T::kChunks) * 16 < c.head_dim * esz;
-  auto tile_key = [&](int i) { return base + (t0 + warp + kWarps * i) * T::kKeys; };
-  // This lane's key of tile i: its page (negative: not a key any row sees, or
-  // no page of the cache) and its place in the page.
-  int page = -1, place = 0;
+  auto tile_key = [&](int i) { return rg.base + (rg.t0 + warp + kWarps * i) * T::kKeys; };
+  Slot slot;  // of this lane's key of the tile to load next
   auto look_up = [&](int i) {
-    const int key = tile_key(i) + lane % T::kKeys;
-    page = -1;
-    if (i < mine && key >= lo_min && key <= hi_max) {
-      const int n = div(prm.page_div, key);
-      place = key - n * c.page_size;
-      page = __ldg(a.table + (int64_t)b * c.max_pages + n);
-      if (page >= c.n_pages) page = -1;
-    }
+    slot = {-1, 0};
+    if (i < mine) slot = slot_of(prm, it, rg, tile_key(i) + lane % T::kKeys);
   };
-  auto load = [&](int i) {  // tile i, the lane's page of it at hand
+  auto load = [&](int i) {
     if (i < mine) {
-      int64_t off = -1;
-      if (page >= 0)
-        off = ((int64_t)page * c.page_stride + (int64_t)place * c.token_stride +
-               (int64_t)kh * c.head_stride) * esz;
+      const int64_t off = slot.page >= 0 ? slot.at(c, it.kh) * esz : -1;
       const uint32_t st = ring + (i % kS) * T::kStage;
       constexpr int kPer = 32 / T::kChunks;  // keys one instruction copies
 #pragma unroll
@@ -179,8 +121,8 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
         ptx::cp_async16(dst + T::kBytes, vc + src, n);
       }
       if (kF8) {
-        const int64_t s = page >= 0 ? ((int64_t)page * c.n_kv_heads + kh) * c.page_size + place : 0;
-        const uint32_t n = page >= 0 ? 4u : 0u, dst = st + 2 * T::kBytes + lane * 4;
+        const int64_t s = slot.page >= 0 ? slot.scale_at(c, it.kh) : 0;
+        const uint32_t n = slot.page >= 0 ? 4u : 0u, dst = st + 2 * T::kBytes + lane * 4;
         ptx::cp_async4(dst, a.k_scale + s, n);
         ptx::cp_async4(dst + T::kKeys * 4, a.v_scale + s, n);
       }
@@ -198,14 +140,9 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
   uint32_t q[kNT][kDT][2];
   float sc[kNT][2];  // factor of the scores of this lane's two columns, log2 units
   const float scale = c.scale * 1.4426950408889634f;
-  auto q_row = [&](int r) {
-    r = min(row0 + r, R - 1);
-    return static_cast<const uint8_t*>(a.q) +
-           ((int64_t)(sq.row0 + r / G) * c.q_stride + (int64_t)(kh * G + r % G) * c.head_dim) * 2;
-  };
 #pragma unroll
   for (int n = 0; n < kNT; ++n) {
-    const uint8_t* p = q_row(8 * n + oct);
+    const uint8_t* p = static_cast<const uint8_t*>(a.q) + it.q_at(c, 8 * n + oct) * 2;
     sc[n][0] = sc[n][1] = scale;
     if (!kF8) {
 #pragma unroll
@@ -256,8 +193,8 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
   for (int n = 0; n < kNT; ++n)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      hi[n][j] = row_pos(8 * n + 2 * quad + j);
-      lo[n][j] = row_first(hi[n][j]);
+      hi[n][j] = it.pos(8 * n + 2 * quad + j);
+      lo[n][j] = it.first(hi[n][j]);
     }
 
   // ---- the pass over the keys ----
@@ -324,7 +261,7 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
           vs[t][h] = f[T::kKeys + 16 * t + 8 * h + oct];
         }
     }
-    const bool edge = key0 + T::kKeys - 1 > hi_min || key0 < lo_max;
+    const bool edge = key0 + T::kKeys - 1 > rg.hi_min || key0 < rg.lo_max;
     bool raise = false;
 #pragma unroll
     for (int t = 0; t < kMT; ++t)
@@ -387,7 +324,7 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
 
     // A key that some rows see and others do not may hold values that are not
     // finite, and 0 times those is not 0: such a tile goes element by element.
-    if (edge && !one_range) {
+    if (edge && rg.hi_min != rg.hi_max) {
       bool wild = false;
 #pragma unroll 1
       for (int d = 0; d < T::kChunks / 2 * kMT; ++d) {
@@ -464,10 +401,9 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
       if (!kF8) {
         ptx::ldmatrix4<true>(V + T::at(lane % 8 + lane / 16 * 8, 2 * d + lane / 8 % 2), r);
 #pragma unroll
-        for (int n = 0; n < kNT; ++n) {
-          ptx::mma16816<false>(o[n][d], r, ph[0][n][0], ph[0][n][1]);
-          ptx::mma16816<false>(o[n][d], r, pl[0][n][0], pl[0][n][1]);
-        }
+        for (int n = 0; n < kNT; ++n) ptx::mma16816<false>(o[n][d], r, ph[0][n][0], ph[0][n][1]);
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) ptx::mma16816<false>(o[n][d], r, pl[0][n][0], pl[0][n][1]);
       } else {
         // 16-bit units of V are element pairs (2 oct, 2 oct + 1): rows 0-7 of
         // the product take the even elements and rows 8-15 the odd ones.
@@ -531,80 +467,15 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
               o[n][d][2 * h + j] * f;
     }
   __syncthreads();
-  const int rows = min(kRows, R - row0), vecs = c.head_dim / 4;
-  const float4* w0 = reinterpret_cast<const float4*>(smem);
-  constexpr int kWarpVecs = kS * T::kStage / 16;
-  auto block_sum = [&](int r, int v) {
-    float4 x = w0[r * (kLd / 4) + v];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) {
-      const float4 y = w0[w * kWarpVecs + r * (kLd / 4) + v];
-      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-    }
-    return x;
-  };
-  auto write = [&](int r, int v, float4 x, float top, float sum) {
-    const float f = sum > 0.f ? 1.f / sum : sum;  // a NaN stays one
-    if (sum == 0.f) x = make_float4(0.f, 0.f, 0.f, 0.f);
-    else x.x *= f, x.y *= f, x.z *= f, x.w *= f;
-    const int g = row0 + r;
-    const int64_t at = (int64_t)(sq.row0 + g / G) * c.n_heads + kh * G + g % G;
-    reinterpret_cast<uint2*>(a.out)[at * vecs + v] =
-        make_uint2(f32x2_to_bf16x2(x.x, x.y), f32x2_to_bf16x2(x.z, x.w));
-    if (v == 0 && a.lse)
-      a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-  };
-  if (prm.parts == 1) {
-    for (int i = threadIdx.x; i < rows * vecs; i += kThreads) {
-      const int r = i / vecs, v = i - r * vecs;
-      write(r, v, block_sum(r, v), joined[r], joined[kRows + r]);
-    }
-    return;
-  }
-  float4* sum0 = reinterpret_cast<float4*>(smem);  // the block's O, in the first warp's place
-  for (int i = threadIdx.x; i < rows * vecs; i += kThreads) {
-    const int r = i / vecs, v = i - r * vecs;
-    sum0[r * (kLd / 4) + v] = block_sum(r, v);
-  }
-  ptx::cluster_sync();
-  const uint32_t sum_at = ptx::smem_addr(smem), joined_at = ptx::smem_addr(joined);
-  for (int i = part * kThreads + threadIdx.x; i < rows * vecs; i += prm.parts * kThreads) {
-    const int r = i / vecs, v = i - r * vecs;
-    float top = -INFINITY, sum = 0.f;
-    for (int p = 0; p < prm.parts; ++p)
-      top = fmaxf(top, ptx::ld_cluster_f32(ptx::mapa_shared(joined_at + r * 4, p)));
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p = 0; p < prm.parts; ++p) {
-      const uint32_t jp = ptx::mapa_shared(joined_at + r * 4, p);
-      const float f = ptx::ex2(ptx::ld_cluster_f32(jp) - top);
-      const float4 y = ptx::ld_cluster_v4(ptx::mapa_shared(sum_at + (r * kLd + 4 * v) * 4, p));
-      sum += ptx::ld_cluster_f32(jp + kRows * 4) * f;
-      x.x += y.x * f, x.y += y.y * f, x.z += y.z * f, x.w += y.w * f;
-    }
-    write(r, v, x, top, sum);
-  }
-  ptx::cluster_sync();  // no block leaves while another reads its memory
+  finish<kRows, kWarps, kThreads, __nv_bfloat16>(prm, it, reinterpret_cast<float*>(smem),
+                                                 kS * T::kStage / 4, kLd, joined);
 }
 
-// Launches the kernel for n_tiles x 8 query rows.
 template <int kDim, int kNT, bool kF8>
-cudaError_t launch(const Params& p, unsigned blocks, cudaStream_t s) {
-  constexpr int smem = smem_bytes<kDim, kNT, kF8>();
-  static thread_local int device = -1;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (device != dev) {
-    e = cudaFuncSetAttribute(mma_kernel<kDim, kNT, kF8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             smem);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(mma_kernel<kDim, kNT, kF8>,
-                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    device = dev;
-  }
-  return launch_pdl(mma_kernel<kDim, kNT, kF8>, dim3(blocks), dim3(kThreads), (size_t)smem, s, p.parts,
-                    p);
+cudaError_t launch_mma(const Params& p, unsigned blocks, cudaStream_t s) {
+  static thread_local int configured = -1;
+  return launch(mma_kernel<kDim, kNT, kF8>, &configured, p, blocks, kThreads,
+                smem_bytes<kDim, kNT, kF8>(), s);
 }
 
 }  // namespace attn

@@ -10,11 +10,10 @@
 // arithmetic is the angle modulo one turn, off by at most p * 2^-53 of f_i's
 // rounding. sincospi of that fraction is then fp32-exact to its own bounds.
 //
-// One block per token. A head is held by a group of lanes (a power of two,
+// One block or one warp per token. A head is held by a group of lanes (a power of two,
 // 8 elements a lane), so the E4M3 scale of a key or value is a shuffle
-// reduction inside the group, and both halves of every pair are read by the
-// lanes that need them (the second read hits L1) with no staging. The
-// token's sines and cosines are computed once, by the block, for all heads.
+// reduction inside the group, and so is the exchange of the pairs' halves. The
+// token's sines and cosines are computed once for all heads.
 // One block more checks the lists and writes the status.
 // Bound by memory; what it costs beyond that is the latency of one block's
 // chain (sequence of the token, its page, the sines, the stores).
@@ -27,34 +26,33 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = 2;  // heads a group holds in registers at a time
 constexpr int kMaxPairs = kAttnMaxDim / 2;
 
 struct RopeTable {
   uint64_t turns[kMaxPairs];  // f_i
 };
 
-// Eight elements of a row as fp32.
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+// Eight elements of a row, as stored and as fp32.
+template <typename T>
+struct alignas(16) Eight {
+  T v[8];
+};
+template <typename T>
+__device__ __forceinline__ Eight<T> load8(const T* p) {
+  Eight<T> r;
+  constexpr int n = (int)sizeof(r) / 16;
+#pragma unroll
+  for (int i = 0; i < n; ++i) reinterpret_cast<uint4*>(&r)[i] = reinterpret_cast<const uint4*>(p)[i];
+  return r;
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 q = *reinterpret_cast<const uint4*>(p);
-  bf16x2_to_f32(q.x, x[0], x[1]);
-  bf16x2_to_f32(q.y, x[2], x[3]);
-  bf16x2_to_f32(q.z, x[4], x[5]);
-  bf16x2_to_f32(q.w, x[6], x[7]);
-}
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
-  *reinterpret_cast<uint4*>(p) =
-      make_uint4(f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(x[2], x[3]),
-                 f32x2_to_bf16x2(x[4], x[5]), f32x2_to_bf16x2(x[6], x[7]));
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
+  Eight<T> r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r.v[i] = from_f32<T>(x[i]);
+  constexpr int n = (int)sizeof(r) / 16;
+#pragma unroll
+  for (int i = 0; i < n; ++i) reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(&r)[i];
 }
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;
@@ -62,87 +60,113 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
-template <typename T, bool kE4M3>
+// The first sequence whose rows end after row t, found by a whole warp in
+// steps of 32 comparisons (n_seqs if none).
+__device__ __forceinline__ int seq_of_row(const int32_t* cu_new, int n_seqs, int t, int lane) {
+  int lo = 0, hi = n_seqs;  // the answer is in lo .. hi
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32, i = lo + (lane + 1) * step - 1;
+    const unsigned after = __ballot_sync(0xffffffffu, i >= hi || __ldg(cu_new + i + 1) > t);
+    if (!after) return hi;  // only where the list does not ascend
+    const int f = __ffs(after) - 1;
+    hi = min(hi, lo + (f + 1) * step - 1);
+    lo += f * step;
+  }
+  return lo;
+}
+
+// kWarps warps a token (1 or all of the block's).
+template <typename T, bool kE4M3, int kWarps>
 __global__ void __launch_bounds__(kThreads)
     rope_append_kernel(const AttnArgs a, const __grid_constant__ RopeTable rope, int lane_bits) {
-  __shared__ float2 turn[kMaxPairs];  // (cos, sin) of this token's pairs
-  __shared__ int s_at, s_page;
+  constexpr int kTokens = kThreads / 32 / kWarps;
+  constexpr int kUnits = kWarps == 1 ? 8 : 3;  // heads a group of lanes has in flight
+  // (cos, sin) of each token's pairs, padded against bank conflicts
+  __shared__ float2 turns[kTokens][kMaxPairs + kMaxPairs / 8];
   const moe_attn_config& c = a.c;
-  const int t = blockIdx.x, lanes = 1 << lane_bits, groups = kThreads >> lane_bits;
-  const int group = threadIdx.x >> lane_bits, gl = threadIdx.x & (lanes - 1);
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 % kWarps;
+  const int slot = threadIdx.x / 32 / kWarps, t = (int)blockIdx.x * kTokens + slot - kTokens;
+  const int lanes = 1 << lane_bits, groups = (32 * kWarps) >> lane_bits;
+  const int group = (warp * 32 + lane) >> lane_bits, gl = lane & (lanes - 1);
   const int pairs = c.rot_dim / 2, e0 = gl * 8;
   const bool held = e0 < c.head_dim;
-  const int nq = a.q ? c.n_heads : 0, units = nq + 2 * c.n_kv_heads;
-
-  // Element e0 + i turns with its partner: the same vector's neighbour
-  // (interleaved), or the element rot_dim/2 away.
-  const bool low = e0 < pairs;
-  const bool vec_partner = !c.rot_interleaved && pairs % 8 == 0;
-  auto source = [&](int u) -> const T* {
-    if (u < nq) return static_cast<const T*>(a.q) + (int64_t)t * c.q_stride + u * c.head_dim;
-    if (u < nq + c.n_kv_heads)
-      return static_cast<const T*>(a.k) + (int64_t)t * c.k_stride + (u - nq) * c.head_dim;
-    return static_cast<const T*>(a.v) + (int64_t)t * c.v_stride +
-           (u - nq - c.n_kv_heads) * c.head_dim;
-  };
-  float x[kUnits][8], y[kUnits][8];  // own elements and partners
-  auto load = [&](int u0) {
-#pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-      const int u = u0 + k * groups;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[k][i] = y[k][i] = 0.f;
-      if (u >= units || !held) continue;
-      const T* p = source(u);
-      load8(p + e0, x[k]);
-      if (u >= nq + c.n_kv_heads || e0 >= c.rot_dim) continue;
-      if (c.rot_interleaved) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[k][i] = x[k][i ^ 1];
-      } else if (vec_partner) {
-        load8(p + (low ? e0 + pairs : e0 - pairs), y[k]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int e = e0 + i;
-          if (e < c.rot_dim) y[k][i] = to_f32(p[e < pairs ? e + pairs : e - pairs]);
-        }
-      }
-    }
-  };
+  const int nq = a.q ? c.n_heads : 0, nk = c.n_kv_heads, units = nq + 2 * nk;
+  float2* turn = turns[slot];
 
   pdl_wait();
   pdl_trigger();
-  if (t == c.n_tokens) {
+  if (blockIdx.x == 0) {
     // a token before the first position has no slot
     check_lists<kThreads>(a, [](const SeqRange& r) { return r.len - r.n; });
     return;
   }
+  if (kWarps == 1 && t >= c.n_tokens) return;
+
+  const T* qr = static_cast<const T*>(a.q) + (int64_t)t * c.q_stride + e0;
+  const T* kr = static_cast<const T*>(a.k) + (int64_t)t * c.k_stride + e0;
+  const T* vr = static_cast<const T*>(a.v) + (int64_t)t * c.v_stride + e0;
+  auto source = [&](int u) {
+    return u < nq        ? qr + u * c.head_dim
+           : u < nq + nk ? kr + (u - nq) * c.head_dim
+                         : vr + (u - nq - nk) * c.head_dim;
+  };
+  Eight<T> x[kUnits];
+  auto load = [&](int u0) {
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      const int u = u0 + k * groups;
+      x[k] = {};
+      if (u < units && held) x[k] = load8(source(u));
+    }
+  };
+  // Element e0 + i turns with its partner: the same vector's neighbour
+  // (interleaved), or the element rot_dim/2 away, which another lane of the
+  // group holds (whole vectors away) or which is read again.
+  const bool vec_partner = pairs % 8 == 0;
+  const int away = e0 < pairs ? pairs : -pairs;
+  auto partners = [&](int u, const Eight<T>& own) {
+    Eight<T> y = own;
+    if (c.rot_interleaved) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y.v[i] = own.v[i ^ 1];
+    } else if (vec_partner) {
+      constexpr int n = (int)sizeof(y) / 4;
+#pragma unroll
+      for (int i = 0; i < n; ++i)
+        reinterpret_cast<uint32_t*>(&y)[i] = __shfl_sync(
+            0xffffffffu, reinterpret_cast<const uint32_t*>(&own)[i], lane + away / 8);
+    } else if (u < units && held) {
+      const T* p = source(u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (e0 + i < c.rot_dim) y.v[i] = p[e0 + i < pairs ? i + pairs : i - pairs];
+    }
+    return y;
+  };
   load(group);  // in flight while the token's place is looked up
 
-  // The token's sequence is found by one comparison a thread (a search would
-  // be a chain of reads), and its thread goes on to the page.
-  if (threadIdx.x == 0) s_page = -1, s_at = 0;
-  __syncthreads();
-  for (int b = threadIdx.x; b < c.n_seqs; b += kThreads) {
+  // The token's sequence, position and page.
+  const int b = seq_of_row(a.cu_new, c.n_seqs, t, lane);
+  int at = -1, page = -1;
+  if (b < c.n_seqs) {
     const SeqRange r = seq_range(a, b);
-    const int j = t - r.row0, p = r.len - r.n + j;
-    if (!r.ok || j < 0 || j >= r.n) continue;
-    s_at = p;
-    if (p >= 0) s_page = page_of(a, b, p);
+    const int j = t - r.row0;
+    if (r.ok && j >= 0 && j < r.n) at = r.len - r.n + j;
+    if (at >= 0) page = page_of(a, b, at);
   }
-  __syncthreads();
-  const int at = s_at, page = s_page;
-  const bool ok = page >= 0 && at >= 0;
-  for (int i = threadIdx.x; i < pairs; i += kThreads) {
+  for (int i = warp * 32 + lane; i < pairs; i += 32 * kWarps) {
     const int axis = (i >= c.rot_sections[0]) + (i >= c.rot_sections[0] + c.rot_sections[1]);
     const int64_t pos = a.positions ? a.positions[(int64_t)axis * c.n_tokens + t] : at;
     const int64_t angle = (int64_t)((uint64_t)pos * rope.turns[i]);
     float2 cs;
-    sincospif((float)angle * 0x1p-63f, &cs.y, &cs.x);
-    turn[i] = cs;
+    // the high word is enough: 2^-32 of half a turn
+    sincospif((float)(int32_t)(angle >> 32) * 0x1p-31f, &cs.y, &cs.x);
+    turn[i + i / 8] = cs;
   }
-  __syncthreads();
+  if (kWarps == 1)
+    __syncwarp();
+  else
+    __syncthreads();
   // This lane's elements are the same of every head: factors of the element
   // and of its partner, kept in registers.
   float own[8], other[8];
@@ -152,25 +176,31 @@ __global__ void __launch_bounds__(kThreads)
     own[i] = 1.f, other[i] = 0.f;
     if (e < c.rot_dim) {
       const bool first = c.rot_interleaved ? i % 2 == 0 : e < pairs;
-      const float2 cs = turn[c.rot_interleaved ? e / 2 : first ? e : e - pairs];
+      const int n = c.rot_interleaved ? e / 2 : first ? e : e - pairs;
+      const float2 cs = turn[n + n / 8];
       own[i] = cs.x;
       other[i] = first ? -cs.y : cs.y;
     }
   }
 
-  const int place = at % c.page_size;
-  const int64_t row = (int64_t)page * c.page_stride + (int64_t)place * c.token_stride;
+  const int place = page >= 0 ? at % c.page_size : 0;
+  const int64_t row = (int64_t)page * c.page_stride + (int64_t)place * c.token_stride + e0;
+  T* out = static_cast<T*>(a.out) + (int64_t)t * c.n_heads * c.head_dim + e0;
   for (int u0 = group; u0 - group < units; u0 += kUnits * groups) {
     if (u0 != group) load(u0);
-    __syncwarp();  // in place: the partners are read before they are overwritten
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
       const int u = u0 + k * groups;
+      if (u - group >= units) break;  // the same for the whole warp
       float o[8];
-      const bool turned = u < nq + c.n_kv_heads;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        o[i] = turned ? x[k][i] * own[i] + y[k][i] * other[i] : x[k][i];
+      for (int i = 0; i < 8; ++i) o[i] = to_f32(x[k].v[i]);
+      const Eight<T> y = partners(u, x[k]);
+      if (u < nq + nk) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = o[i] * own[i] + to_f32(y.v[i]) * other[i];
+      }
+      __syncwarp();  // in place: the partners are read before they are overwritten
       float amax = 0.f;
       if (kE4M3) {
 #pragma unroll
@@ -180,13 +210,13 @@ __global__ void __launch_bounds__(kThreads)
       }
       if (u >= units || !held) continue;
       if (u < nq) {
-        store8(static_cast<T*>(a.out) + ((int64_t)t * c.n_heads + u) * c.head_dim + e0, o);
+        store8(out + u * c.head_dim, o);
         continue;
       }
-      if (!ok) continue;
-      const bool key = u < nq + c.n_kv_heads;
-      const int h = key ? u - nq : u - nq - c.n_kv_heads;
-      const int64_t off = row + h * c.head_stride + e0;
+      if (page < 0) continue;
+      const bool key = u < nq + nk;
+      const int h = u - nq - (key ? 0 : nk);
+      const int64_t off = row + h * c.head_stride;
       if (kE4M3) {
         const float inv = amax > 0.f ? fminf(__fdiv_rn(448.f, amax), FLT_MAX) : 0.f;
         uint32_t w[4];
@@ -196,13 +226,26 @@ __global__ void __launch_bounds__(kThreads)
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(key ? a.k_cache : a.v_cache) + off) =
             make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
         if (gl == 0)
-          (key ? a.k_scale : a.v_scale)[((int64_t)page * c.n_kv_heads + h) * c.page_size + place] =
+          (key ? a.k_scale : a.v_scale)[((int64_t)page * nk + h) * c.page_size + place] =
               __fdiv_rn(amax, 448.f);
       } else {
         store8(static_cast<T*>(key ? a.k_cache : a.v_cache) + off, o);
       }
     }
   }
+}
+
+template <typename T, bool kE4M3>
+cudaError_t launch(const AttnArgs& a, const RopeTable& rope, int lane_bits, cudaStream_t s) {
+  // Few tokens: a block each, for the latency of one; many: a warp each, so
+  // that a token's lookups and sines are issued by one warp and not by eight.
+  constexpr int kAll = kThreads / 32;
+  if (a.c.n_tokens < 8 * num_sms())
+    return launch_pdl(rope_append_kernel<T, kE4M3, kAll>, dim3((unsigned)a.c.n_tokens + 1),
+                      dim3(kThreads), 0, s, 1, a, rope, lane_bits);
+  return launch_pdl(rope_append_kernel<T, kE4M3, 1>,
+                    dim3((unsigned)ceil_div(a.c.n_tokens, kAll) + 1), dim3(kThreads), 0, s, 1, a,
+                    rope, lane_bits);
 }
 
 }  // namespace
@@ -216,14 +259,9 @@ cudaError_t launch_rope_append(const AttnArgs& a, cudaStream_t s) {
   int lane_bits = 0;
   while ((8 << lane_bits) < a.c.head_dim) ++lane_bits;
   ProfScope p(K_ROPE_APPEND, s);
-  const dim3 grid((unsigned)a.c.n_tokens + 1), block(kThreads);
-  if (a.c.dtype == MOE_F32)
-    return launch_pdl(rope_append_kernel<float, false>, grid, block, 0, s, 1, a, rope, lane_bits);
-  if (a.c.cache_dtype == MOE_E4M3)
-    return launch_pdl(rope_append_kernel<__nv_bfloat16, true>, grid, block, 0, s, 1, a, rope,
-                      lane_bits);
-  return launch_pdl(rope_append_kernel<__nv_bfloat16, false>, grid, block, 0, s, 1, a, rope,
-                    lane_bits);
+  if (a.c.dtype == MOE_F32) return launch<float, false>(a, rope, lane_bits, s);
+  if (a.c.cache_dtype == MOE_E4M3) return launch<__nv_bfloat16, true>(a, rope, lane_bits, s);
+  return launch<__nv_bfloat16, false>(a, rope, lane_bits, s);
 }
 
 }  // namespace moe

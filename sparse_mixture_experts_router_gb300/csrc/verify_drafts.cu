@@ -19,6 +19,8 @@
 // rows a sequence) and by latency for a single sequence: five dependent
 // reads (rows, draft, its probabilities, the row, the segment) and one
 // exchange between the blocks.
+#include <algorithm>
+
 #include "serve_util.cuh"
 #include "sm103_ptx.cuh"
 
@@ -37,26 +39,38 @@ __device__ __forceinline__ float prob(float x) { return __saturatef(x); }
 // five times as long as reading the row. Adding a constant whose last bit
 // weighs 2^-22 rounds p to such units and leaves them in the sum's own bit
 // pattern; what was rounded off is exact, and goes the same way in units of
-// 2^-44 and 2^-60. So an element costs seven fp32 additions, and the three
-// digits are summed as 32-bit integers, the constants' patterns cancelling
+// 2^-44 and 2^-60. So a pair (p, q) costs seven packed fp32 additions, and the
+// three digits are summed as 32-bit integers, the constants' patterns cancelling
 // between p and q.
 struct Digits {
   int a = 0, b = 0, c = 0;  // units 2^-22, 2^-44, 2^-60
-  template <int kSign>
-  __device__ __forceinline__ void add(float x) {
-    constexpr float k1 = 2.f, k2 = 0x1.8p-21f, k3 = 0x1.8p-37f;
-    const float y1 = __fadd_rn(x, k1), r1 = __fsub_rn(x, __fsub_rn(y1, k1));
-    const float y2 = __fadd_rn(r1, k2), r2 = __fsub_rn(r1, __fsub_rn(y2, k2));
-    const float y3 = __fadd_rn(r2, k3);
-    a += kSign * __float_as_int(y1);
-    b += kSign * __float_as_int(y2);
-    c += kSign * __float_as_int(y3);
-  }
   __device__ __forceinline__ void add(float p, float q) {
     const float x = prob(p), y = prob(q);
     const bool over = x > y;
-    add<1>(over ? x : 0.f);
-    add<-1>(over ? y : 0.f);
+    // p and q go through the additions as one pair of fp32
+    const uint64_t v = pair(over ? x : 0.f, over ? y : 0.f);
+    const uint64_t y1 = add2(v, twice(2.f));
+    const uint64_t r1 = sub2(v, add2(y1, twice(-2.f)));
+    const uint64_t y2 = add2(r1, twice(0x1.8p-21f));
+    const uint64_t r2 = sub2(r1, add2(y2, twice(-0x1.8p-21f)));
+    const uint64_t y3 = add2(r2, twice(0x1.8p-37f));
+    a += (int)(uint32_t)y1 - (int)(uint32_t)(y1 >> 32);
+    b += (int)(uint32_t)y2 - (int)(uint32_t)(y2 >> 32);
+    c += (int)(uint32_t)y3 - (int)(uint32_t)(y3 >> 32);
+  }
+  static __device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    return (uint64_t)__float_as_uint(hi) << 32 | __float_as_uint(lo);
+  }
+  static __device__ __forceinline__ uint64_t twice(float x) { return pair(x, x); }
+  static __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+  }
+  static __device__ __forceinline__ uint64_t sub2(uint64_t x, uint64_t y) {
+    uint64_t r;  // x - y, rounded once: y * -1 + x
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(y), "l"(twice(-1.f)), "l"(x));
+    return r;
   }
   // At most 256 elements fit the digits.
   __device__ __forceinline__ uint64_t value() const {
@@ -242,16 +256,20 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a,
   }
   const uint64_t mark = __umul64hi(__float2ull_rz(u * 0x1p64f), total);
   if (mark < before || mark - before >= mine) return;
-  for (int v = v0; v < v1; v += 32) {
-    float x[kE], y[kE];
-    uint64_t s[kE], sum = 0;
-    res.load(min(v + lane, v1 - 1), x, y);
-#pragma unroll
-    for (int i = 0; i < kE; ++i) {
+  // The segment holds the mark: 32 ranges of it, one a lane, until a range is
+  // one vector.
+  int lo = v0, hi = v1;
+  while (true) {
+    const int per = (hi - lo + 31) / 32, b0 = min(lo + lane * per, hi), b1 = min(b0 + per, hi);
+    uint64_t sum = 0;
+#pragma unroll 4
+    for (int v = b0; v < b1; ++v) {
+      float x[kE], y[kE];
       Digits d;
-      d.add(x[i], y[i]);
-      if (v + lane < v1) sum += d.value();
-      s[i] = sum;
+      res.load(v, x, y);
+#pragma unroll
+      for (int i = 0; i < kE; ++i) d.add(x[i], y[i]);
+      sum += d.value();
     }
     uint64_t upto = sum;
 #pragma unroll
@@ -259,17 +277,24 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a,
       const uint64_t w = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += w;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, before + upto > mark);
-    if (hit) {
-      if (lane == __ffs(hit) - 1) {
-        int e = 0;
+    const int at = __ffs(__ballot_sync(0xffffffffu, before + upto > mark)) - 1;
+    before += __shfl_sync(0xffffffffu, upto - sum, at);
+    lo = __shfl_sync(0xffffffffu, b0, at);
+    hi = __shfl_sync(0xffffffffu, b1, at);
+    if (hi - lo <= 1) break;
+  }
+  if (lane == 0) {
+    float x[kE], y[kE];
+    res.load(lo, x, y);
+    int e = 0;
 #pragma unroll
-        for (int i = 0; i < kE - 1; ++i) e += before + (upto - sum) + s[i] <= mark;
-        a.out_tokens[row] = (v + lane) * kE - res.shift + e;
-      }
-      return;
+    for (int i = 0; i < kE; ++i) {
+      Digits d;
+      d.add(x[i], y[i]);
+      before += d.value();
+      e += before <= mark;
     }
-    before += __shfl_sync(0xffffffffu, upto, 31);
+    a.out_tokens[row] = lo * kE - res.shift + e;
   }
 }
 
@@ -292,13 +317,11 @@ cudaError_t launch(const VerifyArgs& a, int parts, cudaStream_t s) {
 
 cudaError_t launch_verify_drafts(const VerifyArgs& a, cudaStream_t s) {
   if (a.c.n_seqs == 0) return launch_reset_status(a.status, s);
-  // Blocks a sequence: while they all still run at once (4 an SM) and half
-  // their threads have a vector.
-  int parts = 1;
+  // Blocks a sequence: as many as all run at once (4 an SM), with a vector
+  // for half their threads at least.
   const long long vectors = (long long)a.c.vocab * (a.c.dtype == MOE_F32 ? 4 : 2) / 16;
-  while (parts < kMaxParts && 2LL * parts * a.c.n_seqs <= 4LL * num_sms() &&
-         vectors >= (long long)parts * kThreads)
-    parts *= 2;
+  const long long fit = 4LL * num_sms() / (a.c.n_seqs + 1), fed = vectors / (kThreads / 2);
+  const int parts = (int)std::max(1LL, std::min({(long long)kMaxParts, fit, fed}));
   ProfScope p(K_VERIFY, s);
   return a.c.dtype == MOE_F32 ? launch<float>(a, parts, s) : launch<__nv_bfloat16>(a, parts, s);
 }
