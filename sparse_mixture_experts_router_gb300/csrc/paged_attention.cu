@@ -6,85 +6,15 @@
 // exp(m_old - m_new). Partial (m, l, o) of disjoint key ranges join the same
 // way, so a row's keys are split over warps, and over the blocks of a cluster.
 //
-// bf16 and E4M3 caches run on the matrix kernel of paged_attention_mma.cuh.
-// fp32 caches run on the kernel below, on the CUDA cores: one block per (new
-// token, query head), one key a warp and step, the head's elements spread
-// over the lanes.
+// Here: how a call is cut, and the join of splits. bf16 and E4M3 caches run on
+// the matrix kernel of paged_attention_mma.cuh, fp32 caches on that of
+// paged_attention_f32.cu.
 #include <algorithm>
 
 #include "paged_attention.cuh"
 
 namespace moe {
 namespace {
-
-constexpr int kWarps = 8;
-constexpr int kPerLane = kAttnMaxDim / 32;
-
-__global__ void __launch_bounds__(kWarps * 32) f32_kernel(const AttnArgs a) {
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][kAttnMaxDim];
-  const moe_attn_config& c = a.c;
-  const int j = blockIdx.x, b = (int)blockIdx.y - 1, h = blockIdx.z;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  pdl_wait();
-  pdl_trigger();
-  if (b < 0) {
-    if (j == 0 && h == 0) check_lists<kWarps * 32>(a, attn::FirstKey{c.window});
-    return;
-  }
-  const SeqRange r = seq_range(a, b);
-  if (j >= r.n) return;
-  const int t = r.row0 + j, pos = r.len - r.n + j, kh = h / (c.n_heads / c.n_kv_heads);
-  const int first = c.window ? max(0, pos - c.window + 1) : 0;
-  float q[kPerLane], o[kPerLane] = {}, m = -INFINITY, l = 0.f;
-  const float* qp = static_cast<const float*>(a.q) + (int64_t)t * c.q_stride + h * c.head_dim;
-#pragma unroll
-  for (int i = 0; i < kPerLane; ++i) {
-    const int e = lane + 32 * i;
-    q[i] = e < c.head_dim ? qp[e] * c.scale : 0.f;
-  }
-  for (int key = first + warp; key <= pos; key += kWarps) {
-    const int page = page_of(a, b, key), at = key % c.page_size;
-    if (page < 0) continue;
-    const int64_t off =
-        (int64_t)page * c.page_stride + (int64_t)at * c.token_stride + kh * c.head_stride;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-      const int e = lane + 32 * i;
-      if (e < c.head_dim) s += q[i] * static_cast<const float*>(a.k_cache)[off + e];
-    }
-    s = warp_sum(s);
-    const float top = fmaxf(m, s), f = m == -INFINITY ? 0.f : __expf(m - top);
-    const float w = s == -INFINITY ? 0.f : __expf(s - top);
-    if (top == -INFINITY) continue;
-    m = top;
-    l = l * f + w;
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-      const int e = lane + 32 * i;
-      if (e < c.head_dim)
-        o[i] = o[i] * f + w * static_cast<const float*>(a.v_cache)[off + e];
-    }
-  }
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
-#pragma unroll
-  for (int i = 0; i < kPerLane; ++i) so[warp][lane + 32 * i] = o[i];
-  __syncthreads();
-  float top = -INFINITY, total = 0.f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w]);
-  for (int w = 0; w < kWarps; ++w)
-    if (sm[w] != -INFINITY) total += sl[w] * __expf(sm[w] - top);
-  for (int e = threadIdx.x; e < c.head_dim; e += kWarps * 32) {
-    float v = 0.f;
-    for (int w = 0; w < kWarps; ++w)
-      if (sm[w] != -INFINITY) v += so[w][e] * __expf(sm[w] - top);
-    static_cast<float*>(a.out)[((int64_t)t * c.n_heads + h) * c.head_dim + e] =
-        total > 0.f ? v / total : 0.f;
-  }
-  if (a.lse && threadIdx.x == 0)
-    a.lse[(int64_t)t * c.n_heads + h] = total > 0.f ? top + logf(total) : -INFINITY;
-}
-
 
 // Rows whose keys were cut into splits: one warp a row.
 constexpr int kJoinWarps = 4;
@@ -130,31 +60,40 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 
 // How a call is cut; of cfg alone, so that the workspace holds its splits.
 struct Plan {
-  int nt;  // query rows of an item / 8
+  int unit, nt;  // query rows of an item: unit * nt
   int row_blocks, parts, splits;
   long long items;
 };
 Plan plan_of(const moe_attn_config& c) {
   Plan p;
-  const int tiles = ceil_div((long long)(c.n_heads / c.n_kv_heads) * c.max_new, 8);
-  p.row_blocks = ceil_div(tiles, c.head_dim <= 128 ? 4 : 2);
-  p.nt = ceil_div(tiles, p.row_blocks);
+  const bool f32 = c.cache_dtype == MOE_F32, f8 = c.cache_dtype == MOE_E4M3;
+  const int tile = f32 ? 8 : f8 ? 32 : 16;  // keys
+  p.unit = f32 ? 4 : 8;
+  const int units = ceil_div((long long)(c.n_heads / c.n_kv_heads) * c.max_new, p.unit);
+  p.row_blocks = ceil_div(units, c.head_dim <= 128 ? 4 : 2);
+  p.nt = ceil_div(units, p.row_blocks);
   p.items = (long long)c.n_seqs * c.n_kv_heads * p.row_blocks;
   long long keys = (long long)c.max_pages * c.page_size;
   if (c.window) keys = std::min(keys, (long long)c.window + c.max_new);
-  const long long key_tiles = ceil_div(keys, c.cache_dtype == MOE_E4M3 ? 32 : 16);
-  // Parts: four waves of blocks, so that uneven sequences even out, as long
-  // as every warp has a tile.
+  const long long tiles = ceil_div(keys, tile);
+  // Parts: as many as fill the SMs, while every warp has a tile; then on to
+  // three waves of blocks (three an SM, two where the query rows fill the
+  // registers, one of the longest heads), so that uneven sequences even out,
+  // while a warp has eight tiles (a block costs about what those take). 64 sequences of 37 to 8190
+  // keys take 182 us in two parts, 172 in four, 183 in eight; 32 of 100 to
+  // 12000 with 20 rows 174, 168, 182.
+  const int per_sm = c.head_dim > 128 ? 1 : p.nt > (f8 ? 1 : 2) ? 2 : 3;
   p.parts = 1;
-  while (p.parts < attn::kMaxParts && p.items * p.parts < 4LL * 2 * attn::kPlanSms &&
-         key_tiles >= 8 * p.parts)
+  while (p.parts < attn::kMaxParts && tiles >= 8 * p.parts &&
+         (p.items * p.parts < attn::kPlanSms ||
+          (p.items * p.parts < 3LL * per_sm * attn::kPlanSms && tiles >= 64 * p.parts)))
     p.parts *= 2;
   // Splits: where the largest clusters still leave SMs idle and a warp has 16
   // tiles or more.
   p.splits = 1;
-  if (p.parts == attn::kMaxParts && p.items > 0 && c.cache_dtype != MOE_F32)
+  if (p.parts == attn::kMaxParts && p.items > 0)
     p.splits = (int)std::max(1LL, std::min({2LL * attn::kPlanSms / (p.items * p.parts),
-                                            key_tiles / (16 * 4 * p.parts),
+                                            tiles / (16 * 4 * p.parts),
                                             (long long)attn::kMaxSplits}));
   return p;
 }
@@ -167,6 +106,7 @@ size_t split_rows(const Plan& p) {
 namespace attn {
 cudaError_t launch_bf16(const Params& p, int dim, int nt, unsigned blocks, cudaStream_t s);
 cudaError_t launch_e4m3(const Params& p, int dim, int nt, unsigned blocks, cudaStream_t s);
+cudaError_t launch_f32(const Params& p, int dim, int nt, unsigned blocks, cudaStream_t s);
 }  // namespace attn
 
 size_t attention_scratch_bytes(const moe_attn_config& c) {
@@ -176,11 +116,6 @@ size_t attention_scratch_bytes(const moe_attn_config& c) {
 cudaError_t launch_paged_attention(const AttnArgs& a, void* scratch, cudaStream_t s) {
   const moe_attn_config& c = a.c;
   if (c.n_tokens == 0) return launch_reset_status(a.status, s);
-  if (c.cache_dtype == MOE_F32) {
-    ProfScope p(K_ATTENTION, s);
-    const dim3 grid((unsigned)c.max_new, (unsigned)c.n_seqs + 1, (unsigned)c.n_heads);
-    return launch_pdl(f32_kernel, grid, dim3(kWarps * 32), 0, s, 1, a);
-  }
   const Plan plan = plan_of(c);
   attn::Params prm = {};
   prm.a = a;
@@ -194,14 +129,17 @@ cudaError_t launch_paged_attention(const AttnArgs& a, void* scratch, cudaStream_
   cudaError_t e;
   {
     ProfScope p(K_ATTENTION, s);
-    e = c.cache_dtype == MOE_E4M3 ? attn::launch_e4m3(prm, c.head_dim, plan.nt, blocks, s)
-                                  : attn::launch_bf16(prm, c.head_dim, plan.nt, blocks, s);
+    e = c.cache_dtype == MOE_F32    ? attn::launch_f32(prm, c.head_dim, plan.nt, blocks, s)
+        : c.cache_dtype == MOE_E4M3 ? attn::launch_e4m3(prm, c.head_dim, plan.nt, blocks, s)
+                                    : attn::launch_bf16(prm, c.head_dim, plan.nt, blocks, s);
   }
   if (e != cudaSuccess || plan.splits == 1) return e;
   ProfScope p(K_ATTENTION_JOIN, s);
-  const int rows = (int)(plan.items * 8 * plan.nt);
-  return launch_pdl(join_kernel<__nv_bfloat16>, dim3((unsigned)ceil_div(rows, kJoinWarps)),
-                    dim3(kJoinWarps * 32), 0, s, 1, prm, 8 * plan.nt, rows);
+  const int block_rows = plan.unit * plan.nt, rows = (int)(plan.items * block_rows);
+  const dim3 grid((unsigned)ceil_div(rows, kJoinWarps)), block(kJoinWarps * 32);
+  return c.dtype == MOE_F32
+             ? launch_pdl(join_kernel<float>, grid, block, 0, s, 1, prm, block_rows, rows)
+             : launch_pdl(join_kernel<__nv_bfloat16>, grid, block, 0, s, 1, prm, block_rows, rows);
 }
 
 }  // namespace moe

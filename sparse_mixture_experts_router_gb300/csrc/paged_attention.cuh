@@ -120,10 +120,14 @@ __device__ __forceinline__ Range range_of(const Params& p, const Item& it, int b
   return r;
 }
 
-// A key's place in the cache: its page (negative: a key no row sees, or no
-// page of the cache) and its place in the page.
+// A key's place in the cache: its page as the table has it (-1 for a key no
+// row sees) and its place in the page. Nothing here uses the page, so a lookup
+// for a later tile does not wait for the table.
 struct Slot {
   int page, place;
+  __device__ __forceinline__ bool in(const moe_attn_config& c) const {
+    return page >= 0 && page < c.n_pages;
+  }
   __device__ __forceinline__ int64_t at(const moe_attn_config& c, int kh) const {
     return (int64_t)page * c.page_stride + (int64_t)place * c.token_stride +
            (int64_t)kh * c.head_stride;
@@ -138,7 +142,6 @@ __device__ __forceinline__ Slot slot_of(const Params& p, const Item& it, const R
     const int n = div(p.page_div, key);
     s.place = key - n * p.a.c.page_size;
     s.page = __ldg(p.a.table + (int64_t)it.b * p.a.c.max_pages + n);
-    if (s.page >= p.a.c.n_pages) s.page = -1;
   }
   return s;
 }

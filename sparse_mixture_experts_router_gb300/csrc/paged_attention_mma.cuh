@@ -98,43 +98,61 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
   const uint8_t* kc = static_cast<const uint8_t*>(a.k_cache);
   const uint8_t* vc = static_cast<const uint8_t*>(a.v_cache);
   const int esz = kF8 ? 1 : 2;
-  const bool chunk_in = (lane % T::kChunks) * 16 < c.head_dim * esz;
+  // This lane's part of a key: its chunk, and where that is from the first
+  // key of a tile that lies in one page.
+  const uint32_t chunk_bytes = (lane % T::kChunks) * 16 < c.head_dim * esz ? 16u : 0u;
+  const int64_t token_step = c.token_stride * esz;
+  const int64_t lane_off = chunk_bytes ? lane / T::kChunks * token_step + lane % T::kChunks * 16 : 0;
+  const bool pages_hold_tiles = c.page_size % T::kKeys == 0;
   auto tile_key = [&](int i) { return rg.base + (rg.t0 + warp + kWarps * i) * T::kKeys; };
-  Slot slot;  // of this lane's key of the tile to load next
   auto look_up = [&](int i) {
-    slot = {-1, 0};
+    Slot slot = {-1, 0};
     if (i < mine) slot = slot_of(prm, it, rg, tile_key(i) + lane % T::kKeys);
+    return slot;
   };
-  auto load = [&](int i) {
+  auto load = [&](int i, const Slot& slot) {
     if (i < mine) {
-      const int64_t off = slot.page >= 0 ? slot.at(c, it.kh) * esz : -1;
+      const int64_t off = slot.in(c) ? slot.at(c, it.kh) * esz : -1;
+      const bool whole =
+          pages_hold_tiles && __all_sync(0xffffffffu, off >= 0);  // tiles start on their multiples
       const uint32_t st = ring + (i % kS) * T::kStage;
       constexpr int kPer = 32 / T::kChunks;  // keys one instruction copies
+      if (whole) {  // one page, every key of it: one offset and a step
+        const int64_t o = __shfl_sync(0xffffffffu, off, 0) + lane_off;
+        const uint8_t *ks = kc + o, *vs = vc + o;
 #pragma unroll
-      for (int k = 0; k < T::kKeys; k += kPer) {
-        const int key = k + lane / T::kChunks;
-        const int64_t o = __shfl_sync(0xffffffffu, off, key);
-        const uint32_t n = o >= 0 && chunk_in ? 16u : 0u;
-        const int64_t src = n ? o + (lane % T::kChunks) * 16 : 0;
-        const uint32_t dst = st + T::at(key, lane % T::kChunks);
-        ptx::cp_async16(dst, kc + src, n);
-        ptx::cp_async16(dst + T::kBytes, vc + src, n);
+        for (int k = 0; k < T::kKeys; k += kPer) {
+          const uint32_t dst = st + T::at(k + lane / T::kChunks, lane % T::kChunks);
+          ptx::cp_async16(dst, ks + k * token_step, chunk_bytes);
+          ptx::cp_async16(dst + T::kBytes, vs + k * token_step, chunk_bytes);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < T::kKeys; k += kPer) {
+          const int key = k + lane / T::kChunks;
+          const int64_t o = __shfl_sync(0xffffffffu, off, key);
+          const uint32_t n = o >= 0 ? chunk_bytes : 0u;
+          const int64_t src = n ? o + (lane % T::kChunks) * 16 : 0;
+          const uint32_t dst = st + T::at(key, lane % T::kChunks);
+          ptx::cp_async16(dst, kc + src, n);
+          ptx::cp_async16(dst + T::kBytes, vc + src, n);
+        }
       }
       if (kF8) {
-        const int64_t s = slot.page >= 0 ? slot.scale_at(c, it.kh) : 0;
-        const uint32_t n = slot.page >= 0 ? 4u : 0u, dst = st + 2 * T::kBytes + lane * 4;
+        const int64_t s = off >= 0 ? slot.scale_at(c, it.kh) : 0;
+        const uint32_t n = off >= 0 ? 4u : 0u, dst = st + 2 * T::kBytes + lane * 4;
         ptx::cp_async4(dst, a.k_scale + s, n);
         ptx::cp_async4(dst + T::kKeys * 4, a.v_scale + s, n);
       }
     }
     ptx::cp_async_commit();
   };
+  Slot ahead[kS];  // of this lane's key of the first tiles
 #pragma unroll
-  for (int i = 0; i < kS - 1; ++i) {
-    look_up(i);
-    load(i);
-  }
-  look_up(kS - 1);
+  for (int i = 0; i < kS; ++i) ahead[i] = look_up(i);
+#pragma unroll
+  for (int i = 0; i < kS - 1; ++i) load(i, ahead[i]);
+  Slot next = ahead[kS - 1];
 
   // ---- queries, as the second operand of S^T = K Q^T ----
   uint32_t q[kNT][kDT][2];
@@ -211,8 +229,8 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
   for (int i = 0; i < mine; ++i) {
     ptx::cp_async_wait_group<kS - 2>();
     __syncwarp();
-    load(i + kS - 1);  // into the stage that step i - 1 has read
-    look_up(i + kS);
+    load(i + kS - 1, next);  // into the stage that step i - 1 has read
+    next = look_up(i + kS);
     const uint32_t K = ring + (i % kS) * T::kStage, V = K + T::kBytes;
     const int key0 = tile_key(i);
 
@@ -262,6 +280,9 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
         }
     }
     const bool edge = key0 + T::kKeys - 1 > rg.hi_min || key0 < rg.lo_max;
+    // Weights against the running maximum; over the bound, the maximum is
+    // raised and they are taken again.
+    float p[kMT][kNT][4];
     bool raise = false;
 #pragma unroll
     for (int t = 0; t < kMT; ++t)
@@ -276,12 +297,12 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
             if (key > hi[n][x % 2] || key < lo[n][x % 2]) v = -INFINITY;
           }
           s[t][n][x] = v;
-          if (!kF8) {
+          p[t][n][x] = ptx::ex2(v - m[n][x % 2]);
+          if (!kF8)
             raise = raise || v > m[n][x % 2] + 8.f;
-          } else {
-            const float p = ptx::ex2(v - m[n][x % 2]);
-            raise = raise || !(p <= 0x1p68f && (v == -INFINITY || p * vs[t][x / 2] <= 256.f));
-          }
+          else  // 0 * vs may be a NaN of a key that is not seen
+            raise = raise || !(p[t][n][x] <= 0x1p68f) ||
+                    (v != -INFINITY && !(p[t][n][x] * vs[t][x / 2] <= 256.f));
         }
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -309,6 +330,10 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
             o[n][d][j] *= f;
             o[n][d][2 + j] *= f;
           }
+#pragma unroll
+          for (int t = 0; t < kMT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) p[t][n][2 * h + j] = ptx::ex2(s[t][n][2 * h + j] - top);
         }
     }
 #pragma unroll
@@ -317,9 +342,8 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const float p = ptx::ex2(s[t][n][x] - m[n][x % 2]);
-          l[n][x % 2] += p;
-          s[t][n][x] = kF8 && p > 0.f ? p * vs[t][x / 2] : p;
+          l[n][x % 2] += p[t][n][x];
+          if (kF8 && p[t][n][x] > 0.f) p[t][n][x] *= vs[t][x / 2];
         }
 
     // A key that some rows see and others do not may hold values that are not
@@ -351,7 +375,7 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
               for (int n = 0; n < kNT; ++n)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                  const float p = __shfl_sync(0xffffffffu, s[t][n][2 * h + j], 4 * k8 + quad);
+                  const float w = __shfl_sync(0xffffffffu, p[t][n][2 * h + j], 4 * k8 + quad);
                   if (key > hi[n][j] || key < lo[n][j]) continue;
 #pragma unroll
                   for (int d = 0; d < kDT; ++d)
@@ -367,7 +391,7 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
                         v = __uint_as_float(
                             (uint32_t) * reinterpret_cast<const uint16_t*>(smem + at + e % 8 * 2) << 16);
                       }
-                      o[n][d][2 * r + j] += p * v;
+                      o[n][d][2 * r + j] += w * v;
                     }
                 }
             }
@@ -384,7 +408,7 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float x = s[t][n][2 * h], y = s[t][n][2 * h + 1];
+          const float x = p[t][n][2 * h], y = p[t][n][2 * h + 1];
           if (kF8) {
             ph[t][n][h] = ptx::movmatrix_trans(pack_f16(x, y));
           } else {

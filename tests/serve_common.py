@@ -35,6 +35,7 @@ class Batch:
     seed: int = 0
     max_new: int = 0
     values: float = 1.0       # standard deviation of q
+    columns: int = 1          # of the block table, at least
 
     def __post_init__(self):
         rs = self.rs = np.random.RandomState(self.seed)
@@ -43,7 +44,7 @@ class Batch:
         pages = [-(-max(n, 0) // self.page) for n in self.length]
         self.n_pages = sum(pages) + self.spare
         ids = rs.permutation(self.n_pages)
-        self.table = np.full((self.B, max(1, max(pages, default=1))), -7, np.int32)  # unused: no page
+        self.table = np.full((self.B, max(self.columns, max(pages, default=1))), -7, np.int32)  # unused: no page
         at = 0
         for b, n in enumerate(pages):
             self.table[b, :n] = ids[at:at + n]

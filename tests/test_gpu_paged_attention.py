@@ -115,6 +115,34 @@ def test_long_sequences(cache):
 
 
 @pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("heads,kv_heads,dim", [(8, 1, 64), (20, 2, 128), (3, 3, 256)])
+def test_splits_of_few_sequences(cache, heads, kv_heads, dim):
+    """A wide block table with a sequence or two: the keys are cut into more
+    parts than a cluster has, most of them empty for a short sequence."""
+    for new, length in (([1], [1999]), ([3, 1], [700, 1]), ([1, 2], [0, 40])):
+        bt = Batch(new=new, length=length, heads=heads, kv_heads=kv_heads, dim=dim, page=16, cache=cache,
+                   columns=16384, seed=19)
+        assert moe.workspace_size(bt.cfg(), "attention") > 256
+        check(bt)
+
+
+@pytest.mark.parametrize("cache", CACHES)
+def test_values_not_finite_behind_a_row(cache):
+    """The last new token's value holds infinities: only its own row shows it."""
+    bt = Batch(new=[3], length=[45], heads=4, kv_heads=2, dim=64, page=16, cache=cache, seed=20)
+    page, at = int(bt.table[0, 44 // 16]), 44 % 16
+    if cache == "e4m3":
+        bt.v[page, at] = 0x7F
+    else:
+        bt.v[page, at] = float("inf")
+    out, lse, tol, _ = attention64(bt)
+    r = Call(bt)()
+    got = r.out.double().cpu().numpy()
+    assert (np.abs(got[:2] - out[:2]) <= tol[:2]).all()
+    assert not np.isfinite(got[2]).any()
+
+
+@pytest.mark.parametrize("cache", CACHES)
 def test_scale_and_strides(cache):
     for scale in (1.0, 1e-6, -0.2):
         check(Batch(new=[1, 2], length=[45, 70], heads=4, kv_heads=2, dim=64, page=16, cache=cache, q_pad=64, seed=8), scale)
