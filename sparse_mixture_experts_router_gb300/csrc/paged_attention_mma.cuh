@@ -25,9 +25,9 @@
 // Rounding: scores, maxima, sums and O are fp32. The weights p are rounded to
 // the type of the second product: bf16 twice (p = hi + lo, 2^-17 of p, two
 // products) for a bf16 cache, whose error one rounding would double; fp16
-// (2^-12) for an E4M3 cache. E4M3 elements and queries become fp16 exactly,
-// each query row scaled by a power of two, and the scales of keys multiply
-// scores, those of values multiply weights.
+// (2^-12) for an E4M3 cache. E4M3 keys meet queries in E4M3 products, each
+// query as a sum of two E4M3 terms; values become fp16 exactly. The scales of
+// keys multiply scores, those of values multiply weights.
 #pragma once
 #include "paged_attention.cuh"
 
@@ -49,11 +49,26 @@ struct Tile {
   // sequences 175 -> 173 us, 256 short ones in E4M3 130 -> 116 us; four
   // stages, one block an SM: 268 and 221 us).
   static constexpr int kStages = kStage >= 16384 || kNT == 4 ? 3 : kStage >= 8192 ? 2 : 4;
-  // Byte offset of 16-byte chunk c of key k: the chunks of 8 consecutive keys
-  // fall into different banks.
-  static __device__ __forceinline__ uint32_t at(int k, int c) {
-    return kChunks >= 8 ? (uint32_t)(k * kRow + ((c ^ (k & 7)) << 4))
-                        : (uint32_t)(k * kRow + ((c ^ ((k >> 1) & 3)) << 4));
+  // Byte offset of 16-byte chunk c of key k: chunk c of the 8 keys that one
+  // matrix load takes falls into 8 different bank groups. Those are 8
+  // consecutive keys, and of E4M3 keys also the 8 of 16 that agree in bit 1
+  // (see key_of).
+  static __host__ __device__ constexpr uint32_t at(int k, int c) {
+    if (!kF8) return (uint32_t)(k * kRow + ((c ^ (k & 7)) << 4));
+    const int mixed = (k & 5) | (((k >> 1) ^ (k >> 3)) & 1) << 1;
+    return (uint32_t)(k * kRow + ((c ^ (kChunks >= 8 ? mixed : mixed >> 1)) << 4));
+  }
+  // at() is linear over exclusive or, and stages start on multiples of 256
+  // bytes (bf16: 1024): one lane's addresses differ by a constant exclusive
+  // or (chunks, kChunkBit) or by a constant and one (keys), which is all that
+  // a copy or a matrix load then computes.
+  static constexpr uint32_t kChunkBit = 16;
+  static constexpr uint32_t key_xor(int k) { return at(k, 0) - (uint32_t)(k * kRow); }
+  // Row r (0..15) of a score product is this key of its 16. The byte-wise
+  // transposed load of values gives a lane 4 consecutive keys, and the second
+  // product pairs them with the weights' rows (2q, 2q+1, 2q+8, 2q+9).
+  static __host__ __device__ constexpr int key_of(int r) {
+    return kF8 ? (r % 8 / 2) * 4 + r / 8 * 2 + r % 2 : r;
   }
 };
 
@@ -63,6 +78,12 @@ constexpr int smem_bytes() {
          (2 * kWarps + 2) * 8 * kNT * 4;
 }
 
+// Two fp32 values as E4M3 codes, lo in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 // Two E4M3 codes (the low 16 bits of v) as fp16.
 __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t v) {
   uint32_t r;
@@ -103,6 +124,9 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
   const uint32_t chunk_bytes = (lane % T::kChunks) * 16 < c.head_dim * esz ? 16u : 0u;
   const int64_t token_step = c.token_stride * esz;
   const int64_t lane_off = chunk_bytes ? lane / T::kChunks * token_step + lane % T::kChunks * 16 : 0;
+  constexpr int kPer = 32 / T::kChunks;  // keys one instruction copies
+  const int64_t step = kPer * token_step;
+  const uint32_t copy_at = T::at(lane / T::kChunks, lane % T::kChunks);
   const bool pages_hold_tiles = c.page_size % T::kKeys == 0;
   auto tile_key = [&](int i) { return rg.base + (rg.t0 + warp + kWarps * i) * T::kKeys; };
   auto look_up = [&](int i) {
@@ -116,15 +140,14 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
       const bool whole =
           pages_hold_tiles && __all_sync(0xffffffffu, off >= 0);  // tiles start on their multiples
       const uint32_t st = ring + (i % kS) * T::kStage;
-      constexpr int kPer = 32 / T::kChunks;  // keys one instruction copies
       if (whole) {  // one page, every key of it: one offset and a step
         const int64_t o = __shfl_sync(0xffffffffu, off, 0) + lane_off;
         const uint8_t *ks = kc + o, *vs = vc + o;
 #pragma unroll
-        for (int k = 0; k < T::kKeys; k += kPer) {
-          const uint32_t dst = st + T::at(k + lane / T::kChunks, lane % T::kChunks);
-          ptx::cp_async16(dst, ks + k * token_step, chunk_bytes);
-          ptx::cp_async16(dst + T::kBytes, vs + k * token_step, chunk_bytes);
+        for (int k = 0; k < T::kKeys; k += kPer, ks += step, vs += step) {
+          const uint32_t dst = ((st + copy_at) ^ T::key_xor(k)) + k * T::kRow;
+          ptx::cp_async16(dst, ks, chunk_bytes);
+          ptx::cp_async16(dst + T::kBytes, vs, chunk_bytes);
         }
       } else {
 #pragma unroll
@@ -133,7 +156,7 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
           const int64_t o = __shfl_sync(0xffffffffu, off, key);
           const uint32_t n = o >= 0 ? chunk_bytes : 0u;
           const int64_t src = n ? o + (lane % T::kChunks) * 16 : 0;
-          const uint32_t dst = st + T::at(key, lane % T::kChunks);
+          const uint32_t dst = ((st + copy_at) ^ T::key_xor(k)) + k * T::kRow;
           ptx::cp_async16(dst, kc + src, n);
           ptx::cp_async16(dst + T::kBytes, vc + src, n);
         }
@@ -155,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
   Slot next = ahead[kS - 1];
 
   // ---- queries, as the second operand of S^T = K Q^T ----
-  uint32_t q[kNT][kDT][2];
+  uint32_t q[kNT][kDT][2];  // bf16: elements 0-7 and 8-15 of a product's 16; E4M3: high and low terms
   float sc[kNT][2];  // factor of the scores of this lane's two columns, log2 units
   const float scale = c.scale * 1.4426950408889634f;
 #pragma unroll
@@ -172,38 +195,51 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
               e < c.head_dim ? *reinterpret_cast<const uint32_t*>(p + 2 * (e + 2 * quad)) : 0u;
         }
     } else {
-      // Four consecutive elements a lane: keys are read in the same order, so
-      // the products pair up. The row is scaled to [1, 2) for fp16.
+      // Four consecutive elements a lane and chunk. The row is scaled by a
+      // power of two to the top of E4M3's range and split into two E4M3 terms,
+      // high and low: exact but for elements below 2^-9 of the row's largest,
+      // which are off by up to 2^-18 of that.
       uint2 raw[kDT];
-      float amax = 0.f;
+      float amax = 0.f, odd = 0.f;  // odd: a NaN where the row has one, or an infinity
+      auto value = [&](int d, int x) {
+        const uint32_t w = x < 2 ? raw[d].x : raw[d].y;
+        return __uint_as_float(x % 2 ? w & 0xffff0000u : w << 16);
+      };
 #pragma unroll
       for (int d = 0; d < kDT; ++d) {
         raw[d] = make_uint2(0u, 0u);
-        if (16 * d < c.head_dim)
-          raw[d] = *reinterpret_cast<const uint2*>(p + 2 * (16 * d + 4 * quad));
-        float x, y;
-        bf16x2_to_f32(raw[d].x, x, y);
-        amax = fmaxf(amax, fmaxf(fabsf(x), fabsf(y)));
-        bf16x2_to_f32(raw[d].y, x, y);
-        amax = fmaxf(amax, fmaxf(fabsf(x), fabsf(y)));
+        if (16 * d < c.head_dim) raw[d] = *reinterpret_cast<const uint2*>(p + 2 * (16 * d + 4 * quad));
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          amax = fmaxf(amax, fabsf(value(d, x)));
+          odd = fmaf(value(d, x), 0.f, odd);
+        }
       }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      // 2^-e and 2^e of the row's largest, kept normal
-      const int e = clamp_int((int)(__float_as_uint(amax) >> 23) - 127, -126, 126);
-      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+      odd += __shfl_xor_sync(0xffffffffu, odd, 1);
+      odd += __shfl_xor_sync(0xffffffffu, odd, 2);
+      // 2^e times the largest is in (224, 448]; e and -e kept in fp32's range
+      const uint32_t bits = __float_as_uint(amax);
+      const int e = clamp_int(127 + 8 - (int)(bits >> 23) - ((bits & 0x7fffffu) > 0x600000u), -126, 126);
       const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+      const float back = __uint_as_float((uint32_t)(127 - e) << 23) + odd;
 #pragma unroll
       for (int d = 0; d < kDT; ++d) {
-        float x, y;
-        bf16x2_to_f32(raw[d].x, x, y);
-        q[n][d][0] = pack_f16(x * down, y * down);
-        bf16x2_to_f32(raw[d].y, x, y);
-        q[n][d][1] = pack_f16(x * down, y * down);
+        float high[4], low[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) high[x] = value(d, x) * up;
+        q[n][d][0] = e4m3x2(high[0], high[1]) | e4m3x2(high[2], high[3]) << 16;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t h = e4m3x2_f16(q[n][d][0] >> x / 2 * 16) >> x % 2 * 16;
+          low[x] = high[x] - __half2float(__ushort_as_half((uint16_t)h));
+        }
+        q[n][d][1] = e4m3x2(low[0], low[1]) | e4m3x2(low[2], low[3]) << 16;
       }
       // columns 2 quad and 2 quad + 1 belong to the lanes of those rows
-      sc[n][0] *= __shfl_sync(0xffffffffu, up, 8 * quad);
-      sc[n][1] *= __shfl_sync(0xffffffffu, up, 8 * quad + 4);
+      sc[n][0] *= __shfl_sync(0xffffffffu, back, 8 * quad);
+      sc[n][1] *= __shfl_sync(0xffffffffu, back, 8 * quad + 4);
     }
   }
   int hi[kNT][2], lo[kNT][2];
@@ -216,6 +252,9 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
     }
 
   // ---- the pass over the keys ----
+  const uint32_t k_lane = T::at(T::key_of(lane % 16), lane / 16);
+  const uint32_t v_lane =
+      kF8 ? T::at(lane, 0) : T::at(lane % 8 + lane / 16 * 8, lane / 8 % 2);
   float o[kNT][kDT][4], m[kNT][2], l[kNT][2];
 #pragma unroll
   for (int n = 0; n < kNT; ++n) {
@@ -232,6 +271,7 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
     load(i + kS - 1, next);  // into the stage that step i - 1 has read
     next = look_up(i + kS);
     const uint32_t K = ring + (i % kS) * T::kStage, V = K + T::kBytes;
+    const uint32_t k_at = K + k_lane, v_at = V + v_lane;
     const int key0 = tile_key(i);
 
     float s[kMT][kNT][4];
@@ -245,7 +285,7 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
 #pragma unroll
       for (int d = 0; d < kDT; ++d) {
         uint32_t k[4];
-        ptx::ldmatrix4<false>(K + T::at(lane % 16, 2 * d + lane / 16), k);
+        ptx::ldmatrix4<false>(k_at ^ 2 * d * T::kChunkBit, k);
 #pragma unroll
         for (int n = 0; n < kNT; ++n) ptx::mma16816<false>(s[0][n], k, q[n][d][0], q[n][d][1]);
       }
@@ -255,19 +295,17 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
 #pragma unroll
         for (int d = 0; d < kDT; d += 2) {
           uint32_t r[4];
-          ptx::ldmatrix4<false>(K + T::at(16 * t + lane % 16, d + lane / 16), r);
+          ptx::ldmatrix4<false>((k_at ^ d * T::kChunkBit ^ T::key_xor(16 * t)) + 16 * t * T::kRow, r);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t k[4] = {e4m3x2_f16(r[2 * h]), e4m3x2_f16(r[2 * h + 1]),
-                                   e4m3x2_f16(r[2 * h] >> 16), e4m3x2_f16(r[2 * h + 1] >> 16)};
+          for (int h = 0; h < 2; ++h)  // high terms, low terms
 #pragma unroll
             for (int n = 0; n < kNT; ++n)
-              ptx::mma16816<true>(s[t][n], k, q[n][d + h][0], q[n][d + h][1]);
-          }
+              ptx::mma16832_e4m3(s[t][n], r, q[n][d][h], q[n][d + 1][h]);
         }
     }
 
-    // Scores of keys key0 + 16 t + oct (+ 8), columns 2 quad (+ 1).
+    // Scores of keys key0 + 16 t + key_of(oct) (and of oct + 8), columns 2 quad
+    // (+ 1).
     float ks[kMT][2], vs[kMT][2];
     if (kF8) {
       const float* f = reinterpret_cast<const float*>(smem + (V + T::kBytes - ptx::smem_addr(smem)));
@@ -275,8 +313,8 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
       for (int t = 0; t < kMT; ++t)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          ks[t][h] = f[16 * t + 8 * h + oct];
-          vs[t][h] = f[T::kKeys + 16 * t + 8 * h + oct];
+          ks[t][h] = f[16 * t + T::key_of(8 * h + oct)];
+          vs[t][h] = f[T::kKeys + 16 * t + T::key_of(8 * h + oct)];
         }
     }
     const bool edge = key0 + T::kKeys - 1 > rg.hi_min || key0 < rg.lo_max;
@@ -293,7 +331,7 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
           float v = s[t][n][x] * sc[n][x % 2];
           if (kF8) v *= ks[t][x / 2];
           if (edge) {
-            const int key = key0 + 16 * t + 8 * (x / 2) + oct;
+            const int key = key0 + 16 * t + T::key_of(8 * (x / 2) + oct);
             if (key > hi[n][x % 2] || key < lo[n][x % 2]) v = -INFINITY;
           }
           s[t][n][x] = v;
@@ -370,7 +408,7 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
           for (int h = 0; h < 2; ++h)
 #pragma unroll 1
             for (int k8 = 0; k8 < 8; ++k8) {
-              const int k = 16 * t + 8 * h + k8, key = key0 + k;
+              const int k = 16 * t + T::key_of(8 * h + k8), key = key0 + k;
 #pragma unroll
               for (int n = 0; n < kNT; ++n)
 #pragma unroll
@@ -381,7 +419,7 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
                   for (int d = 0; d < kDT; ++d)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                      const int e = kF8 ? 16 * d + 2 * oct + r : 16 * d + oct + 8 * r;
+                      const int e = 16 * d + oct + 8 * r;
                       const uint32_t at = V - ptx::smem_addr(smem) + T::at(k, e * (kF8 ? 1 : 2) / 16);
                       float v;
                       if (kF8) {
@@ -423,22 +461,18 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
     for (int d = 0; d < kDT; ++d) {
       uint32_t r[4];
       if (!kF8) {
-        ptx::ldmatrix4<true>(V + T::at(lane % 8 + lane / 16 * 8, 2 * d + lane / 8 % 2), r);
+        ptx::ldmatrix4<true>(v_at ^ 2 * d * T::kChunkBit, r);
 #pragma unroll
         for (int n = 0; n < kNT; ++n) ptx::mma16816<false>(o[n][d], r, ph[0][n][0], ph[0][n][1]);
 #pragma unroll
         for (int n = 0; n < kNT; ++n) ptx::mma16816<false>(o[n][d], r, pl[0][n][0], pl[0][n][1]);
       } else {
-        // 16-bit units of V are element pairs (2 oct, 2 oct + 1): rows 0-7 of
-        // the product take the even elements and rows 8-15 the odd ones.
-        ptx::ldmatrix4<true>(V + T::at(lane, d), r);
+        ptx::ldmatrix2_bytes_trans(v_at ^ d * T::kChunkBit, r);
 #pragma unroll
         for (int t = 0; t < kMT; ++t) {
           const uint32_t x = r[2 * t], y = r[2 * t + 1];
-          const uint32_t v[4] = {e4m3x2_f16(__byte_perm(x, 0, 0x4420)),
-                                 e4m3x2_f16(__byte_perm(x, 0, 0x4431)),
-                                 e4m3x2_f16(__byte_perm(y, 0, 0x4420)),
-                                 e4m3x2_f16(__byte_perm(y, 0, 0x4431))};
+          const uint32_t v[4] = {e4m3x2_f16(x), e4m3x2_f16(y), e4m3x2_f16(x >> 16),
+                                 e4m3x2_f16(y >> 16)};
 #pragma unroll
           for (int n = 0; n < kNT; ++n) ptx::mma16816<true>(o[n][d], v, ph[t][n][0], ph[t][n][1]);
         }
@@ -487,7 +521,7 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
       for (int d = 0; d < kDT; ++d)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          mine_o[r * kLd + (kF8 ? 16 * d + 2 * oct + h : 16 * d + oct + 8 * h)] =
+          mine_o[r * kLd + 16 * d + oct + 8 * h] =
               o[n][d][2 * h + j] * f;
     }
   __syncthreads();
