@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const int r = i % block_rows, rb = it.index % prm.row_blocks, head = it.index / prm.row_blocks;
   it.kh = head % c.n_kv_heads;
   it.sq = seq_range(prm.a, head / c.n_kv_heads);
-  it.G = c.n_heads / c.n_kv_heads;
+  it.G = prm.group;
   it.row0 = rb * block_rows;
   if (it.row0 + r >= it.G * it.sq.n) return;
   const int64_t row0 = (int64_t)it.index * prm.splits * attn::kMaxRows + r;
@@ -119,10 +119,17 @@ cudaError_t launch_paged_attention(const AttnArgs& a, void* scratch, cudaStream_
   const Plan plan = plan_of(c);
   attn::Params prm = {};
   prm.a = a;
-  prm.page_div = attn::fast_div((uint32_t)c.page_size);
   prm.parts = plan.parts;
   prm.splits = plan.splits;
   prm.row_blocks = plan.row_blocks;
+  prm.group = c.n_heads / c.n_kv_heads;
+  prm.by_page = attn::fast_div((uint32_t)c.page_size);
+  prm.by_group = attn::fast_div((uint32_t)prm.group);
+  prm.by_parts = attn::fast_div((uint32_t)prm.parts);
+  prm.by_splits = attn::fast_div((uint32_t)prm.splits);
+  prm.by_rows = attn::fast_div((uint32_t)prm.row_blocks);
+  prm.by_heads = attn::fast_div((uint32_t)c.n_kv_heads);
+  prm.by_vecs = attn::fast_div((uint32_t)c.head_dim / 4);
   prm.split_o = static_cast<float*>(scratch);
   prm.split_ml = reinterpret_cast<float2*>(prm.split_o + split_rows(plan) * c.head_dim);
   const unsigned blocks = (unsigned)((plan.items * plan.splits + 1) * plan.parts);

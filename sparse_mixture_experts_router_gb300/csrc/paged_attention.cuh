@@ -37,9 +37,12 @@ __device__ __forceinline__ int div(const FastDiv& f, int n) {
 
 struct Params {
   AttnArgs a;
-  FastDiv page_div;
   int parts, splits;
   int row_blocks;  // of one (sequence, key-value head)
+  int group;       // heads a key-value head
+  // divisions by page_size, heads a key-value head, parts, splits,
+  // row_blocks, n_kv_heads and head_dim / 4
+  FastDiv by_page, by_group, by_parts, by_splits, by_rows, by_heads, by_vecs;
   // splits > 1: O [item][split][kMaxRows][head_dim] relative to its maximum,
   // and (maximum in log2 units, sum) [item][split][kMaxRows]
   float* split_o;
@@ -63,14 +66,16 @@ struct Item {
   __device__ __forceinline__ int clip(int r) const { return row0 + min(r, rows - 1); }
   // Position of row r's token and the first it sees. Rows past the last one
   // repeat it and are not written.
-  __device__ __forceinline__ int pos(int r) const { return sq.len - sq.n + clip(r) / G; }
+  __device__ __forceinline__ int pos(const Params& p, int r) const {
+    return sq.len - sq.n + div(p.by_group, clip(r));
+  }
   __device__ __forceinline__ int first(int at) const {
     return window ? max(0, at - window + 1) : 0;
   }
   // Elements from q's start to row r.
-  __device__ __forceinline__ int64_t q_at(const moe_attn_config& c, int r) const {
-    const int g = clip(r);
-    return (int64_t)(sq.row0 + g / G) * c.q_stride + (int64_t)(kh * G + g % G) * c.head_dim;
+  __device__ __forceinline__ int64_t q_at(const Params& p, int r) const {
+    const int g = clip(r), j = div(p.by_group, g);
+    return (int64_t)(sq.row0 + j) * p.a.c.q_stride + (kh * G + g - j * G) * p.a.c.head_dim;
   }
 };
 // This block's item, false where it has none (the first cluster checks the
@@ -78,20 +83,24 @@ struct Item {
 template <int kThreads>
 __device__ __forceinline__ bool item_of(const Params& p, int block_rows, Item& it) {
   const moe_attn_config& c = p.a.c;
-  it.part = (int)(blockIdx.x % p.parts);
-  int i = (int)(blockIdx.x / p.parts) - 1;
-  if (i < 0) {
+  int i = div(p.by_parts, (int)blockIdx.x);
+  it.part = (int)blockIdx.x - i * p.parts;
+  if (--i < 0) {
     if (it.part == 0) check_lists<kThreads>(p.a, FirstKey{c.window});
     return false;
   }
-  it.split = i % p.splits;
-  it.index = i /= p.splits;
-  const int rb = i % p.row_blocks;
-  i /= p.row_blocks;
-  it.kh = i % c.n_kv_heads;
-  it.b = i / c.n_kv_heads;
+  auto next = [&](const FastDiv& f, int d) {  // i / d, and the remainder
+    const int q = div(f, i), r = i - q * d;
+    i = q;
+    return r;
+  };
+  it.split = next(p.by_splits, p.splits);
+  it.index = i;
+  const int rb = next(p.by_rows, p.row_blocks);
+  it.kh = next(p.by_heads, c.n_kv_heads);
+  it.b = i;
   it.sq = seq_range(p.a, it.b);
-  it.G = c.n_heads / c.n_kv_heads;
+  it.G = p.group;
   it.row0 = rb * block_rows;
   it.rows = min(block_rows, it.G * it.sq.n - it.row0);
   it.window = c.window;
@@ -108,15 +117,16 @@ struct Range {
 __device__ __forceinline__ Range range_of(const Params& p, const Item& it, int block_rows,
                                           int keys) {
   Range r;
-  r.hi_min = it.pos(0);
-  r.hi_max = it.pos(block_rows - 1);
+  r.hi_min = it.pos(p, 0);
+  r.hi_max = it.pos(p, block_rows - 1);
   r.lo_min = it.first(r.hi_min);
   r.lo_max = it.first(r.hi_max);
   r.base = r.lo_min / keys * keys;
-  const long long tiles = r.hi_max < 0 ? 0 : (r.hi_max - r.base) / keys + 1;
+  const int tiles = r.hi_max < 0 ? 0 : (r.hi_max - r.base) / keys + 1;
   const int at = it.split * p.parts + it.part, of = p.splits * p.parts;
-  r.t0 = (int)(tiles * at / of);
-  r.t1 = (int)(tiles * (at + 1) / of);
+  const int each = tiles / of, more = tiles - each * of;  // the first `more` blocks take one more
+  r.t0 = at * each + min(at, more);
+  r.t1 = r.t0 + each + (at < more);
   return r;
 }
 
@@ -139,7 +149,7 @@ struct Slot {
 __device__ __forceinline__ Slot slot_of(const Params& p, const Item& it, const Range& r, int key) {
   Slot s = {-1, 0};
   if (key >= r.lo_min && key <= r.hi_max) {
-    const int n = div(p.page_div, key);
+    const int n = div(p.by_page, key);
     s.place = key - n * p.a.c.page_size;
     s.page = __ldg(p.a.table + (int64_t)it.b * p.a.c.max_pages + n);
   }
@@ -170,20 +180,33 @@ __device__ __forceinline__ void write_row(const Params& p, const Item& it, int r
   const float f = 1.f / sum;  // a NaN stays one
   x = sum == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
                  : make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
-  const int g = it.row0 + r;
-  const int64_t at = (int64_t)(it.sq.row0 + g / it.G) * c.n_heads + it.kh * it.G + g % it.G;
-  store4(static_cast<Elem*>(p.a.out), at * vecs + v, x);
+  const int g = it.row0 + r, j = div(p.by_group, g);
+  const int at = (it.sq.row0 + j) * c.n_heads + it.kh * it.G + g - j * it.G;  // T * Hq < 2^30
+  store4(static_cast<Elem*>(p.a.out), (int64_t)at * vecs + v, x);
   if (v == 0 && p.a.lse)
     p.a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
+// Where the blocks of a cluster leave what one of them joins: (maximum, sum)
+// of every block's rows, and of O the slice of rows x vectors that this block
+// writes, from every block.
+template <int kRows, int kDim>
+struct Inbox {
+  float2 ml[kMaxParts][kRows];
+  // slices of ceil(n / parts) of the n <= kRows * kDim / 4 vectors
+  float4 o[kRows * kDim / 4 + kMaxParts];
+};
+
 // Joins a block's kWarps partial O (row r at o + w * stride + r * ld floats,
 // all relative to the block's maximum joined[r]; joined[kRows + r] its sum of
-// weights) and then the cluster's blocks, and writes the rows.
-template <int kRows, int kWarps, int kThreads, typename Elem>
-__device__ __forceinline__ void finish(const Params& p, const Item& it, float* o, int stride, int ld,
-                                       const float* joined) {
-  const int vecs = p.a.c.head_dim / 4;
+// weights) and then the cluster's blocks, and writes the rows. Each block
+// sends every other its slice and then reads its own shared memory only: one
+// barrier, and none to keep blocks from leaving. The cluster's blocks have
+// all started (start_cluster) before the first sends.
+template <int kRows, int kDim, int kWarps, int kThreads, typename Elem>
+__device__ __forceinline__ void finish(const Params& p, const Item& it, const float* o, int stride,
+                                       int ld, const float* joined, Inbox<kRows, kDim>* inbox) {
+  const int vecs = p.a.c.head_dim / 4, n = it.rows * vecs;
   auto block_sum = [&](int r, int v) {
     float4 x = *reinterpret_cast<const float4*>(o + r * ld + 4 * v);
 #pragma unroll
@@ -194,37 +217,51 @@ __device__ __forceinline__ void finish(const Params& p, const Item& it, float* o
     return x;
   };
   if (p.parts == 1) {
-    for (int i = threadIdx.x; i < it.rows * vecs; i += kThreads) {
-      const int r = i / vecs, v = i - r * vecs;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const int r = div(p.by_vecs, i), v = i - r * vecs;
       write_row<Elem>(p, it, r, v, block_sum(r, v), joined[r], joined[kRows + r]);
     }
     return;
   }
-  if (kWarps > 1)  // the block's O, in the first warp's place
-    for (int i = threadIdx.x; i < it.rows * vecs; i += kThreads) {
-      const int r = i / vecs, v = i - r * vecs;
-      *reinterpret_cast<float4*>(o + r * ld + 4 * v) = block_sum(r, v);
-    }
+  const int slice = div(p.by_parts, n + p.parts - 1);
+  __syncwarp();
+  ptx::cluster_wait();  // pairs with start_cluster
+  for (int i = threadIdx.x; i < kRows * p.parts; i += kThreads) {
+    const int r = div(p.by_parts, i);
+    ptx::st_cluster_v2(
+        ptx::mapa_shared(ptx::smem_addr(&inbox->ml[it.part][r]), i - r * p.parts), joined[r],
+        joined[kRows + r]);
+  }
+  int to = 0;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int r = div(p.by_vecs, i), v = i - r * vecs;
+    while ((to + 1) * slice <= i) ++to;
+    ptx::st_cluster_v4(
+        ptx::mapa_shared(ptx::smem_addr(&inbox->o[it.part * slice + i - to * slice]), to),
+        block_sum(r, v));
+  }
   __syncwarp();
   ptx::cluster_sync();
-  const uint32_t o_at = ptx::smem_addr(o), joined_at = ptx::smem_addr(joined);
-  for (int i = it.part * kThreads + threadIdx.x; i < it.rows * vecs; i += p.parts * kThreads) {
-    const int r = i / vecs, v = i - r * vecs;
+  const int i0 = it.part * slice;
+  for (int i = i0 + threadIdx.x; i < min(i0 + slice, n); i += kThreads) {
+    const int r = div(p.by_vecs, i), v = i - r * vecs;
     float top = -INFINITY, sum = 0.f;
-    for (int b = 0; b < p.parts; ++b)
-      top = fmaxf(top, ptx::ld_cluster_f32(ptx::mapa_shared(joined_at + r * 4, b)));
+#pragma unroll 4
+    for (int b = 0; b < p.parts; ++b) top = fmaxf(top, inbox->ml[b][r].x);
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int b = 0; b < p.parts; ++b) {
-      const uint32_t jb = ptx::mapa_shared(joined_at + r * 4, b);
-      const float f = ptx::ex2(ptx::ld_cluster_f32(jb) - top);
-      const float4 y = ptx::ld_cluster_v4(ptx::mapa_shared(o_at + (r * ld + 4 * v) * 4, b));
-      sum += ptx::ld_cluster_f32(jb + kRows * 4) * f;
+      const float2 ml = inbox->ml[b][r];
+      const float4 y = inbox->o[b * slice + i - i0];
+      const float f = ptx::ex2(ml.x - top);
+      sum += ml.y * f;
       x.x += y.x * f, x.y += y.y * f, x.z += y.z * f, x.w += y.w * f;
     }
     write_row<Elem>(p, it, r, v, x, top, sum);
   }
-  __syncwarp();
-  ptx::cluster_sync();  // no block leaves while another reads its memory
+}
+__device__ __forceinline__ void start_cluster(const Params& p) {
+  if (p.parts > 1) ptx::cluster_arrive();
 }
 
 // Sets a kernel's shared memory and cluster attributes (once a thread and

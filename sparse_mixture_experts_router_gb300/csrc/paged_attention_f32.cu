@@ -41,7 +41,8 @@ struct Smem {
   static constexpr int kQ = kRows * (kDim + 4) * 4;
   static constexpr int kP = kWarps * kKeys * kRows * 4;
   static constexpr int kStat = (2 * kWarps + 2) * kRows * 4;
-  static constexpr int kAll = kRing + kQ + kP + kStat;
+  static constexpr int kInbox = (int)sizeof(Inbox<kRows, kDim>);
+  static constexpr int kAll = kRing + kInbox + kQ + kP + kStat;
 };
 
 template <int kDim, int kR>
@@ -56,15 +57,18 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const __grid_constant__ P
   const AttnArgs& a = prm.a;
   const moe_attn_config& c = a.c;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, key8 = lane % 8, rg = lane / 8;
-  float* qs = reinterpret_cast<float*>(smem + M::kRing);
-  float* ps = reinterpret_cast<float*>(smem + M::kRing + M::kQ) + warp * kKeys * kRows;
-  float* stat = reinterpret_cast<float*>(smem + M::kRing + M::kQ + M::kP);
+  auto* inbox = reinterpret_cast<Inbox<kRows, kDim>*>(smem + M::kRing);
+  uint8_t* rest = smem + M::kRing + M::kInbox;
+  float* qs = reinterpret_cast<float*>(rest);
+  float* ps = reinterpret_cast<float*>(rest + M::kQ) + warp * kKeys * kRows;
+  float* stat = reinterpret_cast<float*>(rest + M::kQ + M::kP);
   float* joined = stat + 2 * kWarps * kRows;
 
   pdl_wait();
   pdl_trigger();
   Item it;
   if (!item_of<kThreads>(prm, kRows, it)) return;
+  start_cluster(prm);
   const Range rg_ = range_of(prm, it, kRows, kKeys);
   const int mine = rg_.t1 - rg_.t0 > warp ? (rg_.t1 - rg_.t0 - warp - 1) / kWarps + 1 : 0;
 
@@ -111,14 +115,14 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const __grid_constant__ P
     const int r = i / T::kChunks, v = i % T::kChunks;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (4 * v < c.head_dim)
-      x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + it.q_at(c, r) + 4 * v);
+      x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + it.q_at(prm, r) + 4 * v);
     *reinterpret_cast<float4*>(qs + r * (kDim + 4) + 4 * v) = x;
   }
   __syncthreads();
   int hi[kR], lo[kR];  // of this lane's rows rg + 4 i
 #pragma unroll
   for (int i = 0; i < kR; ++i) {
-    hi[i] = it.pos(rg + 4 * i);
+    hi[i] = it.pos(prm, rg + 4 * i);
     lo[i] = it.first(hi[i]);
   }
 
@@ -142,8 +146,8 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const __grid_constant__ P
     float s[kR];
 #pragma unroll
     for (int r = 0; r < kR; ++r) s[r] = 0.f;
-#pragma unroll 8
-    for (int v = 0; v < T::kChunks; ++v) {
+#pragma unroll 4
+    for (int v = 0; v < c.head_dim / 4; ++v) {
       const float4 k = *reinterpret_cast<const float4*>(K + T::at(key8, v));
 #pragma unroll
       for (int r = 0; r < kR; ++r) {
@@ -258,8 +262,8 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const __grid_constant__ P
     }
   }
   __syncthreads();
-  finish<kRows, kWarps, kThreads, float>(prm, it, reinterpret_cast<float*>(smem),
-                                         kS * T::kStage / 4, kLd, joined);
+  finish<kRows, kDim, kWarps, kThreads, float>(prm, it, reinterpret_cast<float*>(smem),
+                                               kS * T::kStage / 4, kLd, joined, inbox);
 }
 
 template <int kDim, int kR>

@@ -25,9 +25,11 @@
 // Rounding: scores, maxima, sums and O are fp32. The weights p are rounded to
 // the type of the second product: bf16 twice (p = hi + lo, 2^-17 of p, two
 // products) for a bf16 cache, whose error one rounding would double; fp16
-// (2^-12) for an E4M3 cache. E4M3 keys meet queries in E4M3 products, each
-// query as a sum of two E4M3 terms; values become fp16 exactly. The scales of
-// keys multiply scores, those of values multiply weights.
+// (2^-12) for an E4M3 cache, whose elements and queries become fp16 (exactly;
+// each query row scaled by a power of two first). Scores by E4M3 products, with
+// queries as sums of two E4M3 terms, took 108 us where these take 101 (256
+// sequences of 1 to 2047 keys, 8 rows). The scales of keys multiply scores,
+// those of values multiply weights.
 #pragma once
 #include "paged_attention.cuh"
 
@@ -75,15 +77,9 @@ struct Tile {
 template <int kDim, int kNT, bool kF8>
 constexpr int smem_bytes() {
   return kWarps * Tile<kDim, kNT, kF8>::kStages * Tile<kDim, kNT, kF8>::kStage +
-         (2 * kWarps + 2) * 8 * kNT * 4;
+         (int)sizeof(Inbox<8 * kNT, kDim>) + (2 * kWarps + 2) * 8 * kNT * 4;
 }
 
-// Two fp32 values as E4M3 codes, lo in the low byte.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 // Two E4M3 codes (the low 16 bits of v) as fp16.
 __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t v) {
   uint32_t r;
@@ -104,13 +100,15 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
   const AttnArgs& a = prm.a;
   const moe_attn_config& c = a.c;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, quad = lane % 4, oct = lane / 4;
-  float* stat = reinterpret_cast<float*>(smem + kWarps * kS * T::kStage);  // m, l of each warp's rows
-  float* joined = stat + 2 * kWarps * kRows;                               // m, l of the block's
+  auto* inbox = reinterpret_cast<Inbox<kRows, kDim>*>(smem + kWarps * kS * T::kStage);
+  float* stat = reinterpret_cast<float*>(inbox + 1);  // m, l of each warp's rows
+  float* joined = stat + 2 * kWarps * kRows;          // m, l of the block's
 
   pdl_wait();
   pdl_trigger();
   Item it;
   if (!item_of<kThreads>(prm, kRows, it)) return;
+  start_cluster(prm);
   const Range rg = range_of(prm, it, kRows, T::kKeys);
   const int mine = rg.t1 - rg.t0 > warp ? (rg.t1 - rg.t0 - warp - 1) / kWarps + 1 : 0;
 
@@ -178,12 +176,12 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
   Slot next = ahead[kS - 1];
 
   // ---- queries, as the second operand of S^T = K Q^T ----
-  uint32_t q[kNT][kDT][2];  // bf16: elements 0-7 and 8-15 of a product's 16; E4M3: high and low terms
+  uint32_t q[kNT][kDT][2];
   float sc[kNT][2];  // factor of the scores of this lane's two columns, log2 units
   const float scale = c.scale * 1.4426950408889634f;
 #pragma unroll
   for (int n = 0; n < kNT; ++n) {
-    const uint8_t* p = static_cast<const uint8_t*>(a.q) + it.q_at(c, 8 * n + oct) * 2;
+    const uint8_t* p = static_cast<const uint8_t*>(a.q) + it.q_at(prm, 8 * n + oct) * 2;
     sc[n][0] = sc[n][1] = scale;
     if (!kF8) {
 #pragma unroll
@@ -195,51 +193,38 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
               e < c.head_dim ? *reinterpret_cast<const uint32_t*>(p + 2 * (e + 2 * quad)) : 0u;
         }
     } else {
-      // Four consecutive elements a lane and chunk. The row is scaled by a
-      // power of two to the top of E4M3's range and split into two E4M3 terms,
-      // high and low: exact but for elements below 2^-9 of the row's largest,
-      // which are off by up to 2^-18 of that.
+      // Four consecutive elements a lane: keys are read in the same order, so
+      // the products pair up. The row is scaled to [1, 2) for fp16.
       uint2 raw[kDT];
-      float amax = 0.f, odd = 0.f;  // odd: a NaN where the row has one, or an infinity
-      auto value = [&](int d, int x) {
-        const uint32_t w = x < 2 ? raw[d].x : raw[d].y;
-        return __uint_as_float(x % 2 ? w & 0xffff0000u : w << 16);
-      };
+      float amax = 0.f;
 #pragma unroll
       for (int d = 0; d < kDT; ++d) {
         raw[d] = make_uint2(0u, 0u);
-        if (16 * d < c.head_dim) raw[d] = *reinterpret_cast<const uint2*>(p + 2 * (16 * d + 4 * quad));
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          amax = fmaxf(amax, fabsf(value(d, x)));
-          odd = fmaf(value(d, x), 0.f, odd);
-        }
+        if (16 * d < c.head_dim)
+          raw[d] = *reinterpret_cast<const uint2*>(p + 2 * (16 * d + 4 * quad));
+        float x, y;
+        bf16x2_to_f32(raw[d].x, x, y);
+        amax = fmaxf(amax, fmaxf(fabsf(x), fabsf(y)));
+        bf16x2_to_f32(raw[d].y, x, y);
+        amax = fmaxf(amax, fmaxf(fabsf(x), fabsf(y)));
       }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      odd += __shfl_xor_sync(0xffffffffu, odd, 1);
-      odd += __shfl_xor_sync(0xffffffffu, odd, 2);
-      // 2^e times the largest is in (224, 448]; e and -e kept in fp32's range
-      const uint32_t bits = __float_as_uint(amax);
-      const int e = clamp_int(127 + 8 - (int)(bits >> 23) - ((bits & 0x7fffffu) > 0x600000u), -126, 126);
+      // 2^-e and 2^e of the row's largest, kept normal
+      const int e = clamp_int((int)(__float_as_uint(amax) >> 23) - 127, -126, 126);
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
       const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-      const float back = __uint_as_float((uint32_t)(127 - e) << 23) + odd;
 #pragma unroll
       for (int d = 0; d < kDT; ++d) {
-        float high[4], low[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) high[x] = value(d, x) * up;
-        q[n][d][0] = e4m3x2(high[0], high[1]) | e4m3x2(high[2], high[3]) << 16;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t h = e4m3x2_f16(q[n][d][0] >> x / 2 * 16) >> x % 2 * 16;
-          low[x] = high[x] - __half2float(__ushort_as_half((uint16_t)h));
-        }
-        q[n][d][1] = e4m3x2(low[0], low[1]) | e4m3x2(low[2], low[3]) << 16;
+        float x, y;
+        bf16x2_to_f32(raw[d].x, x, y);
+        q[n][d][0] = pack_f16(x * down, y * down);
+        bf16x2_to_f32(raw[d].y, x, y);
+        q[n][d][1] = pack_f16(x * down, y * down);
       }
       // columns 2 quad and 2 quad + 1 belong to the lanes of those rows
-      sc[n][0] *= __shfl_sync(0xffffffffu, back, 8 * quad);
-      sc[n][1] *= __shfl_sync(0xffffffffu, back, 8 * quad + 4);
+      sc[n][0] *= __shfl_sync(0xffffffffu, up, 8 * quad);
+      sc[n][1] *= __shfl_sync(0xffffffffu, up, 8 * quad + 4);
     }
   }
   int hi[kNT][2], lo[kNT][2];
@@ -247,7 +232,7 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
   for (int n = 0; n < kNT; ++n)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      hi[n][j] = it.pos(8 * n + 2 * quad + j);
+      hi[n][j] = it.pos(prm, 8 * n + 2 * quad + j);
       lo[n][j] = it.first(hi[n][j]);
     }
 
@@ -297,10 +282,13 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
           uint32_t r[4];
           ptx::ldmatrix4<false>((k_at ^ d * T::kChunkBit ^ T::key_xor(16 * t)) + 16 * t * T::kRow, r);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)  // high terms, low terms
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t k[4] = {e4m3x2_f16(r[2 * h]), e4m3x2_f16(r[2 * h + 1]),
+                                   e4m3x2_f16(r[2 * h] >> 16), e4m3x2_f16(r[2 * h + 1] >> 16)};
 #pragma unroll
             for (int n = 0; n < kNT; ++n)
-              ptx::mma16832_e4m3(s[t][n], r, q[n][d][h], q[n][d + 1][h]);
+              ptx::mma16816<true>(s[t][n], k, q[n][d + h][0], q[n][d + h][1]);
+          }
         }
     }
 
@@ -525,8 +513,8 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
               o[n][d][2 * h + j] * f;
     }
   __syncthreads();
-  finish<kRows, kWarps, kThreads, __nv_bfloat16>(prm, it, reinterpret_cast<float*>(smem),
-                                                 kS * T::kStage / 4, kLd, joined);
+  finish<kRows, kDim, kWarps, kThreads, __nv_bfloat16>(
+      prm, it, reinterpret_cast<float*>(smem), kS * T::kStage / 4, kLd, joined, inbox);
 }
 
 template <int kDim, int kNT, bool kF8>
