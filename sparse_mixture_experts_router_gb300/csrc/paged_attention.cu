@@ -82,7 +82,7 @@ Plan plan_of(const moe_attn_config& c) {
   // while a warp has eight tiles (a block costs about what those take). 64 sequences of 37 to 8190
   // keys take 182 us in two parts, 172 in four, 183 in eight; 32 of 100 to
   // 12000 with 20 rows 174, 168, 182.
-  const int per_sm = c.head_dim > 128 ? 1 : p.nt > (f8 ? 1 : 2) ? 2 : 3;
+  const int per_sm = attn::blocks_per_sm(c.head_dim, p.nt, f8);
   p.parts = 1;
   while (p.parts < attn::kMaxParts && tiles >= 8 * p.parts &&
          (p.items * p.parts < attn::kPlanSms ||

@@ -20,6 +20,12 @@ constexpr int kMaxSplits = 32;
 constexpr int kPlanSms = 152;   // the plan does not ask the device, so that the workspace's size is a constant of cfg
 constexpr int kMaxRows = 32;    // query rows of an item
 
+// Blocks of the bf16 and E4M3 kernel an SM holds: by registers, and for heads
+// above 128 by shared memory.
+constexpr int blocks_per_sm(int dim, int nt, bool f8) {
+  return dim > 128 ? 1 : nt <= (f8 ? 2 : 3) ? 3 : 2;
+}
+
 // n / d for 0 <= n < 2^30 and 1 <= d < 2^30 as a multiplication.
 struct FastDiv {
   uint64_t mul;
@@ -200,18 +206,23 @@ struct Inbox {
 // Joins a block's kWarps partial O (row r at o + w * stride + r * ld floats,
 // all relative to the block's maximum joined[r]; joined[kRows + r] its sum of
 // weights) and then the cluster's blocks, and writes the rows. Each block
-// sends every other its slice and then reads its own shared memory only: one
-// barrier, and none to keep blocks from leaving. The cluster's blocks have
-// all started (start_cluster) before the first sends.
-template <int kRows, int kDim, int kWarps, int kThreads, typename Elem>
-__device__ __forceinline__ void finish(const Params& p, const Item& it, const float* o, int stride,
-                                       int ld, const float* joined, Inbox<kRows, kDim>* inbox) {
+// sends every other its slice and then reads its own shared memory only, so no
+// barrier has to keep blocks from leaving. With kOwnInbox the inbox is memory
+// of its own and a block sends as soon as all have started (start_cluster);
+// otherwise it lies over the stages of the warps after the first, and blocks
+// send when all have read theirs: one barrier more, 8 to 16 KB less.
+template <int kRows, int kDim, int kWarps, int kThreads, bool kOwnInbox, typename Elem>
+__device__ __forceinline__ void finish(const Params& p, const Item& it, float* o, int stride, int ld,
+                                       const float* joined, Inbox<kRows, kDim>* inbox) {
   const int vecs = p.a.c.head_dim / 4, n = it.rows * vecs;
+  auto at = [&](int w, int r, int v) {
+    return reinterpret_cast<float4*>(o + w * stride + r * ld + 4 * v);
+  };
   auto block_sum = [&](int r, int v) {
-    float4 x = *reinterpret_cast<const float4*>(o + r * ld + 4 * v);
+    float4 x = *at(0, r, v);
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) {
-      const float4 y = *reinterpret_cast<const float4*>(o + w * stride + r * ld + 4 * v);
+      const float4 y = *at(w, r, v);
       x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
     }
     return x;
@@ -226,6 +237,14 @@ __device__ __forceinline__ void finish(const Params& p, const Item& it, const fl
   const int slice = div(p.by_parts, n + p.parts - 1);
   __syncwarp();
   ptx::cluster_wait();  // pairs with start_cluster
+  if (!kOwnInbox) {
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const int r = div(p.by_vecs, i), v = i - r * vecs;
+      *at(0, r, v) = block_sum(r, v);
+    }
+    __syncwarp();
+    ptx::cluster_sync();
+  }
   for (int i = threadIdx.x; i < kRows * p.parts; i += kThreads) {
     const int r = div(p.by_parts, i);
     ptx::st_cluster_v2(
@@ -238,7 +257,7 @@ __device__ __forceinline__ void finish(const Params& p, const Item& it, const fl
     while ((to + 1) * slice <= i) ++to;
     ptx::st_cluster_v4(
         ptx::mapa_shared(ptx::smem_addr(&inbox->o[it.part * slice + i - to * slice]), to),
-        block_sum(r, v));
+        kOwnInbox ? block_sum(r, v) : *at(0, r, v));
   }
   __syncwarp();
   ptx::cluster_sync();

@@ -262,8 +262,8 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const __grid_constant__ P
     }
   }
   __syncthreads();
-  finish<kRows, kDim, kWarps, kThreads, float>(prm, it, reinterpret_cast<float*>(smem),
-                                               kS * T::kStage / 4, kLd, joined, inbox);
+  finish<kRows, kDim, kWarps, kThreads, true, float>(prm, it, reinterpret_cast<float*>(smem),
+                                                     kS * T::kStage / 4, kLd, joined, inbox);
 }
 
 template <int kDim, int kR>

@@ -6,7 +6,7 @@
 // shared head), R multiply-adds an element. So the kernel is a stream of the
 // cache through shared memory, and everything else is arranged to stay out of
 // that stream's way:
-//  - A block of 4 warps holds one (sequence, key-value head, up to 8 NT query
+//  - A block of 4 warps (6 for heads above 128) holds one (sequence, key-value head, up to 8 NT query
 //    rows) item, or one of the C parts that its keys are cut into: the parts
 //    are a thread-block cluster and join through its distributed shared
 //    memory, so one launch and no scratch in global memory.
@@ -36,8 +36,9 @@
 namespace moe {
 namespace attn {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
+// Warps of a block: four, three blocks an SM; heads above 128 fill an SM's
+// shared memory with one block of six.
+constexpr int warps_of(int dim) { return dim > 128 ? 6 : 4; }
 
 template <int kDim, int kNT, bool kF8>
 struct Tile {
@@ -50,7 +51,7 @@ struct Tile {
   // more warps hide more than more bytes in flight do (the batch of 64 uneven
   // sequences 175 -> 173 us, 256 short ones in E4M3 130 -> 116 us; four
   // stages, one block an SM: 268 and 221 us).
-  static constexpr int kStages = kStage >= 16384 || kNT == 4 ? 3 : kStage >= 8192 ? 2 : 4;
+  static constexpr int kStages = kNT == 4 && kStage == 8192 ? 3 : kStage >= 8192 ? 2 : 4;
   // Byte offset of 16-byte chunk c of key k: chunk c of the 8 keys that one
   // matrix load takes falls into 8 different bank groups. Those are 8
   // consecutive keys, and of E4M3 keys also the 8 of 16 that agree in bit 1
@@ -74,11 +75,25 @@ struct Tile {
   }
 };
 
+// Shared memory after the rings, and how the variants differ.
 template <int kDim, int kNT, bool kF8>
-constexpr int smem_bytes() {
-  return kWarps * Tile<kDim, kNT, kF8>::kStages * Tile<kDim, kNT, kF8>::kStage +
-         (int)sizeof(Inbox<8 * kNT, kDim>) + (2 * kWarps + 2) * 8 * kNT * 4;
-}
+struct Layout {
+  using T = Tile<kDim, kNT, kF8>;
+  static constexpr int kWarps = warps_of(kDim), kThreads = kWarps * 32, kRows = 8 * kNT;
+  // Queries in shared memory where they would take 32 registers a thread and
+  // more: the third block that fits an SM then pays more than their reads cost
+  // (20 rows, bf16: 159 us with two blocks, 145 with three).
+  static constexpr bool kSharedQ = kNT >= 2;
+  static constexpr int kQRow = kDim * 2 + 16;  // bytes; 16 against bank conflicts
+  static constexpr bool kOwnInbox = kNT == 1;  // the others' would cost the third block
+  static constexpr int kRing = kWarps * T::kStages * T::kStage;
+  static constexpr int kInbox = kOwnInbox ? (int)sizeof(Inbox<kRows, kDim>) : 0;
+  static constexpr int kStat = (2 * kWarps + 2) * kRows * 4;
+  static constexpr int kRange = kRows * 8;   // last and first position of a row
+  static constexpr int kFactor = kRows * 4;  // of a row's scores
+  static constexpr int kQ = kSharedQ ? kRows * kQRow : 0;
+  static constexpr int kAll = kRing + kInbox + kStat + kRange + kFactor + kQ;
+};
 
 // Two E4M3 codes (the low 16 bits of v) as fp16.
 __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t v) {
@@ -93,16 +108,24 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 
 template <int kDim, int kNT, bool kF8>
-__global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ Params prm) {
+__global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim, kNT, kF8))
+    mma_kernel(const __grid_constant__ Params prm) {
   using T = Tile<kDim, kNT, kF8>;
-  constexpr int kS = T::kStages, kMT = T::kKeys / 16, kDT = kDim / 16, kRows = 8 * kNT;
+  using L = Layout<kDim, kNT, kF8>;
+  constexpr int kS = T::kStages, kMT = T::kKeys / 16, kDT = kDim / 16;
+  constexpr int kRows = L::kRows, kWarps = L::kWarps, kThreads = L::kThreads;
   extern __shared__ __align__(1024) uint8_t smem[];
   const AttnArgs& a = prm.a;
   const moe_attn_config& c = a.c;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, quad = lane % 4, oct = lane / 4;
-  auto* inbox = reinterpret_cast<Inbox<kRows, kDim>*>(smem + kWarps * kS * T::kStage);
-  float* stat = reinterpret_cast<float*>(inbox + 1);  // m, l of each warp's rows
-  float* joined = stat + 2 * kWarps * kRows;          // m, l of the block's
+  auto* inbox = reinterpret_cast<Inbox<kRows, kDim>*>(
+      L::kOwnInbox ? smem + L::kRing : smem + kS * T::kStage);
+  uint8_t* rest = smem + L::kRing + L::kInbox;
+  float* stat = reinterpret_cast<float*>(rest);  // m, l of each warp's rows
+  float* joined = stat + 2 * kWarps * kRows;     // m, l of the block's
+  int2* range = reinterpret_cast<int2*>(rest + L::kStat);
+  float* factor = reinterpret_cast<float*>(rest + L::kStat + L::kRange);
+  uint8_t* qs = rest + L::kStat + L::kRange + L::kFactor;
 
   pdl_wait();
   pdl_trigger();
@@ -176,32 +199,28 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
   Slot next = ahead[kS - 1];
 
   // ---- queries, as the second operand of S^T = K Q^T ----
-  uint32_t q[kNT][kDT][2];
-  float sc[kNT][2];  // factor of the scores of this lane's two columns, log2 units
+  // Elements (bf16: 2 quad, + 1 of 8; fp16: 4 quad, .. + 3 of 16, in the order
+  // the keys' are read) of row 8 n + oct.
   const float scale = c.scale * 1.4426950408889634f;
-#pragma unroll
-  for (int n = 0; n < kNT; ++n) {
+  auto query = [&](int n, uint32_t (&q)[kDT][2]) {
     const uint8_t* p = static_cast<const uint8_t*>(a.q) + it.q_at(prm, 8 * n + oct) * 2;
-    sc[n][0] = sc[n][1] = scale;
+    float f = scale;
     if (!kF8) {
 #pragma unroll
       for (int d = 0; d < kDT; ++d)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int e = 16 * d + 8 * h;  // head_dim is a multiple of 8
-          q[n][d][h] =
+          q[d][h] =
               e < c.head_dim ? *reinterpret_cast<const uint32_t*>(p + 2 * (e + 2 * quad)) : 0u;
         }
     } else {
-      // Four consecutive elements a lane: keys are read in the same order, so
-      // the products pair up. The row is scaled to [1, 2) for fp16.
       uint2 raw[kDT];
       float amax = 0.f;
 #pragma unroll
       for (int d = 0; d < kDT; ++d) {
         raw[d] = make_uint2(0u, 0u);
-        if (16 * d < c.head_dim)
-          raw[d] = *reinterpret_cast<const uint2*>(p + 2 * (16 * d + 4 * quad));
+        if (16 * d < c.head_dim) raw[d] = *reinterpret_cast<const uint2*>(p + 2 * (16 * d + 4 * quad));
         float x, y;
         bf16x2_to_f32(raw[d].x, x, y);
         amax = fmaxf(amax, fmaxf(fabsf(x), fabsf(y)));
@@ -210,31 +229,62 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
       }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      // 2^-e and 2^e of the row's largest, kept normal
+      // The row is scaled to [1, 2) for fp16, by 2^-e of its largest element
+      // (kept normal).
       const int e = clamp_int((int)(__float_as_uint(amax) >> 23) - 127, -126, 126);
       const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-      const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+      f *= __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
       for (int d = 0; d < kDT; ++d) {
         float x, y;
         bf16x2_to_f32(raw[d].x, x, y);
-        q[n][d][0] = pack_f16(x * down, y * down);
+        q[d][0] = pack_f16(x * down, y * down);
         bf16x2_to_f32(raw[d].y, x, y);
-        q[n][d][1] = pack_f16(x * down, y * down);
+        q[d][1] = pack_f16(x * down, y * down);
       }
-      // columns 2 quad and 2 quad + 1 belong to the lanes of those rows
-      sc[n][0] *= __shfl_sync(0xffffffffu, up, 8 * quad);
-      sc[n][1] *= __shfl_sync(0xffffffffu, up, 8 * quad + 4);
     }
+    return f;
+  };
+  uint32_t q[L::kSharedQ ? 1 : kNT][kDT][2];
+  float sc[kNT][2];  // factor of the scores of this lane's two columns, log2 units
+  for (int r = threadIdx.x; r < kRows; r += kThreads) {
+    const int last = it.pos(prm, r);
+    range[r] = make_int2(last, it.first(last));
   }
-  int hi[kNT][2], lo[kNT][2];
+  if (L::kSharedQ) {
+    if (warp < kNT) {  // a warp a tile of 8 rows
+      const float f = query(warp, q[0]);
+      if (quad == 0) factor[8 * warp + oct] = f;
+      uint8_t* row = qs + (8 * warp + oct) * L::kQRow + 4 * quad;
 #pragma unroll
-  for (int n = 0; n < kNT; ++n)
+      for (int d = 0; d < kDT; ++d)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      hi[n][j] = it.pos(prm, 8 * n + 2 * quad + j);
-      lo[n][j] = it.first(hi[n][j]);
+        for (int h = 0; h < 2; ++h) *reinterpret_cast<uint32_t*>(row + 32 * d + 16 * h) = q[0][d][h];
     }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < kNT; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) sc[n][j] = kF8 ? factor[8 * n + 2 * quad + j] : scale;
+  } else {
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) {
+      const float f = query(n, q[n]);
+      // columns 2 quad and 2 quad + 1 belong to the lanes of those rows
+      sc[n][0] = kF8 ? __shfl_sync(0xffffffffu, f, 8 * quad) : scale;
+      sc[n][1] = kF8 ? __shfl_sync(0xffffffffu, f, 8 * quad + 4) : scale;
+    }
+    __syncthreads();
+  }
+  const uint32_t q_lane = ptx::smem_addr(qs) + lane % 8 * L::kQRow + lane / 8 * 16;
+  // Two steps of 16 elements of query tile n.
+  auto query_frag = [&](int n, int d, uint32_t (&r)[4]) {
+    if (L::kSharedQ) {
+      ptx::ldmatrix4<false>(q_lane + 8 * n * L::kQRow + 32 * d, r);
+    } else {
+      r[0] = q[n][d][0], r[1] = q[n][d][1], r[2] = q[n][d + 1][0], r[3] = q[n][d + 1][1];
+    }
+  };
 
   // ---- the pass over the keys ----
   const uint32_t k_lane = T::at(T::key_of(lane % 16), lane / 16);
@@ -266,30 +316,36 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
         for (int x = 0; x < 4; ++x) s[t][n][x] = 0.f;
-    if (!kF8) {
 #pragma unroll
-      for (int d = 0; d < kDT; ++d) {
-        uint32_t k[4];
-        ptx::ldmatrix4<false>(k_at ^ 2 * d * T::kChunkBit, k);
+    for (int d = 0; d < kDT; d += 2) {
+      uint32_t k[kMT][2][4];  // two steps of 16 elements of the tile's keys
 #pragma unroll
-        for (int n = 0; n < kNT; ++n) ptx::mma16816<false>(s[0][n], k, q[n][d][0], q[n][d][1]);
-      }
-    } else {
-#pragma unroll
-      for (int t = 0; t < kMT; ++t)
-#pragma unroll
-        for (int d = 0; d < kDT; d += 2) {
+      for (int t = 0; t < kMT; ++t) {
+        if (!kF8) {
+          ptx::ldmatrix4<false>(k_at ^ 2 * d * T::kChunkBit, k[t][0]);
+          ptx::ldmatrix4<false>(k_at ^ (2 * d + 2) * T::kChunkBit, k[t][1]);
+        } else {
           uint32_t r[4];
           ptx::ldmatrix4<false>((k_at ^ d * T::kChunkBit ^ T::key_xor(16 * t)) + 16 * t * T::kRow, r);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t k[4] = {e4m3x2_f16(r[2 * h]), e4m3x2_f16(r[2 * h + 1]),
-                                   e4m3x2_f16(r[2 * h] >> 16), e4m3x2_f16(r[2 * h + 1] >> 16)};
-#pragma unroll
-            for (int n = 0; n < kNT; ++n)
-              ptx::mma16816<true>(s[t][n], k, q[n][d + h][0], q[n][d + h][1]);
+            k[t][h][0] = e4m3x2_f16(r[2 * h]);
+            k[t][h][1] = e4m3x2_f16(r[2 * h + 1]);
+            k[t][h][2] = e4m3x2_f16(r[2 * h] >> 16);
+            k[t][h][3] = e4m3x2_f16(r[2 * h + 1] >> 16);
           }
         }
+      }
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        uint32_t f[4];
+        query_frag(n, d, f);
+#pragma unroll
+        for (int t = 0; t < kMT; ++t) {
+          ptx::mma16816<kF8>(s[t][n], k[t][0], f[0], f[1]);
+          ptx::mma16816<kF8>(s[t][n], k[t][1], f[2], f[3]);
+        }
+      }
     }
 
     // Scores of keys key0 + 16 t + key_of(oct) (and of oct + 8), columns 2 quad
@@ -316,13 +372,29 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          float v = s[t][n][x] * sc[n][x % 2];
-          if (kF8) v *= ks[t][x / 2];
-          if (edge) {
+          s[t][n][x] *= sc[n][x % 2];
+          if (kF8) s[t][n][x] *= ks[t][x / 2];
+        }
+    if (edge) {
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int2 seen = range[8 * n + 2 * quad + x % 2];
+#pragma unroll
+          for (int t = 0; t < kMT; ++t) {
             const int key = key0 + 16 * t + T::key_of(8 * (x / 2) + oct);
-            if (key > hi[n][x % 2] || key < lo[n][x % 2]) v = -INFINITY;
+            if (key > seen.x || key < seen.y) s[t][n][x] = -INFINITY;
           }
-          s[t][n][x] = v;
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < kMT; ++t)
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float v = s[t][n][x];
           p[t][n][x] = ptx::ex2(v - m[n][x % 2]);
           if (!kF8)
             raise = raise || v > m[n][x % 2] + 8.f;
@@ -402,7 +474,8 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                   const float w = __shfl_sync(0xffffffffu, p[t][n][2 * h + j], 4 * k8 + quad);
-                  if (key > hi[n][j] || key < lo[n][j]) continue;
+                  const int2 seen = range[8 * n + 2 * quad + j];
+                  if (key > seen.x || key < seen.y) continue;
 #pragma unroll
                   for (int d = 0; d < kDT; ++d)
 #pragma unroll
@@ -513,15 +586,15 @@ __global__ void __launch_bounds__(kThreads) mma_kernel(const __grid_constant__ P
               o[n][d][2 * h + j] * f;
     }
   __syncthreads();
-  finish<kRows, kDim, kWarps, kThreads, __nv_bfloat16>(
+  finish<kRows, kDim, kWarps, kThreads, L::kOwnInbox, __nv_bfloat16>(
       prm, it, reinterpret_cast<float*>(smem), kS * T::kStage / 4, kLd, joined, inbox);
 }
 
 template <int kDim, int kNT, bool kF8>
 cudaError_t launch_mma(const Params& p, unsigned blocks, cudaStream_t s) {
   static thread_local int configured = -1;
-  return launch(mma_kernel<kDim, kNT, kF8>, &configured, p, blocks, kThreads,
-                smem_bytes<kDim, kNT, kF8>(), s);
+  return launch(mma_kernel<kDim, kNT, kF8>, &configured, p, blocks, warps_of(kDim) * 32,
+                Layout<kDim, kNT, kF8>::kAll, s);
 }
 
 }  // namespace attn
