@@ -67,7 +67,7 @@ struct Plan {
 Plan plan_of(const moe_attn_config& c) {
   Plan p;
   const bool f32 = c.cache_dtype == MOE_F32, f8 = c.cache_dtype == MOE_E4M3;
-  const int tile = f32 ? 8 : f8 ? 32 : 16;  // keys
+  const int tile = f32 ? 8 : attn::keys_of(c.head_dim, f8);
   p.unit = f32 ? 4 : 8;
   const int units = ceil_div((long long)(c.n_heads / c.n_kv_heads) * c.max_new, p.unit);
   p.row_blocks = ceil_div(units, c.head_dim <= 128 ? 4 : 2);

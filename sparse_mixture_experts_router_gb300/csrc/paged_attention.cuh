@@ -26,6 +26,9 @@ constexpr int blocks_per_sm(int dim, int nt, bool f8) {
   return dim > 128 ? 1 : nt <= (f8 ? 2 : 3) ? 3 : 2;
 }
 
+// Keys of a tile of the bf16 and E4M3 kernel.
+constexpr int keys_of(int dim, bool f8) { return f8 || dim <= 64 ? 32 : 16; }
+
 // n / d for 0 <= n < 2^30 and 1 <= d < 2^30 as a multiplication.
 struct FastDiv {
   uint64_t mul;

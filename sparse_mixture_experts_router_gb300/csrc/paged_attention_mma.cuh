@@ -10,7 +10,7 @@
 //    rows) item, or one of the C parts that its keys are cut into: the parts
 //    are a thread-block cluster and join through its distributed shared
 //    memory, so one launch and no scratch in global memory.
-//  - Each warp streams its own tiles (16 keys of bf16, 32 of E4M3) through its
+//  - Each warp streams its own tiles (8 KB: 16 keys of 128 bf16 elements, 32 of E4M3 or of 64 bf16) through its
 //    own ring of stages with cp.async and no block-wide synchronisation; the
 //    pages of the tile after next are looked up one step ahead.
 //  - The products are taken transposed, S^T = K Q^T and O^T = V^T P^T: keys
@@ -42,7 +42,7 @@ constexpr int warps_of(int dim) { return dim > 128 ? 6 : 4; }
 
 template <int kDim, int kNT, bool kF8>
 struct Tile {
-  static constexpr int kKeys = kF8 ? 32 : 16;
+  static constexpr int kKeys = keys_of(kDim, kF8);
   static constexpr int kRow = kDim * (kF8 ? 1 : 2);  // bytes of a key in shared memory
   static constexpr int kChunks = kRow / 16;
   static constexpr int kBytes = kKeys * kRow;        // one of K, V
@@ -322,8 +322,8 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim, kNT, 
 #pragma unroll
       for (int t = 0; t < kMT; ++t) {
         if (!kF8) {
-          ptx::ldmatrix4<false>(k_at ^ 2 * d * T::kChunkBit, k[t][0]);
-          ptx::ldmatrix4<false>(k_at ^ (2 * d + 2) * T::kChunkBit, k[t][1]);
+          ptx::ldmatrix4<false>((k_at ^ 2 * d * T::kChunkBit) + 16 * t * T::kRow, k[t][0]);
+          ptx::ldmatrix4<false>((k_at ^ (2 * d + 2) * T::kChunkBit) + 16 * t * T::kRow, k[t][1]);
         } else {
           uint32_t r[4];
           ptx::ldmatrix4<false>((k_at ^ d * T::kChunkBit ^ T::key_xor(16 * t)) + 16 * t * T::kRow, r);
@@ -522,11 +522,14 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim, kNT, 
     for (int d = 0; d < kDT; ++d) {
       uint32_t r[4];
       if (!kF8) {
-        ptx::ldmatrix4<true>(v_at ^ 2 * d * T::kChunkBit, r);
 #pragma unroll
-        for (int n = 0; n < kNT; ++n) ptx::mma16816<false>(o[n][d], r, ph[0][n][0], ph[0][n][1]);
+        for (int t = 0; t < kMT; ++t) {
+          ptx::ldmatrix4<true>((v_at ^ 2 * d * T::kChunkBit) + 16 * t * T::kRow, r);
 #pragma unroll
-        for (int n = 0; n < kNT; ++n) ptx::mma16816<false>(o[n][d], r, pl[0][n][0], pl[0][n][1]);
+          for (int n = 0; n < kNT; ++n) ptx::mma16816<false>(o[n][d], r, ph[t][n][0], ph[t][n][1]);
+#pragma unroll
+          for (int n = 0; n < kNT; ++n) ptx::mma16816<false>(o[n][d], r, pl[t][n][0], pl[t][n][1]);
+        }
       } else {
         ptx::ldmatrix2_bytes_trans(v_at ^ d * T::kChunkBit, r);
 #pragma unroll
