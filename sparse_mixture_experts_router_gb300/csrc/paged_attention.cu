@@ -16,16 +16,20 @@
 namespace moe {
 namespace {
 
+// Query rows of a bf16 head group above which the tcgen05 kernel runs.
+constexpr int kTcRows = 32;
+
 // Rows whose keys were cut into splits: one warp a row.
 constexpr int kJoinWarps = 4;
 template <typename Elem>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-    join_kernel(const __grid_constant__ attn::Params prm, int block_rows, int rows) {
+    join_kernel(const __grid_constant__ attn::Params prm, int rows) {
   const moe_attn_config& c = prm.a.c;
   const int i = (int)blockIdx.x * kJoinWarps + threadIdx.x / 32, lane = threadIdx.x % 32;
   pdl_wait();
   pdl_trigger();
   if (i >= rows) return;
+  const int block_rows = prm.item_rows;
   attn::Item it;
   it.index = i / block_rows;
   const int r = i % block_rows, rb = it.index % prm.row_blocks, head = it.index / prm.row_blocks;
@@ -34,8 +38,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   it.G = prm.group;
   it.row0 = rb * block_rows;
   if (it.row0 + r >= it.G * it.sq.n) return;
-  const int64_t row0 = (int64_t)it.index * prm.splits * attn::kMaxRows + r;
-  const float2 ml = lane < prm.splits ? prm.split_ml[row0 + (int64_t)lane * attn::kMaxRows]
+  const int64_t row0 = (int64_t)it.index * prm.splits * block_rows + r;
+  const float2 ml = lane < prm.splits ? prm.split_ml[row0 + (int64_t)lane * block_rows]
                                       : make_float2(-INFINITY, 0.f);
   float top = ml.x;
 #pragma unroll
@@ -51,7 +55,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
       const float fs = __shfl_sync(0xffffffffu, f, s);
       if (v >= vecs) continue;
       const float4 y = reinterpret_cast<const float4*>(
-          prm.split_o)[(row0 + (int64_t)s * attn::kMaxRows) * vecs + v];
+          prm.split_o)[(row0 + (int64_t)s * block_rows) * vecs + v];
       x.x += y.x * fs, x.y += y.y * fs, x.z += y.z * fs, x.w += y.w * fs;
     }
     if (v < vecs) attn::write_row<Elem>(out, it, r, v, x, top, sum);
@@ -60,45 +64,51 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 
 // How a call is cut; of cfg alone, so that the workspace holds its splits.
 struct Plan {
-  int unit, nt;  // query rows of an item: unit * nt
+  bool tc;                // the tcgen05 kernel
+  int unit, nt;           // query rows of an item: unit * nt
   int row_blocks, parts, splits;
   long long items;
+  int rows() const { return unit * nt; }
 };
 Plan plan_of(const moe_attn_config& c) {
   Plan p;
   const bool f32 = c.cache_dtype == MOE_F32, f8 = c.cache_dtype == MOE_E4M3;
-  const int tile = f32 ? 8 : attn::keys_of(c.head_dim, f8);
-  p.unit = f32 ? 4 : 8;
-  const int units = ceil_div((long long)(c.n_heads / c.n_kv_heads) * c.max_new, p.unit);
-  p.row_blocks = ceil_div(units, c.head_dim <= 128 ? 4 : 2);
+  const long long all_rows = (long long)(c.n_heads / c.n_kv_heads) * c.max_new;
+  p.tc = c.cache_dtype == MOE_BF16 && c.head_dim <= 128 && all_rows > kTcRows;
+  p.unit = p.tc ? 16 : f32 ? 4 : 8;
+  const int units = ceil_div(all_rows, p.unit);
+  p.row_blocks = ceil_div(units, p.tc ? 8 : c.head_dim <= 128 ? 4 : 2);
   p.nt = ceil_div(units, p.row_blocks);
   p.items = (long long)c.n_seqs * c.n_kv_heads * p.row_blocks;
   long long keys = (long long)c.max_pages * c.page_size;
   if (c.window) keys = std::min(keys, (long long)c.window + c.max_new);
-  const long long tiles = ceil_div(keys, tile);
-  // Parts: as many as fill the SMs, while every warp has a tile; then on to
-  // three waves of blocks (three an SM, two where the query rows fill the
-  // registers, one of the longest heads), so that uneven sequences even out,
-  // while a warp has eight tiles (a block costs about what those take). 64 sequences of 37 to 8190
-  // keys take 182 us in two parts, 172 in four, 183 in eight; 32 of 100 to
-  // 12000 with 20 rows 174, 168, 182.
-  const int per_sm = attn::blocks_per_sm(c.head_dim, p.nt, f8);
+  // A part's unit of work: a tile for each of a block's warps.
+  const int warps = p.tc ? 1 : 4;
+  const int tile = p.tc ? 128 : f32 ? 8 : attn::keys_of(c.head_dim, f8);
+  const long long steps = ceil_div(keys, warps * tile);
+  // Parts: as many as fill the SMs, while a block has two steps; then on to
+  // three waves of blocks, so that uneven sequences even out, while a block
+  // has sixteen (it costs about what eight take). Fewer: 64 sequences of 37 to
+  // 8190 keys take 182 us in two parts, 172 in four, 183 in eight; 32 of 100
+  // to 12000 with 20 rows 174, 168, 182.
+  const int per_sm = p.tc ? 1 : attn::blocks_per_sm(c.head_dim, p.nt, f8);
+  const int most = p.tc ? 8 : attn::kMaxParts;  // 16 whole SMs are more than some GPCs have
   p.parts = 1;
-  while (p.parts < attn::kMaxParts && tiles >= 8 * p.parts &&
+  while (p.parts < most && steps >= 2 * p.parts &&
          (p.items * p.parts < attn::kPlanSms ||
-          (p.items * p.parts < 3LL * per_sm * attn::kPlanSms && tiles >= 64 * p.parts)))
+          (p.items * p.parts < 3LL * per_sm * attn::kPlanSms && steps >= 16 * p.parts)))
     p.parts *= 2;
-  // Splits: where the largest clusters still leave SMs idle and a warp has 16
-  // tiles or more.
+  // Splits: where the largest clusters still leave SMs idle and a block has 16
+  // steps or more.
   p.splits = 1;
-  if (p.parts == attn::kMaxParts && p.items > 0)
-    p.splits = (int)std::max(1LL, std::min({2LL * attn::kPlanSms / (p.items * p.parts),
-                                            tiles / (16 * 4 * p.parts),
+  if (p.parts == most && p.items > 0)
+    p.splits = (int)std::max(1LL, std::min({(p.tc ? 1LL : 2LL) * attn::kPlanSms / (p.items * p.parts),
+                                            steps / (16 * p.parts),
                                             (long long)attn::kMaxSplits}));
   return p;
 }
 size_t split_rows(const Plan& p) {
-  return p.splits > 1 ? (size_t)p.items * p.splits * attn::kMaxRows : 0;
+  return p.splits > 1 ? (size_t)p.items * p.splits * p.rows() : 0;
 }
 
 }  // namespace
@@ -107,6 +117,7 @@ namespace attn {
 cudaError_t launch_bf16(const Params& p, int dim, int nt, unsigned blocks, cudaStream_t s);
 cudaError_t launch_e4m3(const Params& p, int dim, int nt, unsigned blocks, cudaStream_t s);
 cudaError_t launch_f32(const Params& p, int dim, int nt, unsigned blocks, cudaStream_t s);
+cudaError_t launch_tc(const Params& p, int dim, unsigned blocks, cudaStream_t s);
 }  // namespace attn
 
 size_t attention_scratch_bytes(const moe_attn_config& c) {
@@ -123,6 +134,7 @@ cudaError_t launch_paged_attention(const AttnArgs& a, void* scratch, cudaStream_
   prm.splits = plan.splits;
   prm.row_blocks = plan.row_blocks;
   prm.group = c.n_heads / c.n_kv_heads;
+  prm.item_rows = plan.rows();
   prm.by_page = attn::fast_div((uint32_t)c.page_size);
   prm.by_group = attn::fast_div((uint32_t)prm.group);
   prm.by_parts = attn::fast_div((uint32_t)prm.parts);
@@ -136,17 +148,17 @@ cudaError_t launch_paged_attention(const AttnArgs& a, void* scratch, cudaStream_
   cudaError_t e;
   {
     ProfScope p(K_ATTENTION, s);
-    e = c.cache_dtype == MOE_F32    ? attn::launch_f32(prm, c.head_dim, plan.nt, blocks, s)
+    e = plan.tc                     ? attn::launch_tc(prm, c.head_dim, blocks, s)
+        : c.cache_dtype == MOE_F32  ? attn::launch_f32(prm, c.head_dim, plan.nt, blocks, s)
         : c.cache_dtype == MOE_E4M3 ? attn::launch_e4m3(prm, c.head_dim, plan.nt, blocks, s)
                                     : attn::launch_bf16(prm, c.head_dim, plan.nt, blocks, s);
   }
   if (e != cudaSuccess || plan.splits == 1) return e;
   ProfScope p(K_ATTENTION_JOIN, s);
-  const int block_rows = plan.unit * plan.nt, rows = (int)(plan.items * block_rows);
+  const int rows = (int)(plan.items * plan.rows());
   const dim3 grid((unsigned)ceil_div(rows, kJoinWarps)), block(kJoinWarps * 32);
-  return c.dtype == MOE_F32
-             ? launch_pdl(join_kernel<float>, grid, block, 0, s, 1, prm, block_rows, rows)
-             : launch_pdl(join_kernel<__nv_bfloat16>, grid, block, 0, s, 1, prm, block_rows, rows);
+  return c.dtype == MOE_F32 ? launch_pdl(join_kernel<float>, grid, block, 0, s, 1, prm, rows)
+                            : launch_pdl(join_kernel<__nv_bfloat16>, grid, block, 0, s, 1, prm, rows);
 }
 
 }  // namespace moe

@@ -18,7 +18,6 @@ namespace attn {
 constexpr int kMaxParts = 16;   // the largest cluster
 constexpr int kMaxSplits = 32;
 constexpr int kPlanSms = 152;   // the plan does not ask the device, so that the workspace's size is a constant of cfg
-constexpr int kMaxRows = 32;    // query rows of an item
 
 // Blocks of the bf16 and E4M3 kernel an SM holds: by registers, and for heads
 // above 128 by shared memory.
@@ -52,8 +51,9 @@ struct Params {
   // divisions by page_size, heads a key-value head, parts, splits,
   // row_blocks, n_kv_heads and head_dim / 4
   FastDiv by_page, by_group, by_parts, by_splits, by_rows, by_heads, by_vecs;
-  // splits > 1: O [item][split][kMaxRows][head_dim] relative to its maximum,
-  // and (maximum in log2 units, sum) [item][split][kMaxRows]
+  int item_rows;   // query rows of an item
+  // splits > 1: O [item][split][item_rows][head_dim] relative to its maximum,
+  // and (maximum in log2 units, sum) [item][split][item_rows]
   float* split_o;
   float2* split_ml;
 };
@@ -181,7 +181,7 @@ __device__ __forceinline__ void write_row(const Params& p, const Item& it, int r
   const moe_attn_config& c = p.a.c;
   const int vecs = c.head_dim / 4;
   if (p.splits > 1) {
-    const int64_t row = ((int64_t)it.index * p.splits + it.split) * kMaxRows + r;
+    const int64_t row = ((int64_t)it.index * p.splits + it.split) * p.item_rows + r;
     reinterpret_cast<float4*>(p.split_o)[row * vecs + v] = x;
     if (v == 0) p.split_ml[row] = make_float2(top, sum);
     return;

@@ -246,3 +246,47 @@ def test_lse_is_optional():
     r.lse = None
     r()
     assert torch.equal(r.out, want.out)
+
+
+@pytest.mark.parametrize("dim", [8, 64, 80, 128])
+@pytest.mark.parametrize("group,new", [(33, 1), (12, 4), (8, 8), (16, 8), (40, 4), (5, 30)])
+def test_many_query_rows(dim, group, new):
+    """Head groups of 33 rows and more: the keys that all rows see, and those
+    that only some do."""
+    check(Batch(new=[new, 1, new, max(1, new - 1)], length=[300, 1, new, 129 + new], heads=2 * group, kv_heads=2, dim=dim,
+                page=16, seed=group))
+
+
+@pytest.mark.parametrize("length", [1, 7, 127, 128, 129, 135, 136, 255, 256, 257, 640, 1500])
+def test_many_query_rows_lengths(length):
+    check(Batch(new=[8, 3], length=[length, length], heads=12, kv_heads=2, dim=64, page=7, seed=length))
+
+
+@pytest.mark.parametrize("window", [1, 3, 8, 64, 129, 300])
+def test_many_query_rows_window(window):
+    check(Batch(new=[8, 5, 2], length=[700, 90, 1], heads=16, kv_heads=2, dim=64, page=16, window=window, seed=window))
+
+
+def test_many_query_rows_split_and_peaked():
+    for columns, lengths in ((1, [3000, 2049]), (16384, [2500, 3])):
+        check(Batch(new=[6, 3], length=lengths, heads=24, kv_heads=2, dim=128, page=32, columns=columns, seed=21))
+        check(Batch(new=[6, 3], length=lengths, heads=24, kv_heads=2, dim=128, page=32, columns=columns, values=60.0,
+                    order="head", q_pad=64, seed=22))
+
+
+def test_many_query_rows_values_not_finite():
+    bt = Batch(new=[5], length=[300], heads=16, kv_heads=2, dim=64, page=16, seed=23)
+    page, at = int(bt.table[0, 299 // 16]), 299 % 16
+    bt.v[page, at] = float("nan")
+    out, lse, tol, _ = attention64(bt)
+    got = Call(bt)().out.double().cpu().numpy()
+    assert (np.abs(got[:4] - out[:4]) <= tol[:4]).all() and np.isnan(got[4]).all()
+
+
+def test_many_query_rows_equal_bits_and_bad_pages():
+    bt = Batch(new=[5, 2], length=[900, 300], heads=16, kv_heads=2, dim=64, page=16, seed=24)
+    a, b = Call(bt)(), Call(bt)()
+    assert torch.equal(a.out, b.out) and torch.equal(a.lse, b.lse) and a.status == moe.MOE_OK
+    bt.table[0, 3] = 1 << 20
+    bt.table[1, 18] = -5
+    assert Call(bt)().status == moe.MOE_ERR_DEVICE_CHECK
