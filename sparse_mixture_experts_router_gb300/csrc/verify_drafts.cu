@@ -48,7 +48,7 @@ struct Digits {
     const float x = prob(p), y = prob(q);
     const bool over = x > y;
     // p and q go through the additions as one pair of fp32
-    const uint64_t v = pair(over ? x : 0.f, over ? y : 0.f);
+    const uint64_t v = ptx::f32x2(over ? x : 0.f, over ? y : 0.f);
     const uint64_t y1 = add2(v, twice(2.f));
     const uint64_t r1 = sub2(v, add2(y1, twice(-2.f)));
     const uint64_t y2 = add2(r1, twice(0x1.8p-21f));
@@ -58,19 +58,12 @@ struct Digits {
     b += (int)(uint32_t)y2 - (int)(uint32_t)(y2 >> 32);
     c += (int)(uint32_t)y3 - (int)(uint32_t)(y3 >> 32);
   }
-  static __device__ __forceinline__ uint64_t pair(float lo, float hi) {
-    return (uint64_t)__float_as_uint(hi) << 32 | __float_as_uint(lo);
-  }
-  static __device__ __forceinline__ uint64_t twice(float x) { return pair(x, x); }
+  static __device__ __forceinline__ uint64_t twice(float x) { return ptx::f32x2(x, x); }
   static __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-    return r;
+    return ptx::add_f32x2(x, y);
   }
   static __device__ __forceinline__ uint64_t sub2(uint64_t x, uint64_t y) {
-    uint64_t r;  // x - y, rounded once: y * -1 + x
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(y), "l"(twice(-1.f)), "l"(x));
-    return r;
+    return ptx::fma_f32x2(y, twice(-1.f), x);  // x - y, rounded once
   }
   // At most 256 elements fit the digits.
   __device__ __forceinline__ uint64_t value() const {
