@@ -10,7 +10,7 @@
 // joins.
 #pragma once
 #include "serve_util.cuh"
-#include "sm103_ptx.cuh"
+#include "serve_ptx.cuh"
 
 namespace moe {
 namespace attn {

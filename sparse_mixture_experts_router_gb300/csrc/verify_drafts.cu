@@ -22,7 +22,7 @@
 #include <algorithm>
 
 #include "serve_util.cuh"
-#include "sm103_ptx.cuh"
+#include "serve_ptx.cuh"
 
 namespace moe {
 namespace {
