@@ -46,13 +46,28 @@ __device__ __forceinline__ Eight<T> load8(const T* p) {
   return r;
 }
 template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
-  Eight<T> r;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) r.v[i] = from_f32<T>(x[i]);
+__device__ __forceinline__ void store8(T* p, const Eight<T>& r) {
   constexpr int n = (int)sizeof(r) / 16;
 #pragma unroll
   for (int i = 0; i < n; ++i) reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(&r)[i];
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(x[2], x[3]),
+                 f32x2_to_bf16x2(x[4], x[5]), f32x2_to_bf16x2(x[6], x[7]));
+}
+__device__ __forceinline__ void widen(const Eight<float>& r, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = r.v[i];
+}
+__device__ __forceinline__ void widen(const Eight<__nv_bfloat16>& r, float (&x)[8]) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bf16x2_to_f32(w[i], x[2 * i], x[2 * i + 1]);
 }
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;
@@ -121,27 +136,35 @@ __global__ void __launch_bounds__(kThreads)
   };
   // Element e0 + i turns with its partner: the same vector's neighbour
   // (interleaved), or the element rot_dim/2 away, which another lane of the
-  // group holds (whole vectors away) or which is read again.
+  // group holds (whole vectors away) or which is read again. Zero where an
+  // element does not turn, so that whatever it is passes.
   const bool vec_partner = pairs % 8 == 0;
-  const int away = e0 < pairs ? pairs : -pairs;
-  auto partners = [&](int u, const Eight<T>& own) {
-    Eight<T> y = own;
-    if (c.rot_interleaved) {
+  const int from = lane + (e0 < pairs ? pairs : -pairs) / 8;
+  const bool turns_here = e0 < c.rot_dim;
+  auto partners = [&](int u, const Eight<T>& x, float (&y)[8]) {
+    if (!c.rot_interleaved && vec_partner) {
+      Eight<T> z;
+      constexpr int n = (int)sizeof(z) / 4;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y.v[i] = own.v[i ^ 1];
-    } else if (vec_partner) {
-      constexpr int n = (int)sizeof(y) / 4;
+      for (int i = 0; i < n; ++i) {
+        const uint32_t w =
+            __shfl_sync(0xffffffffu, reinterpret_cast<const uint32_t*>(&x)[i], from);
+        reinterpret_cast<uint32_t*>(&z)[i] = turns_here ? w : 0u;
+      }
+      widen(z, y);
+    } else {
+      const T* p = source(u < units ? u : 0);
 #pragma unroll
-      for (int i = 0; i < n; ++i)
-        reinterpret_cast<uint32_t*>(&y)[i] = __shfl_sync(
-            0xffffffffu, reinterpret_cast<const uint32_t*>(&own)[i], lane + away / 8);
-    } else if (u < units && held) {
-      const T* p = source(u);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (e0 + i < c.rot_dim) y.v[i] = p[e0 + i < pairs ? i + pairs : i - pairs];
+      for (int i = 0; i < 8; ++i) {
+        const int e = e0 + i;
+        if (e >= c.rot_dim)
+          y[i] = 0.f;
+        else if (c.rot_interleaved)
+          y[i] = to_f32(x.v[i ^ 1]);
+        else
+          y[i] = to_f32(p[e < pairs ? i + pairs : i - pairs]);
+      }
     }
-    return y;
   };
   load(group);  // in flight while the token's place is looked up
 
@@ -192,13 +215,20 @@ __global__ void __launch_bounds__(kThreads)
     for (int k = 0; k < kUnits; ++k) {
       const int u = u0 + k * groups;
       if (u - group >= units) break;  // the same for the whole warp
-      float o[8];
+      const bool in = u < units && held;
+      const bool turned = u < nq + nk;
+      if (!kE4M3 && u - group + ((warp * 32) >> lane_bits) >= nq + nk) {
+        // the whole warp has values, and the cache is of their type: as they are
+        const int64_t off = row + (u - nq - nk) * c.head_stride;
+        if (in && page >= 0) store8(static_cast<T*>(a.v_cache) + off, x[k]);
+        continue;
+      }
+      float o[8], y[8];
+      widen(x[k], o);
+      partners(u, x[k], y);
+      if (turned) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = to_f32(x[k].v[i]);
-      const Eight<T> y = partners(u, x[k]);
-      if (u < nq + nk) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = o[i] * own[i] + to_f32(y.v[i]) * other[i];
+        for (int i = 0; i < 8; ++i) o[i] = o[i] * own[i] + y[i] * other[i];
       }
       __syncwarp();  // in place: the partners are read before they are overwritten
       float amax = 0.f;
@@ -208,7 +238,7 @@ __global__ void __launch_bounds__(kThreads)
         for (int m = lanes / 2; m > 0; m >>= 1)
           amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
       }
-      if (u >= units || !held) continue;
+      if (!in) continue;
       if (u < nq) {
         store8(out + u * c.head_dim, o);
         continue;

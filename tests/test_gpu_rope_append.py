@@ -175,6 +175,40 @@ def test_strided_in_place_and_without_queries():
     assert torch.equal(vc[page, :2], k) and torch.equal(kc[page, 0], k[0])
 
 
+@pytest.mark.parametrize("rot,interleaved", [(32, False), (32, True), (20, False), (0, False)])
+@pytest.mark.parametrize("tokens", [2, 1500])
+def test_elements_that_do_not_turn_pass_as_they_are(rot, interleaved, tokens):
+    """Infinities past rot_dim reach their own element only."""
+    bt = Batch(new=[tokens], length=[tokens], heads=2, kv_heads=1, dim=64, page=16, seed=14)
+    bt.q_rows[:, 40] = float("inf")
+    bt.q_rows[:, 64 + 63] = float("-inf")
+    status, q, *_ = run(bt, rot, interleaved)
+    assert status == moe.MOE_OK
+    assert torch.equal(q[..., rot:], bt.q[..., rot:]) and torch.isfinite(q[..., :rot]).all()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "f32", "e4m3"])
+@pytest.mark.parametrize("rot,interleaved", [(64, False), (42, False), (64, True)])
+def test_runs_of_tokens(cache, rot, interleaved):
+    """Enough tokens that a warp takes a run of them, over the ends of sequences,
+    idle ones and pages; in place as well."""
+    rs = np.random.RandomState(6)
+    new = [700, 0, 0, 1, 3, 0, 511, 1, 80, 0, 1, 44]
+    bt = dict(new=new, length=[n + int(rs.randint(0, 30)) for n in new], heads=6, kv_heads=2, dim=64, page=7, cache=cache)
+    check(Batch(**bt, seed=15), rot, interleaved)
+    check(Batch(**bt, seed=16), rot, interleaved, inplace=True)
+    one = Batch(new=[1] * 1300, length=[1 + i % 9 for i in range(1300)], heads=2, kv_heads=1, dim=80, page=4, cache=cache, seed=17)
+    check(one, rot, interleaved, (rot // 2 - 10, 5, 5), positions=one.rs.randint(0, 5000, (3, one.T)))
+
+
+def test_runs_of_tokens_bad_lists():
+    new = [700, 600]
+    for name, i, v in (("length", 0, 699), ("table", (0, 5), 9999), ("cu", 1, 701), ("cu", 2, 1299)):
+        bt = Batch(new=new, length=[710, 600], heads=2, kv_heads=1, dim=64, page=16, seed=18)
+        getattr(bt, name)[i] = v
+        assert run(bt, 64)[0] == moe.MOE_ERR_DEVICE_CHECK, name
+
+
 def test_many_tokens():
     rs = np.random.RandomState(3)
     new = rs.randint(0, 40, 50).tolist()
