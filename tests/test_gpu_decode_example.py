@@ -34,3 +34,33 @@ def test_drafts_do_not_change_what_is_decided():
         got = decode_step.decode(block, first, 24)
         for a, b in zip(plain, got):
             assert a == b[:24]
+
+
+def test_calls_of_a_step_in_one_graph():
+    """The step's calls captured once and replayed give what they give launched."""
+    B, n = 4, 3
+    block = decode_step.Block(B, n - 1, 64, seed=3)
+    tokens = torch.randint(0, block.V, (B, n), device="cuda").int()
+    kv_len = torch.tensor([3, 10, 40, 64], device="cuda").int()
+    u, us = torch.rand(B * n, device="cuda"), torch.rand(B, device="cuda")
+    _, q = block.draft(tokens[:, 0].contiguous())
+
+    def calls():
+        p = block.target(tokens, kv_len)
+        moe.moe_verify_drafts(block.verify, p, q, tokens, u, us, block.cu, kv_len, block.decided, block.accepted,
+                              block.next, block.ws["verify"])
+
+    calls()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (block.context, block.y, block.decided, block.accepted, block.next)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls()
+    for t in (block.context, block.y, block.decided, block.accepted, block.next):
+        t.zero_()
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    assert not any(block.status().values())
+    for a, b in zip(want, (block.context, block.y, block.decided, block.accepted, block.next)):
+        assert torch.equal(a, b)

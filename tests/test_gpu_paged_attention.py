@@ -290,3 +290,43 @@ def test_many_query_rows_equal_bits_and_bad_pages():
     bt.table[0, 3] = 1 << 20
     bt.table[1, 18] = -5
     assert Call(bt)().status == moe.MOE_ERR_DEVICE_CHECK
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("max_new", [2, 7, 50])
+def test_bound_of_new_tokens_above_what_comes(cache, max_new):
+    """max_new is a bound: it chooses the kernel's rows, not the result."""
+    check(Batch(new=[1, 0, 2], length=[90, 3, 200], heads=16, kv_heads=2, dim=64, page=16, cache=cache, max_new=max_new,
+                seed=25))
+
+
+def test_many_query_rows_negative_scale():
+    check(Batch(new=[5, 4], length=[300, 70], heads=16, kv_heads=2, dim=64, page=16, seed=26), -0.1)
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("group", [2, 40])
+def test_cache_beyond_32_bits(cache, group):
+    """Pages whose elements lie past 2^32 bytes and 2^31 elements."""
+    bt = Batch(new=[1, 2], length=[70, 33], heads=2 * group, kv_heads=2, dim=64, page=16, cache=cache, seed=27)
+    r = Call(bt)
+    small = [r.cache[i] for i in (0, 1)]
+    pages = (1 << 31) // (16 * 2 * 64) + 5000
+    big = [torch.empty((pages,) + x.shape[1:], dtype=x.dtype, device="cuda") for x in small]
+    first = pages - bt.n_pages
+    for b, x in zip(big, small):
+        b[first:] = x
+    scales = [None, None]
+    if cache == "e4m3":
+        scales = [torch.empty((pages,) + x.shape[1:], device="cuda") for x in r.cache[2:]]
+        for b, x in zip(scales, r.cache[2:]):
+            b[first:] = x
+    want = Call(bt)()
+    r.cache = (*big, *scales)
+    r.cfg = moe.attn_config(**{n: getattr(r.cfg, n) for n in (
+        "n_seqs", "n_tokens", "max_new", "n_heads", "n_kv_heads", "head_dim", "page_size", "max_pages", "dtype",
+        "cache_dtype", "q_stride")}, n_pages=pages)
+    r.lists = (r.lists[0], r.lists[1], torch.where(r.lists[2] >= 0, r.lists[2] + first, r.lists[2]))
+    r()
+    assert r.status == moe.MOE_OK
+    assert torch.equal(r.out, want.out) and torch.equal(r.lse, want.lse)

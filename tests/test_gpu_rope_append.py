@@ -246,3 +246,29 @@ def test_bad_lists_are_reported():
     for edit in (put("length", 0, 1), put("length", 1, -4), put("length", 0, 9), put("table", (0, 1), 99),
                  put("table", (0, 1), -1), put("cu", 1, 1000), put("cu", 0, -1), put("cu", 2, 2)):
         assert status(edit) == moe.MOE_ERR_DEVICE_CHECK
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_cache_beyond_32_bits(cache):
+    bt = Batch(new=[3, 2], length=[20, 17], heads=2, kv_heads=2, dim=64, page=16, cache=cache, seed=19)
+    kind = torch.uint8 if cache == "e4m3" else torch.bfloat16
+    pages = (1 << 31) // (16 * 2 * 64) + 5000
+    first = pages - bt.n_pages
+    caches = [torch.zeros((pages, 16, 2, 64), dtype=kind, device="cuda") for _ in range(2)]
+    scales = [torch.zeros((pages, 2, 16), device="cuda") for _ in range(2)] if cache == "e4m3" else [None, None]
+    cfg = bt.cfg(rot_dim=0, n_pages=pages)
+    cu, length, table = bt.lists()
+    x = torch.randn(5, 2, 64).bfloat16().cuda()
+    ws = moe.workspace(cfg, "append")
+    moe.moe_rope_append(cfg, x, x, x, None, cu, length, table + first, torch.empty_like(x), *caches, *scales, ws)
+    assert moe.moe_stream_status(ws) == moe.MOE_OK
+    for b in range(2):
+        for j in range(bt.new[b]):
+            at, t = bt.length[b] - bt.new[b] + j, int(bt.cu[b]) + j
+            page = first + int(bt.table[b, at // 16])
+            for c, s in zip(caches, scales):
+                got = c[page, at % 16]
+                if cache == "e4m3":
+                    got = got.view(torch.float8_e4m3fn).float() * s[page, :, at % 16, None]
+                assert torch.allclose(got.float(), x[t].float(), rtol=2.0 ** -4, atol=2.0 ** -6)
+    assert sum(int((c != 0).any(-1).sum()) for c in caches) == 2 * 5 * 2
