@@ -158,6 +158,8 @@ _lib = None
 def lib():
     """The loaded libmoe.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -182,10 +184,16 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_torch_c = None
+
+
 def _stream(stream):
     if stream is None:
-        from torch import _C  # the stream's handle alone: torch.cuda.current_stream() takes 3 us
-        return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
+        global _torch_c
+        if _torch_c is None:
+            from torch import _C as _torch_c
+        # the stream's handle alone: torch.cuda.current_stream() takes 3 us
+        return _torch_c._cuda_getCurrentRawStream(_torch_c._cuda_getDevice())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 

@@ -271,14 +271,18 @@ int reset_status(int* status, cudaStream_t s) {
   return e == cudaSuccess ? MOE_OK : fail_cuda(e);
 }
 
-// The library's code for one device: sm_103a.
+// The library's code for one device: sm_103a. A thread asks once a device.
 int check_sm103() {
+  static thread_local int fine = -1;
   int dev = 0, major = 0, minor = 0;
   cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev == fine) return MOE_OK;
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
   if (e != cudaSuccess) return fail_cuda(e);
-  return (major == 10 && minor == 3) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+  if (major != 10 || minor != 3) return MOE_ERR_UNSUPPORTED;
+  fine = dev;
+  return MOE_OK;
 }
 // The bf16 path is built for sm_103a only.
 int check_device(const moe_config& c) { return c.dtype == MOE_BF16 ? check_sm103() : MOE_OK; }
