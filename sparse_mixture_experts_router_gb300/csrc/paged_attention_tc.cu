@@ -18,11 +18,12 @@
 // are used: K0 K1 V0 K2 V1 ... The products of tile i + 1 run under the softmax
 // of tile i.
 //
-// Only keys that every row of the item sees go this way. The few that some
-// rows see and others do not (at most the item's new tokens at either end)
-// are added at the end row by row with fused multiply-adds: no masks in the
-// products, and a value that is not finite stays out of rows that do not see
-// it.
+// Keys that some rows of the item see and others do not (at most its new tokens
+// at either end) are masked row by row in the first and last tiles. A masked
+// weight is 0, and 0 times a value that is not finite is not 0: the block looks
+// at those keys' values first, and where one is not finite the products take
+// only the keys that every row sees, and the others are added at the end, row
+// by row, with fused multiply-adds.
 //
 // One block an SM. At 128 rows, 32 sequences of 500 to 8000 keys: 185 us, 0.46 of
 // measured HBM bandwidth, 385 TFLOP/s (warp-level products, four blocks of 32
@@ -108,21 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
   Item it;
   if (!item_of<kThreads>(prm, prm.item_rows, it)) return;
   start_cluster(prm);
-  // Keys lo_max .. hi_min, which every row sees, in tiles from lo_max on.
   Range rg = range_of(prm, it, prm.item_rows, kKeys);
-  const int common = max(0, rg.hi_min + 1 - rg.lo_max);
-  const int tiles = (common + kKeys - 1) / kKeys;
-  {
-    const int at = it.split * prm.parts + it.part, of = prm.splits * prm.parts;
-    const int each = tiles / of, more = tiles - each * of;
-    rg.t0 = at * each + min(at, more);
-    rg.t1 = rg.t0 + each + (at < more);
-  }
-  const int n = rg.t1 - rg.t0;
-  auto tile_key = [&](int i) { return rg.lo_max + (rg.t0 + i) * kKeys; };
-  Range seen = rg;  // for lookups
-  seen.lo_min = rg.lo_max;
-  seen.hi_max = rg.hi_min;
 
   volatile int* abort_flag = &bars.abort_flag;
   // A warp's wait: all lanes go on, or none. After a wait has run out the
@@ -150,24 +137,71 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     ptx::tmem_alloc(ptx::smem_addr(&bars.tmem), kTmemCols);
     ptx::tmem_relinquish();
   }
-  // Queries, in the layout of a K-major operand; negated for a negative scale,
-  // so that larger products are larger scores.
-  const uint32_t flip = c.scale < 0.f ? 0x80008000u : 0u;
-  for (int i = threadIdx.x; i < kRows * kDim / 8; i += kThreads) {
-    const int r = i / (kDim / 8), v = i % (kDim / 8);
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (8 * v < c.head_dim)
-      x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + it.q_at(prm, r) +
-                                          8 * v);
-    x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
-    *reinterpret_cast<uint4*>(qs + v / 8 * L::kHalf + r * 128 + ((v % 8 ^ (r & 7)) << 4)) = x;
+  // The values of the keys that not every row sees.
+  const int low = min(rg.lo_max, rg.hi_max + 1);         // lo_min .. low - 1
+  const int after = max(rg.hi_min + 1, rg.lo_max);       // after .. hi_max
+  const int below = max(0, low - rg.lo_min), edges = below + max(0, rg.hi_max + 1 - after);
+  auto edge_key = [&](int e) { return e < below ? rg.lo_min + e : after + e - below; };
+  bool wild = false;
+  for (int i = threadIdx.x; i < edges * (kDim / 8); i += kThreads) {
+    const Slot s = slot_of(prm, it, rg, edge_key(i / (kDim / 8)));
+    const int v = i % (kDim / 8);
+    if (!s.in(c) || 8 * v >= c.head_dim) continue;
+    const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v_cache) +
+                                                    s.at(c, it.kh) + 8 * v);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+      wild = wild || (w[y] & 0x7f80u) == 0x7f80u || (w[y] & 0x7f800000u) == 0x7f800000u;
   }
-  ptx::fence_proxy_async_smem();
   ptx::tc_fence_before();
-  __syncthreads();
+  wild = __syncthreads_or(wild);  // and the barriers and Tensor Memory are ready
   ptx::tc_fence_after();
   const uint32_t tmem = bars.tmem;
   const uint32_t ring = ptx::smem_addr(smem);
+
+  // The keys of the products, in tiles of kKeys from key0 on.
+  Range seen = rg;
+  if (wild) seen.lo_min = rg.lo_max, seen.hi_max = rg.hi_min;
+  const int key0 = seen.lo_min, keys = max(0, seen.hi_max + 1 - key0);
+  {
+    const int tiles = (keys + kKeys - 1) / kKeys;
+    const int at = it.split * prm.parts + it.part, of = prm.splits * prm.parts;
+    const int each = tiles / of, more = tiles - each * of;
+    rg.t0 = at * each + min(at, more);
+    rg.t1 = rg.t0 + each + (at < more);
+  }
+  const int n = rg.t1 - rg.t0;
+  auto tile_key = [&](int i) { return key0 + (rg.t0 + i) * kKeys; };
+
+  // Queries, in the layout of a K-major operand; negated for a negative scale,
+  // so that larger products are larger scores. The copying warps are off
+  // already; the warp that issues the products waits for the queries.
+  if (warp <= kMmaWarp) {
+    constexpr int kFill = kSoftmax + 32, kAll = kRows * kDim / 8;
+    const uint32_t flip = c.scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int i0 = 0; i0 < kAll; i0 += 4 * kFill) {
+      uint4 x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + k * kFill + threadIdx.x, r = i / (kDim / 8), v = i % (kDim / 8);
+        x[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (i < kAll && 8 * v < c.head_dim)
+          x[k] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                 it.q_at(prm, r) + 8 * v);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + k * kFill + threadIdx.x, r = i / (kDim / 8), v = i % (kDim / 8);
+        if (i >= kAll) continue;
+        x[k].x ^= flip, x[k].y ^= flip, x[k].z ^= flip, x[k].w ^= flip;
+        *reinterpret_cast<uint4*>(qs + v / 8 * L::kHalf + r * 128 + ((v % 8 ^ (r & 7)) << 4)) = x[k];
+      }
+    }
+    ptx::fence_proxy_async_smem();
+    asm volatile("bar.sync 2, %0;" ::"n"(kFill) : "memory");
+  }
 
   float m = -3.0e38f, l = 0.f;  // of this thread's row (l: of its half of the keys)
   const float scale = fabsf(c.scale) * 1.4426950408889634f;
@@ -175,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
   const bool active = warp < 8 && warp % 4 * 32 < it.rows;
   const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
   constexpr int kCols = kDim / 2;  // columns of O a thread keeps
+  const int pos = it.pos(prm, row), first = it.first(pos);
 
   if (warp < 8) {
     // ------------------------------------------------------------- softmax --
@@ -185,15 +220,17 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
       const uint32_t s_at = tmem + lanes + buf * kKeys;
       uint32_t w[2][32];
       float top = -INFINITY;
-      const int cols = common - (rg.t0 + i) * kKeys - 64 * half;  // of these 64 that are keys
       if (go) {
         ptx::tmem_ld32(s_at + 64 * half, w[0]);
         ptx::tmem_ld32(s_at + 64 * half + 32, w[1]);
         ptx::tmem_ld_wait();
-        if (cols < 64) {
+        // columns from .. to - 1 of these 64 are keys that the row sees
+        const int at = tile_key(i) + 64 * half;
+        const int from = first - at, to = min(pos, seen.hi_max) + 1 - at;
+        if (__any_sync(0xffffffffu, from > 0 || to < 64)) {
 #pragma unroll
           for (int x = 0; x < 64; ++x)
-            if (x >= cols) w[x / 32][x % 32] = 0xff800000u;  // -inf
+            if (x < from || x >= to) w[x / 32][x % 32] = 0xff800000u;  // -inf
         }
 #pragma unroll
         for (int x = 0; x < 64; ++x) top = fmaxf(top, __uint_as_float(w[x / 32][x % 32]));
@@ -399,20 +436,13 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     half_max[half * kRows + row] = l;
     softmax_sync();
     l += half_max[(half ^ 1) * kRows + row];
-    if (it.split == 0 && it.part == 0) {
-      const int pos = it.pos(prm, row), first = it.first(pos);
-      const int after = max(rg.hi_min + 1, rg.lo_max);  // the common keys end before it
-      const int low = min(rg.lo_max, rg.hi_max + 1), total = max(0, low - rg.lo_min) + max(0, rg.hi_max + 1 - after);
-      auto edge_key = [&](int e) {
-        const int below = max(0, low - rg.lo_min);
-        return e < below ? rg.lo_min + e : after + e - below;
-      };
-      for (int e0 = 0; e0 < total; e0 += kEdgeKeys) {
+    if (wild && it.split == 0 && it.part == 0) {
+      for (int e0 = 0; e0 < edges; e0 += kEdgeKeys) {
         softmax_sync();  // the lines and half_max are free
         for (int x = threadIdx.x; x < kEdgeKeys * kDim / 4; x += kSoftmax) {
           const int e = e0 + x / (kDim / 4), v = x % (kDim / 8);
           uint4 y = make_uint4(0u, 0u, 0u, 0u);
-          if (e < total && 8 * v < c.head_dim) {
+          if (e < edges && 8 * v < c.head_dim) {
             const Slot s = slot_of(prm, it, rg, edge_key(e));
             if (s.in(c))
               y = *reinterpret_cast<const uint4*>(
@@ -422,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
           reinterpret_cast<uint4*>(lines)[x] = y;
         }
         softmax_sync();
-        for (int e = e0; e < min(total, e0 + kEdgeKeys); ++e) {
+        for (int e = e0; e < min(edges, e0 + kEdgeKeys); ++e) {
           const uint4* line = reinterpret_cast<const uint4*>(lines + (e - e0) * L::kLine);
           const int key = edge_key(e);
           float dot = 0.f;
@@ -463,11 +493,21 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     }
     ptx::tc_fence_before();
   }
+  if (prm.parts == 1 && warp < 8 && row < it.rows) {
+#pragma unroll
+    for (int x = 0; x < kCols; x += 4) {
+      const int v = (half * kCols + x) / 4;
+      if (4 * v < c.head_dim)
+        write_row<__nv_bfloat16>(prm, it, row, v, make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]),
+                                 m, l);
+    }
+  }
   __syncthreads();  // all products and copies are done: the ring is free
   if (warp == kMmaWarp) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmemCols);
   }
+  if (prm.parts == 1) return;
   if (warp < 8) {
     float* at = reinterpret_cast<float*>(smem) + row * L::kLd + half * kCols;
 #pragma unroll
