@@ -135,6 +135,9 @@ cudaError_t launch_paged_attention(const AttnArgs& a, void* scratch, cudaStream_
   prm.row_blocks = plan.row_blocks;
   prm.group = c.n_heads / c.n_kv_heads;
   prm.item_rows = plan.rows();
+  // One block looks at 4096 pages in about 5 us; 79 sequences of 440 to 940
+  // pages took it 86 us, where the attention takes 15.
+  prm.check_in_use = (long long)c.n_seqs * c.max_pages > 4096;
   prm.by_page = attn::fast_div((uint32_t)c.page_size);
   prm.by_group = attn::fast_div((uint32_t)prm.group);
   prm.by_parts = attn::fast_div((uint32_t)prm.parts);
@@ -145,7 +148,8 @@ cudaError_t launch_paged_attention(const AttnArgs& a, void* scratch, cudaStream_
   prm.split_o = static_cast<float*>(scratch);
   prm.split_ml = reinterpret_cast<float2*>(prm.split_o + split_rows(plan) * c.head_dim);
   const unsigned blocks = (unsigned)((plan.items * plan.splits + 1) * plan.parts);
-  cudaError_t e;
+  cudaError_t e = prm.check_in_use ? launch_reset_status(a.status, s) : cudaSuccess;
+  if (e != cudaSuccess) return e;
   {
     ProfScope p(K_ATTENTION, s);
     e = plan.tc                     ? attn::launch_tc(prm, c.head_dim, blocks, s)

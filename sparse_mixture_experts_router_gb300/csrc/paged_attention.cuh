@@ -48,6 +48,9 @@ struct Params {
   int parts, splits;
   int row_blocks;  // of one (sequence, key-value head)
   int group;       // heads a key-value head
+  // The lists are checked as they are used, after a launch that clears the
+  // status word, and not by a block of their own: for long tables.
+  int check_in_use;
   // divisions by page_size, heads a key-value head, parts, splits,
   // row_blocks, n_kv_heads and head_dim / 4
   FastDiv by_page, by_group, by_parts, by_splits, by_rows, by_heads, by_vecs;
@@ -95,7 +98,7 @@ __device__ __forceinline__ bool item_of(const Params& p, int block_rows, Item& i
   int i = div(p.by_parts, (int)blockIdx.x);
   it.part = (int)blockIdx.x - i * p.parts;
   if (--i < 0) {
-    if (it.part == 0) check_lists<kThreads>(p.a, FirstKey{c.window});
+    if (it.part == 0 && !p.check_in_use) check_lists<kThreads>(p.a, FirstKey{c.window});
     return false;
   }
   auto next = [&](const FastDiv& f, int d) {  // i / d, and the remainder
@@ -109,6 +112,7 @@ __device__ __forceinline__ bool item_of(const Params& p, int block_rows, Item& i
   it.kh = next(p.by_heads, c.n_kv_heads);
   it.b = i;
   it.sq = seq_range(p.a, it.b);
+  if (p.check_in_use && !it.sq.ok && threadIdx.x == 0) set_status(p.a.status, status_check());
   it.G = p.group;
   it.row0 = rb * block_rows;
   it.rows = min(block_rows, it.G * it.sq.n - it.row0);
@@ -139,11 +143,14 @@ __device__ __forceinline__ Range range_of(const Params& p, const Item& it, int b
   return r;
 }
 
-// A key's place in the cache: its page as the table has it (-1 for a key no
-// row sees) and its place in the page. Nothing here uses the page, so a lookup
+// A key's place in the cache: its page as the table has it and its place in the
+// page (both -1 for a key no row sees). Nothing here uses the page, so a lookup
 // for a later tile does not wait for the table.
 struct Slot {
   int page, place;
+  __device__ __forceinline__ void check(const Params& p) const {
+    if (p.check_in_use && place >= 0 && !in(p.a.c)) set_status(p.a.status, status_check());
+  }
   __device__ __forceinline__ bool in(const moe_attn_config& c) const {
     return page >= 0 && page < c.n_pages;
   }
@@ -156,7 +163,7 @@ struct Slot {
   }
 };
 __device__ __forceinline__ Slot slot_of(const Params& p, const Item& it, const Range& r, int key) {
-  Slot s = {-1, 0};
+  Slot s = {-1, -1};
   if (key >= r.lo_min && key <= r.hi_max) {
     const int n = div(p.by_page, key);
     s.place = key - n * p.a.c.page_size;

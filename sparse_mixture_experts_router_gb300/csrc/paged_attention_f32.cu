@@ -79,12 +79,13 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const __grid_constant__ P
   const float* vc = static_cast<const float*>(a.v_cache);
   auto tile_key = [&](int i) { return rg_.base + (rg_.t0 + warp + kWarps * i) * kKeys; };
   auto look_up = [&](int i) {
-    Slot slot = {-1, 0};
+    Slot slot = {-1, -1};
     if (i < mine) slot = slot_of(prm, it, rg_, tile_key(i) + key8);
     return slot;
   };
   auto load = [&](int i, const Slot& slot) {
     if (i < mine) {
+      slot.check(prm);
       const int64_t off = slot.in(c) ? slot.at(c, it.kh) : -1;
       const uint32_t st = ring + (i % kS) * T::kStage;
       constexpr int kAll = kKeys * T::kChunks / 32;

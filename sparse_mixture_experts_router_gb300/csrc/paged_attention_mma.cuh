@@ -151,12 +151,13 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim, kNT, 
   const bool pages_hold_tiles = c.page_size % T::kKeys == 0;
   auto tile_key = [&](int i) { return rg.base + (rg.t0 + warp + kWarps * i) * T::kKeys; };
   auto look_up = [&](int i) {
-    Slot slot = {-1, 0};
+    Slot slot = {-1, -1};
     if (i < mine) slot = slot_of(prm, it, rg, tile_key(i) + lane % T::kKeys);
     return slot;
   };
   auto load = [&](int i, const Slot& slot) {
     if (i < mine) {
+      slot.check(prm);
       const int64_t off = slot.in(c) ? slot.at(c, it.kh) * esz : -1;
       const bool whole =
           pages_hold_tiles && __all_sync(0xffffffffu, off >= 0);  // tiles start on their multiples

@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
   bool wild = false;
   for (int i = threadIdx.x; i < edges * (kDim / 8); i += kThreads) {
     const Slot s = slot_of(prm, it, rg, edge_key(i / (kDim / 8)));
+    s.check(prm);
     const int v = i % (kDim / 8);
     if (!s.in(c) || 8 * v >= c.head_dim) continue;
     const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v_cache) +
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
       Keys k;
 #pragma unroll
       for (int x = 0; x < kSets; ++x) {
-        k.s[x] = {-1, 0};
+        k.s[x] = {-1, -1};
         if (i < n)
           k.s[x] = slot_of(prm, it, seen, tile_key(i) + 32 * (w + kLoadWarps * x) + lane);
       }
@@ -372,8 +373,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     auto offsets = [&](const Keys& k) {
       Offsets r;
 #pragma unroll
-      for (int x = 0; x < kSets; ++x)
+      for (int x = 0; x < kSets; ++x) {
+        k.s[x].check(prm);
         r.o[x] = k.s[x].in(c) ? k.s[x].at(c, it.kh) : (int64_t)-1;
+      }
       return r;
     };
     int g = 0;

@@ -223,9 +223,12 @@ def test_in_a_graph_while_the_cache_grows():
         assert (np.abs(r.out.double().cpu().numpy() - out) <= tol).all()
 
 
-def test_bad_lists_are_reported():
+@pytest.mark.parametrize("columns", [1, 8000])  # a long table is checked as it is used
+@pytest.mark.parametrize("cache,heads", [("bf16", 2), ("e4m3", 2), ("f32", 2), ("bf16", 40)])
+def test_bad_lists_are_reported(columns, cache, heads):
     def status(edit):
-        bt = Batch(new=[2, 1], length=[50, 35], heads=2, kv_heads=1, dim=64, page=16, seed=17)
+        bt = Batch(new=[2, 1], length=[50, 35], heads=heads, kv_heads=1, dim=64, page=16, cache=cache, columns=columns,
+                   seed=17)
         edit(bt)
         return Call(bt)().status
 
@@ -234,9 +237,12 @@ def test_bad_lists_are_reported():
             getattr(bt, name)[i] = v
         return edit
     assert status(lambda bt: None) == moe.MOE_OK
-    for edit in (put("length", 1, -4), put("length", 0, 65), put("table", (0, 1), 99), put("table", (0, 0), -1),
+    for edit in (put("length", 1, -4), put("length", 0, 16 * columns + 64), put("table", (0, 1), 99), put("table", (0, 0), -1),
                  put("table", (1, 2), 1 << 30), put("cu", 1, 1000), put("cu", 0, -1), put("cu", 2, 2)):
         assert status(edit) == moe.MOE_ERR_DEVICE_CHECK
+    assert status(put("table", (0, 3), 1 << 20)) == moe.MOE_ERR_DEVICE_CHECK  # positions 48 and 49
+    if columns > 4:
+        assert status(put("table", (0, 4), 1 << 20)) == moe.MOE_OK  # behind the last
 
 
 def test_lse_is_optional():
