@@ -86,24 +86,30 @@ Plan plan_of(const moe_attn_config& c) {
   const int warps = p.tc ? 1 : 4;
   const int tile = p.tc ? 128 : f32 ? 8 : attn::keys_of(c.head_dim, f8);
   const long long steps = ceil_div(keys, warps * tile);
-  // Parts: as many as fill the SMs, while a block has two steps; then on to
-  // three waves of blocks, so that uneven sequences even out, while a block
-  // has sixteen (it costs about what eight take). Fewer: 64 sequences of 37 to
-  // 8190 keys take 182 us in two parts, 172 in four, 183 in eight; 32 of 100
-  // to 12000 with 20 rows 174, 168, 182.
-  const int per_sm = p.tc ? 1 : attn::blocks_per_sm(c.head_dim, p.nt, f8);
+  // Parts. A block costs its steps and about kPartCost more (its start, its
+  // turn to join), blocks on all slots share the work, and the longest block
+  // ends last: items x (steps + kPartCost x parts) / slots + steps / parts,
+  // least where items x kPartCost x parts^2 = steps x slots; parts is the power
+  // of two nearest to that, and leaves a block two steps. Over 115 drawn calls
+  // a cost of 2, 4, 6, 7, 12 took 1.03, 0.99, 0.98, 0.97, 0.99 of filling the
+  // SMs and then up to three waves of at least eight steps. Clusters of 16 are
+  // placed badly unless all run at once: 84 sequences of 8000 keys take 79 us
+  // in 16 parts, 65 in eight.
+  const int per_sm = p.tc ? 1 : attn::blocks_per_sm(c.head_dim, p.nt, f8 || f32);
+  const long long slots = (long long)per_sm * attn::kPlanSms;
   const int most = p.tc ? 8 : attn::kMaxParts;  // 16 whole SMs are more than some GPCs have
+  constexpr long long kPartCost = 7;
   p.parts = 1;
   while (p.parts < most && steps >= 2 * p.parts &&
-         (p.items * p.parts < attn::kPlanSms ||
-          (p.items * p.parts < 3LL * per_sm * attn::kPlanSms && steps >= 16 * p.parts)))
+         2 * p.items * p.parts * p.parts * kPartCost <= steps * slots &&
+         (p.parts < 8 || 2 * p.items * p.parts <= slots))
     p.parts *= 2;
-  // Splits: where the largest clusters still leave SMs idle and a block has 16
-  // steps or more.
+  // Splits: where the largest clusters still leave SMs idle (their blocks two
+  // an SM where they fit) and a block keeps four steps.
   p.splits = 1;
   if (p.parts == most && p.items > 0)
-    p.splits = (int)std::max(1LL, std::min({(p.tc ? 1LL : 2LL) * attn::kPlanSms / (p.items * p.parts),
-                                            steps / (16 * p.parts),
+    p.splits = (int)std::max(1LL, std::min({std::min(slots, 2LL * attn::kPlanSms) / (p.items * p.parts),
+                                            steps / (4 * p.parts),
                                             (long long)attn::kMaxSplits}));
   return p;
 }
