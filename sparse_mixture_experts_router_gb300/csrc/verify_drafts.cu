@@ -45,10 +45,10 @@ __device__ __forceinline__ float prob(float x) { return __saturatef(x); }
 struct Digits {
   int a = 0, b = 0, c = 0;  // units 2^-22, 2^-44, 2^-60
   __device__ __forceinline__ void add(float p, float q) {
-    const float x = prob(p), y = prob(q);
-    const bool over = x > y;
-    // p and q go through the additions as one pair of fp32
-    const uint64_t v = ptx::f32x2(over ? x : 0.f, over ? y : 0.f);
+    // p and q go through the additions as one pair of fp32; where p <= q it is
+    // (q, q), whose digits cancel
+    const float y = prob(q);
+    const uint64_t v = ptx::f32x2(fmaxf(prob(p), y), y);
     const uint64_t y1 = add2(v, twice(2.f));
     const uint64_t r1 = sub2(v, add2(y1, twice(-2.f)));
     const uint64_t y2 = add2(r1, twice(0x1.8p-21f));
@@ -130,38 +130,63 @@ struct Residual {
       for (int i = 0; i < kE; ++i) y[i] = e + i == hot ? 1.f : 0.f;
     }
   }
-  // The sum over vectors v, v + 32, .. (kU of them, those below end).
-  template <int kU>
-  __device__ __forceinline__ uint64_t step(int v, int end) const {
+  // A warp's vectors v .. v + kStep - 1, in flight at once: each lane's sum.
+  // The pass is bound by instructions as much as by memory, so a step inside
+  // the row has no checks of its own (17.6 us for the batch of 64, with them
+  // 18.4; copied ahead through shared memory, more instructions yet, 20.3).
+  static constexpr int kU = 16 / kE, kStep = 32 * kU;
+  __device__ __forceinline__ uint64_t step(int v, int lane, int end) const {
     float x[kU][kE], y[kU][kE];
-#pragma unroll
-    for (int k = 0; k < kU; ++k) load(min(v + 32 * k, end - 1), x[k], y[k]);
     Digits d;
+    if (v * kE >= shift && (v + kStep) * kE - shift <= vocab && (!q || q_grid)) {
+      const uint4* from = reinterpret_cast<const uint4*>(p + (v + lane) * kE - shift);
 #pragma unroll
-    for (int k = 0; k < kU; ++k)
-      if (v + 32 * k < end) {
+      for (int k = 0; k < kU; ++k) unpack(__ldg(from + 32 * k), x[k]);
+      if (q) {
+        from = reinterpret_cast<const uint4*>(q + (v + lane) * kE - shift);
 #pragma unroll
-        for (int i = 0; i < kE; ++i) d.add(x[k][i], y[k][i]);
+        for (int k = 0; k < kU; ++k) unpack(__ldg(from + 32 * k), y[k]);
+#pragma unroll
+        for (int k = 0; k < kU; ++k)
+#pragma unroll
+          for (int i = 0; i < kE; ++i) d.add(x[k][i], y[k][i]);
+      } else {
+        const int at = hot - (v + lane) * kE + shift;
+#pragma unroll
+        for (int k = 0; k < kU; ++k)
+#pragma unroll
+          for (int i = 0; i < kE; ++i) d.add(x[k][i], at == 32 * kE * k + i ? 1.f : 0.f);
       }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kU; ++k) load(min(v + lane + 32 * k, end - 1), x[k], y[k]);
+#pragma unroll
+      for (int k = 0; k < kU; ++k)
+        if (v + lane + 32 * k < end) {
+#pragma unroll
+          for (int i = 0; i < kE; ++i) d.add(x[k][i], y[k][i]);
+        }
+    }
     return d.value();
   }
 };
 
-// The lists' check: one block, a few threads a sequence.
-__device__ void check_lists(const VerifyArgs& a) {
+
+// Whether the lists are wrong, as far as thread t of n has looked: a few
+// threads a sequence.
+__device__ bool bad_lists(const VerifyArgs& a, int t, int n) {
   const moe_verify_config& c = a.c;
-  const int per = max(1, kThreads / c.n_seqs), sub = threadIdx.x % per;
+  const int per = max(1, n / c.n_seqs), sub = t % per;
   bool bad = false;
-  for (int b = threadIdx.x / per; b < c.n_seqs; b += kThreads / per) {
+  for (int b = t / per; b < c.n_seqs && t < n / per * per; b += n / per) {
     const SeqRange r = seq_rows(a.cu_new, b, c.n_seqs, c.n_tokens, c.max_new);
-    bad = bad || !r.ok;
+    bad |= !r.ok;
     for (int j = 1 + sub; j < r.n; j += per) {
       const int x = a.tokens[r.row0 + j];
-      bad = bad || x < 0 || x >= c.vocab;
+      bad |= x < 0 || x >= c.vocab;
     }
   }
-  bad = __syncthreads_or(bad);
-  if (threadIdx.x == 0) *a.status = bad ? status_check() : MOE_OK;
+  return bad;
 }
 
 template <typename T>
@@ -177,17 +202,12 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a,
   ptx::cluster_arrive();  // the cluster's blocks have started before any is written to
   pdl_wait();
   pdl_trigger();
-  if (b == c.n_seqs) {
-    if (part == 0) check_lists(a);
-    __syncwarp();
-    ptx::cluster_wait();
-    return;
-  }
   const SeqRange r = seq_rows(a.cu_new, b, c.n_seqs, c.n_tokens, c.max_new);
   const T* p = static_cast<const T*>(a.p);
   const T* q = static_cast<const T*>(a.q);
   const int drafts = max(r.n - 1, 0);
 
+  bool bad = false;
   if (warp == 0) {
     int acc = 0;
     for (int j0 = 0; j0 < drafts; j0 += 32) {
@@ -208,8 +228,11 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a,
       if (no) break;
     }
     if (lane == 0) s_accepted = min(acc, drafts);
+  } else if (blockIdx.x == 0) {
+    bad = bad_lists(a, (int)threadIdx.x - 32, kThreads - 32);
   }
-  __syncthreads();
+  bad = __syncthreads_or(bad);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = bad ? status_check() : MOE_OK;
   const int acc = s_accepted;
   if (part == 0) {
     if (threadIdx.x == 0) {
@@ -228,19 +251,20 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a,
   Residual<T> res(p + row * c.p_stride, rejected && q ? q + row * c.q_stride : nullptr,
                   rejected && !q ? a.tokens[row + 1] : -1, c.vocab);
   const float u = fminf(fmaxf(a.u_sample[b], 0.f), 0x1.fffffep-1f);
-  // This warp's segment of the row's vectors.
+  // This warp's segment of the row: whole steps, the row's end aside.
+  constexpr int kU = Residual<T>::kU, kStep = Residual<T>::kStep;
   const int nv = res.vectors(), segs = parts * kWarps, seg = part * kWarps + warp;
-  const int v0 = (int)((long long)nv * seg / segs), v1 = (int)((long long)nv * (seg + 1) / segs);
-  constexpr int kU = 16 / kE;  // vectors a lane has in flight: 16 elements
-  constexpr int kStep = 32 * kU;
-  const int per_slot = ((v1 - v0 + kStep - 1) / kStep + 31) / 32;  // steps a stretch
+  const int row_steps = (nv + kStep - 1) / kStep;
+  const int v0 = (int)((long long)row_steps * seg / segs) * kStep;
+  const int v1 = min((int)((long long)row_steps * (seg + 1) / segs) * kStep, nv);
+  const int per_slot = (max(v1 - v0, 0) + 32 * kStep - 1) / (32 * kStep);  // steps a stretch
   uint64_t total = 0, before = 0, mine = 0;
   for (int pass = 0; pass < 2; ++pass) {
     uint64_t sum = 0, run = 0;
     slot_part[warp][lane] = 0;
     __syncwarp();
     for (int v = v0, step = 0; v < v1; v += kStep, ++step) {
-      run += res.template step<kU>(v + lane, v1);
+      run += res.step(v, lane, v1);
       if ((step + 1) % per_slot && v + kStep < v1) continue;
       run = warp_sum_u64(run);
       if (lane == 0) slot_part[warp][step / per_slot] = run;
@@ -315,33 +339,46 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs a,
 }
 
 template <typename T>
-cudaError_t launch(const VerifyArgs& a, int parts, cudaStream_t s) {
-  static thread_local int device = -1;
+cudaError_t launch(const VerifyArgs& a, cudaStream_t s) {
+  static thread_local int device = -1, room[kMaxParts + 1];  // clusters that run at once
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (device != dev) {
     e = cudaFuncSetAttribute(verify_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
+    for (int n = 1; n <= kMaxParts; ++n) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(n);
+      cfg.blockDim = dim3(kThreads);
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim = {(unsigned)n, 1, 1};
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&room[n], verify_kernel<T>, &cfg);
+      if (e != cudaSuccess) return e;
+    }
     device = dev;
   }
-  const unsigned blocks = (unsigned)(a.c.n_seqs + 1) * (unsigned)parts;
-  return launch_pdl(verify_kernel<T>, dim3(blocks), dim3(kThreads), 0, s, parts, a, parts);
+  // Blocks a sequence: as many as let all sequences run at once, with a vector
+  // for half their threads at least (64 sequences of 129280 tokens: 23 us by
+  // 4, 18 by 8, 28 by 16; 200 of 50021: 28 by 1, 24 by 2, 27 by 3, of which
+  // the GPU's parts hold a few clusters too few). Clusters between 8 and 16
+  // leave parts of the GPU empty: 30 us by 9 where 8 take 24.
+  const long long fed = ((long long)a.c.vocab * sizeof(T) / 16) / (kThreads / 2);
+  int parts = kMaxParts;
+  while (parts > 1 && (parts > fed || a.c.n_seqs > room[parts])) parts -= parts > 8 ? 8 : 1;
+  return launch_pdl(verify_kernel<T>, dim3((unsigned)a.c.n_seqs * (unsigned)parts), dim3(kThreads),
+                    0, s, parts, a, parts);
 }
 
 }  // namespace
 
 cudaError_t launch_verify_drafts(const VerifyArgs& a, cudaStream_t s) {
   if (a.c.n_seqs == 0) return launch_reset_status(a.status, s);
-  // Blocks a sequence: as many as all run at once (4 an SM), with a vector
-  // for half their threads at least; clusters between 8 and 16 leave parts of
-  // the GPU empty (64 sequences of 129280 tokens: 24 us by 8, 30 us by 9).
-  const long long vectors = (long long)a.c.vocab * (a.c.dtype == MOE_F32 ? 4 : 2) / 16;
-  const long long fit = 4LL * num_sms() / (a.c.n_seqs + 1), fed = vectors / (kThreads / 2);
-  const long long most = std::min(fit, fed);
-  const int parts = most >= kMaxParts ? kMaxParts : (int)std::max(1LL, std::min(8LL, most));
   ProfScope p(K_VERIFY, s);
-  return a.c.dtype == MOE_F32 ? launch<float>(a, parts, s) : launch<__nv_bfloat16>(a, parts, s);
+  return a.c.dtype == MOE_F32 ? launch<float>(a, s) : launch<__nv_bfloat16>(a, s);
 }
 
 }  // namespace moe
