@@ -86,22 +86,25 @@ Plan plan_of(const moe_attn_config& c) {
   const int warps = p.tc ? 1 : 4;
   const int tile = p.tc ? 128 : f32 ? 8 : attn::keys_of(c.head_dim, f8);
   const long long steps = ceil_div(keys, warps * tile);
-  // Parts. A block costs its steps and about kPartCost more (its start, its
+  // Parts. A block costs its steps and about kPartCost / 2 more (its start, its
   // turn to join), blocks on all slots share the work, and the longest block
-  // ends last: items x (steps + kPartCost x parts) / slots + steps / parts,
-  // least where items x kPartCost x parts^2 = steps x slots; parts is the power
-  // of two nearest to that, and leaves a block two steps. Over 115 drawn calls
-  // a cost of 2, 4, 6, 7, 12 took 1.03, 0.99, 0.98, 0.97, 0.99 of filling the
-  // SMs and then up to three waves of at least eight steps. Clusters of 16 are
-  // placed badly unless all run at once: 84 sequences of 8000 keys take 79 us
-  // in 16 parts, 65 in eight.
-  const int per_sm = p.tc ? 1 : attn::blocks_per_sm(c.head_dim, p.nt, f8 || f32);
+  // ends last: items x (steps + kPartCost / 2 x parts) / slots + steps / parts,
+  // least where items x kPartCost / 2 x parts^2 = steps x slots; parts is the
+  // power of two nearest to that, and leaves a block two steps. Over 115 drawn
+  // calls a cost of 2, 4, 6, 7, 12 steps took 1.03, 0.99, 0.98, 0.97, 0.99 of
+  // filling the SMs and then up to three waves of at least eight steps; over
+  // 50 of an fp32 cache 7, 10, 14, 20 took 0.92, 0.93, 0.94, 0.95. Clusters of
+  // 16 are placed badly unless all run at once: 84 sequences of 8000 keys take
+  // 79 us in 16 parts, 65 in eight.
+  const int per_sm = p.tc  ? 1
+                     : f32 ? attn::f32_blocks_per_sm(c.head_dim, p.nt)
+                           : attn::blocks_per_sm(c.head_dim, p.nt, f8);
   const long long slots = (long long)per_sm * attn::kPlanSms;
   const int most = p.tc ? 8 : attn::kMaxParts;  // 16 whole SMs are more than some GPCs have
-  constexpr long long kPartCost = 7;
+  constexpr long long kPartCost = 15;
   p.parts = 1;
   while (p.parts < most && steps >= 2 * p.parts &&
-         2 * p.items * p.parts * p.parts * kPartCost <= steps * slots &&
+         p.items * p.parts * p.parts * kPartCost <= steps * slots &&
          (p.parts < 8 || 2 * p.items * p.parts <= slots))
     p.parts *= 2;
   // Splits: where the largest clusters still leave SMs idle (their blocks two

@@ -26,6 +26,9 @@ constexpr int blocks_per_sm(int dim, int nt, bool f8) {
 }
 
 // Keys of a tile of the bf16 and E4M3 kernel.
+constexpr int f32_blocks_per_sm(int dim, int nt) {
+  return dim > 128 ? (nt == 1 ? 3 : 2) : nt > 2 ? 3 : dim <= 64 && nt == 1 ? 8 : 5;
+}
 constexpr int keys_of(int dim, bool f8) { return f8 || dim <= 64 ? 32 : 16; }
 
 // n / d for 0 <= n < 2^30 and 1 <= d < 2^30 as a multiplication.

@@ -2,13 +2,18 @@
 //
 // Tensor cores have no fp32 products, and an fp32 cache is asked for by who
 // wants fp32 results, so the products are fused multiply-adds. Per cached
-// element R of them (R query rows of the head group) against 4 bytes: at 8
-// rows two per byte, a third of what the CUDA cores do while memory delivers
-// it, so the kernel stays memory-bound up to about 16 rows; more rows go in
-// blocks of 16 that read the keys again.
+// element R of them (R query rows of the head group) against 4 bytes: up to
+// about four rows memory bounds the kernel, beyond that the instructions a
+// warp issues (half of them multiply-adds, a quarter loads of shared memory);
+// more than 16 rows go in blocks of 16 that read the keys again.
 //
-// Work, parts and join are those of the other caches: each warp streams tiles
-// of 8 keys through its own ring with cp.async. Scores: lane (key, row group)
+// Work, parts and join are those of the other caches. Each warp has one tile
+// of 8 keys and one of their values in shared memory, filled by cp.async: the
+// next keys are on their way while the weights are taken to the values, the
+// next values during the scores. Two of each a warp hid no more latency than
+// the warps they cost did: with one, three to eight blocks fit an SM instead
+// of one to three, and 58 drawn calls take 8% less time (heads above 128:
+// 1486 -> 1020 us for 7 sequences of 20000 to 45000 keys). Scores: lane (key, row group)
 // takes the dot products of one key with kR rows, 4 elements at a time, keys
 // and queries both from shared memory without bank conflicts. Output: each
 // lane owns 4 (8 for heads above 128) elements of every row and takes the
@@ -23,13 +28,11 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kKeys = 8;
-constexpr int kS = 2;  // stages a warp
 
 template <int kDim>
 struct Tile {
   static constexpr int kChunks = kDim / 4;  // 16-byte chunks of a key
   static constexpr int kBytes = kKeys * kDim * 4;
-  static constexpr int kStage = 2 * kBytes;
   static __device__ __forceinline__ uint32_t at(int k, int c) {
     return (uint32_t)(k * kDim * 4 + ((c ^ k) << 4));
   }
@@ -37,16 +40,20 @@ struct Tile {
 template <int kDim, int kR>
 struct Smem {
   static constexpr int kRows = 4 * kR;
-  static constexpr int kRing = kWarps * kS * Tile<kDim>::kStage;
+  // A warp's tile of keys and of values, later its rows of the join.
+  static constexpr int kWarp = std::max(2 * Tile<kDim>::kBytes, kRows * (kDim + 4) * 4);
+  static constexpr int kRing = kWarps * kWarp;
   static constexpr int kQ = kRows * (kDim + 4) * 4;
   static constexpr int kP = kWarps * kKeys * kRows * 4;
   static constexpr int kStat = (2 * kWarps + 2) * kRows * 4;
   static constexpr int kInbox = (int)sizeof(Inbox<kRows, kDim>);
   static constexpr int kAll = kRing + kInbox + kQ + kP + kStat;
+  static_assert(f32_blocks_per_sm(kDim, kR) * (kAll + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
 template <int kDim, int kR>
-__global__ void __launch_bounds__(kThreads) f32_kernel(const __grid_constant__ Params prm) {
+__global__ void __launch_bounds__(kThreads, f32_blocks_per_sm(kDim, kR))
+    f32_kernel(const __grid_constant__ Params prm) {
   using T = Tile<kDim>;
   using M = Smem<kDim, kR>;
   constexpr int kRows = M::kRows;
@@ -73,8 +80,9 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const __grid_constant__ P
   const int mine = rg_.t1 - rg_.t0 > warp ? (rg_.t1 - rg_.t0 - warp - 1) / kWarps + 1 : 0;
 
   // ---- the stream of tiles ----
-  uint8_t* ring_p = smem + warp * kS * T::kStage;
-  const uint32_t ring = ptx::smem_addr(ring_p);
+  uint8_t* const K = smem + warp * M::kWarp;
+  uint8_t* const V = K + T::kBytes;
+  const uint32_t ring = ptx::smem_addr(K);
   const float* kc = static_cast<const float*>(a.k_cache);
   const float* vc = static_cast<const float*>(a.v_cache);
   auto tile_key = [&](int i) { return rg_.base + (rg_.t0 + warp + kWarps * i) * kKeys; };
@@ -83,11 +91,13 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const __grid_constant__ P
     if (i < mine) slot = slot_of(prm, it, rg_, tile_key(i) + key8);
     return slot;
   };
-  auto load = [&](int i, const Slot& slot) {
+  // Elements to this lane's key, -1 where there is none.
+  auto offset = [&](const Slot& slot) -> int64_t {
+    slot.check(prm);
+    return slot.in(c) ? slot.at(c, it.kh) : -1;
+  };
+  auto load = [&](const float* cache, uint32_t to, int i, int64_t off) {
     if (i < mine) {
-      slot.check(prm);
-      const int64_t off = slot.in(c) ? slot.at(c, it.kh) : -1;
-      const uint32_t st = ring + (i % kS) * T::kStage;
       constexpr int kAll = kKeys * T::kChunks / 32;
 #pragma unroll
       for (int x = 0; x < kAll; ++x) {
@@ -95,20 +105,15 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const __grid_constant__ P
         const int chunk = (x * 32 + lane) % T::kChunks;
         const int64_t o = __shfl_sync(0xffffffffu, off, key);
         const uint32_t n = o >= 0 && 4 * chunk < c.head_dim ? 16u : 0u;
-        const int64_t src = n ? o + 4 * chunk : 0;
-        const uint32_t dst = st + T::at(key, chunk);
-        ptx::cp_async16(dst, kc + src, n);
-        ptx::cp_async16(dst + T::kBytes, vc + src, n);
+        ptx::cp_async16(to + T::at(key, chunk), cache + (n ? o + 4 * chunk : 0), n);
       }
     }
     ptx::cp_async_commit();
   };
-  Slot ahead[kS];  // of this lane's key of the first tiles
-#pragma unroll
-  for (int i = 0; i < kS; ++i) ahead[i] = look_up(i);
-#pragma unroll
-  for (int i = 0; i < kS - 1; ++i) load(i, ahead[i]);
-  Slot next = ahead[kS - 1];
+  int64_t off = offset(look_up(0));
+  load(kc, ring, 0, off);
+  load(vc, ring + T::kBytes, 0, off);
+  Slot next = look_up(1);
 
   // ---- queries, in log2 units ----
   const float scale = c.scale * 1.4426950408889634f;
@@ -136,12 +141,8 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const __grid_constant__ P
     for (int x = 0; x < 4 * kVecs; ++x) o[r][x] = 0.f;
 
   for (int i = 0; i < mine; ++i) {
-    ptx::cp_async_wait_group<kS - 2>();
+    ptx::cp_async_wait_group<1>();
     __syncwarp();
-    load(i + kS - 1, next);  // into the stage that step i - 1 has read
-    next = look_up(i + kS);
-    const uint8_t* K = ring_p + (i % kS) * T::kStage;
-    const uint8_t* V = K + T::kBytes;
     const int key0 = tile_key(i), key = key0 + key8;
 
     float s[kR];
@@ -156,6 +157,10 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const __grid_constant__ P
         s[r] = fmaf(k.x, q.x, fmaf(k.y, q.y, fmaf(k.z, q.z, fmaf(k.w, q.w, s[r]))));
       }
     }
+    __syncwarp();  // every lane has read the keys
+    off = offset(next);
+    load(kc, ring, i + 1, off);
+    next = look_up(i + 2);
     const bool edge = key0 + kKeys - 1 > rg_.hi_min || key0 < rg_.lo_max;
     bool raise = false;
 #pragma unroll
@@ -191,6 +196,7 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const __grid_constant__ P
       l[r] += p;
       ps[key8 * kRows + rg + 4 * r] = mixed && (key > hi[r] || key < lo[r]) ? -1.f : p;
     }
+    ptx::cp_async_wait_group<1>();
     __syncwarp();
 #pragma unroll
     for (int k0 = 0; k0 < kKeys; k0 += kGroups) {
@@ -217,7 +223,8 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const __grid_constant__ P
         }
       }
     }
-    __syncwarp();  // every lane has read this stage and the weights
+    __syncwarp();  // every lane has read the values and the weights
+    load(vc, ring + T::kBytes, i + 1, off);
   }
   ptx::cp_async_wait_all();
 
@@ -233,8 +240,7 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const __grid_constant__ P
   }
   __syncthreads();
   constexpr int kLd = kDim + 4;
-  static_assert(kRows * kLd * 4 <= kS * T::kStage, "the joined rows fit the stages");
-  float* mine_o = reinterpret_cast<float*>(ring_p);
+  float* mine_o = reinterpret_cast<float*>(K);
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     float top = stat[r];
@@ -264,7 +270,7 @@ __global__ void __launch_bounds__(kThreads) f32_kernel(const __grid_constant__ P
   }
   __syncthreads();
   finish<kRows, kDim, kWarps, kThreads, true, float>(prm, it, reinterpret_cast<float*>(smem),
-                                                     kS * T::kStage / 4, kLd, joined, inbox);
+                                                     M::kWarp / 4, kLd, joined, inbox);
 }
 
 template <int kDim, int kR>

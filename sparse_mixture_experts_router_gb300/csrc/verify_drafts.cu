@@ -8,15 +8,16 @@
 // sum passes u R. Running sums in floating point depend on the order they
 // are taken in, which a split over many threads changes; so every entry is
 // held as an integer of 2^-60 units (rounded to nearest) and the sums are
-// exact, whatever the split: one pass over the row for the sums of segments (one a warp), and a
-// second over the one segment that holds u R.
+// exact, whatever the split: one pass over the row for the sums of segments
+// (one a warp), and a second over the one segment that holds u R.
 //
 // A sequence is a cluster of up to 16 blocks, so that a single row of the
 // vocabulary spreads over 16 SMs; the blocks' sums meet in distributed shared
 // memory. Every block finds the accepted drafts by itself: that takes the
-// same time as being told. One block more checks the lists and writes the
-// status, so the call is one launch. Bound by memory for a batch (one or two
-// rows a sequence) and by latency for a single sequence: five dependent
+// same time as being told. The first block's other warps check the lists
+// meanwhile and it writes the status, so the call is one launch. Bound by
+// memory and by the additions for a batch (one or two rows a sequence), and by
+// latency for a single sequence: five dependent
 // reads (rows, draft, its probabilities, the row, the segment) and one
 // exchange between the blocks.
 #include <algorithm>
