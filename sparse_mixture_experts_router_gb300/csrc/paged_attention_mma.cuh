@@ -6,13 +6,14 @@
 // shared head), R multiply-adds an element. So the kernel is a stream of the
 // cache through shared memory, and everything else is arranged to stay out of
 // that stream's way:
-//  - A block of 4 warps (6 for heads above 128) holds one (sequence, key-value head, up to 8 NT query
-//    rows) item, or one of the C parts that its keys are cut into: the parts
-//    are a thread-block cluster and join through its distributed shared
-//    memory, so one launch and no scratch in global memory.
-//  - Each warp streams its own tiles (8 KB: 16 keys of 128 bf16 elements, 32 of E4M3 or of 64 bf16) through its
-//    own ring of stages with cp.async and no block-wide synchronisation; the
-//    pages of the tile after next are looked up one step ahead.
+//  - A block of 4 warps (6 for heads above 128) holds one (sequence, key-value
+//    head, up to 8 NT query rows) item, or one of the C parts that its keys are
+//    cut into: the parts are a thread-block cluster and join through its
+//    distributed shared memory, so one launch and no scratch in global memory.
+//  - Each warp streams its own tiles (8 KB: 16 keys of 128 bf16 elements, 32 of
+//    E4M3 or of 64 bf16) through its own ring of stages with cp.async and no
+//    block-wide synchronisation; the pages of the tile after next are looked up
+//    one step ahead.
 //  - The products are taken transposed, S^T = K Q^T and O^T = V^T P^T: keys
 //    and head elements fill the 16 rows of an m16n8k16 product and query rows
 //    its 8 columns, so 8 query rows waste nothing, K and V are read from
