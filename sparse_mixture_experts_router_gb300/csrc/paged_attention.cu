@@ -16,8 +16,10 @@
 namespace moe {
 namespace {
 
-// Query rows of a bf16 head group above which the tcgen05 kernel runs.
-constexpr int kTcRows = 32;
+// Query rows of a bf16 head group above which the tcgen05 kernel runs: with 35
+// rows it takes 47 us where three blocks of 16 take 29, with 42 rows 43.5 and
+// 44.7, with 48 rows 20.5 and 16.9, with 64 rows 19.0 and (four blocks) 25.9.
+constexpr int kTcRows = 48;
 
 // Rows whose keys were cut into splits: one warp a row.
 constexpr int kJoinWarps = 4;
@@ -77,7 +79,11 @@ Plan plan_of(const moe_attn_config& c) {
   p.tc = c.cache_dtype == MOE_BF16 && c.head_dim <= 128 && all_rows > kTcRows;
   p.unit = p.tc ? 16 : f32 ? 4 : 8;
   const int units = ceil_div(all_rows, p.unit);
-  p.row_blocks = ceil_div(units, p.tc ? 8 : c.head_dim <= 128 ? 4 : 2);
+  // Rows of a block: 16 (fp32: 12), although each block of them reads the keys
+  // again, most of the time from L2: more take the registers and the shared
+  // memory of an SM's third block. bf16, 20 rows: 147 us in one block, 138 in
+  // two; E4M3, 28 rows: 282 and 206; fp32, 16 rows: 42.6 and 37.3.
+  p.row_blocks = ceil_div(units, p.tc ? 8 : f32 && c.head_dim <= 128 ? 3 : 2);
   p.nt = ceil_div(units, p.row_blocks);
   p.items = (long long)c.n_seqs * c.n_kv_heads * p.row_blocks;
   long long keys = (long long)c.max_pages * c.page_size;
@@ -98,7 +104,7 @@ Plan plan_of(const moe_attn_config& c) {
   // 79 us in 16 parts, 65 in eight.
   const int per_sm = p.tc  ? 1
                      : f32 ? attn::f32_blocks_per_sm(c.head_dim, p.nt)
-                           : attn::blocks_per_sm(c.head_dim, p.nt, f8);
+                           : attn::blocks_per_sm(c.head_dim);
   const long long slots = (long long)per_sm * attn::kPlanSms;
   const int most = p.tc ? 8 : attn::kMaxParts;  // 16 whole SMs are more than some GPCs have
   constexpr long long kPartCost = 15;

@@ -19,16 +19,14 @@ constexpr int kMaxParts = 16;   // the largest cluster
 constexpr int kMaxSplits = 32;
 constexpr int kPlanSms = 152;   // the plan does not ask the device, so that the workspace's size is a constant of cfg
 
-// Blocks of the bf16 and E4M3 kernel an SM holds: by registers, and for heads
-// above 128 by shared memory.
-constexpr int blocks_per_sm(int dim, int nt, bool f8) {
-  return dim > 128 ? 1 : nt <= (f8 ? 2 : 3) ? 3 : 2;
-}
-
-// Keys of a tile of the bf16 and E4M3 kernel.
+// Blocks an SM holds, by registers and by shared memory: of the bf16 and E4M3
+// kernel, and of the fp32 one with nt groups of four rows.
+constexpr int blocks_per_sm(int dim) { return dim > 128 ? 1 : 3; }
 constexpr int f32_blocks_per_sm(int dim, int nt) {
   return dim > 128 ? (nt == 1 ? 3 : 2) : nt > 2 ? 3 : dim <= 64 && nt == 1 ? 8 : 5;
 }
+
+// Keys of a tile of the bf16 and E4M3 kernel.
 constexpr int keys_of(int dim, bool f8) { return f8 || dim <= 64 ? 32 : 16; }
 
 // n / d for 0 <= n < 2^30 and 1 <= d < 2^30 as a multiplication.

@@ -6,15 +6,11 @@ namespace attn {
 cudaError_t launch_bf16(const Params& p, int dim, int nt, unsigned blocks, cudaStream_t s) {
   if (dim <= 64) {
     if (nt == 1) return launch_mma<64, 1, false>(p, blocks, s);
-    if (nt == 2) return launch_mma<64, 2, false>(p, blocks, s);
-    if (nt == 3) return launch_mma<64, 3, false>(p, blocks, s);
-    return launch_mma<64, 4, false>(p, blocks, s);
+    return launch_mma<64, 2, false>(p, blocks, s);
   }
   if (dim <= 128) {
     if (nt == 1) return launch_mma<128, 1, false>(p, blocks, s);
-    if (nt == 2) return launch_mma<128, 2, false>(p, blocks, s);
-    if (nt == 3) return launch_mma<128, 3, false>(p, blocks, s);
-    return launch_mma<128, 4, false>(p, blocks, s);
+    return launch_mma<128, 2, false>(p, blocks, s);
   }
   if (nt == 1) return launch_mma<256, 1, false>(p, blocks, s);
   return launch_mma<256, 2, false>(p, blocks, s);

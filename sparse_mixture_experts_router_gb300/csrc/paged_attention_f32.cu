@@ -5,7 +5,7 @@
 // element R of them (R query rows of the head group) against 4 bytes: up to
 // about four rows memory bounds the kernel, beyond that the instructions a
 // warp issues (half of them multiply-adds, a quarter loads of shared memory);
-// more than 16 rows go in blocks of 16 that read the keys again.
+// more than 12 rows go in blocks of up to 12 that read the keys again.
 //
 // Work, parts and join are those of the other caches. Each warp has one tile
 // of 8 keys and one of their values in shared memory, filled by cp.async: the
@@ -285,14 +285,12 @@ cudaError_t launch_f32(const Params& p, int dim, int nt, unsigned blocks, cudaSt
   if (dim <= 64) {
     if (nt == 1) return launch_one<64, 1>(p, blocks, s);
     if (nt == 2) return launch_one<64, 2>(p, blocks, s);
-    if (nt == 3) return launch_one<64, 3>(p, blocks, s);
-    return launch_one<64, 4>(p, blocks, s);
+    return launch_one<64, 3>(p, blocks, s);
   }
   if (dim <= 128) {
     if (nt == 1) return launch_one<128, 1>(p, blocks, s);
     if (nt == 2) return launch_one<128, 2>(p, blocks, s);
-    if (nt == 3) return launch_one<128, 3>(p, blocks, s);
-    return launch_one<128, 4>(p, blocks, s);
+    return launch_one<128, 3>(p, blocks, s);
   }
   if (nt == 1) return launch_one<256, 1>(p, blocks, s);
   return launch_one<256, 2>(p, blocks, s);

@@ -7,7 +7,7 @@
 // cache through shared memory, and everything else is arranged to stay out of
 // that stream's way:
 //  - A block of 4 warps (6 for heads above 128) holds one (sequence, key-value
-//    head, up to 8 NT query rows) item, or one of the C parts that its keys are
+//    head, up to 16 query rows) item, or one of the C parts that its keys are
 //    cut into: the parts are a thread-block cluster and join through its
 //    distributed shared memory, so one launch and no scratch in global memory.
 //  - Each warp streams its own tiles (8 KB: 16 keys of 128 bf16 elements, 32 of
@@ -41,7 +41,7 @@ namespace attn {
 // shared memory with one block of six.
 constexpr int warps_of(int dim) { return dim > 128 ? 6 : 4; }
 
-template <int kDim, int kNT, bool kF8>
+template <int kDim, bool kF8>
 struct Tile {
   static constexpr int kKeys = keys_of(kDim, kF8);
   static constexpr int kRow = kDim * (kF8 ? 1 : 2);  // bytes of a key in shared memory
@@ -52,7 +52,7 @@ struct Tile {
   // more warps hide more than more bytes in flight do (the batch of 64 uneven
   // sequences 175 -> 173 us, 256 short ones in E4M3 130 -> 116 us; four
   // stages, one block an SM: 268 and 221 us).
-  static constexpr int kStages = kNT == 4 && kStage == 8192 ? 3 : kStage >= 8192 ? 2 : 4;
+  static constexpr int kStages = kStage >= 8192 ? 2 : 4;
   // Byte offset of 16-byte chunk c of key k: chunk c of the 8 keys that one
   // matrix load takes falls into 8 different bank groups. Those are 8
   // consecutive keys, and of E4M3 keys also the 8 of 16 that agree in bit 1
@@ -79,11 +79,11 @@ struct Tile {
 // Shared memory after the rings, and how the variants differ.
 template <int kDim, int kNT, bool kF8>
 struct Layout {
-  using T = Tile<kDim, kNT, kF8>;
+  using T = Tile<kDim, kF8>;
   static constexpr int kWarps = warps_of(kDim), kThreads = kWarps * 32, kRows = 8 * kNT;
   // Queries in shared memory where they would take 32 registers a thread and
   // more: the third block that fits an SM then pays more than their reads cost
-  // (20 rows, bf16: 159 us with two blocks, 145 with three).
+  // (20 rows in one block, bf16: 159 us with two blocks an SM, 145 with three).
   static constexpr bool kSharedQ = kNT >= 2;
   static constexpr int kQRow = kDim * 2 + 16;  // bytes; 16 against bank conflicts
   static constexpr bool kOwnInbox = kNT == 1;  // the others' would cost the third block
@@ -109,9 +109,9 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 
 template <int kDim, int kNT, bool kF8>
-__global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim, kNT, kF8))
+__global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
     mma_kernel(const __grid_constant__ Params prm) {
-  using T = Tile<kDim, kNT, kF8>;
+  using T = Tile<kDim, kF8>;
   using L = Layout<kDim, kNT, kF8>;
   constexpr int kS = T::kStages, kMT = T::kKeys / 16, kDT = kDim / 16;
   constexpr int kRows = L::kRows, kWarps = L::kWarps, kThreads = L::kThreads;

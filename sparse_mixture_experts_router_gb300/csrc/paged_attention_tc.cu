@@ -1,6 +1,6 @@
 // Attention of many query rows over a paged bf16 cache, on tcgen05.
 //
-// From about 40 query rows of a head group (drafts of a widely shared head) a
+// From about 50 query rows of a head group (drafts of a widely shared head) a
 // cached element meets enough multiply-adds that warp-level products, 0.6
 // PFLOP/s here, bound the kernel and not memory. Here an item has up to 128
 // rows, the M of a tcgen05.mma, so the keys are read once for all of them:
