@@ -173,6 +173,15 @@ __device__ __forceinline__ Slot slot_of(const Params& p, const Item& it, const R
   return s;
 }
 
+// Where the thread with half `half` (0, 1) of a row's keys leaves its maximum of
+// tile i for the other. Between the write and the read stands the tile's only
+// barrier, and nothing holds a thread back from writing tile i + 1's before the
+// other has read tile i's: the tiles alternate between two places, and that of
+// tile i + 2 is written behind the barrier of tile i + 1.
+__host__ __device__ constexpr int max_slot(int tile, int half, int row, int rows) {
+  return ((tile & 1) * 2 + half) * rows + row;
+}
+
 // ---- the join ----------------------------------------------------------------
 __device__ __forceinline__ void store4(float* out, int64_t at, float4 x) {
   reinterpret_cast<float4*>(out)[at] = x;

@@ -62,7 +62,7 @@ struct Layout {
   static constexpr int kLd = kDim + 4;
   static constexpr int kO = kRows * kLd * 4;           // over the ring, at the end
   static constexpr int kBars = 256;
-  static constexpr int kMax = 2 * kRows * 4;           // of the two threads of a row
+  static constexpr int kMax = 4 * kRows * 4;           // of the two threads of a row, two tiles
   static constexpr int kJoined = 2 * kRows * 4;
   static constexpr int kLine = 2 * kDim * 2;           // a key and its value
   static constexpr int kLines = kEdgeKeys * kLine;
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
   uint8_t* qs = smem + L::kRing;
   Bars& bars = *reinterpret_cast<Bars*>(qs + L::kQ);
   float* half_max = reinterpret_cast<float*>(qs + L::kQ + L::kBars);
-  float* joined = half_max + 2 * kRows;
+  float* joined = half_max + 4 * kRows;
   uint8_t* lines = reinterpret_cast<uint8_t*>(joined + 2 * kRows);
   const AttnArgs& a = prm.a;
   const moe_attn_config& c = a.c;
@@ -236,11 +236,11 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
 #pragma unroll
         for (int x = 0; x < 64; ++x) top = fmaxf(top, __uint_as_float(w[x / 32][x % 32]));
         top *= scale;
-        half_max[half * kRows + row] = top;
+        half_max[max_slot(i, half, row, kRows)] = top;
       }
       softmax_sync();  // and both threads of a row have read its scores
       if (go) {
-        top = fmaxf(top, half_max[(half ^ 1) * kRows + row]);
+        top = fmaxf(top, half_max[max_slot(i, half ^ 1, row, kRows)]);
         const bool raise = top > m + 8.f;
         if (__any_sync(0xffffffffu, raise)) {
           const float f = raise ? ptx::ex2(m - top) : 1.f;
