@@ -477,20 +477,22 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
           if (e > e0) softmax_sync();  // half_max has been read
           half_max[half * kRows + row] = dot;
           softmax_sync();
-          if (key > pos || key < first) continue;
-          // both threads of a row add the halves in the same order
-          const float v = (half_max[row] + half_max[kRows + row]) * scale;
-          const float top = fmaxf(m, v), f = ptx::ex2(m - top), p = ptx::ex2(v - top);
-          m = top;
-          l = l * f + p;
-          const uint32_t* value = reinterpret_cast<const uint32_t*>(line) + kDim / 2 + half * kCols / 2;
+          if (key <= pos && key >= first) {
+            // both threads of a row add the halves in the same order
+            const float v = (half_max[row] + half_max[kRows + row]) * scale;
+            const float top = fmaxf(m, v), f = ptx::ex2(m - top), p = ptx::ex2(v - top);
+            m = top;
+            l = l * f + p;
+            const uint32_t* value = reinterpret_cast<const uint32_t*>(line) + kDim / 2 + half * kCols / 2;
 #pragma unroll
-          for (int x = 0; x < kCols; x += 2) {
-            float y0, y1;
-            bf16x2_to_f32(value[x / 2], y0, y1);
-            o[x] = fmaf(p, y0, o[x] * f);
-            o[x + 1] = fmaf(p, y1, o[x + 1] * f);
+            for (int x = 0; x < kCols; x += 2) {
+              float y0, y1;
+              bf16x2_to_f32(value[x / 2], y0, y1);
+              o[x] = fmaf(p, y0, o[x] * f);
+              o[x + 1] = fmaf(p, y1, o[x + 1] * f);
+            }
           }
+          __syncwarp();  // the barriers above are the whole warp's
         }
       }
     }

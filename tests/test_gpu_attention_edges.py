@@ -1,8 +1,9 @@
 """moe_paged_attention where its parts could come apart: bounds of its own, derived beside them."""
+import numpy as np
 import pytest
 import torch
 
-from serve_common import Batch
+from serve_common import Batch, attention64
 from test_gpu_paged_attention import Call, check
 
 pytestmark = pytest.mark.gpu
@@ -25,3 +26,22 @@ def test_maxima_that_rise_with_every_tile(new, heads):
     for _ in range(5):
         b = Call(bt)()
         assert torch.equal(a.out, b.out) and torch.equal(a.lse, b.lse)
+
+
+@pytest.mark.parametrize("cache,group", [("bf16", 1), ("bf16", 4), ("e4m3", 1), ("e4m3", 4), ("f32", 1), ("f32", 4)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_keys_that_only_some_rows_see_at_both_ends(cache, group, dim):
+    """A window and 20 new tokens: 19 keys at either end are seen by some of the rows only.
+    NaN in the first and in the last of them reaches the first and the last token alone."""
+    new, window, length = 20, 100, 400
+    bt = Batch(new=[new, 3], length=[length, 90], heads=2 * group, kv_heads=2, dim=dim, page=16, cache=cache, window=window, seed=32)
+    for i in (length - new - window + 1, length - 1):
+        page, at = int(bt.table[0, i // 16]), i % 16
+        bt.v[page, at] = 0x7F if cache == "e4m3" else float("nan")
+    out, lse, tol, tol_lse = attention64(bt)
+    r = Call(bt)()
+    got, got_lse = r.out.double().cpu().numpy(), r.lse.double().cpu().numpy()
+    wild = [0, new - 1]
+    tame = [t for t in range(bt.T) if t not in wild]
+    assert np.isnan(got[wild]).all() and (np.abs(got[tame] - out[tame]) <= tol[tame]).all()
+    assert (np.abs(got_lse - lse) <= tol_lse).all()
