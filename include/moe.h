@@ -667,7 +667,9 @@ MOE_API int moe_rope_append(const moe_attn_config* cfg, const void* q, const voi
  * A token that sees nothing (a < 0) gets out = 0 and lse = -inf. What the
  * cache holds elsewhere, NaN included, reaches no output.
  * Scores, running maxima and sums are fp32; the weights are rounded to the
- * type they are multiplied in (see the kernels) and out once.
+ * type they are multiplied in (see the kernels) and out once. An infinite
+ * value that a token sees makes its element of out that infinity, unless the
+ * weight has vanished beside the largest (below about 2^-100 of it): then NaN.
  *
  *  q       [device] [T][Hq][D] cfg->dtype, q_stride between tokens.
  *  cu_new, kv_len, block_table, caches, scales: as above.

@@ -182,6 +182,19 @@ __host__ __device__ constexpr int max_slot(int tile, int half, int row, int rows
   return ((tile & 1) * 2 + half) * rows + row;
 }
 
+// Two weights (a pair of fp32) as two bf16 terms each, together within 2^-16 of
+// the weight: hi, and the rounded rest. Were hi rounded to nearest (2^-17), the
+// rest could be 0 or negative, and against an infinite value hi inf + lo inf
+// would be NaN. So hi is rounded down, and the rest is taken from hi (1 - 2^-23),
+// which leaves it positive for a weight above 2^-110. A weight of 0 has both
+// terms 0, a NaN has NaN.
+__device__ __forceinline__ void split_bf16(uint64_t p, uint32_t& hi, uint32_t& lo) {
+  hi = ptx::bf16x2_down(ptx::f32x2_lo(p), ptx::f32x2_hi(p));
+  const uint64_t h = (uint64_t)(hi & 0xffff0000u) << 32 | (hi << 16);
+  const uint64_t rest = ptx::fma_f32x2(h, ptx::f32x2(0x1p-23f - 1.f, 0x1p-23f - 1.f), p);
+  lo = f32x2_to_bf16x2(ptx::f32x2_lo(rest), ptx::f32x2_hi(rest));
+}
+
 // ---- the join ----------------------------------------------------------------
 __device__ __forceinline__ void store4(float* out, int64_t at, float4 x) {
   reinterpret_cast<float4*>(out)[at] = x;

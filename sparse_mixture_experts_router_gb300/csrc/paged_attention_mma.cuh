@@ -24,7 +24,7 @@
 //    precision (fp32 sums; bf16 and fp16 weights keep their relative step)
 //    and spares the reduction across lanes and the scaling of O.
 // Rounding: scores, maxima, sums and O are fp32. The weights p are rounded to
-// the type of the second product: bf16 twice (p = hi + lo, 2^-17 of p, two
+// the type of the second product: bf16 twice (p = hi + lo, 2^-16 of p, two
 // products) for a bf16 cache, whose error one rounding would double; fp16
 // (2^-12) for an E4M3 cache, whose elements and queries become fp16 (exactly;
 // each query row scaled by a power of two first). Scores by E4M3 products, with
@@ -525,11 +525,10 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
           if (kF8) {
             ph[t][n][h] = ptx::movmatrix_trans(pack_f16(x, y));
           } else {
-            const uint32_t w = f32x2_to_bf16x2(x, y);
-            float xh, yh;
-            bf16x2_to_f32(w, xh, yh);
-            ph[t][n][h] = ptx::movmatrix_trans(w);
-            pl[t][n][h] = ptx::movmatrix_trans(f32x2_to_bf16x2(x - xh, y - yh));
+            uint32_t hi, lo;
+            split_bf16(ptx::f32x2(x, y), hi, lo);
+            ph[t][n][h] = ptx::movmatrix_trans(hi);
+            pl[t][n][h] = ptx::movmatrix_trans(lo);
           }
         }
 #pragma unroll

@@ -265,7 +265,6 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         }
         // Weights: high terms over S's columns 0-63, low terms over 64-127.
         const uint64_t scale2 = ptx::f32x2(scale, scale), minus_m = ptx::f32x2(-m, -m);
-        const uint64_t minus_one = ptx::f32x2(-1.f, -1.f);
         uint64_t sum = 0;
 #pragma unroll
         for (int x = 0; x < 64; x += 32) {
@@ -276,10 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                 (uint64_t)w[x / 32][2 * y + 1] << 32 | w[x / 32][2 * y], scale2, minus_m);
             const uint64_t p = ptx::f32x2(ptx::ex2(ptx::f32x2_lo(v)), ptx::ex2(ptx::f32x2_hi(v)));
             sum = ptx::add_f32x2(sum, p);
-            hi[y] = f32x2_to_bf16x2(ptx::f32x2_lo(p), ptx::f32x2_hi(p));
-            const uint64_t h = (uint64_t)(hi[y] & 0xffff0000u) << 32 | (hi[y] << 16);
-            const uint64_t r = ptx::fma_f32x2(h, minus_one, p);
-            lo[y] = f32x2_to_bf16x2(ptx::f32x2_lo(r), ptx::f32x2_hi(r));
+            split_bf16(p, hi[y], lo[y]);
           }
           ptx::tmem_st16(s_at + 32 * half + x / 2, hi);
           ptx::tmem_st16(s_at + 64 + 32 * half + x / 2, lo);

@@ -100,6 +100,12 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t x, uint64_t y, uint64_t z
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
   return r;
 }
+// Two fp32 as bf16, rounded towards zero.
+__device__ __forceinline__ uint32_t bf16x2_down(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

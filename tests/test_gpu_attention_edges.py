@@ -45,3 +45,35 @@ def test_keys_that_only_some_rows_see_at_both_ends(cache, group, dim):
     tame = [t for t in range(bt.T) if t not in wild]
     assert np.isnan(got[wild]).all() and (np.abs(got[tame] - out[tame]) <= tol[tame]).all()
     assert (np.abs(got_lse - lse) <= tol_lse).all()
+
+
+def same_kinds(got, want):
+    """Infinities of the same sign, and NaN, in the same places."""
+    return all(np.array_equal(f(got), f(want)) for f in (np.isposinf, np.isneginf, np.isnan))
+
+
+def check_not_finite(bt):
+    with np.errstate(invalid="ignore"):
+        out, lse, tol, tol_lse = attention64(bt)
+    r = Call(bt)()
+    got, got_lse = r.out.double().cpu().numpy(), r.lse.double().cpu().numpy()
+    assert same_kinds(got, out)
+    fine = np.isfinite(out)
+    assert (np.abs(got[fine] - out[fine]) <= tol[fine]).all()
+    assert (np.abs(got_lse - lse) <= tol_lse).all()  # takes no part in it
+
+
+@pytest.mark.parametrize("cache", ["bf16", "f32"])
+@pytest.mark.parametrize("new,heads,dim", [(1, 2, 64), (1, 16, 128), (2, 16, 128), (3, 24, 64), (7, 16, 64), (16, 16, 128), (1, 4, 256), (2, 16, 192)])
+@pytest.mark.parametrize("columns", [1, 16384])
+def test_infinite_values(cache, new, heads, dim, columns):
+    """A positive weight times an infinite value is that infinity, wherever the key
+    stands; both infinities together are NaN. lse does not see values."""
+    length = 700
+    bt = Batch(new=[new], length=[length], heads=heads, kv_heads=2, dim=dim, page=16, cache=cache, columns=columns, seed=33, values=0.5)
+    inf = float("inf")
+    for i, e, v in ((0, 1, inf), (37, 2, -inf), (300, 3, inf), (301, 3, inf), (302, 4, inf), (600, 4, -inf), (length - 1, 5, inf),
+                    (length - new, 6, -inf), (length - new, 7, inf), (length - 1, 7, -inf), (128, 0, inf)):
+        page, at = int(bt.table[0, i // 16]), i % 16
+        bt.v[page, at, :, e] = v
+    check_not_finite(bt)
