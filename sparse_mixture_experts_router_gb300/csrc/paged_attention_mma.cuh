@@ -427,9 +427,12 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float v = s[t][n][2 * h + j];
-              // E4M3: the largest weight times its value's scale, and no
+              // E4M3: the largest weight times its value's scale (an infinite
+              // one aside: the sum of weights does not see values), and no
               // weight itself above 2^60
-              if (kF8) v = fmaxf(vs[t][h] > 0.f ? v + __log2f(vs[t][h]) : -INFINITY, v - 60.f);
+              if (kF8)
+                v = fmaxf(vs[t][h] > 0.f && vs[t][h] < INFINITY ? v + __log2f(vs[t][h]) : -INFINITY,
+                          v - 60.f);
               top = fmaxf(top, v);
             }
 #pragma unroll

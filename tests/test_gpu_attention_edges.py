@@ -77,3 +77,20 @@ def test_infinite_values(cache, new, heads, dim, columns):
         page, at = int(bt.table[0, i // 16]), i % 16
         bt.v[page, at, :, e] = v
     check_not_finite(bt)
+
+
+@pytest.mark.parametrize("new,heads,dim", [(1, 2, 64), (2, 16, 128), (7, 16, 64), (2, 16, 256)])
+@pytest.mark.parametrize("columns", [1, 16384])
+def test_value_scales_that_are_not_finite(new, heads, dim, columns):
+    """An infinite scale makes its token's values infinite (those of code 0 NaN) for who
+    sees it, and leaves lse alone; so does a NaN."""
+    length = 500
+    for v in (float("inf"), float("nan")):
+        for places in ((3,), (200, 201), (length - 1,), (0, length - new)):
+            bt = Batch(new=[new], length=[length], heads=heads, kv_heads=2, dim=dim, page=16, cache="e4m3", columns=columns,
+                       seed=34, values=0.5)
+            for i in places:
+                page, at = int(bt.table[0, i // 16]), i % 16
+                bt.v_scale[page, :, at] = v
+                bt.v[page, at, :, 3] = 0
+            check_not_finite(bt)
