@@ -25,12 +25,14 @@
 //    and spares the reduction across lanes and the scaling of O.
 // Rounding: scores, maxima, sums and O are fp32. The weights p are rounded to
 // the type of the second product: bf16 twice (p = hi + lo, 2^-16 of p, two
-// products) for a bf16 cache, whose error one rounding would double; fp16
-// (2^-12) for an E4M3 cache, whose elements and queries become fp16 (exactly;
-// each query row scaled by a power of two first). Scores by E4M3 products, with
-// queries as sums of two E4M3 terms, took 108 us where these take 101 (256
-// sequences of 1 to 2047 keys, 8 rows). The scales of keys multiply scores,
-// those of values multiply weights.
+// products) for a bf16 cache, whose error one rounding would double; for an E4M3
+// cache once, times the value's scale, to fp16 (2^-11). The largest of those is
+// kept between 2^7 and 2^15, so that they have fp16's precision down to 2^-21 of
+// it and none is off by more than 2^-32 of it, however many keys a row has. E4M3
+// elements are exact in fp16, and so are queries (exactly; each query row scaled
+// by a power of two first). Scores by E4M3 products, with queries as sums of two
+// E4M3 terms, took 108 us where these take 101 (256 sequences of 1 to 2047 keys,
+// 8 rows). The scales of keys multiply scores, those of values multiply weights.
 #pragma once
 #include "paged_attention.cuh"
 
@@ -414,7 +416,7 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
             raise = raise || v > m[n][x % 2] + 8.f;
           else  // 0 * vs may be a NaN of a key that is not seen
             raise = raise || !(p[t][n][x] <= 0x1p68f) ||
-                    (v != -INFINITY && !(p[t][n][x] * vs[t][x / 2] <= 256.f));
+                    (v != -INFINITY && !(p[t][n][x] * vs[t][x / 2] <= 0x1p15f));
         }
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -427,11 +429,12 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float v = s[t][n][2 * h + j];
-              // E4M3: the largest weight times its value's scale (an infinite
-              // one aside: the sum of weights does not see values), and no
-              // weight itself above 2^60
+              // E4M3: the largest weight times its value's scale becomes 2^7 (an
+              // infinite scale aside: the sum of weights does not see values),
+              // and no weight itself is above 2^60
               if (kF8)
-                v = fmaxf(vs[t][h] > 0.f && vs[t][h] < INFINITY ? v + __log2f(vs[t][h]) : -INFINITY,
+                v = fmaxf(vs[t][h] > 0.f && vs[t][h] < INFINITY ? v + __log2f(vs[t][h]) - 7.f
+                                                                : -INFINITY,
                           v - 60.f);
               top = fmaxf(top, v);
             }

@@ -94,3 +94,37 @@ def test_value_scales_that_are_not_finite(new, heads, dim, columns):
                 bt.v_scale[page, :, at] = v
                 bt.v[page, at, :, 3] = 0
             check_not_finite(bt)
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(1, 1, 64), (16, 1, 64), (4, 1, 256)])
+def test_many_small_weights_beside_a_large_one(heads, kv_heads, dim):
+    """E4M3: of every 32 keys one has nearly all the weight, and the others, 2^-25.5 of
+    it each, are the only ones with a value in element 0."""
+    n = 8000
+    bt = Batch(new=[1], length=[n], heads=heads, kv_heads=kv_heads, dim=dim, page=16, cache="e4m3", seed=35)
+
+    def e4m3(v):
+        return int(torch.tensor(v).to(torch.float8_e4m3fn).view(torch.uint8))
+    large = torch.zeros((bt.n_pages, bt.page), dtype=torch.bool)
+    for i in range(0, n, 32):
+        large[int(bt.table[0, i // 16]), i % 16] = True
+    small = bt.used & ~large
+    bt.q_rows[:] = 0
+    bt.q[..., 0] = 1
+    for x, s in ((bt.k, bt.k_scale), (bt.v, bt.v_scale)):
+        x[bt.used] = 0
+        s[~s.isnan()] = 1.0
+    bt.v_scale /= 64
+    bt.k[..., 0] = torch.where(large[..., None], e4m3(24.0), bt.k[..., 0]).to(torch.uint8)
+    bt.v[..., 1] = torch.where(large[..., None], e4m3(448.0), bt.v[..., 1]).to(torch.uint8)
+    bt.v[..., 0] = torch.where(small[..., None], e4m3(448.0), bt.v[..., 0]).to(torch.uint8)
+    scale = 25.5 * np.log(2) / 24
+    out, lse, tol, tol_lse = attention64(bt, scale)
+    r = Call(bt, scale)()
+    got = r.out.double().cpu().numpy()
+    # a weight is off by 2^-32 of the largest at most: n of them, against n / 32 of the largest's weight
+    tol = tol + 2.0 ** -32 * 32 * 7.0 * 1.01
+    assert 1e-6 < out[0, 0, 0] < 1e-4
+    assert (np.abs(got - out) <= tol).all()
+    assert abs(got[0, 0, 0] - out[0, 0, 0]) <= 0.02 * out[0, 0, 0]
+    assert (np.abs(r.lse.double().cpu().numpy() - lse) <= tol_lse).all()
