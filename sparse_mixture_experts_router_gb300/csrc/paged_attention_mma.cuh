@@ -29,10 +29,12 @@
 // cache once, times the value's scale, to fp16 (2^-11). The largest of those is
 // kept between 2^7 and 2^15, so that they have fp16's precision down to 2^-21 of
 // it and none is off by more than 2^-32 of it, however many keys a row has. E4M3
-// elements are exact in fp16, and so are queries (exactly; each query row scaled
-// by a power of two first). Scores by E4M3 products, with queries as sums of two
-// E4M3 terms, took 108 us where these take 101 (256 sequences of 1 to 2047 keys,
-// 8 rows). The scales of keys multiply scores, those of values multiply weights.
+// elements are exact in fp16. Queries become fp16 too, each row scaled by a power
+// of two so that its largest element is at least 2^14: elements down to 2^-31 of
+// that are exact, those below it off by 2^-39 of it at most. Scores by E4M3
+// products, with queries as sums of two E4M3 terms, took 108 us where these take
+// 101 (256 sequences of 1 to 2047 keys, 8 rows). The scales of keys multiply
+// scores, those of values multiply weights.
 #pragma once
 #include "paged_attention.cuh"
 
@@ -237,11 +239,11 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
       }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      // The row is scaled to [1, 2) for fp16, by 2^-e of its largest element
-      // (kept normal).
-      const int e = clamp_int((int)(__float_as_uint(amax) >> 23) - 127, -126, 126);
-      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-      f *= __uint_as_float((uint32_t)(127 + e) << 23);
+      // The row is scaled to [2^14, 2^15) for fp16, by 2^(14 - e) of its largest
+      // element (both factors kept normal).
+      const int e = clamp_int((int)(__float_as_uint(amax) >> 23) - 127, -112, 128);
+      const float down = __uint_as_float((uint32_t)(141 - e) << 23);
+      f *= __uint_as_float((uint32_t)(113 + e) << 23);
 #pragma unroll
       for (int d = 0; d < kDT; ++d) {
         float x, y;

@@ -128,3 +128,20 @@ def test_many_small_weights_beside_a_large_one(heads, kv_heads, dim):
     assert (np.abs(got - out) <= tol).all()
     assert abs(got[0, 0, 0] - out[0, 0, 0]) <= 0.02 * out[0, 0, 0]
     assert (np.abs(r.lse.double().cpu().numpy() - lse) <= tol_lse).all()
+
+
+@pytest.mark.parametrize("outlier", [2.0 ** 10, 2.0 ** 18, 2.0 ** 22])
+@pytest.mark.parametrize("new,heads", [(1, 2), (2, 16)])
+def test_queries_with_one_large_element(outlier, new, heads):
+    """E4M3: an element of q far above the others, where the keys are 0, takes nothing
+    from the products of the others (exact above 2^-31 of it: but for a few within 0.002 of 0)."""
+    bt = Batch(new=[new, 1], length=[300, 40], heads=heads, kv_heads=2, dim=64, page=16, cache="e4m3", seed=36)
+    bt.q[..., 5] = outlier
+    bt.k[..., 5] = torch.where(bt.used[..., None], 0, bt.k[..., 5]).to(torch.uint8)
+    check(bt)
+
+
+def test_query_rows_over_the_whole_range():
+    """E4M3: rows whose largest element is near the ends of bf16's range, and zero."""
+    for values, scale in ((2.0 ** 124, 2.0 ** -126), (2.0 ** -100, 2.0 ** 97), (0.0, 0.5)):
+        check(Batch(new=[1, 2], length=[45, 70], heads=4, kv_heads=2, dim=64, page=16, cache="e4m3", values=values, seed=37), scale)
