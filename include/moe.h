@@ -638,9 +638,9 @@ MOE_API size_t moe_attention_workspace_size(const moe_attn_config* cfg);
  * position on axis a and theta = p_a * base^(-2i/rot_dim), pair (x, y) of
  * every head of q and k becomes
  *   (x cos theta - y sin theta, y cos theta + x sin theta),
- * computed in fp32 from an angle reduced exactly (64-bit fixed point, so far
- * positions lose nothing) and rounded once. The rotated k and v as it is go
- * into the sequence's slots of the cache.
+ * computed in fp32 from an angle reduced in 64-bit fixed point (off by 2^-34 of
+ * a turn at most at any position, so far ones lose nothing) and rounded once.
+ * The rotated k and v as it is go into the sequence's slots of the cache.
  *
  *  q, k, v   [device] [T][heads][D] cfg->dtype, token strides of cfg (so they
  *            may be slices of one projection's output).

@@ -6,9 +6,10 @@
 // position on the pair's axis (time, height, width). fp32 angles of far
 // positions are useless (at p = 2^20 one ulp is 1/16 rad), so the angle is a
 // 64-bit fraction of a turn: the host gives each pair's turns per position
-// as f_i = 2^64 base^(-2i/rot_dim) / 2 pi, and p * f_i in wrapping integer
-// arithmetic is the angle modulo one turn, off by at most p * 2^-53 of f_i's
-// rounding. sincospi of that fraction is then fp32-exact to its own bounds.
+// as f_i = 2^64 base^(-2i/rot_dim) / 2 pi, rounded (rope_turns.h), and p * f_i in
+// wrapping integer arithmetic is the angle modulo one turn, off by p / 2 units:
+// 2^-34 of a turn at most. As fp32 half turns for sincospi it is off by up to
+// 2^-25 of one, 1.6 x 2^-24 rad, at any position.
 //
 // One block or one warp per token. A head is held by a group of lanes (a power of two,
 // 8 elements a lane), so the E4M3 scale of a key or value is a shuffle
@@ -18,8 +19,8 @@
 // Bound by memory; what it costs beyond that is the latency of one block's
 // chain (sequence of the token, its page, the sines, the stores).
 #include <cfloat>
-#include <cmath>
 
+#include "rope_turns.h"
 #include "serve_util.cuh"
 
 namespace moe {
@@ -283,9 +284,7 @@ cudaError_t launch(const AttnArgs& a, const RopeTable& rope, int lane_bits, cuda
 cudaError_t launch_rope_append(const AttnArgs& a, cudaStream_t s) {
   if (a.c.n_tokens == 0) return launch_reset_status(a.status, s);
   RopeTable rope = {};
-  const double ratio = a.c.rot_dim ? std::pow((double)a.c.rope_base, -2.0 / a.c.rot_dim) : 0.0;
-  double f = 18446744073709551616.0 / 6.283185307179586476925;  // one radian, 2^64 a turn
-  for (int i = 0; i < a.c.rot_dim / 2; ++i, f *= ratio) rope.turns[i] = (uint64_t)(f + 0.5);
+  rope_turns(a.c.rope_base, a.c.rot_dim / 2, rope.turns);
   int lane_bits = 0;
   while ((8 << lane_bits) < a.c.head_dim) ++lane_bits;
   ProfScope p(K_ROPE_APPEND, s);
