@@ -626,7 +626,9 @@ typedef struct moe_attn_config {
 } moe_attn_config;
 
 /* Host-only validation; touches no GPU. MOE_ERR_UNSUPPORTED where a stride or
- * a row is not a multiple of 16 bytes, or a limit above is passed. */
+ * a row is not a multiple of 16 bytes, a limit above is passed, or one of
+ * Hq <= 1024, B <= 65534, T*Hq < 2^30, n_pages*page_size*Hk < 2^40, strides
+ * <= 2^40 and B*Hk*ceil(Hq/Hk*max_new / 8) < 2^27 does not hold. */
 MOE_API int moe_check_attn_config(const moe_attn_config* cfg);
 
 /* Workspace bytes (0 if cfg is invalid); contents as for the layer's. */

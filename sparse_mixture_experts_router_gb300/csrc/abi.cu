@@ -1044,7 +1044,7 @@ int moe_check_attn_config(const moe_attn_config* c) {
     return MOE_ERR_UNSUPPORTED;
   if ((long long)c->max_pages * c->page_size >= (1LL << 30) ||
       (long long)c->n_tokens * c->n_heads >= (1LL << 30) ||
-      (long long)c->n_pages * c->page_size * c->n_kv_heads >= (1LL << 40))
+      (long long)c->n_pages * c->page_size > ((1LL << 40) - 1) / c->n_kv_heads)
     return MOE_ERR_UNSUPPORTED;
   // the attention's blocks: at most 16 for 8 query rows of a (sequence, head)
   const long long row_tiles = (c->n_heads / c->n_kv_heads * (long long)c->max_new + 7) / 8;

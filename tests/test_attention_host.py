@@ -1,6 +1,9 @@
 """What the attention kernels' host-side functions promise (CPU only)."""
 import subprocess
 
+import pytest
+
+import sparse_mixture_experts_router_gb300 as moe
 from sparse_mixture_experts_router_gb300 import _build
 
 # Two threads of a row, one barrier a tile: each leaves tile i's value, passes
@@ -67,3 +70,16 @@ def run(tmp_path, name, source):
 
 def test_a_rows_two_maxima_are_read_before_they_are_overwritten(tmp_path):
     assert run(tmp_path, "order", ORDER).returncode == 0
+
+
+@pytest.mark.parametrize("pages,page,max_pages,kv_heads,rc", [
+    (1 << 30, 1 << 30, 0, 16, moe.MOE_ERR_UNSUPPORTED), (2 ** 31 - 1, 1 << 29, 1, 16, moe.MOE_ERR_UNSUPPORTED),
+    (2 ** 31 - 1, 2 ** 31 - 1, 0, 1024, moe.MOE_ERR_UNSUPPORTED), (1 << 20, 1 << 16, 1, 16, moe.MOE_ERR_UNSUPPORTED),
+    ((1 << 20) - 1, 1 << 16, 1, 16, moe.MOE_OK), (1 << 24, 16, 1 << 16, 8, moe.MOE_OK)])
+def test_caches_of_2_to_the_40_rows_are_refused(pages, page, max_pages, kv_heads, rc):
+    """The product passes 64 bits for the first three."""
+    _build.build()
+    c = moe.attn_config(n_seqs=1, n_tokens=1, n_heads=kv_heads, n_kv_heads=kv_heads, head_dim=64, page_size=page, n_pages=pages,
+                        max_pages=max_pages)
+    assert moe.check_config(c) == rc
+    assert (moe.workspace_size(c, "attention") > 0) == (rc == moe.MOE_OK)
