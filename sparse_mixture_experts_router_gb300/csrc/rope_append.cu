@@ -192,12 +192,13 @@ __global__ void __launch_bounds__(kThreads)
   else
     __syncthreads();
   // This lane's elements are the same of every head: factors of the element
-  // and of its partner, kept in registers.
+  // and of its partner, kept in registers. An element that does not turn is x 1
+  // + 0 (-0), which is x for a zero of either sign.
   float own[8], other[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int e = e0 + i;
-    own[i] = 1.f, other[i] = 0.f;
+    own[i] = 1.f, other[i] = -0.f;
     if (e < c.rot_dim) {
       const bool first = c.rot_interleaved ? i % 2 == 0 : e < pairs;
       const int n = c.rot_interleaved ? e / 2 : first ? e : e - pairs;

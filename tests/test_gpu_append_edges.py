@@ -38,3 +38,16 @@ def test_every_pair_at_the_farthest_positions(rot, base, interleaved):
     bound = 6 * STEP["f32"] * (np.abs(x[..., lo]) + np.abs(x[..., hi]))
     assert (np.abs(got[..., lo] - (x[..., lo] * cos - x[..., hi] * sin)) <= bound).all()
     assert (np.abs(got[..., hi] - (x[..., hi] * cos + x[..., lo] * sin)) <= bound).all()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "f32"])
+@pytest.mark.parametrize("rot,interleaved", [(32, False), (32, True), (20, False), (0, False)])
+@pytest.mark.parametrize("tokens", [2, 1500])
+def test_zeros_that_do_not_turn_keep_their_sign(cache, rot, interleaved, tokens):
+    bt = Batch(new=[tokens], length=[tokens], heads=2, kv_heads=1, dim=64, page=16, cache=cache, seed=41)
+    bt.q_rows[:, rot:64] = -0.0
+    bt.q_rows[:, 64 + rot:] = 0.0
+    status, q, *_ = run(bt, rot, interleaved)
+    assert status == moe.MOE_OK
+    raw = torch.int32 if cache == "f32" else torch.int16
+    assert torch.equal(q[..., rot:].contiguous().view(raw), bt.q[..., rot:].contiguous().view(raw))
