@@ -23,25 +23,30 @@ inline Double2 operator*(Double2 x, Double2 y) {
   return {s, e - (s - p)};
 }
 
-// f_0 .. f_{pairs-1}; base >= 1.
+// f_0 .. f_{pairs-1} (and what follows up to a multiple of 8); base >= 1.
 inline void rope_turns(float base, int pairs, uint64_t* turns) {
   if (pairs == 0) return;
   // The ratio of neighbours, base^(-1/pairs): pow's, and one Newton step for
   // what its pairs-th power times base is off 1.
   Double2 ratio = {std::pow((double)base, -1.0 / pairs), 0.0}, x = {(double)base, 0.0}, square = ratio;
-  for (int n = pairs; n > 0; n /= 2, square = square * square)
+  for (int n = pairs; n > 0; n /= 2) {
     if (n % 2) x = x * square;
-  ratio.lo = ratio.hi * (((1.0 - x.hi) - x.lo) / pairs);
-  // four products in flight, each four pairs on
-  const Double2 two = ratio * ratio, four = two * two;
-  const Double2 one_radian = {0x1.45f306dc9c883p+61, -0x1.6b01ec5417056p+7};  // 2^64 / 2 pi
-  Double2 f[4] = {one_radian, one_radian * ratio, one_radian * two, one_radian * two * ratio};
-  for (int i = 0; i < pairs; ++i) {
-    const Double2 v = f[i % 4];
-    const double whole = std::floor(v.hi);
-    turns[i] = (uint64_t)whole + (uint64_t)(int64_t)std::floor((v.hi - whole) + v.lo + 0.5);
-    f[i % 4] = v * four;
+    square = square * square;
   }
+  ratio.lo = ratio.hi * (((1.0 - x.hi) - x.lo) / pairs);
+  // eight products in flight, each eight pairs on
+  const Double2 two = ratio * ratio, four = two * two, eight = four * four;
+  const Double2 one_radian = {0x1.45f306dc9c883p+61, -0x1.6b01ec5417056p+7};  // 2^64 / 2 pi
+  Double2 f[8] = {one_radian, one_radian * ratio, one_radian * two, one_radian * (two * ratio)};
+  for (int k = 4; k < 8; ++k) f[k] = f[k - 4] * four;
+  for (int i = 0; i < pairs; i += 8)
+    for (int k = 0; k < 8; ++k) {
+      // to nearest; 0 < hi < 2^62 and |lo| < 2^9
+      const int64_t whole = (int64_t)f[k].hi;
+      const double rest = (f[k].hi - (double)whole) + f[k].lo;
+      turns[i + k] = (uint64_t)(whole - 1024 + (int64_t)(rest + 1024.5));
+      f[k] = f[k] * eight;
+    }
 }
 
 }  // namespace moe
