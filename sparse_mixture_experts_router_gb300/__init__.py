@@ -184,16 +184,26 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-_torch_c = None
+_current_stream = None
+
+
+def _current_stream_getter():
+    """A function that gives the handle of torch's current stream. The handle alone where
+    torch has that (no public name): torch.cuda.current_stream() takes 3 us."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or device is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(device())
 
 
 def _stream(stream):
     if stream is None:
-        global _torch_c
-        if _torch_c is None:
-            from torch import _C as _torch_c
-        # the stream's handle alone: torch.cuda.current_stream() takes 3 us
-        return _torch_c._cuda_getCurrentRawStream(_torch_c._cuda_getDevice())
+        global _current_stream
+        if _current_stream is None:
+            _current_stream = _current_stream_getter()
+        return _current_stream()
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
