@@ -1,8 +1,10 @@
 """What the attention kernels' host-side functions promise (CPU only)."""
 import subprocess
 
+import numpy as np
 import pytest
 
+import attention_bounds as ab
 import sparse_mixture_experts_router_gb300 as moe
 from sparse_mixture_experts_router_gb300 import _build
 
@@ -83,3 +85,14 @@ def test_caches_of_2_to_the_40_rows_are_refused(pages, page, max_pages, kv_heads
                         max_pages=max_pages)
     assert moe.check_config(c) == rc
     assert (moe.workspace_size(c, "attention") > 0) == (rc == moe.MOE_OK)
+
+
+@pytest.mark.parametrize("new,length,heads,dim", [([1], [48], 4, 64), ([2, 1], [64, 31], 8, 128), ([7], [64], 16, 64), ([1], [40], 4, 256)])
+def test_the_bound_of_weights_tells_one_term_from_two(new, length, heads, dim):
+    """What test_gpu_attention_edges.py holds the kernels to: weights of one bf16 term pass
+    it by far, two terms stay inside."""
+    bt = ab.cancelling(new, length, heads, 2, dim, seed=50)
+    out, tol = ab.rows64(bt)
+    assert (np.abs(ab.rows64(bt, ab.two_terms)[0] - out) <= tol / 2).all()
+    off = np.abs(ab.rows64(bt, ab.one_term)[0] - out) / tol
+    assert off.max() > 4 and (off > 1).any(-1).mean() > 0.9

@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+import attention_bounds as ab
 from serve_common import Batch, attention64
 from test_gpu_paged_attention import Call, check
 
@@ -145,3 +146,31 @@ def test_query_rows_over_the_whole_range():
     """E4M3: rows whose largest element is near the ends of bf16's range, and zero."""
     for values, scale in ((2.0 ** 124, 2.0 ** -126), (2.0 ** -100, 2.0 ** 97), (0.0, 0.5)):
         check(Batch(new=[1, 2], length=[45, 70], heads=4, kv_heads=2, dim=64, page=16, cache="e4m3", values=values, seed=37), scale)
+
+
+@pytest.mark.parametrize("new,length,heads,dim", [
+    ([1], [48], 4, 64), ([1, 1], [48, 20], 4, 128), ([2, 1], [64, 31], 8, 128), ([1], [40], 4, 256), ([4], [44], 8, 256), ([4], [64], 8, 64),
+    ([7], [64], 16, 64), ([16, 5], [130, 64], 16, 128)])
+@pytest.mark.parametrize("columns", [1, 16384])
+def test_weights_of_two_terms(new, length, heads, dim, columns):
+    """bf16 caches: values that cancel leave the weights' rounding, 2^-16, as the largest
+    part of the error; one bf16 term would pass the bound 4 times and more."""
+    bt = ab.cancelling(new, length, heads, 2, dim, seed=50, columns=columns)
+    out, tol = ab.rows64(bt)
+    got = Call(bt)().out.double().cpu().numpy()
+    assert (np.abs(got - out) <= tol).all()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3", "f32"])
+@pytest.mark.parametrize("heads,dim,window", [(8, 64, 0), (2, 128, 0), (4, 80, 333)])
+def test_a_prompt_beside_decoding_sequences(cache, heads, dim, window):
+    """A chunk of a prompt of more than a thousand tokens, in one batch with single tokens,
+    drafts, an idle sequence and the start of another prompt."""
+    check(Batch(new=[1, 1100, 1, 3, 0, 1, 260], length=[900, 1500, 2500, 70, 10, 1, 260], heads=heads, kv_heads=2, dim=dim, page=16, cache=cache,
+                window=window, seed=51))
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3", "f32"])
+def test_the_most_new_tokens(cache):
+    """4096 of a sequence, some of them before the cache's first position."""
+    check(Batch(new=[4096, 2], length=[4000, 50], heads=1, kv_heads=1, dim=32, page=64, cache=cache, seed=52))
