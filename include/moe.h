@@ -599,7 +599,8 @@ typedef struct moe_attn_config {
   int32_t max_new;    /* most new tokens of one sequence, 1..4096            */
   int32_t n_heads;    /* query heads Hq, a multiple of n_kv_heads            */
   int32_t n_kv_heads; /* key-value heads Hk: head h reads h / (Hq / Hk)      */
-  int32_t head_dim;   /* D, 8..256, a multiple of 8 (E4M3 cache: of 16)      */
+  int32_t head_dim;   /* D of keys and of values, 8..256, a multiple of 8
+                       * (E4M3 cache: of 16)                                 */
   int32_t page_size;  /* tokens a page, >= 1                                 */
   int32_t n_pages;    /* pages of the cache                                  */
   int32_t max_pages;  /* columns of block_table; max_pages*page_size < 2^30  */

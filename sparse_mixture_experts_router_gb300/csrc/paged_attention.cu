@@ -16,9 +16,13 @@
 namespace moe {
 namespace {
 
-// Query rows of a bf16 head group above which the tcgen05 kernel runs: with 35
-// rows it takes 47 us where three blocks of 16 take 29, with 42 rows 43.5 and
-// 44.7, with 48 rows 20.5 and 16.9, with 64 rows 19.0 and (four blocks) 25.9.
+// Query rows of a bf16 head group above which the tcgen05 kernel runs. us of it
+// and of the warp-level kernel's blocks of 16 (8 key-value heads, 8 new tokens):
+//                                            48 rows       56 rows
+//   32 sequences of 100 to 6000 keys, D 128  137 and 143   139 and 177
+//   128 of 30 to 1000, D 128                 115 and 107   118 and 138
+//   32 of 100 to 6000, D 64                  112 and  90   114 and 115
+//   2 of 20000, D 128                         89 and  52    90 and  98
 constexpr int kTcRows = 48;
 
 // Rows whose keys were cut into splits: one warp a row.
@@ -81,8 +85,9 @@ Plan plan_of(const moe_attn_config& c) {
   const int units = ceil_div(all_rows, p.unit);
   // Rows of a block: 16 (fp32: 12), although each block of them reads the keys
   // again, most of the time from L2: more take the registers and the shared
-  // memory of an SM's third block. bf16, 20 rows: 147 us in one block, 138 in
-  // two; E4M3, 28 rows: 282 and 206; fp32, 16 rows: 42.6 and 37.3.
+  // memory of an SM's third block. Against larger blocks, since removed: bf16,
+  // 20 rows: 147 us in one block, 138 in two; E4M3, 28 rows: 282 and 206; fp32,
+  // 16 rows: 42.6 and 37.3.
   p.row_blocks = ceil_div(units, p.tc ? 8 : f32 && c.head_dim <= 128 ? 3 : 2);
   p.nt = ceil_div(units, p.row_blocks);
   p.items = (long long)c.n_seqs * c.n_kv_heads * p.row_blocks;

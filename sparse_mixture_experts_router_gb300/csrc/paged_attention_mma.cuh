@@ -86,8 +86,10 @@ struct Layout {
   using T = Tile<kDim, kF8>;
   static constexpr int kWarps = warps_of(kDim), kThreads = kWarps * 32, kRows = 8 * kNT;
   // Queries in shared memory where they would take 32 registers a thread and
-  // more: the third block that fits an SM then pays more than their reads cost
-  // (20 rows in one block, bf16: 159 us with two blocks an SM, 145 with three).
+  // more, which costs more than their reads. 16 rows, 64 sequences of 100 to 4000
+  // keys, in registers and in shared memory: bf16 101 and 98 us, E4M3 85 and 81,
+  // bf16 heads of 64 61 and 56; 32 sequences, heads of 256, E4M3 (the registers
+  // spill) 48 and 38.
   static constexpr bool kSharedQ = kNT >= 2;
   static constexpr int kQRow = kDim * 2 + 16;  // bytes; 16 against bank conflicts
   static constexpr bool kOwnInbox = kNT == 1;  // the others' would cost the third block
@@ -120,8 +122,10 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
   constexpr int kS = T::kStages, kMT = T::kKeys / 16, kDT = kDim / 16;
   constexpr int kRows = L::kRows, kWarps = L::kWarps, kThreads = L::kThreads;
   // Scores as two chains of products, where few warps an SM leave one chain's
-  // latency uncovered and registers are free (E4M3, heads of 256, 24 rows:
-  // 53.4 -> 47.9 us; heads of 112 with 28 rows: 282 -> 302).
+  // latency uncovered. Heads of 256, 32 sequences of 100 to 4000 keys, one chain
+  // and two: bf16 8 rows 34.4 and 33.9 us, E4M3 16 rows 39.3 and 38.2; smaller
+  // heads have more warps: E4M3 heads of 128 81.5 and 83.1, bf16 of 64 56.5 and
+  // 57.3 (64 sequences, 16 rows).
   constexpr bool kTwoSums = kDim > 128;
   extern __shared__ __align__(1024) uint8_t smem[];
   const AttnArgs& a = prm.a;

@@ -26,8 +26,8 @@
 // by row, with fused multiply-adds.
 //
 // One block an SM. At 128 rows, 32 sequences of 500 to 8000 keys: 185 us, 0.46 of
-// measured HBM bandwidth, 385 TFLOP/s (warp-level products, four blocks of 32
-// rows: 366 us). A tile takes about 3000 cycles: 1300 for the exponentials and
+// measured HBM bandwidth, 385 TFLOP/s (warp-level products, eight blocks of 16
+// rows: 404 us). A tile takes about 3000 cycles: 1300 for the exponentials and
 // the packing of weights, 550 for reading scores and their maximum, the rest
 // waiting for products and copies; what lies outside the tiles (about 10 us a
 // block, nothing else on the SM) is the next largest part.
