@@ -70,3 +70,16 @@ def two_terms(w):
     w = w.astype(np.float32)
     hi = (w.view(np.uint32) & np.uint32(0xFFFF0000)).view(np.float32).astype(np.float64)
     return hi + bf16(w.astype(np.float64) - hi * (1 - 2.0 ** -23))
+
+
+def rounding_of_sums(dim, sums):
+    """The most that `dim` additions of numbers next to 1 can be off in that many sums (of
+    equal length, added pairwise), each addition by half a step of its result."""
+    def half_step(x):
+        return 2.0 ** math.floor(math.log2(x)) * STEP["f32"]
+    length, total = dim // sums, 0.0
+    total += sums * sum(half_step(i + 1e-3) for i in range(1, length + 1))
+    while sums > 1:
+        length, sums = 2 * length, sums // 2
+        total += sums * half_step(length + 1e-3)
+    return total

@@ -174,3 +174,26 @@ def test_a_prompt_beside_decoding_sequences(cache, heads, dim, window):
 def test_the_most_new_tokens(cache):
     """4096 of a sequence, some of them before the cache's first position."""
     check(Batch(new=[4096, 2], length=[4000, 50], heads=1, kv_heads=1, dim=32, page=64, cache=cache, seed=52))
+
+
+@pytest.mark.parametrize("heads", [2, 8, 16, 24])  # 1, 4, 8 and 12 rows a head group
+@pytest.mark.parametrize("dim,sums", [(128, 2), (256, 4)])
+def test_fp32_scores_are_not_one_sum(heads, dim, sums):
+    """fp32: products of 1 and not quite half a step of the last binade more, which a
+    single running sum drops dim / 2 times. One key: lse is its score."""
+    step = dim // 128 * 31 * 2.0 ** -23  # 0.484 of a step between dim / 2 and dim
+    bt = Batch(new=[1], length=[1], heads=heads, kv_heads=2, dim=dim, page=16, cache="f32", seed=53)
+    bt.q_rows[:] = 1
+    bt.k[bt.used] = 1 + step
+    want = dim * (1 + step)
+    # and the roundings of the factor log2 e, its product, the factor ln 2 and its product
+    bound = ab.rounding_of_sums(dim, sums) + 4 * 2.0 ** -24 * want
+    r = Call(bt, 1.0)()
+    got = r.lse.double().cpu().numpy()
+    assert (np.abs(got - want) <= bound).all(), np.abs(got - want).max() / bound
+    assert torch.equal(r.out.cpu(), bt.v[bt.used][0].repeat_interleave(heads // 2, 0)[None])
+    # what one sum would give
+    one = np.float32(0)
+    for _ in range(dim):
+        one = np.float32(one + np.float32(1 + step))
+    assert abs(float(one) - want) > bound
