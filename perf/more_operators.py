@@ -427,7 +427,7 @@ def _plain_append(s):
         for k in range(0, s["T"], step):  # the older codes of the pages whose scale has grown
             p, ratio = pages[k:k + step], (was / now)[k:k + step]
             codes = cache[p]
-            grown = (older[k:k + step, :, None] & (used[k:k + step, None] & (ratio != 1))[:, None])[..., None]
+            grown = (older[k:k + step, :, None] & ((used[k:k + step, None] | (k == 0)) & (ratio != 1))[:, None])[..., None]
             codes = torch.where(grown, (codes.float() * ratio[:, None, :, None]).to(_F8).float(), codes.float()).to(_F8)
             cache.view(torch.uint8)[p] = codes.view(torch.uint8)
         scale[pages] = now
@@ -701,13 +701,14 @@ def _exact_attend(s, c):
         last = n - new + torch.arange(new, device="cuda")[:, None]
         key = torch.arange(n, device="cuda")
         hide = (key > last) | (key <= last - c["window"] if c["window"] else torch.zeros_like(key > last))
-        for h in range(c["heads"]):
-            score = (s["q"][cu[b]:cu[b + 1], h].double() @ k[h // G].T) / math.sqrt(c["dim"])
-            score[hide] = -math.inf
-            z = torch.logsumexp(score, 1)
-            lse[cu[b]:cu[b + 1], h] = z
-            some = z > -math.inf
-            out[cu[b]:cu[b + 1], h][some] = torch.exp(score[some] - z[some, None]) @ v[h // G]
+        for h in range(c["kv_heads"]):
+            mine = slice(h * G, (h + 1) * G)
+            q = s["q"][cu[b]:cu[b + 1], mine].double().transpose(0, 1)  # [of the group][new][dim]
+            score = (q @ k[h].T / math.sqrt(c["dim"])).masked_fill(hide, -math.inf)
+            z = torch.logsumexp(score, 2)
+            lse[cu[b]:cu[b + 1], mine] = z.T
+            weight = torch.exp(score - z.clamp(min=-1e300)[..., None])
+            out[cu[b]:cu[b + 1], mine] = (weight @ v[h]).transpose(0, 1)
     return {"out": out, "lse": lse}
 
 
