@@ -70,7 +70,8 @@ typedef struct CUstream_st* moe_stream_t; /* same type as cudaStream_t */
 typedef enum {
   MOE_F32 = 0,
   MOE_BF16 = 1,
-  MOE_E4M3 = 2 /* moe_attn_config.cache_dtype only */
+  MOE_E4M3 = 2, /* moe_attn_config.cache_dtype only, like the next */
+  MOE_E4M3_PAGE = 3
 } moe_dtype;
 
 typedef enum {
@@ -585,7 +586,9 @@ MOE_API int moe_layer_backward(const moe_config* cfg, const void* x, const void*
  * Cache: k_cache and v_cache [n_pages][page_size][n_kv_heads][head_dim] of
  * cache_dtype, or any other order through the strides. E4M3 caches have one
  * fp32 scale per token and head, [n_pages][n_kv_heads][page_size], formed as
- * moe_quantize_fp8 forms a row's.
+ * moe_quantize_fp8 forms a row's. MOE_E4M3_PAGE caches have one per page and
+ * head, [n_pages][n_kv_heads]: a power of two, the least 2^e (-110 <= e <= 119)
+ * with |x| <= 448 2^e for the page's finite elements of that head.
  *
  * What the lists hold is checked on the device and recorded in the status
  * word (moe_stream_status) as MOE_ERR_DEVICE_CHECK: cu_new not ascending
@@ -600,12 +603,12 @@ typedef struct moe_attn_config {
   int32_t n_heads;    /* query heads Hq, a multiple of n_kv_heads            */
   int32_t n_kv_heads; /* key-value heads Hk: head h reads h / (Hq / Hk)      */
   int32_t head_dim;   /* D of keys and of values, 8..256, a multiple of 8
-                       * (E4M3 cache: of 16)                                 */
+                       * (E4M3 caches: of 16)                                */
   int32_t page_size;  /* tokens a page, >= 1                                 */
   int32_t n_pages;    /* pages of the cache                                  */
   int32_t max_pages;  /* columns of block_table; max_pages*page_size < 2^30  */
   int32_t dtype;      /* moe_dtype of q, k, v, q_out and out: fp32 or bf16   */
-  int32_t cache_dtype; /* dtype, or MOE_E4M3 with bf16                       */
+  int32_t cache_dtype; /* dtype, or MOE_E4M3 or MOE_E4M3_PAGE with bf16      */
   int32_t window;     /* w > 0: a token sees its own position and the w - 1
                        * before it; 0: all of them                           */
   int32_t rot_dim;    /* leading elements of a head that are rotated: even,
@@ -652,6 +655,13 @@ MOE_API size_t moe_attention_workspace_size(const moe_attn_config* cfg);
  *  q_out     [device] [T][Hq][D] cfg->dtype out, packed; may be q if q is
  *            packed. NULL (with q NULL): only the cache is written.
  *  k_cache, v_cache, k_scale, v_scale: as above; scales NULL unless E4M3.
+ *  MOE_E4M3_PAGE: tokens written into a page from its first place on start its
+ *  scales anew; later ones raise a scale that is too small for them, and the
+ *  page's older codes (those of the places before) are multiplied by the ratio,
+ *  which is exact down to E4M3's subnormals. A scale does not fall otherwise: not
+ *  where a rejected draft's slot is written again. Elements that are not finite
+ *  take no part in a scale and are stored as NaN; finite ones above 448 2^119 as
+ *  that. Two sequences must not be given one page.
  *  A token whose position is below 0 (kv_len below the new tokens) has no
  *  slot: MOE_ERR_DEVICE_CHECK. Two sequences must not be given one slot.
  *  ws        [device] moe_append_workspace_size(cfg) bytes.

@@ -311,7 +311,7 @@ bool attn_lists(const moe_attn_config& c, const int32_t* cu, const int32_t* len,
 }
 // E4M3 caches have scales, the others none.
 bool attn_scales(const moe_attn_config& c, const float* ks, const float* vs) {
-  if (c.cache_dtype != MOE_E4M3) return !ks && !vs;
+  if (!is_e4m3(c.cache_dtype)) return !ks && !vs;
   return c.n_tokens == 0 || (ks && vs);
 }
 
@@ -1016,7 +1016,7 @@ int moe_check_attn_config(const moe_attn_config* c) {
   if (c->n_heads % c->n_kv_heads != 0) return MOE_ERR_INVALID_ARG;
   if (c->n_tokens > (long long)c->n_seqs * c->max_new) return MOE_ERR_INVALID_ARG;
   if (c->dtype != MOE_F32 && c->dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
-  if (c->cache_dtype != c->dtype && !(c->cache_dtype == MOE_E4M3 && c->dtype == MOE_BF16))
+  if (c->cache_dtype != c->dtype && !(is_e4m3(c->cache_dtype) && c->dtype == MOE_BF16))
     return MOE_ERR_INVALID_ARG;
   if (c->rot_dim < 0 || c->rot_dim % 2 != 0 || c->rot_dim > c->head_dim ||
       (c->rot_interleaved != 0 && c->rot_interleaved != 1))
@@ -1050,7 +1050,7 @@ int moe_check_attn_config(const moe_attn_config* c) {
   const long long row_tiles = (c->n_heads / c->n_kv_heads * (long long)c->max_new + 7) / 8;
   if (row_tiles * c->n_kv_heads * c->n_seqs >= (1LL << 27)) return MOE_ERR_UNSUPPORTED;
   const int64_t e = (int64_t)elem_bytes(c->dtype);
-  const int64_t ce = c->cache_dtype == MOE_E4M3 ? 1 : e;
+  const int64_t ce = is_e4m3(c->cache_dtype) ? 1 : e;
   if (D % 8 != 0 || D * ce % 16 != 0) return MOE_ERR_UNSUPPORTED;
   for (int64_t n : rows)
     if (n * e % 16 != 0 || n > (1LL << 40)) return MOE_ERR_UNSUPPORTED;

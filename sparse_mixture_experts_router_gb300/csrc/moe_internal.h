@@ -305,6 +305,9 @@ cudaError_t launch_bwd_wgrad(const moe_config& c, const int32_t* seg, const void
 // The batch and cache description with the defaults of moe_attn_config filled
 // in (strides, base, scale). The kernels form no address from cu_new, kv_len
 // or block_table entries that fail the checks of serve_util.cuh.
+inline bool is_e4m3(int cache_dtype) {
+  return cache_dtype == MOE_E4M3 || cache_dtype == MOE_E4M3_PAGE;
+}
 struct AttnArgs {
   moe_attn_config c;
   const int32_t* cu_new;

@@ -78,7 +78,7 @@ struct Plan {
 };
 Plan plan_of(const moe_attn_config& c) {
   Plan p;
-  const bool f32 = c.cache_dtype == MOE_F32, f8 = c.cache_dtype == MOE_E4M3;
+  const bool f32 = c.cache_dtype == MOE_F32, f8 = is_e4m3(c.cache_dtype);
   const long long all_rows = (long long)(c.n_heads / c.n_kv_heads) * c.max_new;
   p.tc = c.cache_dtype == MOE_BF16 && c.head_dim <= 128 && all_rows > kTcRows;
   p.unit = p.tc ? 16 : f32 ? 4 : 8;
@@ -174,7 +174,7 @@ cudaError_t launch_paged_attention(const AttnArgs& a, void* scratch, cudaStream_
     ProfScope p(K_ATTENTION, s);
     e = plan.tc                     ? attn::launch_tc(prm, c.head_dim, blocks, s)
         : c.cache_dtype == MOE_F32  ? attn::launch_f32(prm, c.head_dim, plan.nt, blocks, s)
-        : c.cache_dtype == MOE_E4M3 ? attn::launch_e4m3(prm, c.head_dim, plan.nt, blocks, s)
+        : is_e4m3(c.cache_dtype)    ? attn::launch_e4m3(prm, c.head_dim, plan.nt, blocks, s)
                                     : attn::launch_bf16(prm, c.head_dim, plan.nt, blocks, s);
   }
   if (e != cudaSuccess || plan.splits == 1) return e;

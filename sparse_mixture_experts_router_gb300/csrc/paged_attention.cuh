@@ -160,7 +160,8 @@ struct Slot {
            (int64_t)kh * c.head_stride;
   }
   __device__ __forceinline__ int64_t scale_at(const moe_attn_config& c, int kh) const {
-    return ((int64_t)page * c.n_kv_heads + kh) * c.page_size + place;
+    const int64_t row = (int64_t)page * c.n_kv_heads + kh;
+    return c.cache_dtype == MOE_E4M3_PAGE ? row : row * c.page_size + place;
   }
 };
 __device__ __forceinline__ Slot slot_of(const Params& p, const Item& it, const Range& r, int key) {

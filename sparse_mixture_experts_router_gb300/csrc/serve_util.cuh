@@ -57,9 +57,10 @@ __device__ void check_lists(const AttnArgs& a, First first) {
   for (int b = threadIdx.x / per; b < c.n_seqs; b += kThreads / per) {
     const SeqRange r = seq_range(a, b);
     bad = bad || !r.ok;
-    if (r.n == 0 || r.len == 0) continue;
+    if (r.n == 0) continue;
     const int at = first(r);
     bad = bad || at < 0;
+    if (r.len == 0) continue;
     const int last = (r.len - 1) / c.page_size;
     const int32_t* table = a.table + (int64_t)b * c.max_pages;
 #pragma unroll 4
