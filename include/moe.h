@@ -746,6 +746,162 @@ MOE_API int moe_verify_drafts(const moe_verify_config* cfg, const void* p, const
                     int32_t* n_accepted, int32_t* kv_next, void* ws, size_t ws_bytes,
                     moe_stream_t stream);
 
+/*
+ * Logits to probabilities: what moe_verify_drafts reads, from the target model's
+ * logits. Row t is after new token j of its sequence b (rows as above). With s(v)
+ * whether token v is in b's history or among its new tokens 0 .. j, and c(v) how
+ * often it is among those of the history from entry n_prompt[b] on (what was
+ * generated) and the new tokens 0 .. j:
+ *   x = logit, a NaN as -inf
+ *   x = x > 0 ? x / repetition[b] : x * repetition[b]    where s(v)
+ *   x = x - frequency[b] c(v), then - presence[b] where c(v) > 0
+ *   x = x + bias                                         where b's list has v
+ *   x = -inf                                             where the mask's bit is 0
+ *   p = softmax(x / temperature[b])                      over the row
+ * each step rounded to fp32. temperature 0 gives the whole probability to the
+ * largest x (equal ones: the lowest v). If x is +inf somewhere, those share the
+ * probability equally. A row that the mask or the logits leave nothing (every x
+ * is -inf) is all 0, for which moe_verify_drafts draws -1.
+ *
+ *  logits     [device] [T][V] cfg->dtype, logits_stride between rows.
+ *  cu_new     [device] [B+1] as above.
+ *  tokens     [device] [T] int32, or NULL: new tokens are not counted.
+ *  history    [device] [n_history] int32, cu_history [device] [B+1]: sequence b's
+ *             tokens before the new ones are entries cu_history[b] ..
+ *             cu_history[b+1]-1; n_prompt [device] [B], of which the first
+ *             n_prompt[b] were not generated. With n_history 0 history is NULL and
+ *             the other two are not read.
+ *  repetition, presence, frequency  [device] [B] fp32, or NULL: 1, 0, 0.
+ *             repetition > 0.
+ *  bias_token [device] [n_bias] int32, bias [device] [n_bias] fp32, cu_bias
+ *             [device] [B+1]: b's entries, ascending by token, none twice. With
+ *             n_bias 0 the first two are NULL and cu_bias is not read.
+ *  mask       [device] [n_masks][ceil(V/32)] uint32: bit v % 32 of word v / 32 is 1
+ *             where v is allowed; mask_row [device] [T] int32: the row's mask, -1:
+ *             none. With n_masks 0 mask is NULL and mask_row is not read.
+ *  temperature [device] [B] fp32, or NULL: 1. >= 0, finite.
+ *  p          [device] [T][V] cfg->out_dtype out, p_stride between rows; may be
+ *             logits if dtypes and strides are equal. cfg->out_logits: x times
+ *             1 / temperature (x itself for 0) and no softmax.
+ *  ws         [device] moe_logits_workspace_size(cfg) bytes.
+ * MOE_ERR_DEVICE_CHECK: cu_new as above; cu_history or cu_bias not ascending from 0
+ * to n_history or n_bias; n_prompt outside the history's length; a token or a
+ * bias's token outside [0, V) (left out); a list of biases that does not ascend; a
+ * mask_row outside [-1, n_masks) (taken as -1); repetition <= 0 or temperature < 0
+ * or either not finite. Counts are integers and sums run in a fixed order, so
+ * equal calls give equal bits.
+ */
+typedef struct moe_logits_config {
+  int32_t n_seqs;    /* B >= 0                                               */
+  int32_t n_tokens;  /* T, rows, 0..min(B*max_new, 2^26)                      */
+  int32_t max_new;   /* 1..4096                                              */
+  int32_t vocab;     /* V, 1..2^24                                           */
+  int32_t dtype;     /* of logits: fp32 or bf16                              */
+  int32_t out_dtype; /* of p: fp32 or bf16                                   */
+  int32_t out_logits; /* 1: p receives the logits after all but the softmax  */
+  int32_t n_history; /* entries of history, >= 0                             */
+  int32_t n_bias;    /* entries of bias_token, >= 0                          */
+  int32_t n_masks;   /* rows of mask, >= 0                                   */
+  int64_t logits_stride, p_stride; /* elements between rows, >= V; 0: packed */
+} moe_logits_config;
+MOE_API int moe_check_logits_config(const moe_logits_config* cfg);
+MOE_API size_t moe_logits_workspace_size(const moe_logits_config* cfg);
+MOE_API int moe_logits_probs(const moe_logits_config* cfg, const void* logits,
+                    const int32_t* cu_new, const int32_t* tokens, const int32_t* history,
+                    const int32_t* cu_history, const int32_t* n_prompt, const float* repetition,
+                    const float* presence, const float* frequency, const int32_t* bias_token,
+                    const float* bias, const int32_t* cu_bias, const uint32_t* mask,
+                    const int32_t* mask_row, const float* temperature, void* p, void* ws,
+                    size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * ---- The pages of a cache --------------------------------------------------
+ *
+ * A pool of n_pages pages serves B sequences. Sequence b of len[b] tokens holds the
+ * pages of block_table[b][i], i < ceil(len[b] / page_size); a page may be held
+ * by several (a common prompt). refs [n_pages] counts the holders of each page: the
+ * sequences' table entries and whatever else the caller has added (a prompt kept
+ * for later). A page with count 0 is free. cfg gives the cache's shape, types and
+ * strides, n_seqs and max_pages; its fields of a decode step are checked but not
+ * used. MOE_ERR_UNSUPPORTED above 2^30 pages or 2^30 16-byte vectors a page.
+ *
+ * moe_pages_update makes every sequence anew, in one step:
+ *  - it becomes the first kept[b] tokens of sequence parent[b] (old tables; fork,
+ *    beams, and with parent b itself the trim after rejected drafts; kept 0: freed
+ *    or new) with room for need[b] >= kept[b] tokens;
+ *  - pages that it no longer holds lose a count, shared ones gain one;
+ *  - entries ceil(kept / page_size) .. ceil(need / page_size) - 1 get free pages;
+ *  - where need[b] > kept[b] and the page that holds token kept[b] - 1 has room for
+ *    more and other holders, the sequence gets a free page in its place, with the
+ *    kept tokens of the old one copied (copy on write).
+ * Free pages are those with count 0 once every sequence has given up what it no
+ * longer holds, taken in ascending order by the sequences in ascending order, each
+ * in the order of its entries. When they run out, sequences whose wants, added up in
+ * order, pass the number of free pages get none: granted[b] = kept[b] where need[b]
+ * is granted otherwise (a page given up by copy on write is free in the next call).
+ *
+ *  parent     [device] [B] int32, -1 (no tokens) .. B-1, or NULL: b.
+ *  len        [device] [B] int32: tokens held, in the tables as they are.
+ *  kept, need [device] [B] int32.
+ *  block_table [device] [B][max_pages], refs [device] [n_pages] int32.
+ *  table_out  [device] [B][max_pages] int32 out: entries below
+ *             ceil(granted[b] / page_size) are written, others left as they were.
+ *             May be block_table if parent is NULL.
+ *  refs_out   [device] [n_pages] int32 out; may be refs.
+ *  granted    [device] [B] int32 out: tokens each sequence has room for; the next
+ *             call's len. May be kept or need, and len if parent is NULL.
+ *  k_cache, v_cache, k_scale, v_scale: as moe_rope_append; only the copies of copy
+ *             on write change them.
+ *  ws         [device] moe_pages_workspace_size(cfg) bytes (of all three calls).
+ * MOE_ERR_DEVICE_CHECK: parent outside its range, len or need over max_pages *
+ * page_size or below 0, kept over the parent's len, need below kept, a page
+ * outside [0, n_pages) that is in use, a count that is or falls below 0. No address
+ * is formed from such a value; the outputs it reaches are undefined.
+ */
+MOE_API size_t moe_pages_workspace_size(const moe_attn_config* cfg);
+MOE_API int moe_pages_update(const moe_attn_config* cfg, const int32_t* parent,
+                    const int32_t* len, const int32_t* kept, const int32_t* need,
+                    const int32_t* block_table, const int32_t* refs, int32_t* table_out,
+                    int32_t* refs_out, int32_t* granted, void* k_cache, void* v_cache,
+                    float* k_scale, float* v_scale, void* ws, size_t ws_bytes,
+                    moe_stream_t stream);
+
+/*
+ * Moves the L pages in use to the indexes below L: the i-th of those at L or above,
+ * in ascending order, to the i-th free one below L; the others stay.
+ *
+ *  len, block_table, refs: as above. table_out may be block_table, refs_out refs.
+ *  table_out  [device] [B][max_pages] int32 out: entries in use are written, others
+ *             left as they were.
+ *  refs_out   [device] [n_pages] int32 out: counts at the new indexes.
+ *  page_map   [device] [n_pages] int32 out: each page's new index, -1 for a free one.
+ *  n_live     [device] int32 out: L.
+ *  caches, scales: pages that move are copied, no other is changed.
+ * MOE_ERR_DEVICE_CHECK: len as above, a page in use outside [0, n_pages) or with
+ * count 0 (its entry is left as it was), a count below 0 (taken as 0).
+ */
+MOE_API int moe_pages_compact(const moe_attn_config* cfg, const int32_t* len,
+                    const int32_t* block_table, const int32_t* refs, int32_t* table_out,
+                    int32_t* refs_out, int32_t* page_map, int32_t* n_live, void* k_cache,
+                    void* v_cache, float* k_scale, float* v_scale, void* ws, size_t ws_bytes,
+                    moe_stream_t stream);
+
+/*
+ * Copies pages src[i] of one pair of caches to pages dst[i] of another of the same
+ * types and strides (into a larger pool; out of one and back in).
+ *
+ *  src, dst   [device] [n_copies] int32; no page twice in dst. A pair with a page
+ *             outside [0, n_src_pages) or [0, cfg->n_pages) is left out and sets
+ *             MOE_ERR_DEVICE_CHECK.
+ *  k_from, v_from, k_from_scale, v_from_scale: caches of n_src_pages pages; may be
+ *             the ones written, where no page is in both lists.
+ */
+MOE_API int moe_pages_copy(const moe_attn_config* cfg, int32_t n_copies, const int32_t* src,
+                    const int32_t* dst, int32_t n_src_pages, const void* k_from,
+                    const void* v_from, const float* k_from_scale, const float* v_from_scale,
+                    void* k_cache, void* v_cache, float* k_scale, float* v_scale, void* ws,
+                    size_t ws_bytes, moe_stream_t stream);
+
 /* Synchronises `stream`, then returns the device-side status recorded in the
  * workspace `ws` by the last call that used it (MOE_OK, MOE_ERR_TIMEOUT or
  * MOE_ERR_DEVICE_CHECK), or MOE_ERR_CUDA if the stream reports an error. */

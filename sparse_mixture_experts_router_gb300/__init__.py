@@ -80,6 +80,13 @@ class moe_verify_config(ctypes.Structure):
         ("p_stride", ctypes.c_int64), ("q_stride", ctypes.c_int64)]
 
 
+class moe_logits_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("n_seqs", "n_tokens", "max_new", "vocab", "dtype", "out_dtype", "out_logits",
+                 "n_history", "n_bias", "n_masks")] + [
+        ("logits_stride", ctypes.c_int64), ("p_stride", ctypes.c_int64)]
+
+
 def attn_config(n_seqs, n_tokens, n_heads, n_kv_heads, head_dim, page_size, n_pages, max_pages,
                 max_new=1, dtype=MOE_BF16, cache_dtype=None, window=0, rot_dim=0,
                 rot_interleaved=False, rot_sections=(0, 0, 0), rope_base=0.0, scale=0.0, q_stride=0,
@@ -100,12 +107,21 @@ def verify_config(n_seqs, n_tokens, vocab, max_new=1, dtype=MOE_F32, p_stride=0,
     return moe_verify_config(n_seqs, n_tokens, max_new, vocab, dtype, p_stride, q_stride)
 
 
+def logits_config(n_seqs, n_tokens, vocab, max_new=1, dtype=MOE_F32, out_dtype=MOE_F32,
+                  out_logits=False, n_history=0, n_bias=0, n_masks=0, logits_stride=0,
+                  p_stride=0) -> moe_logits_config:
+    """The batch of ``moe_logits_probs``."""
+    return moe_logits_config(n_seqs, n_tokens, max_new, vocab, dtype, out_dtype, int(out_logits),
+                             n_history, n_bias, n_masks, logits_stride, p_stride)
+
+
 _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _I = ctypes.c_int
 _CFG = ctypes.POINTER(moe_config)
 _ACFG = ctypes.POINTER(moe_attn_config)
 _VCFG = ctypes.POINTER(moe_verify_config)
+_LCFG = ctypes.POINTER(moe_logits_config)
 _SIGS = {
     "moe_version": (_I, []),
     "moe_status_string": (ctypes.c_char_p, [_I]),
@@ -143,6 +159,14 @@ _SIGS = {
     "moe_check_verify_config": (_I, [_VCFG]),
     "moe_verify_workspace_size": (_SZ, [_VCFG]),
     "moe_verify_drafts": (_I, [_VCFG] + [_P] * 10 + [_P, _SZ, _P]),
+    "moe_check_logits_config": (_I, [_LCFG]),
+    "moe_logits_workspace_size": (_SZ, [_LCFG]),
+    "moe_logits_probs": (_I, [_LCFG] + [_P] * 16 + [_P, _SZ, _P]),
+    "moe_pages_workspace_size": (_SZ, [_ACFG]),
+    "moe_pages_update": (_I, [_ACFG] + [_P] * 13 + [_P, _SZ, _P]),
+    "moe_pages_compact": (_I, [_ACFG] + [_P] * 11 + [_P, _SZ, _P]),
+    "moe_pages_copy": (_I, [_ACFG, ctypes.c_int32, _P, _P, ctypes.c_int32] + [_P] * 8
+                       + [_P, _SZ, _P]),
     "moe_stream_status": (_I, [_P, _P]),
     "moe_set_decode_barrier_test": (None, [ctypes.c_int32, ctypes.c_uint64]),
     "moe_profile_enable": (None, [_I]),
@@ -217,9 +241,10 @@ def status_string(rc: int) -> str:
 
 
 def check_config(cfg) -> int:
-    """The status of a moe_config, moe_attn_config or moe_verify_config."""
+    """The status of a moe_config, moe_attn_config, moe_verify_config or moe_logits_config."""
     fn = {moe_attn_config: "moe_check_attn_config",
-          moe_verify_config: "moe_check_verify_config"}.get(type(cfg), "moe_check_config")
+          moe_verify_config: "moe_check_verify_config",
+          moe_logits_config: "moe_check_logits_config"}.get(type(cfg), "moe_check_config")
     return getattr(lib(), fn)(ctypes.byref(cfg))
 
 
@@ -229,7 +254,8 @@ def workspace_size(cfg, kind: str = "layer") -> int:
           "layer_fp8": "moe_workspace_size_fp8", "layer_nvfp4": "moe_workspace_size_nvfp4",
           "backward": "moe_workspace_size_backward", "reroute": "moe_reroute_workspace_size",
           "append": "moe_append_workspace_size", "attention": "moe_attention_workspace_size",
-          "verify": "moe_verify_workspace_size"}[kind]
+          "verify": "moe_verify_workspace_size", "logits": "moe_logits_workspace_size",
+          "pages": "moe_pages_workspace_size"}[kind]
     return int(getattr(lib(), fn)(ctypes.byref(cfg)))
 
 
@@ -371,6 +397,44 @@ def moe_verify_drafts(cfg, p, q, tokens, u_accept, u_sample, cu_new, kv_len, out
         ctypes.byref(cfg), _ptr(p), _ptr(q), _ptr(tokens), _ptr(u_accept), _ptr(u_sample),
         _ptr(cu_new), _ptr(kv_len), _ptr(out_tokens), _ptr(n_accepted), _ptr(kv_next), _ptr(ws),
         ws.numel() if ws is not None else 0, _stream(stream)))
+
+
+def moe_logits_probs(cfg, logits, cu_new, tokens, history, cu_history, n_prompt, repetition, presence,
+                     frequency, bias_token, bias, cu_bias, mask, mask_row, temperature, p, ws,
+                     stream=None):
+    _check("moe_logits_probs", lib().moe_logits_probs(
+        ctypes.byref(cfg), _ptr(logits), _ptr(cu_new), _ptr(tokens), _ptr(history),
+        _ptr(cu_history), _ptr(n_prompt), _ptr(repetition), _ptr(presence), _ptr(frequency),
+        _ptr(bias_token), _ptr(bias), _ptr(cu_bias), _ptr(mask), _ptr(mask_row),
+        _ptr(temperature), _ptr(p), _ptr(ws), ws.numel() if ws is not None else 0,
+        _stream(stream)))
+
+
+def moe_pages_update(cfg, parent, length, kept, need, block_table, refs, table_out, refs_out, granted,
+                     k_cache, v_cache, k_scale, v_scale, ws, stream=None):
+    _check("moe_pages_update", lib().moe_pages_update(
+        ctypes.byref(cfg), _ptr(parent), _ptr(length), _ptr(kept), _ptr(need), _ptr(block_table),
+        _ptr(refs), _ptr(table_out), _ptr(refs_out), _ptr(granted), _ptr(k_cache), _ptr(v_cache),
+        _ptr(k_scale), _ptr(v_scale), _ptr(ws), ws.numel() if ws is not None else 0,
+        _stream(stream)))
+
+
+def moe_pages_compact(cfg, length, block_table, refs, table_out, refs_out, page_map, n_live, k_cache,
+                      v_cache, k_scale, v_scale, ws, stream=None):
+    _check("moe_pages_compact", lib().moe_pages_compact(
+        ctypes.byref(cfg), _ptr(length), _ptr(block_table), _ptr(refs), _ptr(table_out),
+        _ptr(refs_out), _ptr(page_map), _ptr(n_live), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+        _ptr(v_scale), _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)))
+
+
+def moe_pages_copy(cfg, src, dst, n_src_pages, k_from, v_from, k_from_scale, v_from_scale, k_cache,
+                   v_cache, k_scale, v_scale, ws, stream=None):
+    """Copies pages src[i] (of n_src_pages) to pages dst[i]."""
+    _check("moe_pages_copy", lib().moe_pages_copy(
+        ctypes.byref(cfg), src.numel(), _ptr(src), _ptr(dst), n_src_pages, _ptr(k_from),
+        _ptr(v_from), _ptr(k_from_scale), _ptr(v_from_scale), _ptr(k_cache), _ptr(v_cache),
+        _ptr(k_scale), _ptr(v_scale), _ptr(ws), ws.numel() if ws is not None else 0,
+        _stream(stream)))
 
 
 def moe_balance_stats(n_experts, T, top_k, counts, prob_sum, alpha, f, P, aux, stream=None):

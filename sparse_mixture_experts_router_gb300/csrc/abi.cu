@@ -347,7 +347,8 @@ const char* kKernelNames[K_NUM] = {"reset_status",  "router_topk",    "permute_h
                                    "bwd_da",        "bwd_dx",         "bwd_router",
                                    "bwd_wgrad",     "decode_fused",   "reroute",
                                    "decode_front",  "rope_append",    "paged_attention",
-                                   "attention_join", "verify_drafts"};
+                                   "attention_join", "verify_drafts", "logits",
+                                   "pages",         "pages_copy"};
 struct Prof {
   std::mutex mu;
   uint32_t mask = 0;
@@ -1185,6 +1186,210 @@ int moe_verify_drafts(const moe_verify_config* cfg, const void* p, const void* q
   a.kv_next = kv_next;
   a.status = static_cast<int*>(ws);
   cudaError_t e = launch_verify_drafts(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : fail_cuda(e);
+}
+
+int moe_check_logits_config(const moe_logits_config* c) {
+  if (!c) return MOE_ERR_INVALID_ARG;
+  if (c->n_seqs < 0 || c->n_tokens < 0 || c->max_new < 1 || c->vocab < 1 || c->n_history < 0 ||
+      c->n_bias < 0 || c->n_masks < 0 || (c->out_logits != 0 && c->out_logits != 1))
+    return MOE_ERR_INVALID_ARG;
+  if (c->n_tokens > (long long)c->n_seqs * c->max_new) return MOE_ERR_INVALID_ARG;
+  if ((c->dtype != MOE_F32 && c->dtype != MOE_BF16) ||
+      (c->out_dtype != MOE_F32 && c->out_dtype != MOE_BF16))
+    return MOE_ERR_INVALID_ARG;
+  if ((c->logits_stride != 0 && c->logits_stride < c->vocab) ||
+      (c->p_stride != 0 && c->p_stride < c->vocab))
+    return MOE_ERR_INVALID_ARG;
+  if (c->max_new > kMaxNew || c->n_seqs > kMaxSeqs || c->vocab > (1 << 24) ||
+      c->n_tokens > kMaxLogitRows || c->logits_stride > (1LL << 40) || c->p_stride > (1LL << 40))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+size_t moe_logits_workspace_size(const moe_logits_config* c) {
+  return moe_check_logits_config(c) == MOE_OK ? 256 : 0;
+}
+
+int moe_logits_probs(const moe_logits_config* cfg, const void* logits, const int32_t* cu_new,
+                     const int32_t* tokens, const int32_t* history, const int32_t* cu_history,
+                     const int32_t* n_prompt, const float* repetition, const float* presence,
+                     const float* frequency, const int32_t* bias_token, const float* bias,
+                     const int32_t* cu_bias, const uint32_t* mask, const int32_t* mask_row,
+                     const float* temperature, void* p, void* ws, size_t ws_bytes,
+                     moe_stream_t stream) {
+  int rc = moe_check_logits_config(cfg);
+  if (rc != MOE_OK) return rc;
+  LogitsArgs a = {};
+  a.c = *cfg;
+  if (a.c.logits_stride == 0) a.c.logits_stride = a.c.vocab;
+  if (a.c.p_stride == 0) a.c.p_stride = a.c.vocab;
+  if (a.c.n_tokens > 0 && (!logits || !p || !cu_new)) return MOE_ERR_INVALID_ARG;
+  // lists come whole where they have entries, and are not read where they have none
+  if (a.c.n_history > 0 ? !history || !cu_history || !n_prompt : history != nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (a.c.n_bias > 0 ? !bias_token || !bias || !cu_bias : bias_token || bias)
+    return MOE_ERR_INVALID_ARG;
+  if (a.c.n_masks > 0 ? !mask || !mask_row : mask != nullptr) return MOE_ERR_INVALID_ARG;
+  // in place only where every element is written where it was read
+  if (p && p == logits && (a.c.dtype != a.c.out_dtype || a.c.logits_stride != a.c.p_stride))
+    return MOE_ERR_INVALID_ARG;
+  if (!all_aligned({logits, cu_new, tokens, history, cu_history, n_prompt, repetition, presence,
+                    frequency, bias_token, bias, cu_bias, mask, mask_row, temperature, p}))
+    return MOE_ERR_MISALIGNED;
+  if ((rc = check_ws(ws, ws_bytes, moe_logits_workspace_size(cfg))) != MOE_OK) return rc;
+  if ((rc = check_sm103()) != MOE_OK) return rc;
+  a.logits = logits;
+  a.cu_new = cu_new;
+  a.tokens = tokens;
+  a.history = history;
+  a.cu_history = cu_history;
+  a.n_prompt = n_prompt;
+  a.repetition = repetition;
+  a.presence = presence;
+  a.frequency = frequency;
+  a.bias_token = bias_token;
+  a.bias = bias;
+  a.cu_bias = cu_bias;
+  a.mask = mask;
+  a.mask_row = a.c.n_masks > 0 ? mask_row : nullptr;
+  a.temperature = temperature;
+  a.p = p;
+  a.status = static_cast<int*>(ws);
+  cudaError_t e = launch_logits(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : fail_cuda(e);
+}
+
+// The limits of the page calls beside those of the configuration.
+static int check_pages(const moe_attn_config* c) {
+  const int rc = moe_check_attn_config(c);
+  if (rc != MOE_OK) return rc;
+  const long long row = c->head_dim * (is_e4m3(c->cache_dtype) ? 1 : (long long)elem_bytes(c->dtype));
+  if (c->n_pages > (1 << 30) || row / 16 * c->n_kv_heads >= (1LL << 30) / c->page_size)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+size_t moe_pages_workspace_size(const moe_attn_config* c) {
+  if (check_pages(c) != MOE_OK) return 0;
+  return 256 + align_up(pages_scratch_bytes(*c), 256);
+}
+
+// The caches that the page calls read or write: all there are of a type, or none
+// where the pool is empty.
+static int check_caches(const moe_attn_config& c, const void* k, const void* v, const float* ks,
+                        const float* vs) {
+  const bool scales = is_e4m3(c.cache_dtype);
+  if ((!scales && (ks || vs)) || (c.n_pages > 0 && (!k || !v || (scales && (!ks || !vs)))))
+    return MOE_ERR_INVALID_ARG;
+  return all_aligned({k, v, ks, vs}) ? MOE_OK : MOE_ERR_MISALIGNED;
+}
+
+int moe_pages_update(const moe_attn_config* cfg, const int32_t* parent, const int32_t* len,
+                     const int32_t* kept, const int32_t* need, const int32_t* block_table,
+                     const int32_t* refs, int32_t* table_out, int32_t* refs_out, int32_t* granted,
+                     void* k_cache, void* v_cache, float* k_scale, float* v_scale, void* ws,
+                     size_t ws_bytes, moe_stream_t stream) {
+  int rc = check_pages(cfg);
+  if (rc != MOE_OK) return rc;
+  PagesArgs a = {};
+  a.c = attn_defaults(*cfg);
+  if (a.c.n_seqs > 0 && (!len || !kept || !need || !granted ||
+                         (a.c.max_pages > 0 && (!block_table || !table_out))))
+    return MOE_ERR_INVALID_ARG;
+  if (a.c.n_pages > 0 && (!refs || !refs_out)) return MOE_ERR_INVALID_ARG;
+  // a parent's row may be written before another sequence has read it
+  if (parent && ((table_out && table_out == block_table) || (len && granted == len)))
+    return MOE_ERR_INVALID_ARG;
+  if ((rc = check_caches(a.c, k_cache, v_cache, k_scale, v_scale)) != MOE_OK) return rc;
+  if (!all_aligned({parent, len, kept, need, block_table, refs, table_out, refs_out, granted}))
+    return MOE_ERR_MISALIGNED;
+  if ((rc = check_ws(ws, ws_bytes, moe_pages_workspace_size(cfg))) != MOE_OK) return rc;
+  if ((rc = check_sm103()) != MOE_OK) return rc;
+  a.parent = parent;
+  a.len = len;
+  a.kept = kept;
+  a.need = need;
+  a.table = block_table;
+  a.refs = refs;
+  a.table_out = table_out;
+  a.refs_out = refs_out;
+  a.granted = granted;
+  a.k_from = a.k_cache = k_cache;
+  a.v_from = a.v_cache = v_cache;
+  a.k_from_scale = a.k_scale = k_scale;
+  a.v_from_scale = a.v_scale = v_scale;
+  a.status = static_cast<int*>(ws);
+  cudaError_t e = launch_pages_update(a, static_cast<char*>(ws) + 256,
+                                      reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : fail_cuda(e);
+}
+
+int moe_pages_compact(const moe_attn_config* cfg, const int32_t* len, const int32_t* block_table,
+                      const int32_t* refs, int32_t* table_out, int32_t* refs_out,
+                      int32_t* page_map, int32_t* n_live, void* k_cache, void* v_cache,
+                      float* k_scale, float* v_scale, void* ws, size_t ws_bytes,
+                      moe_stream_t stream) {
+  int rc = check_pages(cfg);
+  if (rc != MOE_OK) return rc;
+  PagesArgs a = {};
+  a.c = attn_defaults(*cfg);
+  if (!n_live || (a.c.n_seqs > 0 && (!len || (a.c.max_pages > 0 && (!block_table || !table_out)))))
+    return MOE_ERR_INVALID_ARG;
+  if (a.c.n_pages > 0 && (!refs || !refs_out || !page_map)) return MOE_ERR_INVALID_ARG;
+  if ((rc = check_caches(a.c, k_cache, v_cache, k_scale, v_scale)) != MOE_OK) return rc;
+  if (!all_aligned({len, block_table, refs, table_out, refs_out, page_map, n_live}))
+    return MOE_ERR_MISALIGNED;
+  if ((rc = check_ws(ws, ws_bytes, moe_pages_workspace_size(cfg))) != MOE_OK) return rc;
+  if ((rc = check_sm103()) != MOE_OK) return rc;
+  a.len = len;
+  a.table = block_table;
+  a.refs = refs;
+  a.table_out = table_out;
+  a.refs_out = refs_out;
+  a.page_map = page_map;
+  a.n_live = n_live;
+  a.k_from = a.k_cache = k_cache;
+  a.v_from = a.v_cache = v_cache;
+  a.k_from_scale = a.k_scale = k_scale;
+  a.v_from_scale = a.v_scale = v_scale;
+  a.status = static_cast<int*>(ws);
+  cudaError_t e = launch_pages_compact(a, static_cast<char*>(ws) + 256,
+                                       reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : fail_cuda(e);
+}
+
+int moe_pages_copy(const moe_attn_config* cfg, int32_t n_copies, const int32_t* src,
+                   const int32_t* dst, int32_t n_src_pages, const void* k_from, const void* v_from,
+                   const float* k_from_scale, const float* v_from_scale, void* k_cache,
+                   void* v_cache, float* k_scale, float* v_scale, void* ws, size_t ws_bytes,
+                   moe_stream_t stream) {
+  int rc = check_pages(cfg);
+  if (rc != MOE_OK) return rc;
+  if (n_copies < 0 || n_src_pages < 0) return MOE_ERR_INVALID_ARG;
+  PagesArgs a = {};
+  a.c = attn_defaults(*cfg);
+  if (n_copies > 0 && (!src || !dst)) return MOE_ERR_INVALID_ARG;
+  moe_attn_config from = a.c;
+  from.n_pages = n_src_pages;
+  if ((rc = check_caches(a.c, k_cache, v_cache, k_scale, v_scale)) != MOE_OK) return rc;
+  if ((rc = check_caches(from, k_from, v_from, k_from_scale, v_from_scale)) != MOE_OK) return rc;
+  if (!all_aligned({src, dst})) return MOE_ERR_MISALIGNED;
+  if ((rc = check_ws(ws, ws_bytes, moe_pages_workspace_size(cfg))) != MOE_OK) return rc;
+  if ((rc = check_sm103()) != MOE_OK) return rc;
+  a.n_copies = n_copies;
+  a.n_src_pages = n_src_pages;
+  a.src = src;
+  a.dst = dst;
+  a.k_from = k_from;
+  a.v_from = v_from;
+  a.k_from_scale = k_from_scale;
+  a.v_from_scale = v_from_scale;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.status = static_cast<int*>(ws);
+  cudaError_t e = launch_pages_copy(a, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MOE_OK : fail_cuda(e);
 }
 

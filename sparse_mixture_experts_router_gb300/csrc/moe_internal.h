@@ -23,6 +23,7 @@ constexpr int kAttnMaxDim = 256;    // a head's output stays in one warp's regis
 constexpr int kAttnMaxHeads = 1024;
 constexpr int kMaxNew = 4096;       // new tokens of one sequence
 constexpr int kMaxSeqs = 65534;
+constexpr int kMaxLogitRows = 1 << 26;  // rows x 16 blocks stay below 2^31
 
 // Permutation chunk: pairs handled by one block (8 warps x 8 rounds x 32).
 constexpr int kPermuteChunk = 2048;
@@ -345,6 +346,63 @@ struct VerifyArgs {
   int* status;
 };
 cudaError_t launch_verify_drafts(const VerifyArgs& a, cudaStream_t s);
+struct LogitsArgs {
+  moe_logits_config c;
+  const void* logits;
+  const int32_t* cu_new;
+  const int32_t* tokens;
+  const int32_t* history;
+  const int32_t* cu_history;
+  const int32_t* n_prompt;
+  const float* repetition;
+  const float* presence;
+  const float* frequency;
+  const int32_t* bias_token;
+  const float* bias;
+  const int32_t* cu_bias;
+  const uint32_t* mask;
+  const int32_t* mask_row;
+  const float* temperature;
+  void* p;
+  int* status;
+};
+cudaError_t launch_logits(const LogitsArgs& a, cudaStream_t s);
+struct PagesArgs {
+  moe_attn_config c;
+  // update
+  const int32_t* parent;
+  const int32_t* kept;
+  const int32_t* need;
+  int32_t* granted;
+  // update and compact
+  const int32_t* len;
+  const int32_t* table;
+  const int32_t* refs;
+  int32_t* table_out;
+  int32_t* refs_out;
+  // compact
+  int32_t* page_map;
+  int32_t* n_live;
+  // copy
+  int32_t n_copies, n_src_pages;
+  const int32_t* src;
+  const int32_t* dst;
+  // caches copied from and to
+  const void* k_from;
+  const void* v_from;
+  const float* k_from_scale;
+  const float* v_from_scale;
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  int* status;
+};
+// scratch: pages_scratch_bytes(a.c) bytes, 256-byte aligned.
+size_t pages_scratch_bytes(const moe_attn_config& c);
+cudaError_t launch_pages_update(const PagesArgs& a, void* scratch, cudaStream_t s);
+cudaError_t launch_pages_compact(const PagesArgs& a, void* scratch, cudaStream_t s);
+cudaError_t launch_pages_copy(const PagesArgs& a, cudaStream_t s);
 
 // ---- profiling hooks (abi.cu) ----------------------------------------------
 enum KernelId {
@@ -377,6 +435,9 @@ enum KernelId {
   K_ATTENTION,
   K_ATTENTION_JOIN,
   K_VERIFY,
+  K_LOGITS,
+  K_PAGES,
+  K_PAGES_COPY,
   K_NUM
 };
 void prof_begin(int id, cudaStream_t s);

@@ -1,0 +1,501 @@
+// The pages of a cache: sequences forked, trimmed, freed and given room (update),
+// the pages in use moved to the low end (compact), and pages copied.
+//
+// The page counts and tables are small (a pool of 64k pages has 256 KB of counts), and what
+// happens to them is a chain of steps that each need all of the one before: counts
+// given up and gained, then the pages that are free, then who gets which. So one
+// cluster of blocks works through them, with a cluster barrier between steps; the
+// steps' sums (pages wanted before a sequence, free pages before an index) are block
+// scans and one exchange through distributed shared memory. Counts change by integer
+// atomics, whose order does not matter. What has to be copied goes onto a list that a
+// second kernel, over all SMs, works off: it is launched whatever the list holds,
+// because the host does not know it.
+//
+// The first is bound by the latency of its steps (about a microsecond each), the
+// second by memory: 16-byte loads, eight in flight a thread.
+#include "serve_ptx.cuh"
+#include "serve_util.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 1024;  // of a planning block
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxParts = 16;
+constexpr int kCopyThreads = 256;
+constexpr int kCopyVecs = 8;  // 16-byte vectors a thread has in flight
+
+// A page to copy: its first tokens, from page src to page dst.
+struct PageCopy {
+  int src, dst, tokens, pad;
+};
+struct PlanHead {
+  int n_copies;
+  int pad[63];
+};
+// What lies in the workspace behind the status word's 256 bytes.
+struct Scratch {
+  PlanHead* head;
+  PageCopy* copies;  // at most a page a sequence, or half of the pool
+  long long* before; // [n_seqs] pages that earlier sequences of its block want
+  int* want;         // [n_seqs] pages a sequence wants, times 2, and 1 with a copy on write
+  int* free;         // [n_pages] free pages, or those below the number in use
+  int* high;         // [n_pages] by rank, pages in use at that number or above
+  size_t bytes;
+};
+template <typename T>
+T* carve(char*& at, size_t n) {
+  T* p = reinterpret_cast<T*>(at);
+  at += align_up(n * sizeof(T), 256);
+  return p;
+}
+Scratch scratch_of(const moe_attn_config& c, void* base) {
+  char* at = static_cast<char*>(base);
+  const size_t pages = (size_t)c.n_pages, seqs = (size_t)c.n_seqs;
+  Scratch s;
+  s.head = carve<PlanHead>(at, 1);
+  s.copies = carve<PageCopy>(at, seqs > pages / 2 + 1 ? seqs : pages / 2 + 1);
+  s.before = carve<long long>(at, seqs);
+  s.want = carve<int>(at, seqs);
+  s.free = carve<int>(at, pages);
+  s.high = carve<int>(at, pages);
+  s.bytes = (size_t)(at - static_cast<char*>(base));
+  return s;
+}
+
+// ---- sums over a block and over the cluster ------------------------------------
+struct Shared {
+  long long warp[kWarps];
+  long long inbox[2][kMaxParts];
+};
+// The sum of v over the block's threads before this one; total: over all of them.
+__device__ __forceinline__ long long block_scan(Shared& sh, long long v, long long& total) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  long long upto = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long w = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += w;
+  }
+  if (lane == 31) sh.warp[warp] = upto;
+  __syncthreads();
+  long long s = lane < kWarps ? sh.warp[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long w = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += w;
+  }
+  total = __shfl_sync(0xffffffffu, s, 31);
+  const long long before = warp > 0 ? __shfl_sync(0xffffffffu, s, warp - 1) : 0;
+  __syncthreads();
+  return before + upto - v;
+}
+// Sends the block's sums a and b to all blocks; they are there after the barrier.
+__device__ __forceinline__ void exchange(Shared& sh, int part, int parts, long long a, long long b) {
+  if ((int)threadIdx.x < parts) {
+    ptx::st_cluster_u64(ptx::mapa_shared(ptx::smem_addr(&sh.inbox[0][part]), threadIdx.x), (uint64_t)a);
+    ptx::st_cluster_u64(ptx::mapa_shared(ptx::smem_addr(&sh.inbox[1][part]), threadIdx.x), (uint64_t)b);
+  }
+  __syncwarp();
+  ptx::cluster_sync();
+}
+__device__ __forceinline__ long long sum_before(const Shared& sh, int which, int part) {
+  long long s = 0;
+  for (int i = 0; i < part; ++i) s += sh.inbox[which][i];
+  return s;
+}
+
+// Four counts from page i on (i a multiple of 4); 1 past the end: not free.
+__device__ __forceinline__ int4 counts_at(const int32_t* refs, int i, int n) {
+  if (i + 4 <= n) return __ldcg(reinterpret_cast<const int4*>(refs + i));
+  int4 r = make_int4(1, 1, 1, 1);
+  if (i < n) r.x = __ldcg(refs + i);
+  if (i + 1 < n) r.y = __ldcg(refs + i + 1);
+  if (i + 2 < n) r.z = __ldcg(refs + i + 2);
+  return r;
+}
+__device__ __forceinline__ int get(const int4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// A sequence as the update's lists give it, clamped to the arrays.
+struct Wish {
+  int parent, len, kept, need;
+  bool ok;
+};
+__device__ __forceinline__ Wish wish_of(const PagesArgs& a, int b) {
+  const int most = a.c.max_pages * a.c.page_size;
+  Wish w;
+  const int p = a.parent ? a.parent[b] : b, len = a.len[b], kept = a.kept[b], need = a.need[b];
+  w.parent = p >= 0 && p < a.c.n_seqs ? p : -1;
+  w.len = clamp_int(len, 0, most);
+  const int has = w.parent < 0 ? 0 : clamp_int(a.len[w.parent], 0, most);
+  w.kept = clamp_int(kept, 0, has);
+  w.need = clamp_int(need, w.kept, most);
+  w.ok = p >= -1 && p < a.c.n_seqs && w.len == len && w.kept == kept && w.need == need;
+  return w;
+}
+__device__ __forceinline__ int pages_of(const PagesArgs& a, int tokens) {
+  return (tokens + a.c.page_size - 1) / a.c.page_size;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    pages_update_kernel(const __grid_constant__ PagesArgs a, const Scratch ws, int parts) {
+  __shared__ Shared sh;
+  const moe_attn_config& c = a.c;
+  const int part = blockIdx.x, lane = threadIdx.x % 32;
+  const int thread = part * kThreads + threadIdx.x, threads = parts * kThreads;
+  const int warp = thread / 32, warps = threads / 32;
+  auto valid = [&](int page) { return page >= 0 && page < c.n_pages; };
+  pdl_wait();
+  pdl_trigger();
+
+  // Counts as they are.
+  if (thread == 0) {
+    *a.status = MOE_OK;
+    ws.head->n_copies = 0;
+  }
+  if (a.refs_out != a.refs) {
+    const int vecs = c.n_pages / 4;
+#pragma unroll 4
+    for (int i = thread; i < vecs; i += threads)
+      reinterpret_cast<int4*>(a.refs_out)[i] = reinterpret_cast<const int4*>(a.refs)[i];
+    for (int i = 4 * vecs + thread; i < c.n_pages; i += threads) a.refs_out[i] = a.refs[i];
+  }
+  ptx::cluster_sync();
+
+  // Pages given up and gained.
+  bool bad = false;
+  for (int b = warp; b < c.n_seqs; b += warps) {
+    const Wish w = wish_of(a, b);
+    bad |= !w.ok;
+    const int kept = pages_of(a, w.kept);
+    const int32_t* old = a.table + (int64_t)b * c.max_pages;
+    const int32_t* from = a.table + (int64_t)max(w.parent, 0) * c.max_pages;
+    int32_t* to = a.table_out + (int64_t)b * c.max_pages;
+    const bool same = w.parent == b;
+    for (int i = lane; i < kept; i += 32) {
+      const int page = from[i];
+      if (!valid(page))
+        bad = true;
+      else if (!same)
+        atomicAdd(a.refs_out + page, 1);
+      if (to != from) to[i] = page;
+    }
+    const int held = pages_of(a, w.len);
+    for (int i = (same ? kept : 0) + lane; i < held; i += 32) {
+      const int page = old[i];
+      if (valid(page))
+        atomicSub(a.refs_out + page, 1);
+      else
+        bad = true;
+    }
+  }
+  ptx::cluster_sync();
+
+  // Pages that each sequence of this block's share wants, and free ones of its share
+  // of the pool.
+  const int rows = (c.n_seqs + parts - 1) / parts, row0 = min(part * rows, c.n_seqs);
+  const int row1 = min(row0 + rows, c.n_seqs);
+  long long wanted = 0;
+  for (int b0 = row0; b0 < row1; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    int want = 0;
+    bool copied = false;
+    if (b < row1) {
+      const Wish w = wish_of(a, b);
+      const int kept = pages_of(a, w.kept);
+      if (w.need > w.kept && w.kept % c.page_size != 0) {
+        const int page = a.table[(int64_t)w.parent * c.max_pages + kept - 1];
+        copied = valid(page) && __ldcg(a.refs_out + page) > 1;
+      }
+      want = pages_of(a, w.need) - kept + copied;
+    }
+    long long total;
+    const long long before = block_scan(sh, want, total);
+    if (b < row1) {
+      ws.before[b] = wanted + before;
+      ws.want[b] = 2 * want + copied;
+    }
+    wanted += total;
+  }
+  const int share = ((c.n_pages + parts - 1) / parts + 3) / 4 * 4;
+  const int page0 = (int)min((long long)part * share, (long long)c.n_pages);
+  const int page1 = min(page0 + share, c.n_pages);
+  int count = 0;
+  for (int i = page0 + 4 * (int)threadIdx.x; i < page1; i += 4 * kThreads) {
+    const int4 n = counts_at(a.refs_out, i, page1);
+    count += (n.x == 0) + (n.y == 0) + (n.z == 0) + (n.w == 0);
+    bad |= n.x < 0 || n.y < 0 || n.z < 0 || n.w < 0;
+  }
+  long long free_here;
+  block_scan(sh, count, free_here);
+  exchange(sh, part, parts, wanted, free_here);
+  const long long free_all = sum_before(sh, 1, parts);
+  const long long listed = min(sum_before(sh, 0, parts), free_all);
+
+  // The list of free pages, as far as it will be used.
+  long long rank = sum_before(sh, 1, part);
+  for (int i0 = page0; i0 < page1 && rank < listed; i0 += 4 * kThreads) {
+    const int i = i0 + 4 * (int)threadIdx.x;
+    const int4 n = i < page1 ? counts_at(a.refs_out, i, page1) : make_int4(1, 1, 1, 1);
+    long long total;
+    long long at = rank + block_scan(sh, (n.x == 0) + (n.y == 0) + (n.z == 0) + (n.w == 0), total);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (get(n, k) == 0) {
+        if (at < listed) ws.free[at] = i + k;
+        ++at;
+      }
+    rank += total;
+  }
+  ptx::cluster_sync();
+
+  // Who gets which.
+  for (int b = warp; b < c.n_seqs; b += warps) {
+    const Wish w = wish_of(a, b);
+    const int info = __ldcg(ws.want + b), want = info / 2, copied = info & 1;
+    const long long at = sum_before(sh, 0, b / rows) + __ldcg(ws.before + b);
+    const bool served = at + want <= free_all;
+    __syncwarp();  // granted may be kept or need
+    if (lane == 0) a.granted[b] = served ? w.need : w.kept;
+    if (!served) continue;
+    const int first = pages_of(a, w.kept) - copied;
+    int32_t* to = a.table_out + (int64_t)b * c.max_pages + first;
+    if (copied && lane == 0) {
+      const int src = a.table[(int64_t)w.parent * c.max_pages + first];
+      atomicSub(a.refs_out + src, 1);
+      ws.copies[atomicAdd(&ws.head->n_copies, 1)] = {src, __ldcg(ws.free + at), w.kept % c.page_size, 0};
+    }
+    __syncwarp();  // in place: the old page has been read
+    for (int i = lane; i < want; i += 32) {
+      const int page = __ldcg(ws.free + at + i);
+      to[i] = page;
+      a.refs_out[page] = 1;
+    }
+  }
+  if (__syncthreads_or(bad) && threadIdx.x == 0) set_status(a.status, status_check());
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    pages_compact_kernel(const __grid_constant__ PagesArgs a, const Scratch ws, int parts) {
+  __shared__ Shared sh;
+  const moe_attn_config& c = a.c;
+  const int part = blockIdx.x, lane = threadIdx.x % 32;
+  const int thread = part * kThreads + threadIdx.x, threads = parts * kThreads;
+  pdl_wait();
+  pdl_trigger();
+  if (thread == 0) {
+    *a.status = MOE_OK;
+    ws.head->n_copies = 0;
+  }
+  ptx::cluster_sync();  // the cluster's blocks have started
+
+  // Pages in use, of this block's share of the pool and of all of it.
+  const int share = ((c.n_pages + parts - 1) / parts + 3) / 4 * 4;
+  const int page0 = (int)min((long long)part * share, (long long)c.n_pages);
+  const int page1 = min(page0 + share, c.n_pages);
+  bool bad = false;
+  int count = 0;
+  for (int i = page0 + threadIdx.x; i < page1; i += kThreads) {
+    const int n = a.refs[i];
+    count += n > 0;
+    bad |= n < 0;
+  }
+  long long live_here;
+  block_scan(sh, count, live_here);
+  exchange(sh, part, parts, live_here, 0);
+  const int live = (int)sum_before(sh, 0, parts);
+
+  // Holes below that number and pages in use above it, by rank.
+  int rank = (int)sum_before(sh, 0, part);  // pages in use before
+  for (int i0 = page0; i0 < page1; i0 += kThreads) {
+    const int i = i0 + threadIdx.x;
+    const int n = i < page1 ? max(a.refs[i], 0) : 0;
+    long long total;
+    const int before = rank + (int)block_scan(sh, n > 0, total);
+    if (i < page1) {
+      if (i == live) ws.head->n_copies = live - before;  // the holes below
+      const bool stays = n > 0 && i < live;
+      if (n > 0 && !stays) {
+        ws.high[before] = i;
+      } else {
+        a.page_map[i] = stays ? i : -1;
+        a.refs_out[i] = n;
+        if (i < live && !stays) ws.free[i - before] = i;
+      }
+    }
+    rank += (int)total;
+  }
+  ptx::cluster_sync();
+  const int moves = __ldcg(&ws.head->n_copies);
+  for (int k = thread; k < moves; k += threads) {
+    const int src = __ldcg(ws.high + live - moves + k), dst = __ldcg(ws.free + k);
+    const int n = a.refs[src];
+    a.page_map[src] = dst;
+    a.refs_out[dst] = n;
+    a.refs_out[src] = 0;
+    ws.copies[k] = {src, dst, c.page_size, 0};
+  }
+  ptx::cluster_sync();
+  for (int b = thread / 32; b < c.n_seqs; b += threads / 32) {
+    const int most = c.max_pages * c.page_size, len = a.len[b];
+    bad |= len < 0 || len > most;
+    const int held = pages_of(a, clamp_int(len, 0, most));
+    const int64_t row = (int64_t)b * c.max_pages;
+    for (int i = lane; i < held; i += 32) {
+      int page = a.table[row + i];
+      const int now = page >= 0 && page < c.n_pages ? __ldcg(a.page_map + page) : -1;
+      bad |= now < 0;
+      a.table_out[row + i] = now < 0 ? page : now;
+    }
+  }
+  if (thread == 0) *a.n_live = live;
+  if (__syncthreads_or(bad) && threadIdx.x == 0) set_status(a.status, status_check());
+}
+
+// ---- copies --------------------------------------------------------------------
+struct CopyArgs {
+  PagesArgs a;
+  const PlanHead* head;  // the list of a plan, or null: a's
+  const PageCopy* copies;
+  int elem;              // bytes of a cached element
+  int row_vecs;          // 16-byte vectors of a token's head
+  int page_vecs;         // of a page
+  int chunks;            // of a page, a warp each
+  int units;             // of a copy: the chunks of keys and of values, and one of scales
+  int scale_tokens;      // scales of a head: a token's each, one (a page's), or none (0)
+  int packed;            // a page's tokens are one run of bytes, in order
+};
+
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ CopyArgs p) {
+  const PagesArgs& a = p.a;
+  const moe_attn_config& c = a.c;
+  const int lane = threadIdx.x % 32;
+  const bool list = p.head == nullptr;
+  pdl_wait();
+  pdl_trigger();
+  int block = blockIdx.x, blocks = gridDim.x;
+  if (list) {
+    if (block == 0) {
+      bool bad = false;
+      for (int i = threadIdx.x; i < a.n_copies; i += kCopyThreads) {
+        const int src = a.src[i], dst = a.dst[i];
+        bad |= src < 0 || src >= a.n_src_pages || dst < 0 || dst >= c.n_pages;
+      }
+      bad = __syncthreads_or(bad);
+      if (threadIdx.x == 0) *a.status = bad ? status_check() : MOE_OK;
+      return;
+    }
+    --block, --blocks;
+  }
+  const long long n = list ? a.n_copies : p.head->n_copies, units = n * p.units;
+  constexpr int kBlockWarps = kCopyThreads / 32;
+  for (long long u = (long long)block * kBlockWarps + threadIdx.x / 32; u < units;
+       u += (long long)blocks * kBlockWarps) {
+    const long long i = u / p.units;
+    const int unit = (int)(u - i * p.units);
+    PageCopy cp;
+    if (list) {
+      cp = {a.src[i], a.dst[i], c.page_size, 0};
+      if (cp.src < 0 || cp.src >= a.n_src_pages || cp.dst < 0 || cp.dst >= c.n_pages) continue;
+    } else {
+      cp = p.copies[i];
+    }
+    if (unit == 2 * p.chunks) {  // scales: of every head, those of the tokens
+      const int words = p.scale_tokens == 1 ? 1 : cp.tokens;
+      const int64_t from = (int64_t)cp.src * c.n_kv_heads * p.scale_tokens;
+      const int64_t to = (int64_t)cp.dst * c.n_kv_heads * p.scale_tokens;
+      for (int h = 0; h < c.n_kv_heads; ++h)
+        for (int w = lane; w < words; w += 32) {
+          const int64_t at = (int64_t)h * p.scale_tokens + w;
+          a.k_scale[to + at] = a.k_from_scale[from + at];
+          a.v_scale[to + at] = a.v_from_scale[from + at];
+        }
+      continue;
+    }
+    const bool key = unit < p.chunks;
+    const char* from = static_cast<const char*>(key ? a.k_from : a.v_from) +
+                       (int64_t)cp.src * c.page_stride * p.elem;
+    char* to = static_cast<char*>(key ? a.k_cache : a.v_cache) + (int64_t)cp.dst * c.page_stride * p.elem;
+    const int v0 = (key ? unit : unit - p.chunks) * 32 * kCopyVecs + lane;
+    const int v1 = cp.tokens * c.n_kv_heads * p.row_vecs;
+    uint4 x[kCopyVecs];
+    int64_t at[kCopyVecs];
+#pragma unroll
+    for (int k = 0; k < kCopyVecs; ++k) {
+      const int v = v0 + 32 * k;
+      at[k] = (int64_t)v * 16;
+      if (!p.packed) {
+        const int row = v / p.row_vecs, token = row / c.n_kv_heads;
+        at[k] = ((int64_t)token * c.token_stride + (int64_t)(row - token * c.n_kv_heads) * c.head_stride) *
+                    p.elem +
+                (int64_t)(v - row * p.row_vecs) * 16;
+      }
+      if (v < v1) x[k] = *reinterpret_cast<const uint4*>(from + at[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kCopyVecs; ++k)
+      if (v0 + 32 * k < v1) *reinterpret_cast<uint4*>(to + at[k]) = x[k];
+  }
+}
+
+cudaError_t launch_copies(const PagesArgs& a, const Scratch* ws, long long most, cudaStream_t s) {
+  const moe_attn_config& c = a.c;
+  CopyArgs p = {};
+  p.a = a;
+  p.head = ws ? ws->head : nullptr;
+  p.copies = ws ? ws->copies : nullptr;
+  p.elem = is_e4m3(c.cache_dtype) ? 1 : c.cache_dtype == MOE_F32 ? 4 : 2;
+  p.row_vecs = c.head_dim * p.elem / 16;
+  p.page_vecs = c.page_size * c.n_kv_heads * p.row_vecs;
+  p.chunks = ceil_div(p.page_vecs, 32 * kCopyVecs);
+  p.scale_tokens = c.cache_dtype == MOE_E4M3 ? c.page_size : c.cache_dtype == MOE_E4M3_PAGE ? 1 : 0;
+  p.units = 2 * p.chunks + (p.scale_tokens > 0);
+  p.packed = c.head_stride == c.head_dim && c.token_stride == (int64_t)c.n_kv_heads * c.head_dim;
+  const long long fill = 8LL * num_sms(), need = (most * p.units + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
+  const unsigned blocks = (unsigned)(need < fill ? need : fill) + (ws ? 0 : 1);
+  if (blocks == 0) return cudaSuccess;
+  ProfScope prof(K_PAGES_COPY, s);
+  return launch_pdl(pages_copy_kernel, dim3(blocks), dim3(kCopyThreads), 0, s, 1, p);
+}
+
+// Blocks of a plan's cluster.
+int plan_parts(const moe_attn_config& c) {
+  const long long work = c.n_pages + (long long)c.n_seqs * c.max_pages;
+  int parts = 1;
+  while (parts < 8 && work > 8192LL * parts) parts *= 2;
+  return parts;
+}
+
+}  // namespace
+
+size_t pages_scratch_bytes(const moe_attn_config& c) {
+  return scratch_of(c, reinterpret_cast<void*>(256)).bytes;
+}
+
+cudaError_t launch_pages_update(const PagesArgs& a, void* scratch, cudaStream_t s) {
+  const Scratch ws = scratch_of(a.c, scratch);
+  const int parts = plan_parts(a.c);
+  cudaError_t e;
+  {
+    ProfScope p(K_PAGES, s);
+    e = launch_pdl(pages_update_kernel, dim3((unsigned)parts), dim3(kThreads), 0, s, parts, a, ws, parts);
+  }
+  return e == cudaSuccess ? launch_copies(a, &ws, a.c.n_seqs, s) : e;
+}
+cudaError_t launch_pages_compact(const PagesArgs& a, void* scratch, cudaStream_t s) {
+  const Scratch ws = scratch_of(a.c, scratch);
+  const int parts = plan_parts(a.c);
+  cudaError_t e;
+  {
+    ProfScope p(K_PAGES, s);
+    e = launch_pdl(pages_compact_kernel, dim3((unsigned)parts), dim3(kThreads), 0, s, parts, a, ws, parts);
+  }
+  return e == cudaSuccess ? launch_copies(a, &ws, a.c.n_pages / 2, s) : e;
+}
+cudaError_t launch_pages_copy(const PagesArgs& a, cudaStream_t s) {
+  return launch_copies(a, nullptr, a.n_copies, s);
+}
+
+}  // namespace moe
