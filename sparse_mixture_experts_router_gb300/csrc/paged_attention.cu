@@ -24,6 +24,7 @@ namespace {
 //   32 of 100 to 6000, D 64                  112 and  90   114 and 115
 //   2 of 20000, D 128                         89 and  52    90 and  98
 constexpr int kTcRows = 48;
+constexpr int kTcRowsE4m3 = 48;
 
 // Rows whose keys were cut into splits: one warp a row.
 constexpr int kJoinWarps = 4;
@@ -80,7 +81,8 @@ Plan plan_of(const moe_attn_config& c) {
   Plan p;
   const bool f32 = c.cache_dtype == MOE_F32, f8 = is_e4m3(c.cache_dtype);
   const long long all_rows = (long long)(c.n_heads / c.n_kv_heads) * c.max_new;
-  p.tc = c.cache_dtype == MOE_BF16 && c.head_dim <= 128 && all_rows > kTcRows;
+  p.tc = c.head_dim <= 128 && (c.cache_dtype == MOE_BF16        ? all_rows > kTcRows
+                               : c.cache_dtype == MOE_E4M3_PAGE && all_rows > kTcRowsE4m3);
   p.unit = p.tc ? 16 : f32 ? 4 : 8;
   const int units = ceil_div(all_rows, p.unit);
   // Rows of a block: 16 (fp32: 12), although each block of them reads the keys
@@ -107,7 +109,7 @@ Plan plan_of(const moe_attn_config& c) {
   // 50 of an fp32 cache 7, 10, 14, 20 took 0.92, 0.93, 0.94, 0.95. Clusters of
   // 16 are placed badly unless all run at once: 84 sequences of 8000 keys take
   // 79 us in 16 parts, 65 in eight.
-  const int per_sm = p.tc  ? 1
+  const int per_sm = p.tc  ? (f8 ? 2 : 1)
                      : f32 ? attn::f32_blocks_per_sm(c.head_dim, p.nt)
                            : attn::blocks_per_sm(c.head_dim);
   const long long slots = (long long)per_sm * attn::kPlanSms;
@@ -138,6 +140,7 @@ cudaError_t launch_bf16(const Params& p, int dim, int nt, unsigned blocks, cudaS
 cudaError_t launch_e4m3(const Params& p, int dim, int nt, unsigned blocks, cudaStream_t s);
 cudaError_t launch_f32(const Params& p, int dim, int nt, unsigned blocks, cudaStream_t s);
 cudaError_t launch_tc(const Params& p, int dim, unsigned blocks, cudaStream_t s);
+cudaError_t launch_tc_e4m3(const Params& p, int dim, unsigned blocks, cudaStream_t s);
 }  // namespace attn
 
 size_t attention_scratch_bytes(const moe_attn_config& c) {
@@ -172,7 +175,8 @@ cudaError_t launch_paged_attention(const AttnArgs& a, void* scratch, cudaStream_
   if (e != cudaSuccess) return e;
   {
     ProfScope p(K_ATTENTION, s);
-    e = plan.tc                     ? attn::launch_tc(prm, c.head_dim, blocks, s)
+    e = plan.tc && is_e4m3(c.cache_dtype) ? attn::launch_tc_e4m3(prm, c.head_dim, blocks, s)
+        : plan.tc                   ? attn::launch_tc(prm, c.head_dim, blocks, s)
         : c.cache_dtype == MOE_F32  ? attn::launch_f32(prm, c.head_dim, plan.nt, blocks, s)
         : is_e4m3(c.cache_dtype)    ? attn::launch_e4m3(prm, c.head_dim, plan.nt, blocks, s)
                                     : attn::launch_bf16(prm, c.head_dim, plan.nt, blocks, s);

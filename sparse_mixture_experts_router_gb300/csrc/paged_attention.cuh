@@ -237,6 +237,32 @@ struct Inbox {
   float4 o[kRows * kDim / 4 + kMaxParts];
 };
 
+// Joins the cluster's blocks in this block's slice of the item's rows x vectors, all of
+// which are in its inbox, and writes it.
+template <int kRows, int kDim, int kThreads, typename Elem>
+__device__ __forceinline__ void join_slices(const Params& p, const Item& it,
+                                            const Inbox<kRows, kDim>* inbox) {
+  const int vecs = p.a.c.head_dim / 4, n = it.rows * vecs;
+  const int slice = div(p.by_parts, n + p.parts - 1);
+  const int i0 = it.part * slice;
+  for (int i = i0 + threadIdx.x; i < min(i0 + slice, n); i += kThreads) {
+    const int r = div(p.by_vecs, i), v = i - r * vecs;
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll 4
+    for (int b = 0; b < p.parts; ++b) top = fmaxf(top, inbox->ml[b][r].x);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int b = 0; b < p.parts; ++b) {
+      const float2 ml = inbox->ml[b][r];
+      const float4 y = inbox->o[b * slice + i - i0];
+      const float f = ptx::ex2(ml.x - top);
+      sum += ml.y * f;
+      x.x += y.x * f, x.y += y.y * f, x.z += y.z * f, x.w += y.w * f;
+    }
+    write_row<Elem>(p, it, r, v, x, top, sum);
+  }
+}
+
 // Joins a block's kWarps partial O (row r at o + w * stride + r * ld floats,
 // all relative to the block's maximum joined[r]; joined[kRows + r] its sum of
 // weights) and then the cluster's blocks, and writes the rows. Each block
@@ -295,23 +321,7 @@ __device__ __forceinline__ void finish(const Params& p, const Item& it, float* o
   }
   __syncwarp();
   ptx::cluster_sync();
-  const int i0 = it.part * slice;
-  for (int i = i0 + threadIdx.x; i < min(i0 + slice, n); i += kThreads) {
-    const int r = div(p.by_vecs, i), v = i - r * vecs;
-    float top = -INFINITY, sum = 0.f;
-#pragma unroll 4
-    for (int b = 0; b < p.parts; ++b) top = fmaxf(top, inbox->ml[b][r].x);
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int b = 0; b < p.parts; ++b) {
-      const float2 ml = inbox->ml[b][r];
-      const float4 y = inbox->o[b * slice + i - i0];
-      const float f = ptx::ex2(ml.x - top);
-      sum += ml.y * f;
-      x.x += y.x * f, x.y += y.y * f, x.z += y.z * f, x.w += y.w * f;
-    }
-    write_row<Elem>(p, it, r, v, x, top, sum);
-  }
+  join_slices<kRows, kDim, kThreads, Elem>(p, it, inbox);
 }
 __device__ __forceinline__ void start_cluster(const Params& p) {
   if (p.parts > 1) ptx::cluster_arrive();
