@@ -753,7 +753,7 @@ MOE_API int moe_verify_drafts(const moe_verify_config* cfg, const void* p, const
  * often it is among those of the history from entry n_prompt[b] on (what was
  * generated) and the new tokens 0 .. j:
  *   x = logit, a NaN as -inf
- *   x = x > 0 ? x / repetition[b] : x * repetition[b]    where s(v)
+ *   x = x > 0 ? x * (1 / repetition[b]) : x * repetition[b]   where s(v)
  *   x = x - frequency[b] c(v), then - presence[b] where c(v) > 0
  *   x = x + bias                                         where b's list has v
  *   x = -inf                                             where the mask's bit is 0

@@ -2,7 +2,7 @@
 // launch.
 //
 // A row of the vocabulary is a cluster of up to 16 blocks, each with a slice of it.
-// A thread has 32 of the slice's logits in registers from the load to the store,
+// A thread has up to 64 of the slice's logits in registers from the load to the store,
 // so a row is read once and written once. What a sequence's history does to a
 // token is looked up by token: each block counts the history's tokens that fall
 // into its slice in shared memory, one word a token, with integer additions, whose
@@ -23,12 +23,10 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kHeld = 32;                  // logits a thread holds
-constexpr int kTile = kThreads * kHeld;    // of a block
 constexpr int kMaxParts = 16;
-constexpr uint32_t kInPrompt = 1u << 31;   // of a token's word; below it: times generated
+constexpr uint32_t kInPrompt = 1u << 31;    // of a token's word; below it: times generated
 
 __device__ __forceinline__ void unpack(uint4 v, float (&x)[4]) {
   x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y);
@@ -99,27 +97,47 @@ __device__ bool bad_lists(const LogitsArgs& a, int t, int n) {
 
 // A block's largest x, the sum of exp of the others relative to it, and the lowest
 // index that has it.
-struct Part {
+struct alignas(16) Part {
   float top, sum;
   int at;
-  int pad;
 };
 
-template <typename In, typename Out>
-__global__ void __launch_bounds__(kThreads, 2) logits_kernel(const LogitsArgs a, int parts, int tiles) {
+// A vector that lies partly in the row: its elements of the row, 0 elsewhere.
+template <typename In>
+__device__ __noinline__ uint4 load_edge(const In* row, int e, int V) {
+  constexpr int kE = 16 / (int)sizeof(In);
+  In x[kE];
+#pragma unroll
+  for (int i = 0; i < kE; ++i) x[i] = e + i >= 0 && e + i < V ? row[e + i] : from_f32<In>(0.f);
+  return *reinterpret_cast<const uint4*>(x);
+}
+template <typename Out>
+__device__ __noinline__ void store_edge(Out* row, int e, int V, float4 y) {
+  if (e >= 0 && e < V) row[e] = from_f32<Out>(y.x);
+  if (e + 1 >= 0 && e + 1 < V) row[e + 1] = from_f32<Out>(y.y);
+  if (e + 2 >= 0 && e + 2 < V) row[e + 2] = from_f32<Out>(y.z);
+  if (e + 3 >= 0 && e + 3 < V) row[e + 3] = from_f32<Out>(y.w);
+}
+
+// kHeld: logits a thread holds. kTiles: a block has several tiles of logits and goes through them twice.
+template <typename In, typename Out, int kHeld, bool kTiles>
+__global__ void __launch_bounds__(kThreads, kHeld > 16 ? 2 : 4)
+    logits_kernel(const LogitsArgs a, int part_bits, int tiles) {
   constexpr int kE = 16 / (int)sizeof(In), kV = kHeld / kE;
+  constexpr int kTileVecs = kThreads * kV;
   extern __shared__ uint4 words4[];  // a word for each token of a tile
   uint32_t* words = reinterpret_cast<uint32_t*>(words4);
-  __shared__ Part inbox[kMaxParts];
-  __shared__ float warp_f[kWarps];
-  __shared__ int warp_i[kWarps];
+  __shared__ Part inbox[kMaxParts], of_warps[kWarps];
+  __shared__ uint32_t masks[kThreads * kHeld / 32 + 2];
   const moe_logits_config& c = a.c;
-  const int part = (int)blockIdx.x % parts, row = (int)blockIdx.x / parts - 1;
+  const int parts = 1 << part_bits, part = (int)blockIdx.x & (parts - 1);
+  const int row = (int)(blockIdx.x >> part_bits) - 1;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, V = c.vocab;
 
   pdl_wait();
   pdl_trigger();
-  ptx::cluster_arrive();  // the cluster's blocks have started before any is written to
+  // The cluster's blocks have started before any is written to; nothing to release yet.
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   if (row < 0) {
     const bool bad = __syncthreads_or(bad_lists(a, part * kThreads + threadIdx.x, parts * kThreads));
     ptx::cluster_wait();
@@ -135,19 +153,51 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const LogitsArgs a,
     return;
   }
 
-  // This block's vectors of the row, on the row's 16-byte grid: vector v is elements
-  // v kE - shift ...
+  // This block's vectors v_begin .. v_end-1 of the row, on the row's 16-byte grid: vector v
+  // is elements v kE - shift ...; only the row's first and last may lie partly outside.
   const In* x_row = static_cast<const In*>(a.logits) + row * c.logits_stride;
   Out* p_row = static_cast<Out*>(a.p) + row * c.p_stride;
   const int shift = (int)((uintptr_t)x_row % 16) / (int)sizeof(In);
   const bool out_grid = (uintptr_t)(p_row + kE - shift) % (kE * sizeof(Out) < 16 ? kE * sizeof(Out) : 16) == 0;
-  const int vectors = (V + shift + kE - 1) / kE;
-  const int v_begin = (int)((long long)vectors * part / parts);
-  const int v_end = (int)((long long)vectors * (part + 1) / parts);
-  constexpr int kTileVecs = kTile / kE;
+  const int vectors = (V + shift + kE - 1) / kE;  // at most 2^22 + 1, times 16
+  const int v_begin = vectors * part >> part_bits, v_end = vectors * (part + 1) >> part_bits;
+  const bool edges = v_begin * kE < shift || v_end * kE - shift > V;
 
-  // Its sequence and what that asks for.
-  const int b = seq_of_row(a.cu_new, c.n_seqs, row, lane);
+  // Of a tile: this thread's vectors are k kThreads + threadIdx.x < n; element e0 + k kStep ..
+  constexpr int kStep = kThreads * kE;
+  const int t0 = (int)threadIdx.x;
+  auto count_of = [&](int v0) { return min(kTileVecs, v_end - v0); };
+  auto first_of = [&](int v0) { return (v0 + t0) * kE - shift; };
+  auto whole = [&](int e) { return !edges || (e >= 0 && e + kE <= V); };
+
+  uint4 raw[kV];
+  auto load = [&](int v0) {
+    const int n = count_of(v0), e0 = first_of(v0);
+    const uint4* from = reinterpret_cast<const uint4*>(x_row + e0);
+#pragma unroll
+    for (int k = 0; k < kV; ++k) {
+      raw[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (k * kThreads + t0 < n && whole(e0 + k * kStep)) raw[k] = from[k * kThreads];
+    }
+    if (edges) {
+#pragma unroll
+      for (int k = 0; k < kV; ++k)
+        if (k * kThreads + t0 < n && !whole(e0 + k * kStep)) raw[k] = load_edge(x_row, e0 + k * kStep, V);
+    }
+  };
+  // The row's sequence is counted from the list where the threads hold it, in one round trip.
+  const bool by_count = c.n_seqs <= 2 * kThreads;
+  const int end0 = by_count && t0 < c.n_seqs ? __ldg(a.cu_new + t0 + 1) : 0x7fffffff;
+  const int end1 = by_count && kThreads + t0 < c.n_seqs ? __ldg(a.cu_new + kThreads + t0 + 1) : 0x7fffffff;
+  const int mask_row = a.mask_row ? __ldg(a.mask_row + row) : -1;
+  load(v_begin);  // in flight meanwhile
+  int b;
+  if (by_count) {
+    b = __syncthreads_count(end0 <= row);
+    if (c.n_seqs > kThreads) b += __syncthreads_count(end1 <= row);
+  } else {
+    b = seq_of_row(a.cu_new, c.n_seqs, row, lane);
+  }
   SeqRange sq = {0, 0, 0, false};
   ListRange hist = {0, 0, false}, bias = {0, 0, false};
   int generated = 0;  // first entry of the history that was generated
@@ -165,30 +215,51 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const LogitsArgs a,
     }
     if (c.n_bias) bias = list_range(a.cu_bias, b, c.n_seqs, c.n_bias);
   }
-  if (a.mask_row) {
-    const int m = a.mask_row[row];
-    if (m >= 0 && m < c.n_masks) mask = a.mask + (int64_t)m * ((V + 31) / 32);
-  }
+  if (mask_row >= 0 && mask_row < c.n_masks) mask = a.mask + (int64_t)mask_row * ((V + 31) / 32);
   const int fed = a.tokens && row >= sq.row0 && row < sq.row0 + sq.n ? row + 1 - sq.row0 : 0;
   const bool counts = (rep != 1.f || pres != 0.f || freq != 0.f) && hist.hi - hist.lo + fed > 0;
   const bool biased = bias.hi > bias.lo;
   const bool greedy = temp == 0.f;
-  const float inv_t = greedy ? 1.f : __fdiv_rn(1.f, temp);
+  const float inv_t = greedy ? 1.f : __fdiv_rn(1.f, temp), inv_rep = __fdiv_rn(1.f, rep);
+
+  // The first entries of the history, in flight with the logits.
+  constexpr int kAhead = 8;
+  int ahead[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    ahead[i] = -1;
+    if (counts && hist.lo + i * kThreads + t0 < hist.hi) ahead[i] = __ldg(a.history + hist.lo + i * kThreads + t0);
+  }
+
+  // The mask's words of a tile, from that of its first element on (one before it, unused,
+  // where the row starts inside its first vector).
+  constexpr int kTile = kTileVecs * kE, kMaskAhead = (kTile / 32 + 2 + kThreads - 1) / kThreads;
+  uint32_t mask_ahead[kMaskAhead];
+  auto load_mask = [&](int v0) {
+    const int first = (v0 * kE - shift) >> 5, last = min((v0 + max(0, count_of(v0))) * kE - shift, V) - 1 >> 5;
+#pragma unroll
+    for (int i = 0; i < kMaskAhead; ++i) {
+      const int w = first + i * kThreads + t0;
+      mask_ahead[i] = 0;
+      if (mask && w >= 0 && w <= last) mask_ahead[i] = __ldg(mask + w);
+    }
+  };
+  load_mask(v_begin);
 
   float x[kV][kE];
-  // The tile's logits as the softmax takes them; -inf outside the row.
+  // The tile's logits (loaded before) as the softmax takes them; -inf outside the row.
   auto take = [&](int v0) {
-    const int v1 = max(v0, min(v0 + kTileVecs, v_end)), base = v0 * kE - shift;
-    uint4 raw[kV];
-#pragma unroll
-    for (int k = 0; k < kV; ++k) {
-      const int v = v0 + k * kThreads + threadIdx.x, e = v * kE - shift;
-      if (v < v1 && e >= 0 && e + kE <= V) raw[k] = *reinterpret_cast<const uint4*>(x_row + e);
-    }
-    const int n_words = (v1 - v0) * kE;
-    if (counts || biased) {
+    const int n = count_of(v0), e0 = first_of(v0);
+    const int base = v0 * kE - shift, n_words = max(0, n) * kE;
+    if (counts || biased || mask) {
       __syncthreads();  // the words' last use
-      for (int i = threadIdx.x; i < n_words / 4; i += kThreads) words4[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (counts || biased)
+        for (int i = t0; i < n_words / 4; i += kThreads) words4[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (mask) {
+#pragma unroll
+        for (int i = 0; i < kMaskAhead; ++i)
+          if (i * kThreads + t0 < kTile / 32 + 2) masks[i * kThreads + t0] = mask_ahead[i];
+      }
       __syncthreads();
     }
     if (counts) {
@@ -200,56 +271,49 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const LogitsArgs a,
         else
           atomicAdd(words + at, 1u);
       };
-#pragma unroll 4
-      for (int i = hist.lo + threadIdx.x; i < hist.hi; i += kThreads)
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) count(ahead[i], hist.lo + i * kThreads + t0 < generated);
+#pragma unroll 8
+      for (int i = hist.lo + kAhead * kThreads + t0; i < hist.hi; i += kThreads)
         count(__ldg(a.history + i), i < generated);
-      for (int i = threadIdx.x; i < fed; i += kThreads) count(a.tokens[sq.row0 + i], false);
+      for (int i = t0; i < fed; i += kThreads) count(a.tokens[sq.row0 + i], false);
       __syncthreads();
     }
 #pragma unroll
-    for (int k = 0; k < kV; ++k) {
-      const int at = k * kThreads + threadIdx.x, v = v0 + at, e = v * kE - shift;
-      if (v < v1 && e >= 0 && e + kE <= V) {
-        unpack(raw[k], x[k]);
-      } else {
+    for (int k = 0; k < kV; ++k) unpack(raw[k], x[k]);
+    if (counts) {
 #pragma unroll
-        for (int i = 0; i < kE; ++i)
-          x[k][i] = v < v1 && e + i >= 0 && e + i < V ? to_f32(x_row[e + i]) : -INFINITY;
-      }
-      if (counts && v < v1) {
+      for (int k = 0; k < kV; ++k) {
+        const int at = k * kThreads + t0;
+        if (at >= n) continue;
 #pragma unroll
         for (int i = 0; i < kE; i += 4) {
           const uint4 w4 = words4[(at * kE + i) / 4];
           const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
           if (!(w[0] | w[1] | w[2] | w[3])) continue;
+          if (biased) words4[(at * kE + i) / 4] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            if (!w[y]) continue;
-            float z = x[k][i + y];
-            z = z > 0.f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
-            const uint32_t n = w[y] & ~kInPrompt;
-            if (n) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, (float)n)), pres);
-            x[k][i + y] = z;
+            const float z = x[k][i + y] * (x[k][i + y] > 0.f ? inv_rep : rep);
+            const uint32_t made = w[y] & ~kInPrompt;
+            const float less = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, (float)made)), pres);
+            if (w[y]) x[k][i + y] = made ? less : z;
           }
         }
       }
     }
     if (biased) {
-      if (counts) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < n_words / 4; i += kThreads) words4[i] = make_uint4(0u, 0u, 0u, 0u);
-        __syncthreads();
-      }
-      for (int i = bias.lo + threadIdx.x; i < bias.hi; i += kThreads) {
-        const int token = a.bias_token[i], at = token - base;
+      if (counts) __syncthreads();
+      for (int i = bias.lo + t0; i < bias.hi; i += kThreads) {
+        const int token = __ldg(a.bias_token + i), at = token - base;
         if ((unsigned)at < (unsigned)n_words && (unsigned)token < (unsigned)V)
-          words[at] = __float_as_uint(a.bias[i]);
+          words[at] = __float_as_uint(__ldg(a.bias + i));
       }
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < kV; ++k) {
-        const int at = k * kThreads + threadIdx.x;
-        if (v0 + at >= v1) continue;
+        const int at = k * kThreads + t0;
+        if (at >= n) continue;
 #pragma unroll
         for (int i = 0; i < kE; i += 4) {
           const uint4 w = words4[(at * kE + i) / 4];
@@ -259,171 +323,238 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const LogitsArgs a,
       }
     }
     if (mask) {
+      // kStep is a multiple of 32: a thread's vectors start at the same bit of their words
+      const int bit = e0 & 31;
+      const uint32_t* from = masks + (e0 >> 5) - (base >> 5);
 #pragma unroll
       for (int k = 0; k < kV; ++k) {
-        const int v = v0 + k * kThreads + threadIdx.x, e = v * kE - shift;
-        if (v >= v1) continue;
-        const int first = max(e, 0), last = min(e + kE, V) - 1;  // first <= last
-        const uint32_t lo = __ldg(mask + first / 32), hi = __ldg(mask + last / 32);
-        // bit i: element e + i
-        const uint32_t bits = first / 32 == last / 32
-                                  ? (e >= 0 ? lo >> (e % 32) : lo << -e)
-                                  : __funnelshift_r(lo, hi, (uint32_t)(e % 32));
+        if (k * kThreads + t0 >= n) continue;
+        const uint32_t bits = __funnelshift_r(from[k * (kStep / 32)], from[k * (kStep / 32) + 1], bit);
 #pragma unroll
         for (int i = 0; i < kE; ++i)
           if (!(bits >> i & 1)) x[k][i] = -INFINITY;
       }
     }
 #pragma unroll
+    for (int k = 0; k < kV; ++k) {
+      const bool in = k * kThreads + t0 < n;
+#pragma unroll
+      for (int i = 0; i < kE; ++i) x[k][i] = in ? fmaxf(x[k][i], -INFINITY) : -INFINITY;  // a NaN too
+    }
+    if (edges) {
+#pragma unroll
+      for (int k = 0; k < kV; ++k)
+#pragma unroll
+        for (int i = 0; i < kE; ++i) {
+          const int e = e0 + k * kStep + i;
+          if (e < 0 || e >= V) x[k][i] = -INFINITY;
+        }
+    }
+  };
+  // Writes x times f.
+  auto write = [&](int v0, float f) {
+    const int n = count_of(v0), e0 = first_of(v0);
+#pragma unroll
     for (int k = 0; k < kV; ++k)
 #pragma unroll
-      for (int i = 0; i < kE; ++i)
-        if (x[k][i] != x[k][i]) x[k][i] = -INFINITY;
-  };
-  auto write = [&](int v0, auto value) {
+      for (int i = 0; i < kE; ++i) x[k][i] *= f;
 #pragma unroll
-    for (int k = 0; k < kV; ++k) {
-      const int v = v0 + k * kThreads + threadIdx.x, e = v * kE - shift;
-      if (v >= min(v0 + kTileVecs, v_end)) continue;
-      float y[kE];
+    for (int k = 0; k < kV; ++k)
+      if (k * kThreads + t0 < n && out_grid && whole(e0 + k * kStep)) store(p_row + e0 + k * kStep, x[k]);
+    if (edges || !out_grid) {
 #pragma unroll
-      for (int i = 0; i < kE; ++i) y[i] = value(x[k][i], e + i);
-      if (out_grid && e >= 0 && e + kE <= V) {
-        store(p_row + e, y);
-      } else {
+      for (int k = 0; k < kV; ++k)
+        if (k * kThreads + t0 < n && !(out_grid && whole(e0 + k * kStep))) {
 #pragma unroll
-        for (int i = 0; i < kE; ++i)
-          if (e + i >= 0 && e + i < V) p_row[e + i] = from_f32<Out>(y[i]);
-      }
+          for (int i = 0; i < kE; i += 4)
+            store_edge(p_row, e0 + k * kStep + i, V, make_float4(x[k][i], x[k][i + 1], x[k][i + 2], x[k][i + 3]));
+        }
     }
   };
 
   if (c.out_logits) {
-    for (int t = 0; t < tiles; ++t) {
+    for (int t = 0; t < (kTiles ? tiles : 1); ++t) {
       const int v0 = v_begin + t * kTileVecs;
+      if (t > 0) load(v0), load_mask(v0);
       take(v0);
-      write(v0, [&](float z, int) { return z * inv_t; });
+      write(v0, inv_t);
     }
     ptx::cluster_wait();
     return;
   }
 
-  // exp relative to `top`; equal values (infinities too) give 1
-  auto weight = [&](float z, float top) {
-    return z == top ? 1.f : expf(__fmul_rn(z - top, inv_t));
-  };
-  Part mine = {-INFINITY, 0.f, 0x7fffffff, 0};
-  for (int t = 0; t < tiles; ++t) {
-    const int v0 = v_begin + t * kTileVecs;
-    take(v0);
-    float top = -INFINITY;
+  // exp(z / temperature) relative to `top`; equal values (infinities too) give 1
+  const float scale = fminf(inv_t, 2.0e38f) * 1.4426950408889634f;
+  auto weight = [&](float z, float top) { return z == top ? 1.f : ptx::ex2((z - top) * scale); };
+  // The sum of x's weights relative to top (above -inf), x becoming them.
+  auto weights = [&](float top) {
+    if (top == INFINITY) {
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < kV; ++k)
+#pragma unroll
+        for (int i = 0; i < kE; ++i) sum += x[k][i] = x[k][i] == INFINITY ? 1.f : 0.f;
+      return sum;
+    }
+    const uint64_t minus = ptx::f32x2(-top, -top), by = ptx::f32x2(scale, scale);
+    uint64_t sum[2] = {0, 0};
 #pragma unroll
     for (int k = 0; k < kV; ++k)
 #pragma unroll
-      for (int i = 0; i < kE; ++i) top = fmaxf(top, x[k][i]);
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    __syncthreads();  // the warps' values of the tile before have been read
-    if (lane == 0) warp_f[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, warp_f[w]);
-    if (top == -INFINITY) continue;  // the same for the whole block
-    float sum = 0.f;
-    int at = 0x7fffffff;
-#pragma unroll
-    for (int k = 0; k < kV; ++k)
-#pragma unroll
-      for (int i = 0; i < kE; ++i) {
-        if (greedy) {
-          if (x[k][i] == top)
-            at = min(at, (v0 + k * kThreads + (int)threadIdx.x) * kE - shift + i);
-        } else if (tiles == 1) {
-          x[k][i] = weight(x[k][i], top);
-          sum += x[k][i];
-        } else {
-          sum += weight(x[k][i], top);
-        }
+      for (int i = 0; i < kE; i += 2) {
+        const uint64_t d =
+            ptx::fma_f32x2(ptx::add_f32x2(ptx::f32x2(x[k][i], x[k][i + 1]), minus), by, 0ull);
+        x[k][i] = ptx::ex2(ptx::f32x2_lo(d));
+        x[k][i + 1] = ptx::ex2(ptx::f32x2_hi(d));
+        sum[i / 2 % 2] = ptx::add_f32x2(sum[i / 2 % 2], ptx::f32x2(x[k][i], x[k][i + 1]));
       }
-    sum = warp_sum(sum);
-    if (greedy) at = __reduce_min_sync(0xffffffffu, at);
-    __syncthreads();
-    if (lane == 0) warp_f[warp] = sum, warp_i[warp] = at;
-    __syncthreads();
-    sum = 0.f;
+    sum[0] = ptx::add_f32x2(sum[0], sum[1]);
+    return ptx::f32x2_lo(sum[0]) + ptx::f32x2_hi(sum[0]);
+  };
+  // Two parts of a row as one.
+  auto join = [&](const Part& p, const Part& q) {
+    Part r;
+    r.top = fmaxf(p.top, q.top);
+    r.sum = r.top == -INFINITY ? 0.f : p.sum * weight(p.top, r.top) + q.sum * weight(q.top, r.top);
+    r.at = p.top == q.top ? min(p.at, q.at) : p.top > q.top ? p.at : q.at;
+    return r;
+  };
+  // All lanes' parts as one, in an order that is the same each time.
+  auto join_lanes = [&](Part p) {
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      sum += warp_f[w];
-      at = min(at, warp_i[w]);
+    for (int o = 1; o < 32; o <<= 1) {
+      Part q;
+      q.top = __shfl_xor_sync(0xffffffffu, p.top, o);
+      q.sum = __shfl_xor_sync(0xffffffffu, p.sum, o);
+      q.at = __shfl_xor_sync(0xffffffffu, p.at, o);
+      p = lane & o ? join(q, p) : join(p, q);
     }
-    if (top > mine.top) {
-      mine.sum = mine.top == -INFINITY ? sum : mine.sum * weight(mine.top, top) + sum;
-      mine.top = top;
-      mine.at = at;
-    } else {
-      mine.sum += sum * weight(top, mine.top);
-    }
-  }
-  ptx::cluster_wait();
-  if (threadIdx.x < parts) {
-    const uint32_t to = ptx::mapa_shared(ptx::smem_addr(&inbox[part]), threadIdx.x);
-    ptx::st_cluster_v2(to, mine.top, mine.sum);
-    ptx::st_cluster_v2(to + 8, __int_as_float(mine.at), 0.f);
-  }
-  __syncwarp();
-  ptx::cluster_sync();
-  float top = -INFINITY, sum = 0.f;
-  int at = 0x7fffffff;
-  for (int i = 0; i < parts; ++i) top = fmaxf(top, inbox[i].top);
-  for (int i = 0; i < parts; ++i) {
-    if (inbox[i].top > -INFINITY) sum += inbox[i].sum * weight(inbox[i].top, top);
-    if (inbox[i].top == top) at = min(at, inbox[i].at);
-  }
-  const bool none = top == -INFINITY;
-  const float f = none ? 0.f : __fdiv_rn(1.f, sum);
-  if (tiles == 1 && !greedy) {
-    // x is relative to this block's maximum
-    const float own = mine.top == -INFINITY ? 0.f : f * weight(mine.top, top);
-    write(v_begin, [&](float w, int) { return own == 0.f ? 0.f : w * own; });
-    return;
-  }
-  for (int t = 0; t < tiles; ++t) {
+    return p;
+  };
+  constexpr int kNowhere = 0x7fffffff;
+
+  // A warp's largest, and sum relative to it; x becomes the weights.
+  Part mine = {-INFINITY, 0.f, kNowhere};
+  for (int t = 0; t < (kTiles ? tiles : 1); ++t) {
     const int v0 = v_begin + t * kTileVecs;
-    if (tiles > 1 && !greedy) take(v0);
-    write(v0, [&](float z, int e) {
-      if (greedy) return !none && e == at ? 1.f : 0.f;
-      return none ? 0.f : weight(z, top) * f;
-    });
+    if (t > 0) load(v0), load_mask(v0);
+    take(v0);
+    Part p = {-INFINITY, 0.f, kNowhere};
+#pragma unroll
+    for (int k = 0; k < kV; ++k)
+#pragma unroll
+      for (int i = 0; i < kE; ++i) p.top = fmaxf(p.top, x[k][i]);
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) p.top = fmaxf(p.top, __shfl_xor_sync(0xffffffffu, p.top, o));
+    if (p.top > -INFINITY) {
+      if (greedy) {
+        const int e0 = first_of(v0);
+#pragma unroll
+        for (int k = kV - 1; k >= 0; --k)
+#pragma unroll
+          for (int i = kE - 1; i >= 0; --i)
+            if (x[k][i] == p.top) p.at = e0 + k * kStep + i;  // the lane's lowest
+        p.at = __reduce_min_sync(0xffffffffu, p.at);
+      } else {
+        p.sum = warp_sum(weights(p.top));
+      }
+    }
+    mine = kTiles ? join(mine, p) : p;
+  }
+  // The block's warps, then the cluster's blocks.
+  if (lane == 0) of_warps[warp] = mine;
+  __syncthreads();
+  if (warp == 0) {
+    const Part p = join_lanes(lane < kWarps ? of_warps[lane] : Part{-INFINITY, 0.f, kNowhere});
+    ptx::cluster_wait();
+    if (lane < parts) {
+      const uint32_t to = ptx::mapa_shared(ptx::smem_addr(&inbox[part]), lane);
+      ptx::st_cluster_v2(to, p.top, p.sum);
+      ptx::st_cluster_v2(to + 8, __int_as_float(p.at), 0.f);
+    }
+    __syncwarp();
+  } else {
+    ptx::cluster_wait();
+  }
+  ptx::cluster_sync();
+  const Part all = join_lanes(lane < parts ? inbox[lane] : Part{-INFINITY, 0.f, kNowhere});
+  const bool none = all.top == -INFINITY;
+  const float f = none ? 0.f : __fdiv_rn(1.f, all.sum);
+  for (int t = 0; t < (kTiles ? tiles : 1); ++t) {
+    const int v0 = v_begin + t * kTileVecs;
+    float own = f;
+    if (greedy) {
+      const int e0 = first_of(v0);
+#pragma unroll
+      for (int k = 0; k < kV; ++k)
+#pragma unroll
+        for (int i = 0; i < kE; ++i) x[k][i] = e0 + k * kStep + i == all.at ? 1.f : 0.f;
+      own = 1.f;
+    } else if (none || (!kTiles && mine.top == -INFINITY)) {
+#pragma unroll
+      for (int k = 0; k < kV; ++k)
+#pragma unroll
+        for (int i = 0; i < kE; ++i) x[k][i] = 0.f;
+    } else if (kTiles) {
+      load(v0);
+      load_mask(v0);
+      take(v0);
+      weights(all.top);
+    } else {
+      own = f * weight(mine.top, all.top);  // x is relative to this warp's largest
+    }
+    write(v0, own);
   }
 }
 
-template <typename In, typename Out>
-cudaError_t launch(const LogitsArgs& a, cudaStream_t s) {
+template <typename In, typename Out, int kHeld, bool kTiles>
+cudaError_t launch_one(const LogitsArgs& a, int part_bits, int tiles, int smem, cudaStream_t s) {
   static thread_local int configured = -1;
+  const auto kernel = logits_kernel<In, Out, kHeld, kTiles>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured != dev) {
-    e = cudaFuncSetAttribute(logits_kernel<In, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTile * 4);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(logits_kernel<In, Out>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kThreads * kHeld * 4);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     configured = dev;
   }
-  // Blocks a row: as many as a block's registers need, and more while the GPU has
-  // slots for them (two blocks an SM) and every thread a vector.
-  constexpr int kE = 16 / (int)sizeof(In);
-  const int vectors = a.c.vocab / kE + 2;  // at most, wherever a row starts
-  int parts = 1;
-  while (parts < kMaxParts &&
-         (ceil_div(vectors, parts) > kTile / kE ||
-          ((long long)a.c.n_tokens * 2 * parts <= 2LL * num_sms() && vectors / (2 * parts) >= kThreads)))
-    parts *= 2;
-  const int slice = (int)ceil_div(vectors, parts), tiles = (int)ceil_div(slice, kTile / kE);
-  const int smem = a.c.n_history || a.c.n_bias || a.tokens ? (tiles > 1 ? kTile : slice * kE) * 4 : 0;
   ProfScope p(K_LOGITS, s);
-  return launch_pdl(logits_kernel<In, Out>, dim3((unsigned)(a.c.n_tokens + 1) * (unsigned)parts), dim3(kThreads),
-                    (size_t)smem, s, parts, a, parts, tiles);
+  return launch_pdl(kernel, dim3((unsigned)(a.c.n_tokens + 1) << part_bits), dim3(kThreads), (size_t)smem, s,
+                    1 << part_bits, a, part_bits, tiles);
+}
+
+template <typename In, typename Out>
+cudaError_t launch(const LogitsArgs& a, cudaStream_t s) {
+  constexpr int kE = 16 / (int)sizeof(In);
+  // of the row that starts latest on its grid
+  const int vectors = ceil_div(a.c.vocab + (a.c.logits_stride % kE ? kE - 1 : 0), kE);
+  // 64 logits a thread (two blocks an SM) for the batch; 16 (four blocks) where those
+  // leave the GPU unfilled and 16 blocks hold a row.
+  constexpr int kMany = 64, kFew = 16;
+  auto tile = [](int held) { return kThreads * (held / kE); };
+  auto blocks = [&](int held) {
+    int bits = 0;
+    while ((1 << bits) < kMaxParts && ceil_div(vectors, 1 << bits) > tile(held)) ++bits;
+    return bits;
+  };
+  const int held = ((long long)a.c.n_tokens << blocks(kMany)) <= 2 * num_sms() &&
+                           vectors <= kMaxParts * tile(kFew)
+                       ? kFew
+                       : kMany;
+  // Blocks a row: as many as its registers need, and more while the GPU has slots for
+  // them and every thread a vector.
+  int bits = blocks(held);
+  while ((1 << bits) < kMaxParts &&
+         ((long long)a.c.n_tokens << bits) * 2 <= (held == kFew ? 4 : 2) * num_sms() &&
+         vectors >> (bits + 1) >= kThreads)
+    ++bits;
+  const int slice = ceil_div(vectors, 1 << bits), tiles = ceil_div(slice, tile(held));
+  const int smem = a.c.n_history || a.c.n_bias || a.tokens ? (tiles > 1 ? tile(held) : slice) * kE * 4 : 0;
+  if (held == kFew) return launch_one<In, Out, kFew, false>(a, bits, tiles, smem, s);
+  if (tiles == 1) return launch_one<In, Out, kMany, false>(a, bits, tiles, smem, s);
+  return launch_one<In, Out, kMany, true>(a, bits, tiles, smem, s);
 }
 
 }  // namespace

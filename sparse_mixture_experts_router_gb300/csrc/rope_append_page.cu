@@ -11,11 +11,12 @@
 // item is a (sequence, page) that the call touches. Sequence b's items start at
 // floor(cu_new[b] / page_size) + 2 b, which leaves each sequence at least as many
 // as n tokens can touch (1 + ceil((n - 1) / page_size)); with one new token a
-// sequence, at b. A warp takes a head of the item's keys, values or queries: its
-// rows (8 for each group of lanes that holds a row) stay in registers between
-// the maximum and the write. The item's sines and cosines are computed once a
-// block, in chunks of that many rows; a page with more new rows than a chunk is
-// read twice. One block more checks the lists and writes the status.
+// sequence, at b. A block takes an item, or some heads of it: a warp a row (several
+// a row where there are few), so that a row's sines are computed once for all its
+// heads, a group of lanes a head. It goes over the rows twice, for the maxima (and the
+// queries, which are done then) and to write keys and values; a warp with one row
+// and few heads keeps them in registers in between. One block more checks the lists
+// and writes the status.
 //
 // Bound by memory for prompts and by the latency of one chain (sequence, page,
 // old scale, rows) for a few tokens.
@@ -28,11 +29,7 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kRowsLane = 8;  // rows a group of lanes holds
-// Chunk rows x pairs: 8 (32 / lanes) rows of at most 4 lanes pairs.
-constexpr int kTurns = kRowsLane * 32 * 4;
+constexpr int kUnits = 4;  // heads a group of lanes has in flight
 constexpr int kMinExp = -110, kMaxExp = 119;
 
 // 2^e for elements up to amax (finite, >= 0): 448 = 1.75 x 2^8.
@@ -90,18 +87,25 @@ __device__ __forceinline__ bool page_item(const AttnArgs& a, int per_seq, int in
   return true;
 }
 
-// kBits: a row is held by 1 << kBits lanes.
-template <int kBits>
-__global__ void __launch_bounds__(kThreads, 2)
-    rope_append_page_kernel(const AttnArgs a, const __grid_constant__ RopeTable rope, int per_seq) {
-  constexpr int kLanes = 1 << kBits, kGroups = 32 / kLanes, kChunk = kRowsLane * kGroups;
-  __shared__ float2 turns[kTurns + kTurns / 8];  // (cos, sin) of a chunk's pairs, padded
-  __shared__ float scales[2 * kAttnMaxHeads];    // of keys and values: maximum, then scale
+// kWarps warps a block.
+template <int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, 24 / kWarps)
+    rope_append_page_kernel(const AttnArgs a, const __grid_constant__ RopeTable rope, int lane_bits,
+                            int per_seq) {
+  using T = __nv_bfloat16;
+  constexpr int kThreads = 32 * kWarps;
+  __shared__ float2 turns[kWarps][kMaxPairs + kMaxPairs / 8];  // (cos, sin) of a row's pairs, padded
+  // Of this block's keys' and values' heads: the maximum, then 1 / scale; old scale / new.
+  __shared__ uint32_t largest[2 * kAttnMaxHeads];
+  __shared__ float ratios[2 * kAttnMaxHeads];
   const moe_attn_config& c = a.c;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int group = lane / kLanes, gl = lane % kLanes, e0 = gl * 8;
+  const int lanes = 1 << lane_bits, groups = 32 >> lane_bits;
+  const int group = lane >> lane_bits, gl = lane & (lanes - 1), e0 = gl * 8;
+  const unsigned group_mask = (lanes == 32 ? 0xffffffffu : (1u << lanes) - 1) << (group * lanes);
   const int pairs = c.rot_dim / 2, nk = c.n_kv_heads;
   const bool held = e0 < c.head_dim, turns_here = e0 < c.rot_dim;
+  float2* turn = turns[warp];
 
   pdl_wait();
   pdl_trigger();
@@ -112,165 +116,191 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   PageItem it;
   if (!page_item(a, per_seq, (int)blockIdx.x - 1, lane, it)) return;
-  const int units = 2 * nk + (a.q ? c.n_heads : 0), u0 = (int)blockIdx.y * kWarps + warp;
-  const int u_step = (int)gridDim.y * kWarps;
-  const bool whole = it.rows <= kChunk;
 
-  // Row `row` of unit u: keys, values, queries.
-  using T = __nv_bfloat16;
-  auto source = [&](int u, int row) {
+  // This block's heads j: unit j * G + y of the keys', values' and queries'.
+  const int y = blockIdx.y, G = gridDim.y;
+  const int heads = (2 * nk + (a.q ? c.n_heads : 0) - y + G - 1) / G, cached = (2 * nk - y + G - 1) / G;
+  // Its rows: per_row warps a row.
+  int per_row = kWarps;
+  while (per_row > 1 && it.rows >= 2 * kWarps / per_row) per_row /= 2;
+  const int row_step = kWarps / per_row, first_row = warp / per_row;
+  const int j0 = warp % per_row * groups + group, j_step = per_row * groups, batch = kUnits * j_step;
+  const bool keep = it.rows <= row_step && cached <= batch;
+
+  for (int j = threadIdx.x; j < cached; j += kThreads) largest[j] = 0;
+  // A row's keys, values and queries, at this lane's elements.
+  struct Row {
+    const T *k, *v, *q;
+  };
+  auto row_of = [&](int row) {
     const int64_t t = it.row0 + row;
-    const T* p = u < nk       ? static_cast<const T*>(a.k) + t * c.k_stride + u * c.head_dim
-                 : u < 2 * nk ? static_cast<const T*>(a.v) + t * c.v_stride + (u - nk) * c.head_dim
-                              : static_cast<const T*>(a.q) + t * c.q_stride + (u - 2 * nk) * c.head_dim;
-    return p + e0;
+    return Row{static_cast<const T*>(a.k) + t * c.k_stride + e0,
+               static_cast<const T*>(a.v) + t * c.v_stride - nk * c.head_dim + e0,
+               static_cast<const T*>(a.q) + t * c.q_stride - 2 * nk * c.head_dim + e0};
+  };
+  auto source = [&](const Row& r, int u) {
+    return (u < nk ? r.k : u < 2 * nk ? r.v : r.q) + u * c.head_dim;
+  };
+  Eight<T> x[kUnits];
+  auto load = [&](const Row& r, int j, int n) {
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      x[k] = {};
+      if (j + k * j_step < n && held) x[k] = load8(source(r, (j + k * j_step) * G + y));
+    }
+  };
+  float own[8], other[8];  // factors of this lane's elements and of their partners
+  auto turn_of = [&](int row) {
+    for (int i = lane; i < pairs; i += 32) {
+      const int axis = (i >= c.rot_sections[0]) + (i >= c.rot_sections[0] + c.rot_sections[1]);
+      const int64_t pos = a.positions ? a.positions[(int64_t)axis * c.n_tokens + it.row0 + row] : it.at0 + row;
+      const int64_t angle = (int64_t)((uint64_t)pos * rope.turns[i]);
+      float2 cs;
+      sincospif((float)(int32_t)(angle >> 32) * 0x1p-31f, &cs.y, &cs.x);
+      turn[i + i / 8] = cs;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = e0 + i;
+      own[i] = 1.f, other[i] = -0.f;  // x 1 + 0 (-0) is x for a zero of either sign
+      if (e < c.rot_dim) {
+        const bool first = c.rot_interleaved ? i % 2 == 0 : e < pairs;
+        const int n = c.rot_interleaved ? e / 2 : first ? e : e - pairs;
+        const float2 cs = turn[n + n / 8];
+        own[i] = cs.x;
+        other[i] = first ? -cs.y : cs.y;
+      }
+    }
+    __syncwarp();
   };
   const bool vec_partner = !c.rot_interleaved && pairs % 8 == 0;
   const int from = lane + (e0 < pairs ? pairs : -pairs) / 8;
-  // The chunk's rows of unit u as they are, and turned (0 where there is none).
-  auto read = [&](int u, int r0, int rows, float (&o)[kRowsLane][8]) {
-    Eight<T> x[kRowsLane];
+  // Unit u of a row (x as it was read), turned if it turns; all lanes of a warp alike where
+  // `some` is false: nothing does.
+  auto turned = [&](const Row& r, int u, bool some, const Eight<T>& x, float (&o)[8]) {
+    widen(x, o);
+    if (!some) return;
+    float z[8];
+    if (vec_partner) {
+      Eight<T> w;
 #pragma unroll
-    for (int i = 0; i < kRowsLane; ++i) {
-      x[i] = {};
-      const int r = i * kGroups + group;
-      if (r < rows && held) x[i] = load8(source(u, r0 + r));
-    }
-    const bool turned = u < nk || u >= 2 * nk;
-#pragma unroll
-    for (int i = 0; i < kRowsLane; ++i) {
-      widen(x[i], o[i]);
-      if (!turned || pairs == 0 || i * kGroups >= rows) continue;
-      const int r = i * kGroups + group;
-      float y[8];
-      if (vec_partner) {
-        Eight<T> z;
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-          reinterpret_cast<uint32_t*>(&z)[w] =
-              __shfl_sync(0xffffffffu, reinterpret_cast<const uint32_t*>(&x[i])[w], from);
-        widen(z, y);
-      } else if (c.rot_interleaved) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = o[i][e ^ 1];
-      } else {
-        const T* p = source(u, r0 + min(r, rows - 1));
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          y[e] = e0 + e < c.rot_dim ? to_f32(p[e0 + e < pairs ? e + pairs : e - pairs]) : 0.f;
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t p = __shfl_sync(0xffffffffu, reinterpret_cast<const uint32_t*>(&x)[i], from);
+        reinterpret_cast<uint32_t*>(&w)[i] = turns_here ? p : 0u;
       }
-      if (r < rows && turns_here) {
+      widen(w, z);
+    } else {
+      const T* p = source(r, u);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int at = e0 + e;
-          if (at >= c.rot_dim) break;
-          const bool first = c.rot_interleaved ? e % 2 == 0 : at < pairs;
-          const int n = r * pairs + (c.rot_interleaved ? at / 2 : first ? at : at - pairs);
-          const float2 cs = turns[n + n / 8];
-          const float own = cs.x, other = first ? -cs.y : cs.y;
-          o[i][e] = o[i][e] * own + y[e] * other;
-        }
+      for (int i = 0; i < 8; ++i) {
+        const int e = e0 + i;
+        z[i] = e >= c.rot_dim      ? 0.f
+               : c.rot_interleaved ? to_f32(x.v[i ^ 1])
+                                   : to_f32(p[e < pairs ? i + pairs : i - pairs]);
       }
     }
-  };
-  auto largest = [&](const float (&o)[kRowsLane][8]) {
-    float m = 0.f;
+    if (u < nk || u >= 2 * nk) {
 #pragma unroll
-    for (int i = 0; i < kRowsLane; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = fmaxf(m, finite(o[i][e]) ? fabsf(o[i][e]) : 0.f);
-#pragma unroll
-    for (int x = 16; x > 0; x /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    return m;
+      for (int i = 0; i < 8; ++i) o[i] = o[i] * own[i] + z[i] * other[i];
+    }
   };
 
-  for (int pass = whole ? 1 : 0; pass < 2; ++pass) {
-    for (int r0 = 0; r0 < it.rows; r0 += kChunk) {
-      const int rows = min(kChunk, it.rows - r0);
-      __syncthreads();  // the chunk before has been used
-      for (int i = threadIdx.x; i < rows * pairs; i += kThreads) {
-        const int r = i / pairs, n = i - r * pairs;
-        const int axis = (n >= c.rot_sections[0]) + (n >= c.rot_sections[0] + c.rot_sections[1]);
-        const int64_t pos = a.positions
-                                ? a.positions[(int64_t)axis * c.n_tokens + it.row0 + r0 + r]
-                                : it.at0 + r0 + r;
-        const int64_t angle = (int64_t)((uint64_t)pos * rope.turns[n]);
-        float2 cs;
-        sincospif((float)(int32_t)(angle >> 32) * 0x1p-31f, &cs.y, &cs.x);
-        turns[i + i / 8] = cs;
-      }
-      __syncthreads();
-      for (int u = u0; u < units; u += u_step) {
-        const bool cached = u < 2 * nk;
-        if (pass == 0 && !cached) continue;
-        float o[kRowsLane][8];
-        read(u, r0, rows, o);
+  __syncthreads();
+  for (int row = first_row; row < it.rows; row += row_step) {
+    const Row r = row_of(row);
+    T* out = static_cast<T*>(a.out) + (int64_t)(it.row0 + row) * c.n_heads * c.head_dim - 2 * nk * c.head_dim + e0;
+    // backwards: the keys and values, which may be kept, last
+    const int last = j0 + max(heads - 1 - (j0 - group), 0) / batch * batch;
+    load(r, last, heads);  // in flight while the row's sines are computed
+    turn_of(row);
+    for (int jb = last; jb >= j0; jb -= batch) {
+      if (jb != last) load(r, jb, heads);
+#pragma unroll
+      for (int k = 0; k < kUnits; ++k) {
+        const int j = jb + k * j_step, u = j * G + y;
+        if (j - group >= heads) break;  // the same for the whole warp
+        float o[8];
+        turned(r, min(u, (heads - 1) * G + y), pairs > 0 && __any_sync(0xffffffffu, u < nk || u >= 2 * nk), x[k], o);
         __syncwarp();  // in place: the partners are read before they are overwritten
-        if (!cached) {
+        if (j < cached) {
+          uint32_t m = 0;
 #pragma unroll
-          for (int i = 0; i < kRowsLane; ++i) {
-            const int r = i * kGroups + group;
-            if (r < rows && held)
-              store8(static_cast<T*>(a.out) + ((int64_t)(it.row0 + r0 + r) * c.n_heads + u - 2 * nk) *
-                                                  c.head_dim + e0,
-                     o[i]);
+          for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(o[i]) & 0x7fffffffu);
+          if (m >= 0x7f800000u) {  // some are not finite
+            m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              m = max(m, finite(o[i]) ? __float_as_uint(o[i]) & 0x7fffffffu : 0u);
           }
-          continue;
+          m = __reduce_max_sync(group_mask, m);
+          if (gl == 0) atomicMax(largest + j, m);
+        } else if (j < heads && held) {
+          store8(out + u * c.head_dim, o);
         }
-        if (pass == 0) {
-          const float m = largest(o);
-          if (lane == 0) scales[u] = r0 == 0 ? m : fmaxf(scales[u], m);
-          __syncwarp();
-          continue;
-        }
-        if (it.page < 0) continue;
-        const int h = u < nk ? u : u - nk;
-        uint8_t* cache = static_cast<uint8_t*>(u < nk ? a.k_cache : a.v_cache) +
-                         (int64_t)it.page * c.page_stride + (int64_t)h * c.head_stride;
-        float scale;
-        if (r0 == 0) {
-          scale = page_scale(whole ? largest(o) : scales[u]);
-          float* stored = (u < nk ? a.k_scale : a.v_scale) + (int64_t)it.page * nk + h;
-          if (it.place0 > 0) {
-            const float was = *stored;
-            if (was >= scale) {
-              scale = was;
-            } else if (was < scale) {  // neither for a NaN
-              const float ratio = __fdiv_rn(was, scale);
-              const int vecs = c.head_dim / 16;
-              for (int i = lane; i < it.place0 * vecs; i += 32) {
-                uint4* p = reinterpret_cast<uint4*>(cache + (int64_t)(i / vecs) * c.token_stride) +
-                           i % vecs;
-                uint4 w = *p;
-                w.x = rescale4(w.x, ratio), w.y = rescale4(w.y, ratio);
-                w.z = rescale4(w.z, ratio), w.w = rescale4(w.w, ratio);
-                *p = w;
-              }
-            }
-          }
-          __syncwarp();
-          if (lane == 0) {
-            *stored = scale;
-            scales[u] = scale;
-          }
-          __syncwarp();
-        } else {
-          scale = scales[u];
-        }
-        const float inv = __fdiv_rn(1.f, scale);
+      }
+    }
+  }
+  __syncthreads();
+  if (it.page < 0) return;
+  for (int j = threadIdx.x; j < cached; j += kThreads) {
+    const int u = j * G + y, h = u < nk ? u : u - nk;
+    float* stored = (u < nk ? a.k_scale : a.v_scale) + (int64_t)it.page * nk + h;
+    float scale = page_scale(__uint_as_float(largest[j])), ratio = 1.f;
+    if (it.place0 > 0) {
+      const float was = *stored;
+      if (was >= scale)
+        scale = was;
+      else if (was < scale)  // neither for a NaN
+        ratio = __fdiv_rn(was, scale);
+    }
+    *stored = scale;
+    largest[j] = __float_as_uint(__fdiv_rn(1.f, scale));
+    ratios[j] = ratio;
+  }
+  __syncthreads();
+  for (int j = warp; j < cached; j += kWarps) {
+    const float ratio = ratios[j];
+    if (ratio == 1.f) continue;
+    // the page's older codes under the raised scale
+    const int u = j * G + y, vecs = c.head_dim / 16;
+    uint8_t* cache = static_cast<uint8_t*>(u < nk ? a.k_cache : a.v_cache) +
+                     (int64_t)it.page * c.page_stride + (int64_t)(u < nk ? u : u - nk) * c.head_stride;
+    for (int i = lane; i < it.place0 * vecs; i += 32) {
+      uint4* p = reinterpret_cast<uint4*>(cache + (int64_t)(i / vecs) * c.token_stride) + i % vecs;
+      uint4 w = *p;
+      w.x = rescale4(w.x, ratio), w.y = rescale4(w.y, ratio);
+      w.z = rescale4(w.z, ratio), w.w = rescale4(w.w, ratio);
+      *p = w;
+    }
+  }
+  for (int row = first_row; row < it.rows; row += row_step) {
+    const Row r = row_of(row);
+    const int64_t at = (int64_t)it.page * c.page_stride + (int64_t)(it.place0 + row) * c.token_stride + e0;
+    uint8_t* k_out = static_cast<uint8_t*>(a.k_cache) + at;
+    uint8_t* v_out = static_cast<uint8_t*>(a.v_cache) + at - nk * c.head_stride;
+    if (!keep) {
+      load(r, j0, cached);
+      turn_of(row);
+    }
+    for (int jb = j0; jb - group < cached; jb += batch) {
+      if (jb != j0) load(r, jb, cached);
 #pragma unroll
-        for (int i = 0; i < kRowsLane; ++i) {
-          const int r = i * kGroups + group;
-          if (r >= rows || !held) continue;
-          uint32_t w[4];
+      for (int k = 0; k < kUnits; ++k) {
+        const int j = jb + k * j_step, u = j * G + y;
+        if (j - group >= cached) break;
+        float o[8];
+        turned(r, min(u, (cached - 1) * G + y), pairs > 0 && __any_sync(0xffffffffu, u < nk), x[k], o);
+        if (j >= cached || !held) continue;
+        const float inv = __uint_as_float(largest[j]);
+        uint32_t w[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)  // E4M3 has no infinity
-            o[i][e] = finite(o[i][e]) ? __fmul_rn(o[i][e], inv) : __uint_as_float(0x7fc00000u);
+        for (int i = 0; i < 8; ++i)  // E4M3 has no infinity: inf 0 makes it a NaN
+          o[i] = fmaf(o[i], 0.f, __fmul_rn(o[i], inv));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = e4m3x2(o[i][2 * e], o[i][2 * e + 1]);
-          *reinterpret_cast<uint2*>(cache + (int64_t)(it.place0 + r0 + r) * c.token_stride + e0) =
-              make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-        }
+        for (int i = 0; i < 4; ++i) w[i] = e4m3x2(o[2 * i], o[2 * i + 1]);
+        *reinterpret_cast<uint2*>((u < nk ? k_out : v_out) + u * c.head_stride) =
+            make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
       }
     }
   }
@@ -283,19 +313,20 @@ cudaError_t launch_rope_append_page(const AttnArgs& a, const RopeTable& rope, in
   const moe_attn_config& c = a.c;
   const int per_seq = c.max_new == 1 ? 1 : 2;
   const long long items = c.n_tokens / c.page_size + (long long)per_seq * c.n_seqs;
-  const int units = 2 * c.n_kv_heads + (a.q ? c.n_heads : 0);
-  // A block for every 8 heads where that leaves the GPU's slots unfilled.
-  int groups = 1;
-  while (groups < ceil_div(units, kWarps) && items * (groups + 1) <= 2LL * num_sms()) ++groups;
-  const dim3 grid((unsigned)items + 1, (unsigned)groups), block(kThreads);
-  switch (lane_bits) {
-    case 0:
-    case 1: return launch_pdl(rope_append_page_kernel<1>, grid, block, 0, s, 1, a, rope, per_seq);
-    case 2: return launch_pdl(rope_append_page_kernel<2>, grid, block, 0, s, 1, a, rope, per_seq);
-    case 3: return launch_pdl(rope_append_page_kernel<3>, grid, block, 0, s, 1, a, rope, per_seq);
-    case 4: return launch_pdl(rope_append_page_kernel<4>, grid, block, 0, s, 1, a, rope, per_seq);
-    default: return launch_pdl(rope_append_page_kernel<5>, grid, block, 0, s, 1, a, rope, per_seq);
-  }
+  // A block takes all heads of an item where a warp has a row, or where the GPU's
+  // slots (24 warps an SM) are filled; else some of them. 16 warps a block where items
+  // are few and have the rows.
+  const int heads = 2 * c.n_kv_heads + (a.q ? c.n_heads : 0);
+  const int rows = c.max_new < c.page_size ? c.max_new : c.page_size;
+  const bool wide = rows >= 16 && items < 3LL * num_sms();
+  const int warps = wide ? 16 : 8;
+  int split = 1;
+  while (split < c.n_kv_heads && rows < warps && 2 * split * warps <= heads * rows &&
+         items * split * warps < 24LL * num_sms())
+    split *= 2;
+  const dim3 grid((unsigned)items + 1, (unsigned)split), block((unsigned)(32 * warps));
+  return wide ? launch_pdl(rope_append_page_kernel<16>, grid, block, 0, s, 1, a, rope, lane_bits, per_seq)
+              : launch_pdl(rope_append_page_kernel<8>, grid, block, 0, s, 1, a, rope, lane_bits, per_seq);
 }
 
 }  // namespace moe

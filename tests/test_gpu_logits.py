@@ -96,7 +96,7 @@ class Rows:
         x[np.isnan(x)] = -np.inf
         if self.allowed is not None and self.mask_row[t] >= 0:
             x[~self.allowed[self.mask_row[t]]] = -np.inf
-        return x, 5 * U * size  # five operations
+        return x, 6 * U * size  # six roundings: 1 / repetition, its product, frequency's, two differences, a sum
 
     def want(self):
         p = np.zeros((self.T, self.V))
