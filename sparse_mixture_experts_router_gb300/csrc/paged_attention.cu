@@ -161,13 +161,13 @@ cudaError_t launch_paged_attention(const AttnArgs& a, void* scratch, cudaStream_
   // One block looks at 4096 pages in about 5 us; 79 sequences of 440 to 940
   // pages took it 86 us, where the attention takes 15.
   prm.check_in_use = (long long)c.n_seqs * c.max_pages > 4096;
-  prm.by_page = attn::fast_div((uint32_t)c.page_size);
-  prm.by_group = attn::fast_div((uint32_t)prm.group);
-  prm.by_parts = attn::fast_div((uint32_t)prm.parts);
-  prm.by_splits = attn::fast_div((uint32_t)prm.splits);
-  prm.by_rows = attn::fast_div((uint32_t)prm.row_blocks);
-  prm.by_heads = attn::fast_div((uint32_t)c.n_kv_heads);
-  prm.by_vecs = attn::fast_div((uint32_t)c.head_dim / 4);
+  prm.by_page = fast_div((uint32_t)c.page_size);
+  prm.by_group = fast_div((uint32_t)prm.group);
+  prm.by_parts = fast_div((uint32_t)prm.parts);
+  prm.by_splits = fast_div((uint32_t)prm.splits);
+  prm.by_rows = fast_div((uint32_t)prm.row_blocks);
+  prm.by_heads = fast_div((uint32_t)c.n_kv_heads);
+  prm.by_vecs = fast_div((uint32_t)c.head_dim / 4);
   prm.split_o = static_cast<float*>(scratch);
   prm.split_ml = reinterpret_cast<float2*>(prm.split_o + split_rows(plan) * c.head_dim);
   const unsigned blocks = (unsigned)((plan.items * plan.splits + 1) * plan.parts);

@@ -29,21 +29,6 @@ constexpr int f32_blocks_per_sm(int dim, int nt) {
 // Keys of a tile of the bf16 and E4M3 kernel.
 constexpr int keys_of(int dim, bool f8) { return f8 || dim <= 64 ? 32 : 16; }
 
-// n / d for 0 <= n < 2^30 and 1 <= d < 2^30 as a multiplication.
-struct FastDiv {
-  uint64_t mul;
-  int shift;
-};
-inline FastDiv fast_div(uint32_t d) {
-  int bits = 0;
-  while ((1u << bits) < d) ++bits;
-  const int shift = 30 + bits;
-  return {((1ull << shift) + d - 1) / d, shift};
-}
-__device__ __forceinline__ int div(const FastDiv& f, int n) {
-  return (int)(((uint64_t)n * f.mul) >> f.shift);
-}
-
 struct Params {
   AttnArgs a;
   int parts, splits;

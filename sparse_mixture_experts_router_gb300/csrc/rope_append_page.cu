@@ -25,11 +25,11 @@
 #include <cuda_fp16.h>
 
 #include "rope_append.cuh"
+#include "serve_ptx.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kUnits = 4;  // heads a group of lanes has in flight
 constexpr int kMinExp = -110, kMaxExp = 119;
 
 // 2^e for elements up to amax (finite, >= 0): 448 = 1.75 x 2^8.
@@ -57,41 +57,50 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float ratio) {
 struct PageItem {
   int row0, rows, at0, place0, page;
 };
-// The item of index i (false: none), found by a whole warp.
-__device__ __forceinline__ bool page_item(const AttnArgs& a, int per_seq, int index, int lane,
-                                          PageItem& it) {
+// The item of index i (false: none), found by a whole block.
+template <int kThreads>
+__device__ __forceinline__ bool page_item(const AttnArgs& a, const FastDiv& by_page, int per_seq,
+                                          int index, int lane, PageItem& it) {
   const moe_attn_config& c = a.c;
-  auto start = [&](int b) {
-    return clamp_int(__ldg(a.cu_new + b), 0, c.n_tokens) / c.page_size + per_seq * b;
-  };
-  int lo = 0, hi = c.n_seqs;  // the first sequence whose items end after index
-  while (lo < hi) {
-    const int step = (hi - lo + 31) / 32, i = lo + (lane + 1) * step - 1;
-    const unsigned after = __ballot_sync(0xffffffffu, i >= hi || start(i + 1) > index);
-    if (!after) return false;  // only where the list does not ascend
-    const int f = __ffs(after) - 1;
-    hi = min(hi, lo + (f + 1) * step - 1);
-    lo += f * step;
+  auto start_of = [&](int cu, int b) { return div(by_page, clamp_int(cu, 0, c.n_tokens)) + per_seq * b; };
+  auto start = [&](int b) { return start_of(__ldg(a.cu_new + b), b); };
+  // the first sequence whose items end after index: counted in one round trip where the
+  // threads hold the list, else found in steps of 32 comparisons
+  int lo = 0;
+  if (c.n_seqs <= kThreads) {
+    const int t = threadIdx.x;
+    lo = __syncthreads_count(t < c.n_seqs && start(t + 1) <= index);
+  } else {
+    int hi = c.n_seqs;
+    while (lo < hi) {
+      const int step = (hi - lo + 31) / 32, i = lo + (lane + 1) * step - 1;
+      const unsigned after = __ballot_sync(0xffffffffu, i >= hi || start(i + 1) > index);
+      if (!after) return false;  // only where the list does not ascend
+      const int f = __ffs(after) - 1;
+      hi = min(hi, lo + (f + 1) * step - 1);
+      lo += f * step;
+    }
   }
   if (lo >= c.n_seqs) return false;
   const SeqRange r = seq_range(a, lo);
-  const int first = max(r.len - r.n, 0);  // below 0: no slot, recorded by the check
-  const int page = first / c.page_size + index - start(lo);
-  if (!r.ok || index < start(lo) || page > (r.len - 1) / c.page_size || r.len - r.n < 0 || r.n == 0)
-    return false;
+  const int first = r.len - r.n;  // below 0: no slot, recorded by the check
+  if (!r.ok || first < 0 || r.n == 0) return false;
+  const int nth = index - start_of(r.row0, lo), page = div(by_page, first) + nth;
+  if (nth < 0 || page > div(by_page, r.len - 1)) return false;
   it.at0 = max(first, page * c.page_size);
   it.rows = min(r.len, (page + 1) * c.page_size) - it.at0;
   it.row0 = r.row0 + it.at0 - first;
   it.place0 = it.at0 - page * c.page_size;
-  it.page = page_of(a, lo, it.at0);
+  const int id = __ldg(a.table + (int64_t)lo * c.max_pages + page);
+  it.page = id >= 0 && id < c.n_pages ? id : -1;
   return true;
 }
 
-// kWarps warps a block.
-template <int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, 24 / kWarps)
-    rope_append_page_kernel(const AttnArgs a, const __grid_constant__ RopeTable rope, int lane_bits,
-                            int per_seq) {
+// kWarps warps a block; kUnits heads of a kind that a group of lanes has in flight.
+template <int kWarps, int kUnits>
+__global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
+    rope_append_page_kernel(const AttnArgs a, const __grid_constant__ RopeTable rope,
+                            const FastDiv by_page, int lane_bits, int per_seq) {
   using T = __nv_bfloat16;
   constexpr int kThreads = 32 * kWarps;
   __shared__ float2 turns[kWarps][kMaxPairs + kMaxPairs / 8];  // (cos, sin) of a row's pairs, padded
@@ -115,45 +124,44 @@ __global__ void __launch_bounds__(32 * kWarps, 24 / kWarps)
     return;
   }
   PageItem it;
-  if (!page_item(a, per_seq, (int)blockIdx.x - 1, lane, it)) return;
+  if (!page_item<kThreads>(a, by_page, per_seq, (int)blockIdx.x - 1, lane, it)) return;
 
-  // This block's heads j: unit j * G + y of the keys', values' and queries'.
+  // This block's heads: j * G + y of the keys, of the values and of the queries.
   const int y = blockIdx.y, G = gridDim.y;
-  const int heads = (2 * nk + (a.q ? c.n_heads : 0) - y + G - 1) / G, cached = (2 * nk - y + G - 1) / G;
+  const int n_kv = (nk - y + G - 1) / G, n_q = a.q ? (c.n_heads - y + G - 1) / G : 0;
   // Its rows: per_row warps a row.
   int per_row = kWarps;
   while (per_row > 1 && it.rows >= 2 * kWarps / per_row) per_row /= 2;
   const int row_step = kWarps / per_row, first_row = warp / per_row;
-  const int j0 = warp % per_row * groups + group, j_step = per_row * groups, batch = kUnits * j_step;
-  const bool keep = it.rows <= row_step && cached <= batch;
+  // A group's heads: every j_step-th, kUnits at a time.
+  const int j_first = warp % per_row * groups, j0 = j_first + group, j_step = per_row * groups;
+  const int batch = kUnits * j_step, head0 = (j0 * G + y) * c.head_dim, head_step = j_step * G * c.head_dim;
+  const bool keep = it.rows <= row_step && n_kv <= batch;
 
-  for (int j = threadIdx.x; j < cached; j += kThreads) largest[j] = 0;
-  // A row's keys, values and queries, at this lane's elements.
-  struct Row {
-    const T *k, *v, *q;
+  auto stored_scale = [&](int j) {  // keys', then values'
+    return (j < n_kv ? a.k_scale + j * G : a.v_scale + (j - n_kv) * G) + (int64_t)it.page * nk + y;
   };
-  auto row_of = [&](int row) {
-    const int64_t t = it.row0 + row;
-    return Row{static_cast<const T*>(a.k) + t * c.k_stride + e0,
-               static_cast<const T*>(a.v) + t * c.v_stride - nk * c.head_dim + e0,
-               static_cast<const T*>(a.q) + t * c.q_stride - 2 * nk * c.head_dim + e0};
-  };
-  auto source = [&](const Row& r, int u) {
-    return (u < nk ? r.k : u < 2 * nk ? r.v : r.q) + u * c.head_dim;
-  };
-  Eight<T> x[kUnits];
-  auto load = [&](const Row& r, int j, int n) {
+  for (int j = threadIdx.x; j < 2 * n_kv; j += kThreads) largest[j] = 0;
+  float was0 = 0.f;  // of scale threadIdx.x, in flight with the rows
+  if (it.page >= 0 && it.place0 > 0 && (int)threadIdx.x < 2 * n_kv) was0 = *stored_scale(threadIdx.x);
+  // Heads jb .. of a row (`row`: its first head at this lane's elements), of n in all.
+  auto load = [&](const T* row, int jb, int n, Eight<T> (&x)[kUnits]) {
+    const T* p = row + (int64_t)(jb - j_first) * G * c.head_dim + head0;
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) {
       x[k] = {};
-      if (j + k * j_step < n && held) x[k] = load8(source(r, (j + k * j_step) * G + y));
+      if (jb + group + k * j_step < n && held) x[k] = load8(p + k * head_step);
     }
   };
-  float own[8], other[8];  // factors of this lane's elements and of their partners
+  auto row_at = [&](const void* base, int64_t stride, int row) {
+    return static_cast<const T*>(base) + (it.row0 + row) * stride + e0;
+  };
+  Eight<T> xk[kUnits], xv[kUnits], xq[kUnits];
+  uint64_t own[4], other[4];  // factors of this lane's elements, in pairs, and of their partners
   auto turn_of = [&](int row) {
     for (int i = lane; i < pairs; i += 32) {
       const int axis = (i >= c.rot_sections[0]) + (i >= c.rot_sections[0] + c.rot_sections[1]);
-      const int64_t pos = a.positions ? a.positions[(int64_t)axis * c.n_tokens + it.row0 + row] : it.at0 + row;
+      const int64_t pos = a.positions ? __ldg(a.positions + (int64_t)axis * c.n_tokens + it.row0 + row) : it.at0 + row;
       const int64_t angle = (int64_t)((uint64_t)pos * rope.turns[i]);
       float2 cs;
       sincospif((float)(int32_t)(angle >> 32) * 0x1p-31f, &cs.y, &cs.x);
@@ -161,111 +169,146 @@ __global__ void __launch_bounds__(32 * kWarps, 24 / kWarps)
     }
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = e0 + i;
-      own[i] = 1.f, other[i] = -0.f;  // x 1 + 0 (-0) is x for a zero of either sign
-      if (e < c.rot_dim) {
-        const bool first = c.rot_interleaved ? i % 2 == 0 : e < pairs;
+    for (int p = 0; p < 4; ++p) {
+      float f[2] = {1.f, 1.f}, g[2] = {-0.f, -0.f};  // x 1 + 0 (-0) is x for a zero of either sign
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int e = e0 + 2 * p + h;
+        if (e >= c.rot_dim) continue;
+        const bool first = c.rot_interleaved ? h == 0 : e < pairs;
         const int n = c.rot_interleaved ? e / 2 : first ? e : e - pairs;
         const float2 cs = turn[n + n / 8];
-        own[i] = cs.x;
-        other[i] = first ? -cs.y : cs.y;
+        f[h] = cs.x;
+        g[h] = first ? -cs.y : cs.y;
       }
+      own[p] = ptx::f32x2(f[0], f[1]);
+      other[p] = ptx::f32x2(g[0], g[1]);
     }
     __syncwarp();
   };
   const bool vec_partner = !c.rot_interleaved && pairs % 8 == 0;
   const int from = lane + (e0 < pairs ? pairs : -pairs) / 8;
-  // Unit u of a row (x as it was read), turned if it turns; all lanes of a warp alike where
-  // `some` is false: nothing does.
-  auto turned = [&](const Row& r, int u, bool some, const Eight<T>& x, float (&o)[8]) {
-    widen(x, o);
-    if (!some) return;
-    float z[8];
-    if (vec_partner) {
-      Eight<T> w;
+  auto pair = [](uint32_t w) { return ptx::f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); };
+  const uint64_t zero = ptx::f32x2(0.f, 0.f), minus_zero = ptx::f32x2(-0.f, -0.f);
+  auto widen2 = [&](const Eight<T>& x, uint64_t (&o)[4]) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t p = __shfl_sync(0xffffffffu, reinterpret_cast<const uint32_t*>(&x)[i], from);
-        reinterpret_cast<uint32_t*>(&w)[i] = turns_here ? p : 0u;
+    for (int p = 0; p < 4; ++p) o[p] = pair(reinterpret_cast<const uint32_t*>(&x)[p]);
+  };
+  // Head j of a row, x as it was read, turned. All lanes of the warp.
+  auto turned = [&](const T* row, int j, int n, const Eight<T>& x, uint64_t (&o)[4]) {
+    widen2(x, o);
+    if (pairs == 0) return;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&x);
+    uint64_t z[4];
+    if (vec_partner) {
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const uint32_t q = __shfl_sync(0xffffffffu, w[p], from);
+        z[p] = pair(turns_here ? q : 0u);
       }
-      widen(w, z);
+    } else if (c.rot_interleaved) {
+#pragma unroll
+      for (int p = 0; p < 4; ++p) z[p] = pair(e0 + 2 * p < c.rot_dim ? w[p] << 16 | w[p] >> 16 : 0u);
     } else {
-      const T* p = source(r, u);
+      const T* at = row + (min(j, n - 1) * G + y) * c.head_dim;
+      float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int e = e0 + i;
-        z[i] = e >= c.rot_dim      ? 0.f
-               : c.rot_interleaved ? to_f32(x.v[i ^ 1])
-                                   : to_f32(p[e < pairs ? i + pairs : i - pairs]);
+        v[i] = e >= c.rot_dim ? 0.f : to_f32(at[e < pairs ? i + pairs : i - pairs]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z[i] = ptx::f32x2(v[2 * i], v[2 * i + 1]);
+    }
+#pragma unroll
+    for (int p = 0; p < 4; ++p) o[p] = ptx::fma_f32x2(z[p], other[p], ptx::fma_f32x2(o[p], own[p], minus_zero));
+  };
+  // The largest finite element of a head into its place.
+  auto raise = [&](int j, int n, uint32_t* place, const uint64_t (&o)[4]) {
+    if (j >= n) return;
+    float m = 0.f;  // a NaN is passed over
+#pragma unroll
+    for (int p = 0; p < 4; ++p) m = fmaxf(m, fmaxf(fabsf(ptx::f32x2_lo(o[p])), fabsf(ptx::f32x2_hi(o[p]))));
+    if (m == INFINITY) {
+      m = 0.f;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const float lo = fabsf(ptx::f32x2_lo(o[p])), hi = fabsf(ptx::f32x2_hi(o[p]));
+        m = fmaxf(m, fmaxf(finite(lo) ? lo : 0.f, finite(hi) ? hi : 0.f));
       }
     }
-    if (u < nk || u >= 2 * nk) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = o[i] * own[i] + z[i] * other[i];
-    }
+    const uint32_t bits = __reduce_max_sync(group_mask, __float_as_uint(m));
+    if (gl == 0) atomicMax(place + j, bits);
   };
 
   __syncthreads();
   for (int row = first_row; row < it.rows; row += row_step) {
-    const Row r = row_of(row);
-    T* out = static_cast<T*>(a.out) + (int64_t)(it.row0 + row) * c.n_heads * c.head_dim - 2 * nk * c.head_dim + e0;
-    // backwards: the keys and values, which may be kept, last
-    const int last = j0 + max(heads - 1 - (j0 - group), 0) / batch * batch;
-    load(r, last, heads);  // in flight while the row's sines are computed
+    const T *k_row = row_at(a.k, c.k_stride, row), *v_row = row_at(a.v, c.v_stride, row);
+    const T* q_row = row_at(a.q, c.q_stride, row);
+    // backwards, for the first heads to be kept; in flight while the sines are computed
+    const int last = j_first + max(n_kv - 1 - j_first, 0) / batch * batch;
+    load(k_row, last, n_kv, xk);
+    load(v_row, last, n_kv, xv);
+    load(q_row, j_first, n_q, xq);
     turn_of(row);
-    for (int jb = last; jb >= j0; jb -= batch) {
-      if (jb != last) load(r, jb, heads);
+    for (int jb = last; jb >= j_first; jb -= batch) {
+      if (jb != last) {
+        load(k_row, jb, n_kv, xk);
+        load(v_row, jb, n_kv, xv);
+      }
 #pragma unroll
       for (int k = 0; k < kUnits; ++k) {
-        const int j = jb + k * j_step, u = j * G + y;
-        if (j - group >= heads) break;  // the same for the whole warp
-        float o[8];
-        turned(r, min(u, (heads - 1) * G + y), pairs > 0 && __any_sync(0xffffffffu, u < nk || u >= 2 * nk), x[k], o);
+        if (jb + k * j_step >= n_kv) break;  // the same for the whole warp
+        const int j = jb + k * j_step + group;
+        uint64_t o[4];
+        turned(k_row, j, n_kv, xk[k], o);
+        raise(j, n_kv, largest, o);
+        widen2(xv[k], o);
+        raise(j, n_kv, largest + n_kv, o);
+      }
+    }
+    T* out = static_cast<T*>(a.out) + (int64_t)(it.row0 + row) * c.n_heads * c.head_dim + e0 + head0;
+    for (int jb = j_first; jb < n_q; jb += batch, out += kUnits * head_step) {
+      if (jb != j_first) load(q_row, jb, n_q, xq);
+#pragma unroll
+      for (int k = 0; k < kUnits; ++k) {
+        if (jb + k * j_step >= n_q) break;
+        const int j = jb + k * j_step + group;
+        uint64_t o[4];
+        turned(q_row, j, n_q, xq[k], o);
         __syncwarp();  // in place: the partners are read before they are overwritten
-        if (j < cached) {
-          uint32_t m = 0;
+        if (j >= n_q || !held) continue;
+        uint32_t w[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(o[i]) & 0x7fffffffu);
-          if (m >= 0x7f800000u) {  // some are not finite
-            m = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              m = max(m, finite(o[i]) ? __float_as_uint(o[i]) & 0x7fffffffu : 0u);
-          }
-          m = __reduce_max_sync(group_mask, m);
-          if (gl == 0) atomicMax(largest + j, m);
-        } else if (j < heads && held) {
-          store8(out + u * c.head_dim, o);
-        }
+        for (int p = 0; p < 4; ++p) w[p] = f32x2_to_bf16x2(ptx::f32x2_lo(o[p]), ptx::f32x2_hi(o[p]));
+        *reinterpret_cast<uint4*>(out + k * head_step) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
   }
   __syncthreads();
   if (it.page < 0) return;
-  for (int j = threadIdx.x; j < cached; j += kThreads) {
-    const int u = j * G + y, h = u < nk ? u : u - nk;
-    float* stored = (u < nk ? a.k_scale : a.v_scale) + (int64_t)it.page * nk + h;
+  for (int j = threadIdx.x; j < 2 * n_kv; j += kThreads) {
     float scale = page_scale(__uint_as_float(largest[j])), ratio = 1.f;
     if (it.place0 > 0) {
-      const float was = *stored;
+      const float was = j < kThreads ? was0 : *stored_scale(j);
       if (was >= scale)
         scale = was;
       else if (was < scale)  // neither for a NaN
         ratio = __fdiv_rn(was, scale);
     }
-    *stored = scale;
+    *stored_scale(j) = scale;
     largest[j] = __float_as_uint(__fdiv_rn(1.f, scale));
     ratios[j] = ratio;
   }
   __syncthreads();
-  for (int j = warp; j < cached; j += kWarps) {
+  uint8_t* k_page = static_cast<uint8_t*>(a.k_cache) + (int64_t)it.page * c.page_stride + y * c.head_stride;
+  uint8_t* v_page = static_cast<uint8_t*>(a.v_cache) + (int64_t)it.page * c.page_stride + y * c.head_stride;
+  for (int j = warp; j < 2 * n_kv; j += kWarps) {
     const float ratio = ratios[j];
     if (ratio == 1.f) continue;
     // the page's older codes under the raised scale
-    const int u = j * G + y, vecs = c.head_dim / 16;
-    uint8_t* cache = static_cast<uint8_t*>(u < nk ? a.k_cache : a.v_cache) +
-                     (int64_t)it.page * c.page_stride + (int64_t)(u < nk ? u : u - nk) * c.head_stride;
+    const int vecs = c.head_dim / 16;
+    uint8_t* cache = j < n_kv ? k_page + j * G * c.head_stride : v_page + (j - n_kv) * G * c.head_stride;
     for (int i = lane; i < it.place0 * vecs; i += 32) {
       uint4* p = reinterpret_cast<uint4*>(cache + (int64_t)(i / vecs) * c.token_stride) + i % vecs;
       uint4 w = *p;
@@ -274,33 +317,41 @@ __global__ void __launch_bounds__(32 * kWarps, 24 / kWarps)
       *p = w;
     }
   }
+  // Elements o of a head over its scale, as codes.
+  auto put = [&](uint8_t* to, uint32_t inv, const uint64_t (&o)[4]) {
+    const uint64_t by = (uint64_t)inv << 32 | inv;
+    uint32_t w[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {  // E4M3 has no infinity: inf 0 makes it a NaN
+      const uint64_t q = ptx::fma_f32x2(o[p], zero, ptx::fma_f32x2(o[p], by, minus_zero));
+      w[p] = e4m3x2(ptx::f32x2_lo(q), ptx::f32x2_hi(q));
+    }
+    *reinterpret_cast<uint2*>(to) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+  };
   for (int row = first_row; row < it.rows; row += row_step) {
-    const Row r = row_of(row);
-    const int64_t at = (int64_t)it.page * c.page_stride + (int64_t)(it.place0 + row) * c.token_stride + e0;
-    uint8_t* k_out = static_cast<uint8_t*>(a.k_cache) + at;
-    uint8_t* v_out = static_cast<uint8_t*>(a.v_cache) + at - nk * c.head_stride;
+    const T *k_row = row_at(a.k, c.k_stride, row), *v_row = row_at(a.v, c.v_stride, row);
     if (!keep) {
-      load(r, j0, cached);
+      load(k_row, j_first, n_kv, xk);
+      load(v_row, j_first, n_kv, xv);
       turn_of(row);
     }
-    for (int jb = j0; jb - group < cached; jb += batch) {
-      if (jb != j0) load(r, jb, cached);
+    const int64_t at = (int64_t)(it.place0 + row) * c.token_stride + e0;
+    for (int jb = j_first; jb < n_kv; jb += batch) {
+      if (jb != j_first) {
+        load(k_row, jb, n_kv, xk);
+        load(v_row, jb, n_kv, xv);
+      }
 #pragma unroll
       for (int k = 0; k < kUnits; ++k) {
-        const int j = jb + k * j_step, u = j * G + y;
-        if (j - group >= cached) break;
-        float o[8];
-        turned(r, min(u, (cached - 1) * G + y), pairs > 0 && __any_sync(0xffffffffu, u < nk), x[k], o);
-        if (j >= cached || !held) continue;
-        const float inv = __uint_as_float(largest[j]);
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)  // E4M3 has no infinity: inf 0 makes it a NaN
-          o[i] = fmaf(o[i], 0.f, __fmul_rn(o[i], inv));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = e4m3x2(o[2 * i], o[2 * i + 1]);
-        *reinterpret_cast<uint2*>((u < nk ? k_out : v_out) + u * c.head_stride) =
-            make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+        if (jb + k * j_step >= n_kv) break;
+        const int j = jb + k * j_step + group;
+        uint64_t o[4], v[4];
+        turned(k_row, j, n_kv, xk[k], o);
+        if (j >= n_kv || !held) continue;
+        widen2(xv[k], v);
+        const int64_t head = at + (int64_t)j * G * c.head_stride;
+        put(k_page + head, largest[j], o);
+        put(v_page + head, largest[n_kv + j], v);
       }
     }
   }
@@ -313,20 +364,24 @@ cudaError_t launch_rope_append_page(const AttnArgs& a, const RopeTable& rope, in
   const moe_attn_config& c = a.c;
   const int per_seq = c.max_new == 1 ? 1 : 2;
   const long long items = c.n_tokens / c.page_size + (long long)per_seq * c.n_seqs;
-  // A block takes all heads of an item where a warp has a row, or where the GPU's
-  // slots (24 warps an SM) are filled; else some of them. 16 warps a block where items
-  // are few and have the rows.
+  // Prompts, whose items have a row for each of 16 warps: a block an item, with four heads
+  // in flight (two: 67 us for 59, 8197 tokens). Else blocks of 8 warps with two (four: 12.6
+  // us for 11.2, 225 tokens of 64 sequences), and an item's heads over several
+  // blocks while there are less than 12 warps an SM.
   const int heads = 2 * c.n_kv_heads + (a.q ? c.n_heads : 0);
   const int rows = c.max_new < c.page_size ? c.max_new : c.page_size;
-  const bool wide = rows >= 16 && items < 3LL * num_sms();
+  const bool wide = rows >= 16;
   const int warps = wide ? 16 : 8;
   int split = 1;
   while (split < c.n_kv_heads && rows < warps && 2 * split * warps <= heads * rows &&
-         items * split * warps < 24LL * num_sms())
+         items * split * warps < 12LL * num_sms())
     split *= 2;
+  const FastDiv by_page = fast_div((uint32_t)c.page_size);
   const dim3 grid((unsigned)items + 1, (unsigned)split), block((unsigned)(32 * warps));
-  return wide ? launch_pdl(rope_append_page_kernel<16>, grid, block, 0, s, 1, a, rope, lane_bits, per_seq)
-              : launch_pdl(rope_append_page_kernel<8>, grid, block, 0, s, 1, a, rope, lane_bits, per_seq);
+  return wide ? launch_pdl(rope_append_page_kernel<16, 4>, grid, block, 0, s, 1, a, rope, by_page, lane_bits,
+                           per_seq)
+              : launch_pdl(rope_append_page_kernel<8, 2>, grid, block, 0, s, 1, a, rope, by_page, lane_bits,
+                           per_seq);
 }
 
 }  // namespace moe

@@ -12,6 +12,21 @@ __host__ __device__ __forceinline__ int clamp_int(int v, int lo, int hi) {
   return v < lo ? lo : v > hi ? hi : v;
 }
 
+// n / d for 0 <= n < 2^30 and 1 <= d < 2^30 as a multiplication.
+struct FastDiv {
+  uint64_t mul;
+  int shift;
+};
+inline FastDiv fast_div(uint32_t d) {
+  int bits = 0;
+  while ((1u << bits) < d) ++bits;
+  const int shift = 30 + bits;
+  return {((1ull << shift) + d - 1) / d, shift};
+}
+__device__ __forceinline__ int div(const FastDiv& f, int n) {
+  return (int)(((uint64_t)n * f.mul) >> f.shift);
+}
+
 // A sequence as its lists give it, clamped to the arrays: its new tokens are
 // rows row0 .. row0+n-1 and its cached tokens positions 0 .. len-1, new
 // token j at position len - n + j. ok: nothing had to be clamped.
