@@ -24,7 +24,7 @@ namespace {
 //   32 of 100 to 6000, D 64                  112 and  90   114 and 115
 //   2 of 20000, D 128                         89 and  52    90 and  98
 constexpr int kTcRows = 48;
-constexpr int kTcRowsE4m3 = 48;
+constexpr int kTcRowsE4m3 = 64;
 
 // Rows whose keys were cut into splits: one warp a row.
 constexpr int kJoinWarps = 4;
@@ -90,7 +90,7 @@ Plan plan_of(const moe_attn_config& c) {
   // memory of an SM's third block. Against larger blocks, since removed: bf16,
   // 20 rows: 147 us in one block, 138 in two; E4M3, 28 rows: 282 and 206; fp32,
   // 16 rows: 42.6 and 37.3.
-  p.row_blocks = ceil_div(units, p.tc ? 8 : f32 && c.head_dim <= 128 ? 3 : 2);
+  p.row_blocks = ceil_div(units, p.tc ? (f8 ? 16 : 8) : f32 && c.head_dim <= 128 ? 3 : 2);
   p.nt = ceil_div(units, p.row_blocks);
   p.items = (long long)c.n_seqs * c.n_kv_heads * p.row_blocks;
   long long keys = (long long)c.max_pages * c.page_size;
@@ -109,7 +109,7 @@ Plan plan_of(const moe_attn_config& c) {
   // 50 of an fp32 cache 7, 10, 14, 20 took 0.92, 0.93, 0.94, 0.95. Clusters of
   // 16 are placed badly unless all run at once: 84 sequences of 8000 keys take
   // 79 us in 16 parts, 65 in eight.
-  const int per_sm = p.tc  ? (f8 ? 2 : 1)
+  const int per_sm = p.tc  ? 1
                      : f32 ? attn::f32_blocks_per_sm(c.head_dim, p.nt)
                            : attn::blocks_per_sm(c.head_dim);
   const long long slots = (long long)per_sm * attn::kPlanSms;

@@ -1,8 +1,7 @@
 // Attention of many query rows over an E4M3 cache with a scale per page and head,
 // on tcgen05.
 //
-// An item has up to 128 rows, the M of a tcgen05.mma, and its keys go by in tiles of
-// 128:
+// Per tile of 128 keys and 128 rows (the M of a tcgen05.mma):
 //   S (128 x 128) = Q K^T      fp16, both from shared memory
 //   O (128 x D)  += P V        fp16, P from Tensor Memory (over the S it came from)
 // tcgen05 takes E4M3 only against E4M3, for which queries and weights are too
@@ -20,11 +19,13 @@
 // the largest and none is off by more than 2^-32 of it. The sum of weights
 // is taken without v (the group's sum times 1 / v); no weight without v passes 2^68.
 //
-// A row is a lane of Tensor Memory and one thread, which reads its scores 32 at a time and
-// exchanges nothing; where some of them raise M, O and the tile's weights so far
-// are scaled in place. 4 warps of softmax, 8 that widen keys and values (their codes
-// loaded a tile ahead into registers), one that issues the products. Two blocks an SM, each with half of Tensor Memory (S 128 columns, O
-// 128) and one tile of K and V: one's products run under the other's softmax.
+// A block has the SM and runs two streams of tiles, each with its S and O in Tensor
+// Memory, four warps of softmax and a warp that issues its products, so that one's
+// products run under the other's softmax. An item of more than 128 rows (up to 256) is
+// two streams of rows that share the tiles of keys; one of up to 128 rows is two
+// streams of keys (even tiles and odd ones), joined at the end. A row is a lane of
+// Tensor Memory and one thread, which has the tile's 128 scores in registers. 4 warps
+// widen keys and values, two tiles of each ahead.
 //
 // Keys that some rows of the item see and others do not (at most its new tokens at
 // either end) are masked row by row; where one of their values is NaN (0 times NaN is
@@ -36,39 +37,43 @@ namespace moe {
 namespace attn {
 namespace {
 
-constexpr int kSoftmaxWarps = 4, kCopyWarps = 8;
-constexpr int kMmaWarp = kSoftmaxWarps + kCopyWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 4);  // whole warpgroups
-// Registers a thread: 64 at launch, which the warpgroups share out anew (softmax, two
-// of copies, products: 104 + 2 x 56 + 40 = 4 x 64).
-constexpr int kSoftmaxRegs = 104, kCopyRegs = 56, kMmaRegs = 40;
-static_assert(kSoftmaxRegs + 2 * kCopyRegs + kMmaRegs <= 4 * 64, "");
-constexpr int kKeys = 128, kRows = 128;
+constexpr int kSoftmaxWarps = 8, kCopyWarps = 4;  // four a stream; four
+constexpr int kMmaWarp = kSoftmaxWarps + kCopyWarps;  // a stream's: + 0, + 1
+constexpr int kThreads = 32 * (kMmaWarp + 4);         // whole warpgroups
+// Registers a thread: 128 at launch, which the warpgroups share out anew.
+constexpr int kSoftmaxRegs = 184, kCopyRegs = 104, kMmaRegs = 40;
+static_assert(2 * kSoftmaxRegs + kCopyRegs + kMmaRegs <= 4 * 128, "");
+constexpr int kKeys = 128, kTileRows = 128, kRows = 2 * kTileRows;
 constexpr int kGroup = 32, kGroups = kKeys / kGroup;  // keys that may share a page
-constexpr uint32_t kTmemCols = 256, kTmemO = 128;
+constexpr uint32_t kTmemCols = 512, kTmemO = 256;     // S of each stream, O of each
 constexpr int kEdgeKeys = 8;  // keys that only some rows see, taken at a time
 
 template <int kDim>
 struct Layout {
   static constexpr int kHalves = kDim / 64;      // 128-byte rows of 64 elements
   static constexpr int kHalf = 128 * 128;        // bytes: of 128 rows
-  static constexpr int kTile = kHalves * kHalf;  // Q, K or V
-  static constexpr int kInbox = (int)sizeof(Inbox<kRows, kDim>);
-  static constexpr int kTiles = 3 * kTile > kInbox ? 3 * kTile : (kInbox + 1023) / 1024 * 1024;
-  static constexpr int kBars = 128;
-  static constexpr int kScales = 2 * 4 * kKeys * 4;  // of two tiles: of keys; of values; their log2 and inverse
+  static constexpr int kTile = kHalves * kHalf;  // 128 rows of Q, K or V
+  static constexpr int kK = 2 * kTile, kV = 4 * kTile, kRing = 6 * kTile;
+  static constexpr int kLd = kDim + 4;           // floats a row of a stream's O, to be joined
+  static constexpr int kInbox = ((int)sizeof(Inbox<kRows, kDim>) + 1023) / 1024 * 1024;
+  static constexpr int kTiles = kRing > kInbox ? kRing : kInbox;
+  static_assert(kTileRows * kLd * 4 <= kRing - kK, "a stream's O fits over K and V");
+  static constexpr int kBars = 256;
+  static constexpr int kScales = 4 * 4 * kKeys * 4;  // of four tiles: of keys; of values, their log2 and inverse
   static constexpr int kLines = kEdgeKeys * (2 * kDim + 16);
-  static constexpr int kAll = 1024 + kTiles + kBars + kScales + kLines;
+  static constexpr int kJoin = kTileRows * 8;
+  static constexpr int kAll = 1024 + kTiles + kBars + kScales + kLines + kJoin;
 };
 
 struct Bars {
-  // K, V of a tile are there; its scores (and K's slot is free); its weights; its
-  // part of O (and V's slot and the weights' place are free)
-  uint64_t k_full, v_full, s_full, p_full, pv_done, drained;
+  // of the two slots of K and of V: filled, used by every stream that uses them
+  uint64_t k_full[2], k_free[2], v_full[2], v_free[2];
+  // of a stream: a tile's scores are there, its weights, its part of O
+  uint64_t s_full[2], p_full[2], pv_done[2], drained[2];
   uint32_t tmem;
   int abort_flag;
 };
-static_assert(sizeof(Bars) <= 128, "");
+static_assert(sizeof(Bars) <= 256, "");
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
   return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -101,7 +106,8 @@ __device__ __forceinline__ void tmem_ready(uint32_t (&r)[32]) {
                :
                : "memory");
 }
-__device__ __forceinline__ uint32_t codes_f16(uint32_t v) {  // two codes, the low 16 bits
+// Two codes (the low 16 bits of v) as fp16.
+__device__ __forceinline__ uint32_t codes_f16(uint32_t v) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)v));
   return r;
@@ -117,6 +123,18 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t v) {
       : "=f"(r.x), "=f"(r.y)
       : "r"(v));
   return r;
+}
+// 16 bytes that are read once (not to push other things out of the first-level cache), or
+// zeros. One predicated load, so that nothing waits for it before it is used.
+__device__ __forceinline__ uint4 ld_once(const void* p, bool there) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"((uint32_t)there));
+  return v;
 }
 __device__ __forceinline__ bool has_nan(uint32_t codes) {  // any of four
   return (((codes & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
@@ -143,37 +161,44 @@ __device__ __forceinline__ void softmax_sync() {
 
 // kUniform: pages hold whole groups of 32 keys.
 template <int kDim, bool kUniform>
-__global__ void __launch_bounds__(kThreads, 2) tc_e4m3_kernel(const __grid_constant__ Params prm) {
+__global__ void __launch_bounds__(kThreads, 1) tc_e4m3_kernel(const __grid_constant__ Params prm) {
   using L = Layout<kDim>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (1024 - ptx::smem_addr(smem_raw) % 1024) % 1024;
-  uint8_t *qs = smem, *k_tile = smem + L::kTile, *v_tile = smem + 2 * L::kTile;
   Bars& bars = *reinterpret_cast<Bars*>(smem + L::kTiles);
   float* scales = reinterpret_cast<float*>(smem + L::kTiles + L::kBars);
   uint8_t* lines = reinterpret_cast<uint8_t*>(scales) + L::kScales;
+  float2* of_odd = reinterpret_cast<float2*>(lines + L::kLines);  // the odd stream's (M, sum) of a row
   const AttnArgs& a = prm.a;
   const moe_attn_config& c = a.c;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
 
   pdl_wait();
   pdl_trigger();
   Item it;
   if (!item_of<kThreads>(prm, prm.item_rows, it)) return;
   Range rg = range_of(prm, it, prm.item_rows, kKeys);
+  const bool by_rows = prm.item_rows > kTileRows;  // the streams are of rows, else of keys
+  // streams that use a tile of keys: both, where the item has rows for both
+  const int users = by_rows && it.rows > kTileRows ? 2 : 1;
 
   volatile int* abort_flag = &bars.abort_flag;
   // A warp's wait: all lanes go on, or none. After one has run out the others
   // return at once.
-  auto warp_wait = [&](uint64_t& bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait_phase(ptx::smem_addr(&bar), parity, abort_flag, a.status));
+  auto warp_wait = [&](uint64_t& bar, int phase) {
+    return __all_sync(0xffffffffu, wait_phase(ptx::smem_addr(&bar), (uint32_t)phase & 1, abort_flag, a.status));
   };
   if (threadIdx.x == 0) {
-    ptx::mbar_init(ptx::smem_addr(&bars.k_full), 32 * kCopyWarps);
-    ptx::mbar_init(ptx::smem_addr(&bars.v_full), 32 * kCopyWarps);
-    ptx::mbar_init(ptx::smem_addr(&bars.s_full), 1);
-    ptx::mbar_init(ptx::smem_addr(&bars.p_full), 32 * kSoftmaxWarps);
-    ptx::mbar_init(ptx::smem_addr(&bars.pv_done), 1);
-    ptx::mbar_init(ptx::smem_addr(&bars.drained), 1);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(ptx::smem_addr(&bars.k_full[i]), 32 * kCopyWarps);
+      ptx::mbar_init(ptx::smem_addr(&bars.v_full[i]), 32 * kCopyWarps);
+      ptx::mbar_init(ptx::smem_addr(&bars.k_free[i]), users);
+      ptx::mbar_init(ptx::smem_addr(&bars.v_free[i]), users);
+      ptx::mbar_init(ptx::smem_addr(&bars.s_full[i]), 1);
+      ptx::mbar_init(ptx::smem_addr(&bars.p_full[i]), 32 * kSoftmaxWarps / 2);
+      ptx::mbar_init(ptx::smem_addr(&bars.pv_done[i]), 1);
+      ptx::mbar_init(ptx::smem_addr(&bars.drained[i]), 1);
+    }
     bars.abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -202,178 +227,179 @@ __global__ void __launch_bounds__(kThreads, 2) tc_e4m3_kernel(const __grid_const
   ptx::tc_fence_after();
   const uint32_t tmem = bars.tmem;
 
-  // The keys of the products, in tiles of kKeys from key0 on.
+  // The keys of the products, in tiles of kKeys from key0 on: this block's n tiles.
   Range seen = rg;
   if (wild) seen.lo_min = rg.lo_max, seen.hi_max = rg.hi_min;
-  const int key0 = seen.lo_min / kGroup * kGroup;
+  int key0 = seen.lo_min / kGroup * kGroup, n;
   {
     const int tiles = seen.hi_max < seen.lo_min ? 0 : (seen.hi_max - key0) / kKeys + 1;
     const int at = it.split * prm.parts + it.part, of = prm.splits * prm.parts;
     const int each = tiles / of, more = tiles - each * of;
-    rg.t0 = at * each + min(at, more);
-    rg.t1 = rg.t0 + each + (at < more);
+    key0 += (at * each + min(at, more)) * kKeys;
+    n = each + (at < more);
   }
-  const int n = rg.t1 - rg.t0;
-  auto tile_key = [&](int i) { return key0 + (rg.t0 + i) * kKeys; };
-
-  float m = -3.0e38f, l = 0.f, factor = 0.f;  // of this thread's row; factor of its scores, log2 units
-  bool wide = false;                          // scales outside 2^-40 .. 2^40 have come by
-  const int row = warp * 32 + lane;
-  const bool active = warp < kSoftmaxWarps && warp * 32 < it.rows;
-  const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
-  const int pos = it.pos(prm, row), first = it.first(pos);
+  // Stream st's tiles: all, or every other.
+  const int t_step = by_rows ? 1 : 2;
+  auto tiles_of = [&](int st) { return by_rows ? (st < users ? n : 0) : (n - st + 1) / 2; };
+  auto tile_of = [&](int st, int t) { return by_rows ? t : 2 * t + st; };
 
   if (warp < kSoftmaxWarps) {
     more_registers<kSoftmaxRegs>();
+    const int st = warp / 4, row_in = warp % 4 * 32 + lane, row = by_rows ? st * kTileRows + row_in : row_in;
+    const int rows_here = by_rows ? it.rows - st * kTileRows : it.rows;
+    const bool active = warp % 4 * 32 < rows_here;
+    const int my_tiles = tiles_of(st);
+    uint8_t* qs = smem + (by_rows ? st * L::kTile : 0);
     // ------------------------------------------------------------- queries --
     // As fp16, each row scaled by a power of two to [2^14, 2^15) for its largest element
     // (negated for a negative scale, so that larger products are larger scores).
-    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + it.q_at(prm, row));
-    uint4 x[kDim / 8];
+    float factor;  // of the row's scores, log2 units
+    {
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + it.q_at(prm, row));
+      uint4 x[kDim / 8];
 #pragma unroll
-    for (int v = 0; v < kDim / 8; ++v) {
-      x[v] = make_uint4(0u, 0u, 0u, 0u);
-      if (8 * v < c.head_dim) x[v] = q[v];
-    }
-    float amax = 0.f;
-#pragma unroll
-    for (int v = 0; v < kDim / 8; ++v) {
-      const uint32_t w[4] = {x[v].x, x[v].y, x[v].z, x[v].w};
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        float lo, hi;
-        bf16x2_to_f32(w[y], lo, hi);
-        amax = fmaxf(amax, fmaxf(fabsf(lo), fabsf(hi)));
+      for (int v = 0; v < kDim / 8; ++v) {
+        x[v] = make_uint4(0u, 0u, 0u, 0u);
+        if (8 * v < c.head_dim) x[v] = q[v];
       }
-    }
-    const int e = clamp_int((int)(__float_as_uint(amax) >> 23) - 127, -112, 128);
-    const float down = copysignf(__uint_as_float((uint32_t)(141 - e) << 23), c.scale);
-    factor = fabsf(c.scale) * 1.4426950408889634f * __uint_as_float((uint32_t)(113 + e) << 23);
+      float amax = 0.f;
 #pragma unroll
-    for (int v = 0; v < kDim / 8; ++v) {
-      uint32_t w[4] = {x[v].x, x[v].y, x[v].z, x[v].w};
+      for (int v = 0; v < kDim / 8; ++v) {
+        const uint32_t w[4] = {x[v].x, x[v].y, x[v].z, x[v].w};
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        float lo, hi;
-        bf16x2_to_f32(w[y], lo, hi);
-        w[y] = pack_f16(lo * down, hi * down);
+        for (int y = 0; y < 4; ++y) {
+          float lo, hi;
+          bf16x2_to_f32(w[y], lo, hi);
+          amax = fmaxf(amax, fmaxf(fabsf(lo), fabsf(hi)));
+        }
       }
-      *reinterpret_cast<uint4*>(qs + v / 8 * L::kHalf + row * 128 + ((v % 8 ^ (row & 7)) << 4)) =
-          make_uint4(w[0], w[1], w[2], w[3]);
+      const int e = clamp_int((int)(__float_as_uint(amax) >> 23) - 127, -112, 128);
+      const float down = copysignf(__uint_as_float((uint32_t)(141 - e) << 23), c.scale);
+      factor = fabsf(c.scale) * 1.4426950408889634f * __uint_as_float((uint32_t)(113 + e) << 23);
+      if (by_rows || st == 0) {
+#pragma unroll
+        for (int v = 0; v < kDim / 8; ++v) {
+          uint32_t w[4] = {x[v].x, x[v].y, x[v].z, x[v].w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            float lo, hi;
+            bf16x2_to_f32(w[y], lo, hi);
+            w[y] = pack_f16(lo * down, hi * down);
+          }
+          *reinterpret_cast<uint4*>(qs + v / 8 * L::kHalf + row_in * 128 + ((v % 8 ^ (row_in & 7)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
     }
     ptx::fence_proxy_async_smem();
-    asm volatile("bar.arrive 2, %0;" ::"n"(32 * kSoftmaxWarps + 32) : "memory");
+    asm volatile("bar.arrive 2, %0;" ::"n"(32 * kSoftmaxWarps + 64) : "memory");
     // ------------------------------------------------------------- softmax --
-    // Weights of keys 32 g .. + 31 of tile i from their scores w, into P.
-    auto weights = [&](int i, int g, uint32_t (&w)[32]) {
-      const float* fk = scales + (i & 1) * 4 * kKeys;
-      const float *fv = fk + kKeys, *ev = fv + kKeys, *iv = ev + kKeys;
-      const int at = tile_key(i) + kGroup * g;
-      // columns from .. to - 1 are keys that the row sees
-      const int from = max(first, seen.lo_min) - at, to = min(pos, seen.hi_max) + 1 - at;
-      if (__any_sync(0xffffffffu, from > 0 || to < kGroup)) {
-#pragma unroll
-        for (int x = 0; x < kGroup; ++x)
-          if (x < from || x >= to) w[x] = 0xff800000u;  // -inf
-      }
-      // the largest score, and the largest with its value's scale
-      float top = -INFINITY, top_v = -INFINITY;
-      if (kUniform) {
-        float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int x = 0; x < 32; ++x) t[x % 4] = fmaxf(t[x % 4], __uint_as_float(w[x]));
-        top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * (factor * fk[g]);
-        top_v = top + ev[g];
-        wide = wide || !(fabsf(ev[g]) <= 40.f);
-      } else {
-#pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          const float t = __uint_as_float(w[x]) * (factor * fk[kGroup * g + x]);
-          top = fmaxf(top, t);
-          top_v = fmaxf(top_v, t + ev[kGroup * g + x]);
-        }
-      }
-      const bool raise = top_v > m + 15.f || top > m + 68.f;
-      if (__any_sync(0xffffffffu, raise)) {
-        const float up = raise ? fmaxf(top_v - 7.f, top - 60.f) : m, f = ptx::ex2(m - up);
-        m = up;
-        l *= f;
-        uint32_t o[16];
-        if (i > 0) {  // O is still while P of this tile is not there
-#pragma unroll 1
-          for (int x = 0; x < kDim; x += 16) {
-            ptx::tmem_ld16(tmem + lanes + kTmemO + x, o);
-            ptx::tmem_ld_wait();
-#pragma unroll
-            for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-            ptx::tmem_st16(tmem + lanes + kTmemO + x, o);
-          }
-        }
-#pragma unroll 1
-        for (int x = 0; x < g; ++x) {  // this tile's weights so far
-          ptx::tmem_st_wait();
-          ptx::tmem_ld16(tmem + lanes + 16 * x, o);
-          ptx::tmem_ld_wait();
-#pragma unroll
-          for (int y = 0; y < 16; ++y) {
-            const float2 p = unpack_f16(o[y]);
-            o[y] = pack_f16(p.x * f, p.y * f);
-          }
-          ptx::tmem_st16(tmem + lanes + 16 * x, o);
-        }
-      }
-      uint64_t sum[2] = {0, 0};
-      uint32_t p[16];
-      if (kUniform && !wide) {
-        const float f1 = factor * fk[g], a1 = ev[g] - m;
-        const uint64_t f2 = ptx::f32x2(f1, f1), a2 = ptx::f32x2(a1, a1);
-#pragma unroll
-        for (int y = 0; y < 16; ++y) {
-          const uint64_t v = ptx::fma_f32x2((uint64_t)w[2 * y + 1] << 32 | w[2 * y], f2, a2);
-          const float lo = ptx::ex2(ptx::f32x2_lo(v)), hi = ptx::ex2(ptx::f32x2_hi(v));
-          sum[y % 2] = ptx::add_f32x2(sum[y % 2], ptx::f32x2(lo, hi));
-          p[y] = pack_f16(lo, hi);
-        }
-        sum[0] = ptx::add_f32x2(sum[0], sum[1]);
-        l = fmaf(ptx::f32x2_lo(sum[0]) + ptx::f32x2_hi(sum[0]), iv[g], l);
-      } else {
-#pragma unroll
-        for (int y = 0; y < 16; ++y) {
-          const int k = kUniform ? g : kGroup * g + 2 * y, k1 = kUniform ? g : k + 1;
-          const float lo = ptx::ex2(fmaf(__uint_as_float(w[2 * y]), factor * fk[k], -m));
-          const float hi = ptx::ex2(fmaf(__uint_as_float(w[2 * y + 1]), factor * fk[k1], -m));
-          sum[y % 2] = ptx::add_f32x2(sum[y % 2], ptx::f32x2(lo, hi));
-          p[y] = pack_f16(lo * fv[k], hi * fv[k1]);
-        }
-        sum[0] = ptx::add_f32x2(sum[0], sum[1]);
-        l += ptx::f32x2_lo(sum[0]) + ptx::f32x2_hi(sum[0]);
-      }
-      ptx::tmem_st16(tmem + lanes + 16 * g, p);  // over scores that have been read
-    };
-    for (int i = 0; i < n; ++i) {
-      if (warp_wait(bars.s_full, i & 1) && active) {
+    const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
+    const uint32_t s_at = tmem + lanes + kKeys * st, o_at = tmem + lanes + kTmemO + 128 * st;
+    const int pos = it.pos(prm, row), first = it.first(pos);
+    float m = -3.0e38f, l = 0.f;
+    bool wide = false;  // scales outside 2^-40 .. 2^40 have come by
+    // of the stream's first tile's columns, from .. to - 1 are keys that the row sees
+    int from = max(first, seen.lo_min) - key0 - tile_of(st, 0) * kKeys;
+    int to = min(pos, seen.hi_max) + 1 - key0 - tile_of(st, 0) * kKeys;
+    for (int t = 0; t < my_tiles; ++t, from -= t_step * kKeys, to -= t_step * kKeys) {
+      if (warp_wait(bars.s_full[st], t) && active) {
         ptx::tc_fence_after();
-#pragma unroll 1
+        const float* fk = scales + (tile_of(st, t) & 3) * 4 * kKeys;
+        const float *fv = fk + kKeys, *ev = fv + kKeys, *iv = ev + kKeys;
+        const bool edge = __any_sync(0xffffffffu, from > 0 || to < kKeys);
+        uint32_t w[kGroups][32];
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) ptx::tmem_ld32(s_at + kGroup * g, w[g]);
+        // the largest score, and the largest with its value's scale
+        float top = -INFINITY, top_v = -INFINITY;
+#pragma unroll
         for (int g = 0; g < kGroups; ++g) {
-          uint32_t w[32];
-          ptx::tmem_ld32(tmem + lanes + kGroup * g, w);
-          tmem_ready(w);
-          weights(i, g, w);
+          tmem_ready(w[g]);
+          if (edge) {
+#pragma unroll
+            for (int x = 0; x < kGroup; ++x)
+              if (kGroup * g + x < from || kGroup * g + x >= to) w[g][x] = 0xff800000u;  // -inf
+          }
+          if (kUniform) {
+            float u[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int x = 0; x < 32; ++x) u[x % 4] = fmaxf(u[x % 4], __uint_as_float(w[g][x]));
+            const float v = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])) * (factor * fk[g]), e = ev[g];
+            top = fmaxf(top, v);
+            top_v = fmaxf(top_v, v + e);
+            wide = wide || !(fabsf(e) <= 40.f);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              const float u = __uint_as_float(w[g][x]) * (factor * fk[kGroup * g + x]);
+              top = fmaxf(top, u);
+              top_v = fmaxf(top_v, u + ev[kGroup * g + x]);
+            }
+          }
+        }
+        const bool raise = top_v > m + 15.f || top > m + 68.f;
+        if (__any_sync(0xffffffffu, raise)) {
+          const float up = raise ? fmaxf(top_v - 7.f, top - 60.f) : m, f = ptx::ex2(m - up);
+          m = up;
+          l *= f;
+          if (t > 0) {  // O is still while P of this tile is not there
+#pragma unroll 1
+            for (int x = 0; x < kDim; x += 16) {
+              uint32_t o[16];
+              ptx::tmem_ld16(o_at + x, o);
+              ptx::tmem_ld_wait();
+#pragma unroll
+              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              ptx::tmem_st16(o_at + x, o);
+            }
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          uint64_t sum[2] = {0, 0};
+          uint32_t p[16];
+          if (kUniform && !wide) {
+            const float f1 = factor * fk[g], a1 = ev[g] - m;
+            const uint64_t f2 = ptx::f32x2(f1, f1), a2 = ptx::f32x2(a1, a1);
+#pragma unroll
+            for (int y = 0; y < 16; ++y) {
+              const uint64_t v = ptx::fma_f32x2((uint64_t)w[g][2 * y + 1] << 32 | w[g][2 * y], f2, a2);
+              const float lo = ptx::ex2(ptx::f32x2_lo(v)), hi = ptx::ex2(ptx::f32x2_hi(v));
+              sum[y % 2] = ptx::add_f32x2(sum[y % 2], ptx::f32x2(lo, hi));
+              p[y] = pack_f16(lo, hi);
+            }
+            sum[0] = ptx::add_f32x2(sum[0], sum[1]);
+            l = fmaf(ptx::f32x2_lo(sum[0]) + ptx::f32x2_hi(sum[0]), iv[g], l);
+          } else {
+#pragma unroll
+            for (int y = 0; y < 16; ++y) {
+              const int k = kUniform ? g : kGroup * g + 2 * y, k1 = kUniform ? g : k + 1;
+              const float lo = ptx::ex2(fmaf(__uint_as_float(w[g][2 * y]), factor * fk[k], -m));
+              const float hi = ptx::ex2(fmaf(__uint_as_float(w[g][2 * y + 1]), factor * fk[k1], -m));
+              sum[y % 2] = ptx::add_f32x2(sum[y % 2], ptx::f32x2(lo, hi));
+              p[y] = pack_f16(lo * fv[k], hi * fv[k1]);
+            }
+            sum[0] = ptx::add_f32x2(sum[0], sum[1]);
+            l += ptx::f32x2_lo(sum[0]) + ptx::f32x2_hi(sum[0]);
+          }
+          ptx::tmem_st16(s_at + 16 * g, p);  // over scores, which are in registers
         }
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
       }
-      ptx::mbar_arrive(ptx::smem_addr(&bars.p_full));
+      ptx::mbar_arrive(ptx::smem_addr(&bars.p_full[st]));
     }
-  // ---- the keys that only some rows see, where a value is NaN ----
-  {
-    const bool go = n == 0 || warp_wait(bars.pv_done, (n - 1) & 1);
+
+    // ---- the keys that only some rows see, where a value is NaN ----
+    const bool go = my_tiles == 0 || warp_wait(bars.pv_done[st], my_tiles - 1);
     ptx::tc_fence_after();
-    if (wild && it.split == 0 && it.part == 0 && go) {
-      if (n == 0) {
+    const bool adds = wild && it.split == 0 && it.part == 0 && (by_rows || st == 0) && go;
+    if (wild && it.split == 0 && it.part == 0) {
+      if (adds && my_tiles == 0) {
         uint32_t z[32] = {};
 #pragma unroll
-        for (int x = 0; x < kDim; x += 32) tmem_st32(tmem + lanes + kTmemO + x, z);
+        for (int x = 0; x < kDim; x += 32) tmem_st32(o_at + x, z);
         ptx::tmem_st_wait();
       }
       float* line_scale = reinterpret_cast<float*>(lines + kEdgeKeys * 2 * kDim);
@@ -395,14 +421,14 @@ __global__ void __launch_bounds__(kThreads, 2) tc_e4m3_kernel(const __grid_const
           reinterpret_cast<uint4*>(lines)[x] = y;
         }
         softmax_sync();
-        for (int e = e0; e < min(edges, e0 + kEdgeKeys); ++e) {
+        for (int e = e0; adds && e < min(edges, e0 + kEdgeKeys); ++e) {
           const int key = edge_key(e);
           const uint8_t* line = lines + (e - e0) * 2 * kDim;
           const bool see = key <= pos && key >= first;
           float dot = 0.f;
           for (int v = 0; v < c.head_dim / 8; ++v) {
-            const uint4 x = *reinterpret_cast<const uint4*>(qs + v / 8 * L::kHalf + row * 128 +
-                                                            ((v % 8 ^ (row & 7)) << 4));
+            const uint4 x = *reinterpret_cast<const uint4*>(qs + v / 8 * L::kHalf + row_in * 128 +
+                                                            ((v % 8 ^ (row_in & 7)) << 4));
             const uint2 y = *reinterpret_cast<const uint2*>(line + 8 * v);
             const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
             const uint32_t ys[4] = {codes_f16(y.x), codes_f16(y.x >> 16), codes_f16(y.y), codes_f16(y.y >> 16)};
@@ -419,8 +445,8 @@ __global__ void __launch_bounds__(kThreads, 2) tc_e4m3_kernel(const __grid_const
           l = l * f + p;
           for (int x = 0; x < kDim; x += 32) {
             uint32_t o[32];
-            ptx::tmem_ld32(tmem + lanes + kTmemO + x, o);
-            ptx::tmem_ld_wait();
+            ptx::tmem_ld32(o_at + x, o);
+            tmem_ready(o);
 #pragma unroll
             for (int y = 0; y < 32; y += 2) {
               const float2 v = unpack_f16(codes_f16(*reinterpret_cast<const uint16_t*>(line + kDim + x + y)));
@@ -428,106 +454,152 @@ __global__ void __launch_bounds__(kThreads, 2) tc_e4m3_kernel(const __grid_const
               o[y] = __float_as_uint(see ? fmaf(p * vs, v.x, o0) : o0);
               o[y + 1] = __float_as_uint(see ? fmaf(p * vs, v.y, o1) : o1);
             }
-            tmem_st32(tmem + lanes + kTmemO + x, o);
+            tmem_st32(o_at + x, o);
           }
           ptx::tmem_st_wait();
         }
       }
     }
-  }
-  const bool any = n > 0 || (wild && it.split == 0 && it.part == 0);  // O is there
-  const int vecs = c.head_dim / 4;
-  if (prm.parts == 1) {
-    if (active) {
+    // ---- the rows of O ----
+    const int vecs = c.head_dim / 4;
+    bool any = my_tiles > 0 || adds;  // O is there
+    float scale_o = 1.f, scale_odd = 0.f;
+    float* odd_o = reinterpret_cast<float*>(smem + L::kK) + row_in * L::kLd;  // K and V have been used
+    if (!by_rows) {
+      // the odd stream leaves its O to the even one
+      softmax_sync();  // both streams' products are done
+      if (st == 1) {
+        of_odd[row_in] = make_float2(m, l);
+        if (active && any) {
+#pragma unroll 1
+          for (int x = 0; x < kDim; x += 32) {
+            uint32_t o[32];
+            ptx::tmem_ld32(o_at + x, o);
+            tmem_ready(o);
 #pragma unroll
-      for (int x = 0; x < kDim; x += 32) {
-        uint32_t o[32];
-        ptx::tmem_ld32(tmem + lanes + kTmemO + x, o);
-        ptx::tmem_ld_wait();
-        if (row < it.rows) {
+            for (int y = 0; y < 32; y += 4)
+              *reinterpret_cast<uint4*>(odd_o + x + y) = make_uint4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+          }
+        }
+      }
+      softmax_sync();
+      if (st == 0) {
+        const float2 odd = of_odd[row_in];
+        const float up = fmaxf(m, odd.x);
+        scale_o = ptx::ex2(m - up);
+        scale_odd = ptx::ex2(odd.x - up);
+        m = up;
+        l = l * scale_o + odd.y * scale_odd;
+      }
+    }
+    const bool odd_any = !by_rows && tiles_of(1) > 0;
+    const bool writes = active && (by_rows || st == 0);
+    // 32 elements of this thread's row from x on
+    auto row_of = [&](int x, float (&o)[32]) {
+      uint32_t r[32];
+      ptx::tmem_ld32(o_at + x, r);
+      tmem_ready(r);
 #pragma unroll
-          for (int y = 0; y < 32; y += 4)
-            if (x + y < c.head_dim)
-              write_row<__nv_bfloat16>(prm, it, row, (x + y) / 4,
-                                       any ? make_float4(__uint_as_float(o[y]), __uint_as_float(o[y + 1]),
-                                                         __uint_as_float(o[y + 2]), __uint_as_float(o[y + 3]))
-                                           : make_float4(0.f, 0.f, 0.f, 0.f),
-                                       m, l);
+      for (int y = 0; y < 32; ++y) o[y] = any ? __uint_as_float(r[y]) * scale_o : 0.f;
+      if (odd_any) {
+#pragma unroll
+        for (int y = 0; y < 32; ++y) o[y] = fmaf(odd_o[x + y], scale_odd, o[y]);
+      }
+    };
+    if (prm.parts == 1) {
+      if (writes) {
+#pragma unroll 1
+        for (int x = 0; x < kDim; x += 32) {
+          float o[32];
+          row_of(x, o);
+          if (row < it.rows) {
+#pragma unroll
+            for (int y = 0; y < 32; y += 4)
+              if (x + y < c.head_dim)
+                write_row<__nv_bfloat16>(prm, it, row, (x + y) / 4, make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]),
+                                         m, l);
+          }
         }
       }
       ptx::tc_fence_before();
-    }
-  } else {
-    // Every block's tiles are free: each sends the others their slices of O.
-    auto* inbox = reinterpret_cast<Inbox<kRows, kDim>*>(smem);
-    __syncwarp();
-    ptx::cluster_sync();
-    const int slice = div(prm.by_parts, it.rows * vecs + prm.parts - 1);
-    if (active) {
-      if (row < it.rows)
+      __syncthreads();
+    } else {
+      // O leaves Tensor Memory before every block's tiles are free for what the others send.
+      auto* inbox = reinterpret_cast<Inbox<kRows, kDim>*>(smem);
+      float o[kDim / 32][32];
+      if (writes) {
+#pragma unroll
+        for (int x = 0; x < kDim / 32; ++x) row_of(32 * x, o[x]);
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      ptx::cluster_sync();
+      const int slice = div(prm.by_parts, it.rows * vecs + prm.parts - 1);
+      if (writes && row < it.rows) {
         for (int b = 0; b < prm.parts; ++b)
           ptx::st_cluster_v2(ptx::mapa_shared(ptx::smem_addr(&inbox->ml[it.part][row]), b), m, l);
-      int i = row * vecs, to = i / slice;
+        int i = row * vecs, to_block = i / slice;
 #pragma unroll
-      for (int x = 0; x < kDim; x += 32) {
-        uint32_t o[32];
-        ptx::tmem_ld32(tmem + lanes + kTmemO + x, o);
-        ptx::tmem_ld_wait();
-#pragma unroll
-        for (int y = 0; y < 32; y += 4) {
-          if (row >= it.rows || x + y >= c.head_dim) continue;
-          if (i >= (to + 1) * slice) ++to;
+        for (int x = 0; x < kDim; x += 4) {
+          if (x >= c.head_dim) continue;
+          if (i >= (to_block + 1) * slice) ++to_block;
           ptx::st_cluster_v4(
-              ptx::mapa_shared(ptx::smem_addr(&inbox->o[it.part * slice + i - to * slice]), to),
-              any ? make_float4(__uint_as_float(o[y]), __uint_as_float(o[y + 1]), __uint_as_float(o[y + 2]),
-                                __uint_as_float(o[y + 3]))
-                  : make_float4(0.f, 0.f, 0.f, 0.f));
+              ptx::mapa_shared(ptx::smem_addr(&inbox->o[it.part * slice + i - to_block * slice]), to_block),
+              make_float4(o[x / 32][x % 32], o[x / 32][x % 32 + 1], o[x / 32][x % 32 + 2], o[x / 32][x % 32 + 3]));
           ++i;
         }
       }
-      ptx::tc_fence_before();
+      __syncwarp();
+      ptx::cluster_sync();
+      __syncthreads();
+      join_slices<kRows, kDim, 32 * kSoftmaxWarps, __nv_bfloat16>(prm, it, inbox);
     }
-    __syncwarp();
-    ptx::cluster_sync();
-  }
-  __syncthreads();
-  if (prm.parts > 1)
-    join_slices<kRows, kDim, 32 * kSoftmaxWarps, __nv_bfloat16>(prm, it, reinterpret_cast<Inbox<kRows, kDim>*>(smem));
   } else if (warp >= kMmaWarp) {
     fewer_registers<kMmaRegs>();
     // ------------------------------------------------------------ products --
-    if (warp == kMmaWarp) {
-      asm volatile("bar.sync 2, %0;" ::"n"(32 * kSoftmaxWarps + 32) : "memory");  // the queries
+    if (warp < kMmaWarp + 2) {
+      const int st = warp - kMmaWarp, my_tiles = tiles_of(st);
+      asm volatile("bar.sync 2, %0;" ::"n"(32 * kSoftmaxWarps + 64) : "memory");  // the queries
       const bool issues = elect_one();
-      const uint32_t qk = idesc_f16(kRows, kKeys, false), pv = idesc_f16(kRows, c.head_dim, true);
+      const uint32_t qk = idesc_f16(kTileRows, kKeys, false), pv = idesc_f16(kTileRows, c.head_dim, true);
       // operands: an offset in bytes is added to the address field, in units of 16
-      const uint64_t q_desc = ptx::sdesc_k128(ptx::smem_addr(qs)), k_desc = ptx::sdesc_k128(ptx::smem_addr(k_tile));
-      const uint64_t v_desc = ptx::sdesc_mn128(ptx::smem_addr(v_tile), L::kHalf);
-      for (int i = 0; i < n; ++i) {
-        // K is there; the weights of tile i - 1 have been used
-        if (!warp_wait(bars.k_full, i & 1) || (i > 0 && !warp_wait(bars.pv_done, (i - 1) & 1))) break;
+      const uint64_t q_desc = ptx::sdesc_k128(ptx::smem_addr(smem) + (by_rows ? st * L::kTile : 0));
+      const uint64_t k_desc = ptx::sdesc_k128(ptx::smem_addr(smem) + L::kK);
+      const uint64_t v_desc = ptx::sdesc_mn128(ptx::smem_addr(smem) + L::kV, L::kHalf);
+      const uint32_t s_at = tmem + kKeys * st, o_at = tmem + kTmemO + 128 * st;
+      for (int t = 0; t < my_tiles; ++t) {
+        const int j = tile_of(st, t), slot = j & 1;
+        // K is there; the weights of the tile before have been used
+        if (!warp_wait(bars.k_full[slot], j >> 1) || (t > 0 && !warp_wait(bars.pv_done[st], t - 1))) break;
+        // K was written by plain stores; the fence is here, and not in the copying warps, where
+        // it would wait for their loads of the next tiles
+        ptx::fence_proxy_async_smem();
         ptx::tc_fence_after();
         if (issues) {
 #pragma unroll
           for (int d = 0; d < kDim / 16; ++d) {
             const uint32_t off = (d / 4 * L::kHalf + d % 4 * 32) >> 4;
-            if (d < row_vecs) ptx::mma_bf16(tmem, q_desc + off, k_desc + off, qk, d > 0);
+            if (d < row_vecs)
+              ptx::mma_bf16(s_at, q_desc + off, k_desc + off + (uint32_t)(slot * L::kTile >> 4), qk, d > 0);
           }
-          ptx::mma_commit(ptx::smem_addr(&bars.s_full));
+          ptx::mma_commit(ptx::smem_addr(&bars.s_full[st]));
+          ptx::mma_commit(ptx::smem_addr(&bars.k_free[slot]));
         }
-        if (!warp_wait(bars.v_full, i & 1) || !warp_wait(bars.p_full, i & 1)) break;
+        if (!warp_wait(bars.v_full[slot], j >> 1) || !warp_wait(bars.p_full[st], t)) break;
+        ptx::fence_proxy_async_smem();
         ptx::tc_fence_after();
         if (issues) {
 #pragma unroll
           for (int k = 0; k < kKeys / 16; ++k)
-            mma_ta(tmem + kTmemO, tmem + 8 * k, v_desc + (k * 2048 >> 4), pv, i > 0 || k > 0);
-          ptx::mma_commit(ptx::smem_addr(&bars.pv_done));
+            mma_ta(o_at, s_at + 8 * k, v_desc + (uint32_t)((slot * L::kTile + k * 2048) >> 4), pv, t > 0 || k > 0);
+          ptx::mma_commit(ptx::smem_addr(&bars.pv_done[st]));
+          ptx::mma_commit(ptx::smem_addr(&bars.v_free[slot]));
         }
       }
       __syncwarp();
       if (issues && *abort_flag) {  // leave no product in flight
-        ptx::mma_commit(ptx::smem_addr(&bars.drained));
-        drain_wait(ptx::smem_addr(&bars.drained), 0);
+        ptx::mma_commit(ptx::smem_addr(&bars.drained[st]));
+        drain_wait(ptx::smem_addr(&bars.drained[st]), 0);
       }
       __syncwarp();
     }
@@ -543,118 +615,125 @@ __global__ void __launch_bounds__(kThreads, 2) tc_e4m3_kernel(const __grid_const
   } else {
     fewer_registers<kCopyRegs>();
     // -------------------------------------------------------------- copies --
-    // Keys 16 w .. + 15 of a tile are this warp's. One load takes 16 codes a lane, of
-    // kPer keys a warp; they become two 16-byte chunks of the key's row.
-    constexpr int kMine = kKeys / kCopyWarps, kShare = kGroup / kMine;  // warps of a group
-    constexpr int kVecs = kDim / 16, kPer = 32 / kVecs, kLoads = kMine / kPer;
-    const int w = warp - kSoftmaxWarps, vec = lane % kVecs, sub = lane / kVecs;
-    const bool held = vec < row_vecs;
+    // Keys 32 w .. + 31 of a tile, which may share a page, are this warp's. A load takes 16
+    // codes a lane: 8 keys, and 64 bytes of each; they become two 16-byte chunks of a key's
+    // row, and the 8 lanes of a store have 8 keys' rows, whose swizzles differ.
+    constexpr int kLoads = 4 * kDim / 64;
+    const int w = warp - kSoftmaxWarps, vec = lane / 8, sub = lane % 8;
+    // Lookups are loads without a condition, of the nearest key that a row sees, so that
+    // nothing waits for them a tile ahead of their use.
+    const int32_t* table = a.table + (int64_t)it.b * c.max_pages;
+    const float *ks_head = a.k_scale + it.kh, *vs_head = a.v_scale + it.kh;
+    struct Ahead {
+      int key, page, off;  // of this lane's key: clamped; its page; its place there
+    };
     auto look_up = [&](int i) {
-      Slot s = {-1, -1};
-      if (kUniform) {  // the keys of the group
-        if (i < n) s = slot_of(prm, it, seen, tile_key(i) + kGroup * (w / kShare) + lane);
-      } else if (i < n && lane < kMine) {
-        s = slot_of(prm, it, seen, tile_key(i) + kMine * w + lane);
+      Ahead h = {0, 0, 0};
+      if (n > 0) {
+        const int key = key0 + i * kKeys + kGroup * w + lane;
+        h.key = clamp_int(key, seen.lo_min, seen.hi_max);
+        const int nth = div(prm.by_page, h.key);
+        h.off = key - nth * c.page_size;
+        if (h.key != key) h.key = -1;
+        h.page = __ldg(table + nth);
       }
-      return s;
+      return h;
     };
     // Of this lane's key; where a group has one page, of the group's first key, whether a
     // row sees it or not.
     struct Place {
-      int64_t at;    // -1: none
+      int64_t at;    // -1 (INT64_MIN): none
       float ks, vs;  // its page's scales
       int from;      // the lane that has them
+      bool in;       // the key is seen, its page in the cache
     };
-    auto place = [&](const Slot& s) {
-      s.check(prm);
-      Place p = {-1, 1.f, 1.f, 0};
-      if (s.in(c)) {
-        p.at = s.at(c, it.kh);
-        p.ks = __ldg(a.k_scale + s.scale_at(c, it.kh));
-        p.vs = __ldg(a.v_scale + s.scale_at(c, it.kh));
+    auto place = [&](const Ahead& h) {
+      const bool known = (unsigned)h.page < (unsigned)c.n_pages;
+      if (prm.check_in_use && h.key >= 0 && !known) set_status(a.status, status_check());
+      Place p;
+      p.in = known && h.key >= 0;
+      p.from = lane;
+      p.ks = p.vs = 1.f;
+      const int64_t id = known ? h.page : 0;
+      if (c.n_pages > 0) {
+        p.ks = __ldg(ks_head + id * c.n_kv_heads);
+        p.vs = __ldg(vs_head + id * c.n_kv_heads);
       }
+      p.at = id * c.page_stride + (int64_t)(kUniform ? h.off - lane : h.off) * c.token_stride;
       if (kUniform) {
-        p.at -= lane * c.token_stride;
-        const unsigned with = __ballot_sync(0xffffffffu, s.in(c));
+        const unsigned with = __ballot_sync(0xffffffffu, p.in);
         p.from = with ? __ffs(with) - 1 : 0;
         p.at = __shfl_sync(0xffffffffu, p.at, p.from);
         if (!with) p.at = INT64_MIN;
+      } else if (!p.in) {
+        p.at = -1;
       }
       return p;
     };
-    const int64_t sub_at = (int64_t)(w % kShare * kMine + sub) * c.token_stride + 16 * vec, step = (int64_t)kPer * c.token_stride;
+    k_cache += (int64_t)it.kh * c.head_stride;
+    v_cache += (int64_t)it.kh * c.head_stride;
+    const int64_t sub_at = (int64_t)sub * c.token_stride + 16 * vec, step = 8 * c.token_stride;
     uint4 rk[kLoads], rv[kLoads];
-    // Codes of tile i, whose place is p.
-    auto fetch = [&](const uint8_t* cache, int i, const Place& p, uint4 (&r)[kLoads]) {
-      const int key = tile_key(i) + kMine * w + sub;
-      const uint8_t* at = cache + p.at + sub_at;
+    // Load x is of keys x % 4 * 8 + sub of the group and of their 64 bytes x / 4.
+    auto fetch = [&](int i, const Place& p) {
+      const int key = key0 + i * kKeys + kGroup * w + sub;
+      // keys lo .. hi of the group are seen, from this lane's first on
+      const int lo = kUniform && p.at == INT64_MIN ? kGroup : seen.lo_min - key, hi = seen.hi_max - key;
+      const uint8_t *k_at = k_cache + p.at + sub_at, *v_at = v_cache + p.at + sub_at;
 #pragma unroll
       for (int x = 0; x < kLoads; ++x) {
-        r[x] = make_uint4(0u, 0u, 0u, 0u);
+        const bool held = 4 * (x / 4) + vec < row_vecs;
         if (kUniform) {
-          const int k = key + x * kPer;
-          if (held && p.at != INT64_MIN && k >= seen.lo_min && k <= seen.hi_max)
-            r[x] = __ldg(reinterpret_cast<const uint4*>(at + x * step));
+          const bool there = held && x % 4 * 8 >= lo && x % 4 * 8 <= hi;
+          rk[x] = ld_once(k_at + x / 4 * 64, there);
+          rv[x] = ld_once(v_at + x / 4 * 64, there);
+          k_at += x % 4 == 3 ? -3 * step : step;
+          v_at += x % 4 == 3 ? -3 * step : step;
         } else {
-          const int64_t o = __shfl_sync(0xffffffffu, p.at, x * kPer + sub);
-          if (o >= 0 && held) r[x] = __ldg(reinterpret_cast<const uint4*>(cache + o) + vec);
+          const int64_t o = __shfl_sync(0xffffffffu, p.at, x % 4 * 8 + sub);
+          rk[x] = ld_once(k_cache + o + x / 4 * 64 + 16 * vec, o >= 0 && held);
+          rv[x] = ld_once(v_cache + o + x / 4 * 64 + 16 * vec, o >= 0 && held);
         }
       }
     };
-    // The two chunks in an order that keeps the eight lanes of a store apart.
     auto widen = [&](uint8_t* tile, const uint4 (&r)[kLoads]) {
-      const int half = vec / 4, c0 = 2 * (vec % 4);
 #pragma unroll
       for (int x = 0; x < kLoads; ++x) {
-        const int key = kMine * w + x * kPer + sub;
-        uint8_t* at = tile + half * L::kHalf + key * 128;
+        uint8_t* at = tile + (kGroup * w + sub) * 128 + x / 4 * L::kHalf + x % 4 * 8 * 128;
         uint4 lo, hi;
         lo.x = codes_f16(r[x].x), lo.y = codes_f16(r[x].x >> 16);
         lo.z = codes_f16(r[x].y), lo.w = codes_f16(r[x].y >> 16);
         hi.x = codes_f16(r[x].z), hi.y = codes_f16(r[x].z >> 16);
         hi.z = codes_f16(r[x].w), hi.w = codes_f16(r[x].w >> 16);
-        if (!held) continue;
-        const bool swap = half;
-        *reinterpret_cast<uint4*>(at + (((c0 + swap) ^ (key & 7)) << 4)) = swap ? hi : lo;
-        *reinterpret_cast<uint4*>(at + (((c0 + !swap) ^ (key & 7)) << 4)) = swap ? lo : hi;
+        *reinterpret_cast<uint4*>(at + ((2 * vec ^ sub) << 4)) = lo;
+        *reinterpret_cast<uint4*>(at + (((2 * vec + 1) ^ sub) << 4)) = hi;
       }
     };
-    // K of tile i, with its scales: into the slot that tile i - 1's scores have left.
-    auto put_k = [&](int i, const Place& p) {
-      widen(k_tile, rk);
-      float* fk = scales + (i & 1) * 4 * kKeys;
-      if (kUniform ? lane == p.from && w % kShare == 0 : lane < kMine) {
-        const int k = kUniform ? w / kShare : kMine * w + lane;
-        fk[k] = p.ks;
-        fk[kKeys + k] = p.vs;
-        fk[2 * kKeys + k] = log2f(p.vs);
-        if (kUniform) fk[3 * kKeys + k] = __fdiv_rn(1.f, p.vs);
-      }
-      ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(ptx::smem_addr(&bars.k_full));
-    };
-    Place next = place(look_up(0));  // of the tile after the one at work
-    Slot after_next = look_up(1);
-    if (n > 0) {
-      fetch(k_cache, 0, next, rk);
-      fetch(v_cache, 0, next, rv);
-      put_k(0, next);
-      next = place(after_next);
-      after_next = look_up(2);
-      fetch(k_cache, 1, next, rk);
-    }
+    Place now = place(look_up(0));
+    Ahead ahead = look_up(1);
+    if (n > 0) fetch(0, now);
     for (int i = 0; i < n; ++i) {
-      if (i > 0 && !warp_wait(bars.pv_done, (i - 1) & 1)) break;  // V's slot is free
-      widen(v_tile, rv);
-      ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(ptx::smem_addr(&bars.v_full));
+      const int slot = i & 1;
+      // the scores and the values of tile i - 2 have been taken
+      if (i > 1 && (!warp_wait(bars.k_free[slot], (i >> 1) - 1) || !warp_wait(bars.v_free[slot], (i >> 1) - 1)))
+        break;
+      widen(smem + L::kK + slot * L::kTile, rk);
+      float* fk = scales + (i & 3) * 4 * kKeys;
+      if (!kUniform || lane == now.from) {
+        const int k = kUniform ? w : kGroup * w + lane;
+        const float ks = now.in ? now.ks : 1.f, vs = now.in ? now.vs : 1.f;
+        fk[k] = ks;
+        fk[kKeys + k] = vs;
+        fk[2 * kKeys + k] = __log2f(vs);
+        if (kUniform) fk[3 * kKeys + k] = __frcp_rn(vs);
+      }
+      ptx::mbar_arrive(ptx::smem_addr(&bars.k_full[slot]));
+      widen(smem + L::kV + slot * L::kTile, rv);
+      ptx::mbar_arrive(ptx::smem_addr(&bars.v_full[slot]));
       if (i + 1 == n) break;
-      fetch(v_cache, i + 1, next, rv);
-      if (!warp_wait(bars.s_full, i & 1)) break;  // K's slot is free
-      put_k(i + 1, next);
-      next = place(after_next);
-      after_next = look_up(i + 3);
-      fetch(k_cache, i + 2, next, rk);
+      now = place(ahead);
+      fetch(i + 1, now);
+      ahead = look_up(i + 2);
     }
     __syncwarp();
     if (prm.parts > 1) {
