@@ -33,12 +33,19 @@ struct PlanHead {
   int n_copies;
   int pad[63];
 };
+// What the update keeps of a sequence between its steps: in shared memory for the
+// first kRowsHeld of a block's, in the workspace for others.
+struct RowPlan {
+  int kept, need;   // tokens
+  int last;         // the page of token kept - 1, if the sequence writes behind it, else -1
+  int want;         // pages it wants, times 2, and 1 with a copy on write
+  long long before; // pages that the block's earlier sequences want
+};
 // What lies in the workspace behind the status word's 256 bytes.
 struct Scratch {
   PlanHead* head;
   PageCopy* copies;  // at most a page a sequence, or half of the pool
-  long long* before; // [n_seqs] pages that earlier sequences of its block want
-  int* want;         // [n_seqs] pages a sequence wants, times 2, and 1 with a copy on write
+  RowPlan* rows;     // [n_seqs]
   int* free;         // [n_pages] free pages, or those below the number in use
   int* high;         // [n_pages] by rank, pages in use at that number or above
   size_t bytes;
@@ -55,37 +62,42 @@ Scratch scratch_of(const moe_attn_config& c, void* base) {
   Scratch s;
   s.head = carve<PlanHead>(at, 1);
   s.copies = carve<PageCopy>(at, seqs > pages / 2 + 1 ? seqs : pages / 2 + 1);
-  s.before = carve<long long>(at, seqs);
-  s.want = carve<int>(at, seqs);
+  s.rows = carve<RowPlan>(at, seqs);
   s.free = carve<int>(at, pages);
   s.high = carve<int>(at, pages);
   s.bytes = (size_t)(at - static_cast<char*>(base));
   return s;
 }
 
+static_assert(kWarps == 32, "a block's warps are a warp's lanes");
 // ---- sums over a block and over the cluster ------------------------------------
 struct Shared {
-  long long warp[kWarps];
+  long long warp[kWarps], also[kWarps];
   long long inbox[2][kMaxParts];
 };
-// The sum of v over the block's threads before this one; total: over all of them.
-__device__ __forceinline__ long long block_scan(Shared& sh, long long v, long long& total) {
+// The sum of v over the block's threads before this one; total, also_total: of v and of
+// `also` over all of them.
+__device__ __forceinline__ long long block_scan(Shared& sh, long long v, long long& total, long long also,
+                                                long long& also_total) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   long long upto = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long w = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += w;
+    also += __shfl_xor_sync(0xffffffffu, also, o);
   }
-  if (lane == 31) sh.warp[warp] = upto;
+  if (lane == 31) sh.warp[warp] = upto, sh.also[warp] = also;
   __syncthreads();
-  long long s = lane < kWarps ? sh.warp[lane] : 0;
+  long long s = sh.warp[lane], t = sh.also[lane];  // as many warps as lanes
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long w = __shfl_up_sync(0xffffffffu, s, o);
     if (lane >= o) s += w;
+    t += __shfl_xor_sync(0xffffffffu, t, o);
   }
   total = __shfl_sync(0xffffffffu, s, 31);
+  also_total = t;
   const long long before = warp > 0 ? __shfl_sync(0xffffffffu, s, warp - 1) : 0;
   __syncthreads();
   return before + upto - v;
@@ -139,22 +151,40 @@ __device__ __forceinline__ int pages_of(const PagesArgs& a, int tokens) {
   return (tokens + a.c.page_size - 1) / a.c.page_size;
 }
 
+constexpr int kRowsHeld = 1024;
+
 __global__ void __launch_bounds__(kThreads, 1)
     pages_update_kernel(const __grid_constant__ PagesArgs a, const Scratch ws, int parts) {
   __shared__ Shared sh;
+  __shared__ RowPlan held[kRowsHeld];
   const moe_attn_config& c = a.c;
-  const int part = blockIdx.x, lane = threadIdx.x % 32;
+  const int part = blockIdx.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int thread = part * kThreads + threadIdx.x, threads = parts * kThreads;
-  const int warp = thread / 32, warps = threads / 32;
   auto valid = [&](int page) { return page >= 0 && page < c.n_pages; };
+  // This block's sequences, and its share of the pool.
+  const int rows = (c.n_seqs + parts - 1) / parts, row0 = min(part * rows, c.n_seqs);
+  const int row1 = min(row0 + rows, c.n_seqs);
+  const int share = ((c.n_pages + parts - 1) / parts + 3) / 4 * 4;
+  const int page0 = (int)min((long long)part * share, (long long)c.n_pages);
+  const int page1 = min(page0 + share, c.n_pages);
+  auto plan = [&](int b) { return b - row0 < kRowsHeld ? held + (b - row0) : ws.rows + b; };
   pdl_wait();
   pdl_trigger();
 
-  // Counts as they are.
+  // Counts as they are; meanwhile what the first sequence of each warp becomes, and its pages.
   if (thread == 0) {
     *a.status = MOE_OK;
     ws.head->n_copies = 0;
   }
+  Wish w = {-1, 0, 0, 0, true};
+  int page_kept = -1, page_held = -1;
+  auto look = [&](int b) {
+    w = wish_of(a, b);
+    const int kept = pages_of(a, w.kept), from = w.parent == b ? kept : 0;
+    if (lane < kept) page_kept = a.table[(int64_t)w.parent * c.max_pages + lane];
+    if (from + lane < pages_of(a, w.len)) page_held = a.table[(int64_t)b * c.max_pages + from + lane];
+  };
+  if (row0 + warp < row1) look(row0 + warp);
   if (a.refs_out != a.refs) {
     const int vecs = c.n_pages / 4;
 #pragma unroll 4
@@ -166,25 +196,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Pages given up and gained.
   bool bad = false;
-  for (int b = warp; b < c.n_seqs; b += warps) {
-    const Wish w = wish_of(a, b);
+  for (int b = row0 + warp; b < row1; b += kWarps) {
+    if (b != row0 + warp) look(b);
     bad |= !w.ok;
-    const int kept = pages_of(a, w.kept);
+    const int kept = pages_of(a, w.kept), len = pages_of(a, w.len);
     const int32_t* old = a.table + (int64_t)b * c.max_pages;
     const int32_t* from = a.table + (int64_t)max(w.parent, 0) * c.max_pages;
     int32_t* to = a.table_out + (int64_t)b * c.max_pages;
-    const bool same = w.parent == b;
+    const bool same = w.parent == b, writes = w.need > w.kept && w.kept % c.page_size != 0;
     for (int i = lane; i < kept; i += 32) {
-      const int page = from[i];
+      const int page = i == lane ? page_kept : from[i];
       if (!valid(page))
         bad = true;
       else if (!same)
         atomicAdd(a.refs_out + page, 1);
       if (to != from) to[i] = page;
+      if (i == kept - 1) plan(b)->last = writes && valid(page) ? page : -1;
     }
-    const int held = pages_of(a, w.len);
-    for (int i = (same ? kept : 0) + lane; i < held; i += 32) {
-      const int page = old[i];
+    if (lane == 0) {
+      if (kept == 0) plan(b)->last = -1;
+      plan(b)->kept = w.kept;
+      plan(b)->need = w.need;
+    }
+    const int first = same ? kept : 0;
+    for (int i = first + lane; i < len; i += 32) {
+      const int page = i == first + lane ? page_held : old[i];
       if (valid(page))
         atomicSub(a.refs_out + page, 1);
       else
@@ -193,43 +229,40 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   ptx::cluster_sync();
 
-  // Pages that each sequence of this block's share wants, and free ones of its share
-  // of the pool.
-  const int rows = (c.n_seqs + parts - 1) / parts, row0 = min(part * rows, c.n_seqs);
-  const int row1 = min(row0 + rows, c.n_seqs);
-  long long wanted = 0;
-  for (int b0 = row0; b0 < row1; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
+  // Free pages of this block's share (the first four of each thread stay in registers), and
+  // pages that each of its sequences wants.
+  const int mine = page0 + 4 * (int)threadIdx.x;
+  const int4 none = make_int4(1, 1, 1, 1), n0 = mine < page1 ? counts_at(a.refs_out, mine, page1) : none;
+  auto free_of = [](const int4& n) { return (n.x == 0) + (n.y == 0) + (n.z == 0) + (n.w == 0); };
+  auto below = [](const int4& n) { return n.x < 0 || n.y < 0 || n.z < 0 || n.w < 0; };
+  long long count = 0, wanted = 0, free_here = 0;
+  for (int b0 = row0; b0 < row1 || b0 == row0; b0 += kThreads) {
+    const int b = b0 + (int)threadIdx.x;
     int want = 0;
     bool copied = false;
     if (b < row1) {
-      const Wish w = wish_of(a, b);
-      const int kept = pages_of(a, w.kept);
-      if (w.need > w.kept && w.kept % c.page_size != 0) {
-        const int page = a.table[(int64_t)w.parent * c.max_pages + kept - 1];
-        copied = valid(page) && __ldcg(a.refs_out + page) > 1;
-      }
-      want = pages_of(a, w.need) - kept + copied;
+      const RowPlan* p = plan(b);
+      copied = p->last >= 0 && __ldcg(a.refs_out + p->last) > 1;
+      want = pages_of(a, p->need) - pages_of(a, p->kept) + copied;
     }
-    long long total;
-    const long long before = block_scan(sh, want, total);
+    if (b0 == row0) {
+      count = free_of(n0);
+      bad |= below(n0);
+      for (int i = mine + 4 * kThreads; i < page1; i += 4 * kThreads) {
+        const int4 n = counts_at(a.refs_out, i, page1);
+        count += free_of(n);
+        bad |= below(n);
+      }
+    }
+    long long total, counted;
+    const long long before = block_scan(sh, want, total, b0 == row0 ? count : 0, counted);
     if (b < row1) {
-      ws.before[b] = wanted + before;
-      ws.want[b] = 2 * want + copied;
+      plan(b)->before = wanted + before;
+      plan(b)->want = 2 * want + copied;
     }
     wanted += total;
+    free_here += counted;
   }
-  const int share = ((c.n_pages + parts - 1) / parts + 3) / 4 * 4;
-  const int page0 = (int)min((long long)part * share, (long long)c.n_pages);
-  const int page1 = min(page0 + share, c.n_pages);
-  int count = 0;
-  for (int i = page0 + 4 * (int)threadIdx.x; i < page1; i += 4 * kThreads) {
-    const int4 n = counts_at(a.refs_out, i, page1);
-    count += (n.x == 0) + (n.y == 0) + (n.z == 0) + (n.w == 0);
-    bad |= n.x < 0 || n.y < 0 || n.z < 0 || n.w < 0;
-  }
-  long long free_here;
-  block_scan(sh, count, free_here);
   exchange(sh, part, parts, wanted, free_here);
   const long long free_all = sum_before(sh, 1, parts);
   const long long listed = min(sum_before(sh, 0, parts), free_all);
@@ -238,9 +271,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   long long rank = sum_before(sh, 1, part);
   for (int i0 = page0; i0 < page1 && rank < listed; i0 += 4 * kThreads) {
     const int i = i0 + 4 * (int)threadIdx.x;
-    const int4 n = i < page1 ? counts_at(a.refs_out, i, page1) : make_int4(1, 1, 1, 1);
-    long long total;
-    long long at = rank + block_scan(sh, (n.x == 0) + (n.y == 0) + (n.z == 0) + (n.w == 0), total);
+    const int4 n = i0 == page0 ? n0 : i < page1 ? counts_at(a.refs_out, i, page1) : none;
+    long long total, unused;
+    long long at = rank + block_scan(sh, free_of(n), total, 0, unused);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (get(n, k) == 0) {
@@ -252,22 +285,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::cluster_sync();
 
   // Who gets which.
-  for (int b = warp; b < c.n_seqs; b += warps) {
-    const Wish w = wish_of(a, b);
-    const int info = __ldcg(ws.want + b), want = info / 2, copied = info & 1;
-    const long long at = sum_before(sh, 0, b / rows) + __ldcg(ws.before + b);
+  const long long base = sum_before(sh, 0, part);
+  for (int b = row0 + warp; b < row1; b += kWarps) {
+    const RowPlan p = *plan(b);
+    const int want = p.want / 2, copied = p.want & 1;
+    const long long at = base + p.before;
     const bool served = at + want <= free_all;
-    __syncwarp();  // granted may be kept or need
-    if (lane == 0) a.granted[b] = served ? w.need : w.kept;
+    if (lane == 0) a.granted[b] = served ? p.need : p.kept;
     if (!served) continue;
-    const int first = pages_of(a, w.kept) - copied;
-    int32_t* to = a.table_out + (int64_t)b * c.max_pages + first;
+    int32_t* to = a.table_out + (int64_t)b * c.max_pages + pages_of(a, p.kept) - copied;
     if (copied && lane == 0) {
-      const int src = a.table[(int64_t)w.parent * c.max_pages + first];
-      atomicSub(a.refs_out + src, 1);
-      ws.copies[atomicAdd(&ws.head->n_copies, 1)] = {src, __ldcg(ws.free + at), w.kept % c.page_size, 0};
+      atomicSub(a.refs_out + p.last, 1);
+      ws.copies[atomicAdd(&ws.head->n_copies, 1)] = {p.last, __ldcg(ws.free + at), p.kept % c.page_size, 0};
     }
-    __syncwarp();  // in place: the old page has been read
     for (int i = lane; i < want; i += 32) {
       const int page = __ldcg(ws.free + at + i);
       to[i] = page;
@@ -302,8 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     count += n > 0;
     bad |= n < 0;
   }
-  long long live_here;
-  block_scan(sh, count, live_here);
+  long long live_here, unused;
+  block_scan(sh, count, live_here, 0, unused);
   exchange(sh, part, parts, live_here, 0);
   const int live = (int)sum_before(sh, 0, parts);
 
@@ -313,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i = i0 + threadIdx.x;
     const int n = i < page1 ? max(a.refs[i], 0) : 0;
     long long total;
-    const int before = rank + (int)block_scan(sh, n > 0, total);
+    const int before = rank + (int)block_scan(sh, n > 0, total, 0, unused);
     if (i < page1) {
       if (i == live) ws.head->n_copies = live - before;  // the holes below
       const bool stays = n > 0 && i < live;
