@@ -102,13 +102,13 @@ struct alignas(16) Part {
   int at;
 };
 
-// A vector that lies partly in the row: its elements of the row, 0 elsewhere.
+// A vector that lies partly in the row: its elements of the row, NaN elsewhere.
 template <typename In>
 __device__ __noinline__ uint4 load_edge(const In* row, int e, int V) {
   constexpr int kE = 16 / (int)sizeof(In);
   In x[kE];
 #pragma unroll
-  for (int i = 0; i < kE; ++i) x[i] = e + i >= 0 && e + i < V ? row[e + i] : from_f32<In>(0.f);
+  for (int i = 0; i < kE; ++i) x[i] = e + i >= 0 && e + i < V ? row[e + i] : from_f32<In>(NAN);
   return *reinterpret_cast<const uint4*>(x);
 }
 template <typename Out>
@@ -176,7 +176,8 @@ __global__ void __launch_bounds__(kThreads, kHeld > 16 ? 2 : 4)
     const uint4* from = reinterpret_cast<const uint4*>(x_row + e0);
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
-      raw[k] = make_uint4(0u, 0u, 0u, 0u);
+      // outside the row NaN, which counts as -inf
+      raw[k] = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
       if (k * kThreads + t0 < n && whole(e0 + k * kStep)) raw[k] = from[k * kThreads];
     }
     if (edges) {
@@ -336,28 +337,21 @@ __global__ void __launch_bounds__(kThreads, kHeld > 16 ? 2 : 4)
       }
     }
 #pragma unroll
-    for (int k = 0; k < kV; ++k) {
-      const bool in = k * kThreads + t0 < n;
+    for (int k = 0; k < kV; ++k)
 #pragma unroll
-      for (int i = 0; i < kE; ++i) x[k][i] = in ? fmaxf(x[k][i], -INFINITY) : -INFINITY;  // a NaN too
-    }
-    if (edges) {
-#pragma unroll
-      for (int k = 0; k < kV; ++k)
-#pragma unroll
-        for (int i = 0; i < kE; ++i) {
-          const int e = e0 + k * kStep + i;
-          if (e < 0 || e >= V) x[k][i] = -INFINITY;
-        }
-    }
+      for (int i = 0; i < kE; ++i) x[k][i] = fmaxf(x[k][i], -INFINITY);  // a NaN too
   };
   // Writes x times f.
   auto write = [&](int v0, float f) {
     const int n = count_of(v0), e0 = first_of(v0);
+    const uint64_t by = ptx::f32x2(f, f), minus_zero = ptx::f32x2(-0.f, -0.f);
 #pragma unroll
     for (int k = 0; k < kV; ++k)
 #pragma unroll
-      for (int i = 0; i < kE; ++i) x[k][i] *= f;
+      for (int i = 0; i < kE; i += 2) {
+        const uint64_t y = ptx::fma_f32x2(ptx::f32x2(x[k][i], x[k][i + 1]), by, minus_zero);
+        x[k][i] = ptx::f32x2_lo(y), x[k][i + 1] = ptx::f32x2_hi(y);
+      }
 #pragma unroll
     for (int k = 0; k < kV; ++k)
       if (k * kThreads + t0 < n && out_grid && whole(e0 + k * kStep)) store(p_row + e0 + k * kStep, x[k]);
