@@ -769,8 +769,9 @@ MOE_API int moe_verify_drafts(const moe_verify_config* cfg, const void* p, const
  *  history    [device] [n_history] int32, cu_history [device] [B+1]: sequence b's
  *             tokens before the new ones are entries cu_history[b] ..
  *             cu_history[b+1]-1; n_prompt [device] [B], of which the first
- *             n_prompt[b] were not generated. With n_history 0 history is NULL and
- *             the other two are not read.
+ *             n_prompt[b] were not generated. An entry -1 is no token, so the lists
+ *             may have room to grow. With n_history 0 history is NULL and the other two
+ *             are not read.
  *  repetition, presence, frequency  [device] [B] fp32, or NULL: 1, 0, 0.
  *             repetition > 0.
  *  bias_token [device] [n_bias] int32, bias [device] [n_bias] fp32, cu_bias
@@ -785,8 +786,8 @@ MOE_API int moe_verify_drafts(const moe_verify_config* cfg, const void* p, const
  *             1 / temperature (x itself for 0) and no softmax.
  *  ws         [device] moe_logits_workspace_size(cfg) bytes.
  * MOE_ERR_DEVICE_CHECK: cu_new as above; cu_history or cu_bias not ascending from 0
- * to n_history or n_bias; n_prompt outside the history's length; a token or a
- * bias's token outside [0, V) (left out); a list of biases that does not ascend; a
+ * to n_history or n_bias; n_prompt outside the history's length; a token (of the
+ * history: but -1) or a bias's token outside [0, V) (left out); a list of biases that does not ascend; a
  * mask_row outside [-1, n_masks) (taken as -1); repetition <= 0 or temperature < 0
  * or either not finite. Counts are integers and sums run in a fixed order, so
  * equal calls give equal bits.

@@ -70,7 +70,10 @@ __device__ bool bad_lists(const LogitsArgs& a, int t, int n) {
     if (a.mask_row) bad |= a.mask_row[i] < -1 || a.mask_row[i] >= c.n_masks;
   }
 #pragma unroll 4
-  for (int i = t; i < c.n_history; i += n) bad |= (unsigned)__ldg(a.history + i) >= (unsigned)c.vocab;
+  for (int i = t; i < c.n_history; i += n) {
+    const int x = __ldg(a.history + i);
+    bad |= x < -1 || x >= c.vocab;
+  }
   const int per = max(1, n / max(1, c.n_seqs)), sub = t % per;
   for (int b = t / per; b < c.n_seqs && t < n / per * per; b += n / per) {
     bad |= !seq_rows(a.cu_new, b, c.n_seqs, c.n_tokens, c.max_new).ok;

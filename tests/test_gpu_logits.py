@@ -227,6 +227,18 @@ def test_history_counts():
     assert (np.abs(got - p) <= tol).all()
 
 
+def test_empty_places_of_the_history():
+    """Lists with room to grow: entries -1 change nothing."""
+    r = Rows([2, 1], 500, history=30, biases=5, seed=2)
+    want = r.run()
+    grown, cu, at = [], [0], r.cu_history
+    for b in range(2):
+        grown += list(r.history[at[b]:at[b + 1]]) + [-1] * 7
+        cu.append(len(grown))
+    r.history, r.cu_history = np.array(grown), np.array(cu)
+    assert np.array_equal(r.run(), want) and r.status == 0
+
+
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 def test_logits_out(out):
     r = Rows([2, 1], 5003, history=100, biases=30, masks=2, out=out, p_pad=1)
@@ -275,7 +287,7 @@ def test_in_place_on_another_stream_and_captured():
 
 @pytest.mark.parametrize("name,at,value", [
     ("cu", 1, 9), ("cu_history", 1, -1), ("cu_history", 2, 0), ("cu_history", 0, 1), ("n_prompt", 0, -1), ("n_prompt", 0, 1000), ("history", 2, 100),
-    ("history", 0, -1), ("tokens", 1, 100), ("bias_token", 1, 0), ("bias_token", 0, -1), ("bias_token", 3, 100), ("cu_bias", 1, 77), ("mask_row", 0, 2),
+    ("history", 0, -2), ("tokens", 1, 100), ("bias_token", 1, 0), ("bias_token", 0, -1), ("bias_token", 3, 100), ("cu_bias", 1, 77), ("mask_row", 0, 2),
     ("mask_row", 2, -2), ("rep", 0, 0.0), ("rep", 1, math.nan), ("temp", 0, -1.0), ("temp", 0, math.inf), ("pres", 1, math.nan), ("freq", 1, math.inf),
 ])
 def test_bad_lists_are_recorded(name, at, value):
