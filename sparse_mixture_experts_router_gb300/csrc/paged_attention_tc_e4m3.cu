@@ -30,6 +30,8 @@
 // Keys that some rows of the item see and others do not (at most its new tokens at
 // either end) are masked row by row; where one of their values is NaN (0 times NaN is
 // not 0), those keys are left out of the products and added at the end, row by row.
+#include <cfloat>
+
 #include "paged_attention.cuh"
 #include "sm103_wait.cuh"
 
@@ -298,6 +300,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_e4m3_kernel(const __grid_const
     const uint32_t s_at = tmem + lanes + kKeys * st, o_at = tmem + lanes + kTmemO + 128 * st;
     const int pos = it.pos(prm, row), first = it.first(pos);
     float m = -3.0e38f, l = 0.f;
+    // A score's factor with its key's scale: never 0 (a query of zeros, a page of zeros), by
+    // which -inf would be NaN; products are below 2^33, so the least normal number is 0 to them.
+    auto by = [&](float key_scale) { return fmaxf(factor * key_scale, FLT_MIN); };
     bool wide = false;  // scales outside 2^-40 .. 2^40 have come by
     // of the stream's first tile's columns, from .. to - 1 are keys that the row sees
     int from = max(first, seen.lo_min) - key0 - tile_of(st, 0) * kKeys;
@@ -325,14 +330,14 @@ __global__ void __launch_bounds__(kThreads, 1) tc_e4m3_kernel(const __grid_const
             float u[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int x = 0; x < 32; ++x) u[x % 4] = fmaxf(u[x % 4], __uint_as_float(w[g][x]));
-            const float v = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])) * (factor * fk[g]), e = ev[g];
+            const float v = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])) * by(fk[g]), e = ev[g];
             top = fmaxf(top, v);
             top_v = fmaxf(top_v, v + e);
             wide = wide || !(fabsf(e) <= 40.f);
           } else {
 #pragma unroll
             for (int x = 0; x < 32; ++x) {
-              const float u = __uint_as_float(w[g][x]) * (factor * fk[kGroup * g + x]);
+              const float u = __uint_as_float(w[g][x]) * by(fk[kGroup * g + x]);
               top = fmaxf(top, u);
               top_v = fmaxf(top_v, u + ev[kGroup * g + x]);
             }
@@ -360,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_e4m3_kernel(const __grid_const
           uint64_t sum[2] = {0, 0};
           uint32_t p[16];
           if (kUniform && !wide) {
-            const float f1 = factor * fk[g], a1 = ev[g] - m;
+            const float f1 = by(fk[g]), a1 = ev[g] - m;
             const uint64_t f2 = ptx::f32x2(f1, f1), a2 = ptx::f32x2(a1, a1);
 #pragma unroll
             for (int y = 0; y < 16; ++y) {
@@ -375,8 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_e4m3_kernel(const __grid_const
 #pragma unroll
             for (int y = 0; y < 16; ++y) {
               const int k = kUniform ? g : kGroup * g + 2 * y, k1 = kUniform ? g : k + 1;
-              const float lo = ptx::ex2(fmaf(__uint_as_float(w[g][2 * y]), factor * fk[k], -m));
-              const float hi = ptx::ex2(fmaf(__uint_as_float(w[g][2 * y + 1]), factor * fk[k1], -m));
+              const float lo = ptx::ex2(fmaf(__uint_as_float(w[g][2 * y]), by(fk[k]), -m));
+              const float hi = ptx::ex2(fmaf(__uint_as_float(w[g][2 * y + 1]), by(fk[k1]), -m));
               sum[y % 2] = ptx::add_f32x2(sum[y % 2], ptx::f32x2(lo, hi));
               p[y] = pack_f16(lo * fv[k], hi * fv[k1]);
             }

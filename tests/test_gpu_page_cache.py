@@ -74,6 +74,23 @@ def test_scales_at_the_ends_of_their_range():
         assert (np.abs(out - want) <= tol).all()
 
 
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("new", [1, 12, 60])
+def test_queries_and_keys_of_zeros(new, page):
+    """Some rows' queries are 0, and keys too, whose pages have the least scale: every score is 0, and a
+    masked place is masked all the same."""
+    bt = PageBatch(new=[new, new], length=[200, new], heads=4, kv_heads=2, dim=64, page=page)
+    bt.k[bt.used] = 0
+    bt.k_scale[bt.used.any(1)] = 2.0 ** -110
+    bt.q_rows[::2] = 0
+    out, lse = attend(bt)
+    want, want_lse, tol, tol_lse = attention64(bt)
+    assert (np.abs(out - want) <= tol).all()
+    # n terms summed in fp32 are off by up to n 2^-24 of the sum, 2^-16.3 for 200, and so is its
+    # logarithm: attention64 counts those
+    assert (np.abs(lse - want_lse) <= tol_lse).all()
+
+
 def test_unseen_codes_reach_nothing():
     """NaN codes and NaN scales wherever no row looks (the batch's own), and in the last page's
     places behind the length."""
