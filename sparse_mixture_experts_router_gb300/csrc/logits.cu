@@ -12,9 +12,13 @@
 // shared memory. A vocabulary of more than 16 slices goes through its slices'
 // tiles twice, once for maximum and sum and once more to write.
 //
-// Bound by memory for many rows; for one, by the latency of its chain (row,
-// sequence, history, exchange). One cluster more checks the lists meanwhile and
-// writes the status.
+// One row of 32000 takes 6.7 us, the latency of its chain (row, sequence, history, maximum
+// and sum, exchange). 161 rows of 129280 in fp32 with masks, biases and histories of up to
+// 3000 take 75 us, 2.26 TB/s, 0.33 of a copy's rate: a block runs that chain once, 2800
+// instructions a warp that nothing repeats, so that they wait for their fetch as much as for
+// data, and clusters of eight find 225 of 304 slots. Blocks of 128, 512 and 1024 threads took
+// 78 to 89 us, 32 and 48 logits a thread (below) 78 and 123. One cluster more checks the
+// lists meanwhile and writes the status.
 #include <cfloat>
 
 #include "rope_append.cuh"
@@ -527,8 +531,10 @@ cudaError_t launch(const LogitsArgs& a, cudaStream_t s) {
   constexpr int kE = 16 / (int)sizeof(In);
   // of the row that starts latest on its grid
   const int vectors = ceil_div(a.c.vocab + (a.c.logits_stride % kE ? kE - 1 : 0), kE);
-  // 64 logits a thread (two blocks an SM) for the batch; 16 (four blocks) where those
-  // leave the GPU unfilled and 16 blocks hold a row.
+  // 64 logits a thread (two blocks an SM) for the batch: 75 us for 161 rows of 129280, with
+  // 32 (four blocks) 78, with 48 (rows in 16 blocks) 123. 16 (four blocks) where those
+  // leave the GPU unfilled and 16 blocks hold a row: 1, 16 and 64 rows of 32000 take 6.8,
+  // 7.5 and 9.6 us, with 64 logits a thread 7.7, 8.8 and 11.0.
   constexpr int kMany = 64, kFew = 16;
   auto tile = [](int held) { return kThreads * (held / kE); };
   auto blocks = [&](int held) {

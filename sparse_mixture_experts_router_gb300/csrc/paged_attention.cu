@@ -7,7 +7,9 @@
 // way, so a row's keys are split over warps, and over the blocks of a cluster.
 //
 // Here: how a call is cut, and the join of splits. bf16 and E4M3 caches run on
-// the matrix kernel of paged_attention_mma.cuh, fp32 caches on that of
+// the matrix kernel of paged_attention_mma.cuh, above a number of query rows
+// (not E4M3 with a scale a token) on the tcgen05 kernels of
+// paged_attention_tc.cu and paged_attention_tc_e4m3.cu; fp32 caches on that of
 // paged_attention_f32.cu.
 #include <algorithm>
 
@@ -24,6 +26,9 @@ namespace {
 //   32 of 100 to 6000, D 64                  112 and  90   114 and 115
 //   2 of 20000, D 128                         89 and  52    90 and  98
 constexpr int kTcRows = 48;
+// The same of an E4M3 cache with a scale a page. us of the warp-level kernel and of the
+// tcgen05 kernel (32 sequences of 100 to 12000 keys, 8 key-value heads, 8 new tokens, D 128,
+// pages of 64): 64 rows 314 and 314, 80: 380 and 319, 96: 446 and 322, 128: 572 and 330.
 constexpr int kTcRowsE4m3 = 64;
 
 // Rows whose keys were cut into splits: one warp a row.
@@ -90,6 +95,8 @@ Plan plan_of(const moe_attn_config& c) {
   // memory of an SM's third block. Against larger blocks, since removed: bf16,
   // 20 rows: 147 us in one block, 138 in two; E4M3, 28 rows: 282 and 206; fp32,
   // 16 rows: 42.6 and 37.3.
+  // The tcgen05 kernels take all that they have lanes of Tensor Memory for: 128,
+  // of an E4M3 cache 256 in two streams.
   p.row_blocks = ceil_div(units, p.tc ? (f8 ? 16 : 8) : f32 && c.head_dim <= 128 ? 3 : 2);
   p.nt = ceil_div(units, p.row_blocks);
   p.items = (long long)c.n_seqs * c.n_kv_heads * p.row_blocks;

@@ -169,6 +169,24 @@ def test_update_matches_the_definition(kind, B, page, most, n_pages, order, pad)
         assert equal(pool.state(), pool.copied(before, want[3]))
 
 
+@pytest.mark.parametrize("B,page,most,n_pages", [(1500, 16, 9, 2100), (9000, 4, 6, 11000)])
+@pytest.mark.parametrize("seed", [0, 1])
+def test_update_of_more_sequences_than_a_block_keeps_at_hand(B, page, most, n_pages, seed):
+    """Over 1024 sequences for each block, in one block and in eight; seed 1 runs out of pages."""
+    rs = np.random.RandomState(seed)
+    pool = Pool(n_pages, page, heads=1, dim=16)
+    length, table, refs = random_state(rs, B, page, most, n_pages)
+    kept = [int(rs.randint(0, n + 1)) for n in length]
+    need = [k + int(rs.choice([0, 1, page, 2 * page] if seed else [0, 1])) for k in kept]
+    before = pool.state()
+    want = update_lists(page, None, length, kept, need, table.tolist(), refs.tolist(), table.tolist())
+    if seed:
+        assert want[2] != need
+    got = run_update(pool, None, length, kept, need, table, refs, True)
+    assert got[0] == 0 and got[1] == want[0] and got[2] == want[1] and got[3] == want[2]
+    assert equal(pool.state(), pool.copied(before, want[3]))
+
+
 @pytest.mark.parametrize("n_pages", [6, 7, 8, 9, 10, 40])
 def test_update_when_the_pool_runs_out(n_pages):
     """Wants of 0, 2, 3, 0, 1 pages over a pool with few to spare: what is granted is a prefix."""
