@@ -789,8 +789,9 @@ MOE_API int moe_verify_drafts(const moe_verify_config* cfg, const void* p, const
  * to n_history or n_bias; n_prompt outside the history's length; a token (of the
  * history: but -1) or a bias's token outside [0, V) (left out); a list of biases
  * that does not ascend; a mask_row outside [-1, n_masks) (taken as -1); repetition
- * <= 0 or temperature < 0 or either not finite. Counts are integers and sums run in a fixed order, so
- * equal calls give equal bits.
+ * <= 0, temperature < 0, or a penalty or temperature that is not finite. Rows from
+ * cu_new[B] on are left as they were. Counts are integers and sums run in a fixed
+ * order, so equal calls give equal bits.
  */
 typedef struct moe_logits_config {
   int32_t n_seqs;    /* B >= 0                                               */

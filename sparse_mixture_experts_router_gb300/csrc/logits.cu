@@ -206,23 +206,24 @@ __global__ void __launch_bounds__(kThreads, kHeld > 16 ? 2 : 4)
   } else {
     b = seq_of_row(a.cu_new, c.n_seqs, row, lane);
   }
-  SeqRange sq = {0, 0, 0, false};
   ListRange hist = {0, 0, false}, bias = {0, 0, false};
   int generated = 0;  // first entry of the history that was generated
   float rep = 1.f, pres = 0.f, freq = 0.f, temp = 1.f;
   const uint32_t* mask = nullptr;
-  if (b < c.n_seqs) {
-    sq = seq_rows(a.cu_new, b, c.n_seqs, c.n_tokens, c.max_new);
-    if (a.repetition) rep = a.repetition[b];
-    if (a.presence) pres = a.presence[b];
-    if (a.frequency) freq = a.frequency[b];
-    if (a.temperature) temp = a.temperature[b];
-    if (c.n_history) {
-      hist = list_range(a.cu_history, b, c.n_seqs, c.n_history);
-      generated = hist.lo + clamp_int(a.n_prompt[b], 0, hist.hi - hist.lo);
-    }
-    if (c.n_bias) bias = list_range(a.cu_bias, b, c.n_seqs, c.n_bias);
+  if (b >= c.n_seqs) {  // a row of no sequence, which the check records: left as it was
+    ptx::cluster_wait();
+    return;
   }
+  const SeqRange sq = seq_rows(a.cu_new, b, c.n_seqs, c.n_tokens, c.max_new);
+  if (a.repetition) rep = a.repetition[b];
+  if (a.presence) pres = a.presence[b];
+  if (a.frequency) freq = a.frequency[b];
+  if (a.temperature) temp = a.temperature[b];
+  if (c.n_history) {
+    hist = list_range(a.cu_history, b, c.n_seqs, c.n_history);
+    generated = hist.lo + clamp_int(a.n_prompt[b], 0, hist.hi - hist.lo);
+  }
+  if (c.n_bias) bias = list_range(a.cu_bias, b, c.n_seqs, c.n_bias);
   if (mask_row >= 0 && mask_row < c.n_masks) mask = a.mask + (int64_t)mask_row * ((V + 31) / 32);
   const int fed = a.tokens && row >= sq.row0 && row < sq.row0 + sq.n ? row + 1 - sq.row0 : 0;
   const bool counts = (rep != 1.f || pres != 0.f || freq != 0.f) && hist.hi - hist.lo + fed > 0;

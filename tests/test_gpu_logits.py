@@ -301,6 +301,18 @@ def test_bad_lists_are_recorded(name, at, value):
     assert r.status == moe.MOE_ERR_DEVICE_CHECK
 
 
+@pytest.mark.parametrize("B", [2, 600])
+def test_rows_behind_the_last_sequence(B):
+    """Recorded, and left as they were; rows of sequences are not touched by that."""
+    r = Rows([1] * B, 1000, history=30, biases=5, masks=2, seed=6)
+    want = r.run()
+    lists = r.lists()
+    lists["cu"][B:] = B - 1  # the last sequence has no row
+    got = r.run(lists)
+    assert r.status == moe.MOE_ERR_DEVICE_CHECK
+    assert np.array_equal(got[:B - 1], want[:B - 1]) and (got[B - 1:] == 7).all()
+
+
 def test_no_rows():
     r = Rows([0, 0], 50, history=5)
     r.run()
