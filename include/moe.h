@@ -801,8 +801,8 @@ typedef struct moe_logits_config {
   int32_t dtype;     /* of logits: fp32 or bf16                              */
   int32_t out_dtype; /* of p: fp32 or bf16                                   */
   int32_t out_logits; /* 1: p receives the logits after all but the softmax  */
-  int32_t n_history; /* entries of history, >= 0                             */
-  int32_t n_bias;    /* entries of bias_token, >= 0                          */
+  int32_t n_history; /* entries of history, 0..2^30                          */
+  int32_t n_bias;    /* entries of bias_token, 0..2^30                       */
   int32_t n_masks;   /* rows of mask, >= 0                                   */
   int64_t logits_stride, p_stride; /* elements between rows, >= V; 0: packed */
 } moe_logits_config;

@@ -1202,7 +1202,8 @@ int moe_check_logits_config(const moe_logits_config* c) {
       (c->p_stride != 0 && c->p_stride < c->vocab))
     return MOE_ERR_INVALID_ARG;
   if (c->max_new > kMaxNew || c->n_seqs > kMaxSeqs || c->vocab > (1 << 24) ||
-      c->n_tokens > kMaxLogitRows || c->logits_stride > (1LL << 40) || c->p_stride > (1LL << 40))
+      c->n_tokens > kMaxLogitRows || c->n_history > (1 << 30) || c->n_bias > (1 << 30) ||
+      c->logits_stride > (1LL << 40) || c->p_stride > (1LL << 40))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

@@ -239,6 +239,26 @@ def test_empty_places_of_the_history():
     assert np.array_equal(r.run(), want) and r.status == 0
 
 
+@pytest.mark.parametrize("V,pad", [(40, 3), (20011, 1)])
+def test_long_histories(V, pad):
+    """Histories of 2040 to 9000 tokens that start and end anywhere, some places of them empty."""
+    lengths = [2040, 2047, 2048, 2049, 2050, 2051, 2052, 2053, 2055, 9000, 1, 4099]
+    r = Rows([1, 2] * 6, V, history=0, pad=pad, seed=9)
+    r.cu_history = np.concatenate([[0], np.cumsum(lengths)])
+    r.history = r.rs.randint(0, V, sum(lengths))
+    r.n_prompt = np.array([r.rs.randint(0, n + 1) for n in lengths])
+    want = r.check()
+    empty = r.rs.rand(len(r.history)) < 0.3
+    full, r.history = r.history, np.where(empty, -1, r.history)
+    got = r.run()
+    assert r.status == 0 and not np.array_equal(got, want)
+    # the same without the empty places
+    at = np.concatenate([[0], np.cumsum(~empty)])
+    r.n_prompt = at[r.cu_history[:-1] + r.n_prompt] - at[r.cu_history[:-1]]
+    r.cu_history, r.history = at[r.cu_history], full[~empty]
+    assert np.array_equal(r.check(), got)
+
+
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 def test_logits_out(out):
     r = Rows([2, 1], 5003, history=100, biases=30, masks=2, out=out, p_pad=1)

@@ -12,7 +12,8 @@ BASE = dict(n_seqs=4, n_tokens=8, max_new=3, vocab=1000, n_history=5, n_bias=3, 
 
 @pytest.mark.parametrize("kw,rc", [
     ({}, OK), ({"n_seqs": 0, "n_tokens": 0}, OK), ({"n_seqs": -1}, INV), ({"n_tokens": 13}, INV), ({"n_tokens": -1}, INV), ({"max_new": 0}, INV),
-    ({"max_new": 4097}, UNS), ({"vocab": 0}, INV), ({"vocab": 1}, OK), ({"vocab": (1 << 24) + 1}, UNS), ({"dtype": 2}, INV), ({"out_dtype": 3}, INV),
+    ({"max_new": 4097}, UNS), ({"vocab": 0}, INV), ({"vocab": 1}, OK), ({"vocab": (1 << 24) + 1}, UNS), ({"n_history": 1 << 30}, OK),
+    ({"n_history": (1 << 30) + 1}, UNS), ({"n_bias": (1 << 30) + 1}, UNS), ({"dtype": 2}, INV), ({"out_dtype": 3}, INV),
     ({"dtype": moe.MOE_BF16, "out_dtype": moe.MOE_BF16}, OK), ({"n_history": -1}, INV), ({"n_bias": -1}, INV), ({"n_masks": -1}, INV),
     ({"logits_stride": 999}, INV), ({"p_stride": 999}, INV), ({"p_stride": 1001}, OK), ({"n_seqs": 65535}, UNS), ({"p_stride": (1 << 40) + 1}, UNS),
     ({"n_seqs": 65534, "max_new": 4096, "n_tokens": (1 << 26) + 1}, UNS),
