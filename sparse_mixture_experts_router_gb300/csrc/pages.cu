@@ -12,9 +12,10 @@
 // because the host does not know it.
 //
 // The first is bound by the latency of its steps (about a microsecond each): 128 sequences of
-// up to 2000 tokens, pages of 16, take 11 to 12 us with the launch of the second, and 16
+// up to 2000 tokens, pages of 16, take 10 to 11 us with the launch of the second, and 16
 // prompts forked into 128 sequences, with 128 copies on write (16 MB read and written), 15. Blocks
-// with half or twice the work (below) took as long or longer. The second is bound by
+// with half or twice the work (below) took as long or longer; a pool of 524288 pages
+// takes 26. The second is bound by
 // memory, 16-byte loads, eight in flight a thread: 495 MB read and written by a
 // compaction take 72 us, a copy's rate, of the call's 88.
 #include "serve_ptx.cuh"
@@ -156,6 +157,8 @@ __device__ __forceinline__ int pages_of(const PagesArgs& a, int tokens) {
 }
 
 constexpr int kRowsHeld = 1024;
+// Entries of a table that a lane has in flight: 100 tables of 5000 pages 27 us (one: 47).
+constexpr int kEntries = 4;
 
 __global__ void __launch_bounds__(kThreads, 1)
     pages_update_kernel(const __grid_constant__ PagesArgs a, const Scratch ws, int parts) {
@@ -208,14 +211,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t* from = a.table + (int64_t)max(w.parent, 0) * c.max_pages;
     int32_t* to = a.table_out + (int64_t)b * c.max_pages;
     const bool same = w.parent == b, writes = w.need > w.kept && w.kept % c.page_size != 0;
-    for (int i = lane; i < kept; i += 32) {
-      const int page = i == lane ? page_kept : from[i];
-      if (!valid(page))
-        bad = true;
-      else if (!same)
-        atomicAdd(a.refs_out + page, 1);
-      if (to != from) to[i] = page;
-      if (i == kept - 1) plan(b)->last = writes && valid(page) ? page : -1;
+    for (int i0 = lane; i0 < kept; i0 += 32 * kEntries) {
+      int page[kEntries];
+#pragma unroll
+      for (int k = 0; k < kEntries; ++k) {
+        const int i = i0 + 32 * k;
+        page[k] = i == lane ? page_kept : i < kept ? from[i] : -1;
+      }
+#pragma unroll
+      for (int k = 0; k < kEntries; ++k) {
+        const int i = i0 + 32 * k;
+        if (i >= kept) break;
+        if (!valid(page[k]))
+          bad = true;
+        else if (!same)
+          atomicAdd(a.refs_out + page[k], 1);
+        if (to != from) to[i] = page[k];
+        if (i == kept - 1) plan(b)->last = writes && valid(page[k]) ? page[k] : -1;
+      }
     }
     if (lane == 0) {
       if (kept == 0) plan(b)->last = -1;
@@ -223,12 +236,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       plan(b)->need = w.need;
     }
     const int first = same ? kept : 0;
-    for (int i = first + lane; i < len; i += 32) {
-      const int page = i == first + lane ? page_held : old[i];
-      if (valid(page))
-        atomicSub(a.refs_out + page, 1);
-      else
-        bad = true;
+    for (int i0 = first + lane; i0 < len; i0 += 32 * kEntries) {
+      int page[kEntries];
+#pragma unroll
+      for (int k = 0; k < kEntries; ++k) {
+        const int i = i0 + 32 * k;
+        page[k] = i == first + lane ? page_held : i < len ? old[i] : -1;
+      }
+#pragma unroll
+      for (int k = 0; k < kEntries; ++k) {
+        if (i0 + 32 * k >= len) break;
+        if (valid(page[k]))
+          atomicSub(a.refs_out + page[k], 1);
+        else
+          bad = true;
+      }
     }
   }
   ptx::cluster_sync();
@@ -302,10 +324,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       atomicSub(a.refs_out + p.last, 1);
       ws.copies[atomicAdd(&ws.head->n_copies, 1)] = {p.last, __ldcg(ws.free + at), p.kept % c.page_size, 0};
     }
-    for (int i = lane; i < want; i += 32) {
-      const int page = __ldcg(ws.free + at + i);
-      to[i] = page;
-      a.refs_out[page] = 1;
+    for (int i0 = lane; i0 < want; i0 += 32 * kEntries) {
+      int page[kEntries];
+#pragma unroll
+      for (int k = 0; k < kEntries; ++k) page[k] = i0 + 32 * k < want ? __ldcg(ws.free + at + i0 + 32 * k) : 0;
+#pragma unroll
+      for (int k = 0; k < kEntries; ++k) {
+        if (i0 + 32 * k >= want) break;
+        to[i0 + 32 * k] = page[k];
+        a.refs_out[page[k]] = 1;
+      }
     }
   }
   if (__syncthreads_or(bad) && threadIdx.x == 0) set_status(a.status, status_check());
@@ -494,12 +522,22 @@ cudaError_t launch_copies(const PagesArgs& a, const Scratch* ws, long long most,
 }
 
 // Blocks of a plan's cluster: one for each 8192 counts and entries (4096 and 16384: as long
-// or longer), up to eight.
+// or longer). us of an update in up to eight blocks and in up to 16: 65536 pages and 256
+// sequences 15 and 13, 524288 and 1000 44 and 30, 4 million and 2000 204 and 115.
 int plan_parts(const moe_attn_config& c) {
   const long long work = c.n_pages + (long long)c.n_seqs * c.max_pages;
   int parts = 1;
-  while (parts < 8 && work > 8192LL * parts) parts *= 2;
+  while (parts < kMaxParts && work > 8192LL * parts) parts *= 2;
   return parts;
+}
+// Clusters of more than eight blocks, once per device.
+cudaError_t allow_parts(const void* kernel, int parts, int* configured) {
+  int dev = 0;
+  cudaError_t e = parts > 8 ? cudaGetDevice(&dev) : cudaSuccess;
+  if (e != cudaSuccess || parts <= 8 || *configured == dev) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) *configured = dev;
+  return e;
 }
 
 }  // namespace
@@ -509,20 +547,22 @@ size_t pages_scratch_bytes(const moe_attn_config& c) {
 }
 
 cudaError_t launch_pages_update(const PagesArgs& a, void* scratch, cudaStream_t s) {
+  static thread_local int configured = -1;
   const Scratch ws = scratch_of(a.c, scratch);
   const int parts = plan_parts(a.c);
-  cudaError_t e;
-  {
+  cudaError_t e = allow_parts(reinterpret_cast<const void*>(pages_update_kernel), parts, &configured);
+  if (e == cudaSuccess) {
     ProfScope p(K_PAGES, s);
     e = launch_pdl(pages_update_kernel, dim3((unsigned)parts), dim3(kThreads), 0, s, parts, a, ws, parts);
   }
   return e == cudaSuccess ? launch_copies(a, &ws, a.c.n_seqs, s) : e;
 }
 cudaError_t launch_pages_compact(const PagesArgs& a, void* scratch, cudaStream_t s) {
+  static thread_local int configured = -1;
   const Scratch ws = scratch_of(a.c, scratch);
   const int parts = plan_parts(a.c);
-  cudaError_t e;
-  {
+  cudaError_t e = allow_parts(reinterpret_cast<const void*>(pages_compact_kernel), parts, &configured);
+  if (e == cudaSuccess) {
     ProfScope p(K_PAGES, s);
     e = launch_pdl(pages_compact_kernel, dim3((unsigned)parts), dim3(kThreads), 0, s, parts, a, ws, parts);
   }

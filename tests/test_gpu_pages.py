@@ -187,6 +187,32 @@ def test_update_of_more_sequences_than_a_block_keeps_at_hand(B, page, most, n_pa
     assert equal(pool.state(), pool.copied(before, want[3]))
 
 
+@pytest.mark.parametrize("forks", [False, True])
+def test_updates_and_moves_of_long_tables(forks):
+    """Tables of up to 400 pages over a pool of 120000, which the largest cluster works on: trimmed,
+    grown by up to 300 pages, forked, and the pool compacted."""
+    rs = np.random.RandomState(forks)
+    B, page, most, n_pages = 250, 1, 400, 120000
+    pool = Pool(n_pages, page, heads=1, dim=16)
+    length, table, refs = random_state(rs, B, page, most, n_pages)
+    table = np.concatenate([table, np.full((B, 300), -1)], 1)
+    parent = [int(rs.randint(-1, B)) for _ in range(B)] if forks else None
+    has = [length[b] if parent is None else 0 if parent[b] < 0 else length[parent[b]] for b in range(B)]
+    kept = [int(rs.randint(0, n + 1)) for n in has]
+    need = [k + int(rs.randint(0, 301)) for k in kept]
+    before = pool.state()
+    out0 = np.full_like(table, -5).tolist()
+    want = update_lists(page, parent, length, kept, need, table.tolist(), refs.tolist(), out0)
+    got = run_update(pool, parent, length, kept, need, table, refs)
+    assert got[0] == 0 and got[1] == want[0] and got[2] == want[1] and got[3] == want[2]
+    assert equal(pool.state(), pool.copied(before, want[3]))
+    table, refs = np.array(got[1]), np.array(got[2])
+    before = pool.state()
+    want = compact_lists(page, need, table.tolist(), refs.tolist(), out0)
+    assert run_compact(pool, need, table, refs, False) == (0, *want[:4])
+    assert equal(pool.state(), pool.copied(before, want[4]))
+
+
 @pytest.mark.parametrize("n_pages", [6, 7, 8, 9, 10, 40])
 def test_update_when_the_pool_runs_out(n_pages):
     """Wants of 0, 2, 3, 0, 1 pages over a pool with few to spare: what is granted is a prefix."""
