@@ -82,21 +82,31 @@ __device__ bool bad_lists(const LogitsArgs& a, int t, int n) {
     bad |= wrong(x.x) | wrong(x.y) | wrong(x.z) | wrong(x.w);
   }
   if (t < c.n_history % 4) bad |= wrong(__ldg(a.history + 4 * vecs + t));
-  const int per = max(1, n / max(1, c.n_seqs)), sub = t % per;
-  for (int b = t / per; b < c.n_seqs && t < n / per * per; b += n / per) {
+  // A bias's token is above the one before it, but where a list starts.
+  auto starts = [&](int i) {
+    int lo = 0, hi = c.n_seqs;
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (__ldg(a.cu_bias + mid) < i)
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    return __ldg(a.cu_bias + lo) == i;
+  };
+#pragma unroll 4
+  for (int i = t; i < c.n_bias; i += n) {
+    const int x = __ldg(a.bias_token + i), before = i > 0 ? __ldg(a.bias_token + i - 1) : -1;
+    bad |= (unsigned)x >= (unsigned)c.vocab;
+    if (before >= x) bad |= !starts(i);
+  }
+  for (int b = t; b < c.n_seqs; b += n) {
     bad |= !seq_rows(a.cu_new, b, c.n_seqs, c.n_tokens, c.max_new).ok;
     if (c.n_history) {
       const ListRange r = list_range(a.cu_history, b, c.n_seqs, c.n_history);
       bad |= !r.ok || a.n_prompt[b] < 0 || a.n_prompt[b] > r.hi - r.lo;
     }
-    if (c.n_bias) {
-      const ListRange r = list_range(a.cu_bias, b, c.n_seqs, c.n_bias);
-      bad |= !r.ok;
-      for (int i = r.lo + sub; i < r.hi; i += per) {
-        const int x = a.bias_token[i];
-        bad |= (unsigned)x >= (unsigned)c.vocab || (i > r.lo && a.bias_token[i - 1] >= x);
-      }
-    }
+    if (c.n_bias) bad |= !list_range(a.cu_bias, b, c.n_seqs, c.n_bias).ok;
     // written so that a NaN is bad
     if (a.repetition) bad |= !(a.repetition[b] > 0.f && a.repetition[b] <= FLT_MAX);
     if (a.presence) bad |= !(fabsf(a.presence[b]) <= FLT_MAX);
@@ -329,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, kHeld > 16 ? 2 : 4)
     }
     if (biased) {
       if (counts) __syncthreads();
+#pragma unroll 4
       for (int i = bias.lo + t0; i < bias.hi; i += kThreads) {
         const int token = __ldg(a.bias_token + i), at = token - base;
         if ((unsigned)at < (unsigned)n_words && (unsigned)token < (unsigned)V)
