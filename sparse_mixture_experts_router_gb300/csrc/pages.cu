@@ -17,7 +17,7 @@
 // with half or twice the work (below) took as long or longer; a pool of 524288 pages
 // takes 26. The second is bound by
 // memory, 16-byte loads, eight in flight a thread: 495 MB read and written by a
-// compaction take 72 us, a copy's rate, of the call's 88.
+// compaction take 72 us, a copy's rate, of the call's 87.
 #include "serve_ptx.cuh"
 #include "serve_util.cuh"
 
@@ -359,6 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int page1 = min(page0 + share, c.n_pages);
   bool bad = false;
   int count = 0;
+#pragma unroll 4
   for (int i = page0 + threadIdx.x; i < page1; i += kThreads) {
     const int n = a.refs[i];
     count += n > 0;
@@ -405,11 +406,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     bad |= len < 0 || len > most;
     const int held = pages_of(a, clamp_int(len, 0, most));
     const int64_t row = (int64_t)b * c.max_pages;
-    for (int i = lane; i < held; i += 32) {
-      int page = a.table[row + i];
-      const int now = page >= 0 && page < c.n_pages ? __ldcg(a.page_map + page) : -1;
-      bad |= now < 0;
-      a.table_out[row + i] = now < 0 ? page : now;
+    for (int i0 = lane; i0 < held; i0 += 32 * kEntries) {
+      int page[kEntries], now[kEntries];
+#pragma unroll
+      for (int k = 0; k < kEntries; ++k) page[k] = i0 + 32 * k < held ? a.table[row + i0 + 32 * k] : -1;
+#pragma unroll
+      for (int k = 0; k < kEntries; ++k)
+        now[k] = page[k] >= 0 && page[k] < c.n_pages ? __ldcg(a.page_map + page[k]) : -1;
+#pragma unroll
+      for (int k = 0; k < kEntries; ++k) {
+        if (i0 + 32 * k >= held) break;
+        bad |= now[k] < 0;
+        a.table_out[row + i0 + 32 * k] = now[k] < 0 ? page[k] : now[k];
+      }
     }
   }
   if (thread == 0) *a.n_live = live;
@@ -440,8 +449,9 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_c
   if (list) {
     if (block == 0) {
       bool bad = false;
+#pragma unroll 8
       for (int i = threadIdx.x; i < a.n_copies; i += kCopyThreads) {
-        const int src = a.src[i], dst = a.dst[i];
+        const int src = __ldg(a.src + i), dst = __ldg(a.dst + i);
         bad |= src < 0 || src >= a.n_src_pages || dst < 0 || dst >= c.n_pages;
       }
       bad = __syncthreads_or(bad);
