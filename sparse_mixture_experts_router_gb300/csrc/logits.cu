@@ -123,14 +123,26 @@ struct alignas(16) Part {
   int at;
 };
 
-// A vector that lies partly in the row: its elements of the row, NaN elsewhere.
+// A vector that lies partly in the row: its elements of the row, NaN elsewhere. Put together word
+// by word: an array of elements that is read as one vector has the alignment of an element.
 template <typename In>
 __device__ __noinline__ uint4 load_edge(const In* row, int e, int V) {
-  constexpr int kE = 16 / (int)sizeof(In);
-  In x[kE];
+  constexpr int kPer = 4 / (int)sizeof(In);  // elements a word
+  uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < kE; ++i) x[i] = e + i >= 0 && e + i < V ? row[e + i] : from_f32<In>(NAN);
-  return *reinterpret_cast<const uint4*>(x);
+  for (int i = 0; i < 4; ++i) {
+    w[i] = 0xffffffffu;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int at = e + i * kPer + j;
+      if (at < 0 || at >= V) continue;
+      if (kPer == 1)
+        w[i] = reinterpret_cast<const uint32_t*>(row)[at];
+      else
+        w[i] = (w[i] & ~(0xffffu << 16 * j)) | (uint32_t)reinterpret_cast<const uint16_t*>(row)[at] << 16 * j;
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 template <typename Out>
 __device__ __noinline__ void store_edge(Out* row, int e, int V, float4 y) {
