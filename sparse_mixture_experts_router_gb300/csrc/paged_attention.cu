@@ -31,9 +31,9 @@ constexpr int kTcRows = 48;
 // pages of 64): 64 rows 314 and 314, 80: 380 and 319, 96: 446 and 322, 128: 572 and 330.
 constexpr int kTcRowsE4m3 = 64;
 
-// Rows whose keys were cut into splits: one warp a row.
+// Rows whose keys were cut into splits: one warp a row. kRef: E4M3 caches.
 constexpr int kJoinWarps = 4;
-template <typename Elem>
+template <typename Elem, bool kRef>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     join_kernel(const __grid_constant__ attn::Params prm, int rows) {
   const moe_attn_config& c = prm.a.c;
@@ -56,7 +56,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   float top = ml.x;
 #pragma unroll
   for (int x = 16; x > 0; x /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-  const float f = ptx::ex2(ml.x - top), sum = warp_sum(ml.y * f);
+  float f = ptx::ex2(ml.x - top), ref = 0.f;
+  const float sum = warp_sum(ml.y * f);
+  if (kRef) {
+    const float own = lane < prm.splits ? prm.split_ref[row0 + (int64_t)lane * block_rows] : -INFINITY;
+    ref = own;
+#pragma unroll
+    for (int x = 16; x > 0; x /= 2) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, x));
+    f = ptx::ex2(own - ref);
+  }
   attn::Params out = prm;
   out.splits = 1;
   const int vecs = c.head_dim / 4;
@@ -70,7 +78,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
           prm.split_o)[(row0 + (int64_t)s * block_rows) * vecs + v];
       x.x += y.x * fs, x.y += y.y * fs, x.z += y.z * fs, x.w += y.w * fs;
     }
-    if (v < vecs) attn::write_row<Elem>(out, it, r, v, x, top, sum);
+    if (v < vecs) attn::write_row<Elem, kRef>(out, it, r, v, x, top, sum, ref);
   }
 }
 
@@ -151,7 +159,8 @@ cudaError_t launch_tc_e4m3(const Params& p, int dim, unsigned blocks, cudaStream
 }  // namespace attn
 
 size_t attention_scratch_bytes(const moe_attn_config& c) {
-  return split_rows(plan_of(c)) * ((size_t)c.head_dim * sizeof(float) + sizeof(float2));
+  return split_rows(plan_of(c)) *
+         ((size_t)c.head_dim * sizeof(float) + sizeof(float2) + (is_e4m3(c.cache_dtype) ? sizeof(float) : 0));
 }
 
 cudaError_t launch_paged_attention(const AttnArgs& a, void* scratch, cudaStream_t s) {
@@ -177,6 +186,7 @@ cudaError_t launch_paged_attention(const AttnArgs& a, void* scratch, cudaStream_
   prm.by_vecs = fast_div((uint32_t)c.head_dim / 4);
   prm.split_o = static_cast<float*>(scratch);
   prm.split_ml = reinterpret_cast<float2*>(prm.split_o + split_rows(plan) * c.head_dim);
+  prm.split_ref = reinterpret_cast<float*>(prm.split_ml + split_rows(plan));
   const unsigned blocks = (unsigned)((plan.items * plan.splits + 1) * plan.parts);
   cudaError_t e = prm.check_in_use ? launch_reset_status(a.status, s) : cudaSuccess;
   if (e != cudaSuccess) return e;
@@ -192,8 +202,9 @@ cudaError_t launch_paged_attention(const AttnArgs& a, void* scratch, cudaStream_
   ProfScope p(K_ATTENTION_JOIN, s);
   const int rows = (int)(plan.items * plan.rows());
   const dim3 grid((unsigned)ceil_div(rows, kJoinWarps)), block(kJoinWarps * 32);
-  return c.dtype == MOE_F32 ? launch_pdl(join_kernel<float>, grid, block, 0, s, 1, prm, rows)
-                            : launch_pdl(join_kernel<__nv_bfloat16>, grid, block, 0, s, 1, prm, rows);
+  return c.dtype == MOE_F32       ? launch_pdl(join_kernel<float, false>, grid, block, 0, s, 1, prm, rows)
+         : is_e4m3(c.cache_dtype) ? launch_pdl(join_kernel<__nv_bfloat16, true>, grid, block, 0, s, 1, prm, rows)
+                                  : launch_pdl(join_kernel<__nv_bfloat16, false>, grid, block, 0, s, 1, prm, rows);
 }
 
 }  // namespace moe

@@ -42,9 +42,11 @@ struct Params {
   FastDiv by_page, by_group, by_parts, by_splits, by_rows, by_heads, by_vecs;
   int item_rows;   // query rows of an item
   // splits > 1: O [item][split][item_rows][head_dim] relative to its maximum,
-  // and (maximum in log2 units, sum) [item][split][item_rows]
+  // and (maximum in log2 units, sum) [item][split][item_rows]; E4M3 caches:
+  // O relative to a reference of its own, [item][split][item_rows]
   float* split_o;
   float2* split_ml;
+  float* split_ref;
 };
 
 // The first position that a sequence's new tokens see.
@@ -190,21 +192,29 @@ __device__ __forceinline__ void store4(__nv_bfloat16* out, int64_t at, float4 x)
       make_uint2(f32x2_to_bf16x2(x.x, x.y), f32x2_to_bf16x2(x.z, x.w));
 }
 // Four elements (v) of row r from their sum relative to 2^top and the sum of
-// weights: the output, or the split's part of it.
-template <typename Elem>
+// weights: the output, or the split's part of it. kRef: the sum of weights is
+// relative to 2^top, the elements to 2^ref. With scales of values outside fp32's
+// comfort (paged_attention_mma.cuh) those are up to 2^130 apart, so elements are
+// first divided by the sum, and the power of two between them comes in two halves.
+template <typename Elem, bool kRef = false>
 __device__ __forceinline__ void write_row(const Params& p, const Item& it, int r, int v, float4 x,
-                                          float top, float sum) {
+                                          float top, float sum, float ref = 0.f) {
   const moe_attn_config& c = p.a.c;
   const int vecs = c.head_dim / 4;
   if (p.splits > 1) {
     const int64_t row = ((int64_t)it.index * p.splits + it.split) * p.item_rows + r;
     reinterpret_cast<float4*>(p.split_o)[row * vecs + v] = x;
     if (v == 0) p.split_ml[row] = make_float2(top, sum);
+    if (kRef && v == 0) p.split_ref[row] = ref;
     return;
   }
   const float f = 1.f / sum;  // a NaN stays one
   x = sum == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
                  : make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+  if (kRef && ref != top) {
+    const float half = ptx::ex2(0.5f * (ref - top));
+    x = make_float4(x.x * half * half, x.y * half * half, x.z * half * half, x.w * half * half);
+  }
   const int g = it.row0 + r, j = div(p.by_group, g);
   const int at = (it.sq.row0 + j) * c.n_heads + it.kh * it.G + g - j * it.G;  // T * Hq < 2^30
   store4(static_cast<Elem*>(p.a.out), (int64_t)at * vecs + v, x);
@@ -213,10 +223,16 @@ __device__ __forceinline__ void write_row(const Params& p, const Item& it, int r
 }
 
 // Where the blocks of a cluster leave what one of them joins: (maximum, sum)
-// of every block's rows, and of O the slice of rows x vectors that this block
-// writes, from every block.
-template <int kRows, int kDim>
-struct Inbox {
+// of every block's rows (kRef: and what their O is relative to), and of O the
+// slice of rows x vectors that this block writes, from every block.
+template <int kRows, bool kRef>
+struct InboxRef {};
+template <int kRows>
+struct InboxRef<kRows, true> {
+  float ref[kMaxParts][kRows];
+};
+template <int kRows, int kDim, bool kRef = false>
+struct Inbox : InboxRef<kRows, kRef> {
   float2 ml[kMaxParts][kRows];
   // slices of ceil(n / parts) of the n <= kRows * kDim / 4 vectors
   float4 o[kRows * kDim / 4 + kMaxParts];
@@ -224,41 +240,46 @@ struct Inbox {
 
 // Joins the cluster's blocks in this block's slice of the item's rows x vectors, all of
 // which are in its inbox, and writes it.
-template <int kRows, int kDim, int kThreads, typename Elem>
+template <int kRows, int kDim, int kThreads, typename Elem, bool kRef = false>
 __device__ __forceinline__ void join_slices(const Params& p, const Item& it,
-                                            const Inbox<kRows, kDim>* inbox) {
+                                            const Inbox<kRows, kDim, kRef>* inbox) {
   const int vecs = p.a.c.head_dim / 4, n = it.rows * vecs;
   const int slice = div(p.by_parts, n + p.parts - 1);
   const int i0 = it.part * slice;
   for (int i = i0 + threadIdx.x; i < min(i0 + slice, n); i += kThreads) {
     const int r = div(p.by_vecs, i), v = i - r * vecs;
-    float top = -INFINITY, sum = 0.f;
+    float top = -INFINITY, ref = -INFINITY, sum = 0.f;
 #pragma unroll 4
-    for (int b = 0; b < p.parts; ++b) top = fmaxf(top, inbox->ml[b][r].x);
+    for (int b = 0; b < p.parts; ++b) {
+      top = fmaxf(top, inbox->ml[b][r].x);
+      if constexpr (kRef) ref = fmaxf(ref, inbox->ref[b][r]);
+    }
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int b = 0; b < p.parts; ++b) {
       const float2 ml = inbox->ml[b][r];
       const float4 y = inbox->o[b * slice + i - i0];
-      const float f = ptx::ex2(ml.x - top);
+      float f = ptx::ex2(ml.x - top);
       sum += ml.y * f;
+      if constexpr (kRef) f = ptx::ex2(inbox->ref[b][r] - ref);
       x.x += y.x * f, x.y += y.y * f, x.z += y.z * f, x.w += y.w * f;
     }
-    write_row<Elem>(p, it, r, v, x, top, sum);
+    write_row<Elem, kRef>(p, it, r, v, x, top, sum, ref);
   }
 }
 
 // Joins a block's kWarps partial O (row r at o + w * stride + r * ld floats,
-// all relative to the block's maximum joined[r]; joined[kRows + r] its sum of
-// weights) and then the cluster's blocks, and writes the rows. Each block
+// all relative to the block's maximum joined[r], with kRef to joined[2 kRows + r];
+// joined[kRows + r] its sum of weights) and then the cluster's blocks, and writes
+// the rows. Each block
 // sends every other its slice and then reads its own shared memory only, so no
 // barrier has to keep blocks from leaving. With kOwnInbox the inbox is memory
 // of its own and a block sends as soon as all have started (start_cluster);
 // otherwise it lies over the stages of the warps after the first, and blocks
 // send when all have read theirs: one barrier more, 8 to 16 KB less.
-template <int kRows, int kDim, int kWarps, int kThreads, bool kOwnInbox, typename Elem>
+template <int kRows, int kDim, int kWarps, int kThreads, bool kOwnInbox, typename Elem, bool kRef = false>
 __device__ __forceinline__ void finish(const Params& p, const Item& it, float* o, int stride, int ld,
-                                       const float* joined, Inbox<kRows, kDim>* inbox) {
+                                       const float* joined, Inbox<kRows, kDim, kRef>* inbox) {
   const int vecs = p.a.c.head_dim / 4, n = it.rows * vecs;
   auto at = [&](int w, int r, int v) {
     return reinterpret_cast<float4*>(o + w * stride + r * ld + 4 * v);
@@ -275,7 +296,8 @@ __device__ __forceinline__ void finish(const Params& p, const Item& it, float* o
   if (p.parts == 1) {
     for (int i = threadIdx.x; i < n; i += kThreads) {
       const int r = div(p.by_vecs, i), v = i - r * vecs;
-      write_row<Elem>(p, it, r, v, block_sum(r, v), joined[r], joined[kRows + r]);
+      write_row<Elem, kRef>(p, it, r, v, block_sum(r, v), joined[r], joined[kRows + r],
+                            kRef ? joined[2 * kRows + r] : 0.f);
     }
     return;
   }
@@ -295,6 +317,9 @@ __device__ __forceinline__ void finish(const Params& p, const Item& it, float* o
     ptx::st_cluster_v2(
         ptx::mapa_shared(ptx::smem_addr(&inbox->ml[it.part][r]), i - r * p.parts), joined[r],
         joined[kRows + r]);
+    if constexpr (kRef)
+      ptx::st_cluster(ptx::mapa_shared(ptx::smem_addr(&inbox->ref[it.part][r]), i - r * p.parts),
+                      joined[2 * kRows + r]);
   }
   int to = 0;
   for (int i = threadIdx.x; i < n; i += kThreads) {
@@ -306,7 +331,7 @@ __device__ __forceinline__ void finish(const Params& p, const Item& it, float* o
   }
   __syncwarp();
   ptx::cluster_sync();
-  join_slices<kRows, kDim, kThreads, Elem>(p, it, inbox);
+  join_slices<kRows, kDim, kThreads, Elem, kRef>(p, it, inbox);
 }
 __device__ __forceinline__ void start_cluster(const Params& p) {
   if (p.parts > 1) ptx::cluster_arrive();

@@ -28,7 +28,9 @@
 // products) for a bf16 cache, whose error one rounding would double; for an E4M3
 // cache once, times the value's scale, to fp16 (2^-11). The largest of those is
 // kept between 2^7 and 2^15, so that they have fp16's precision down to 2^-21 of
-// it and none is off by more than 2^-32 of it, however many keys a row has. E4M3
+// it and none is off by more than 2^-32 of it, however many keys a row has. The sum
+// of weights, which has no scales in it, is relative to the same maximum while the
+// scales allow it (from about 2^-53 to 2^80), else to one of its own. E4M3
 // elements are exact in fp16. Queries become fp16 too, each row scaled by a power
 // of two so that its largest element is at least 2^14: elements down to 2^-31 of
 // that are exact, those below it off by 2^-39 of it at most. Scores by E4M3
@@ -36,6 +38,8 @@
 // 101 (256 sequences of 1 to 2047 keys, 8 rows). The scales of keys multiply
 // scores, those of values multiply weights.
 #pragma once
+#include <type_traits>
+
 #include "paged_attention.cuh"
 
 namespace moe {
@@ -94,8 +98,8 @@ struct Layout {
   static constexpr int kQRow = kDim * 2 + 16;  // bytes; 16 against bank conflicts
   static constexpr bool kOwnInbox = kNT == 1;  // the others' would cost the third block
   static constexpr int kRing = kWarps * T::kStages * T::kStage;
-  static constexpr int kInbox = kOwnInbox ? (int)sizeof(Inbox<kRows, kDim>) : 0;
-  static constexpr int kStat = (2 * kWarps + 2) * kRows * 4;
+  static constexpr int kInbox = kOwnInbox ? (int)sizeof(Inbox<kRows, kDim, kF8>) : 0;
+  static constexpr int kStat = (kF8 ? 3 : 2) * (kWarps + 1) * kRows * 4;
   static constexpr int kRange = kRows * 8;   // last and first position of a row
   static constexpr int kFactor = kRows * 4;  // of a row's scores
   static constexpr int kQ = kSharedQ ? kRows * kQRow : 0;
@@ -131,11 +135,12 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
   const AttnArgs& a = prm.a;
   const moe_attn_config& c = a.c;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, quad = lane % 4, oct = lane / 4;
-  auto* inbox = reinterpret_cast<Inbox<kRows, kDim>*>(
+  auto* inbox = reinterpret_cast<Inbox<kRows, kDim, kF8>*>(
       L::kOwnInbox ? smem + L::kRing : smem + kS * T::kStage);
   uint8_t* rest = smem + L::kRing + L::kInbox;
-  float* stat = reinterpret_cast<float*>(rest);  // m, l of each warp's rows
-  float* joined = stat + 2 * kWarps * kRows;     // m, l of the block's
+  float* stat = reinterpret_cast<float*>(rest);  // m, l of each warp's rows; E4M3: l's reference
+  float* joined = stat + (kF8 ? 3 : 2) * kWarps * kRows;  // l's reference and l of the block's rows; E4M3: m
+  float* l_ref = stat + (2 * kWarps + warp) * kRows;      // (E4M3) this warp's
   int2* range = reinterpret_cast<int2*>(rest + L::kStat);
   float* factor = reinterpret_cast<float*>(rest + L::kStat + L::kRange);
   uint8_t* qs = rest + L::kStat + L::kRange + L::kFactor;
@@ -314,11 +319,17 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[n][d][i] = 0.f;
   }
-  for (int i = 0; i < mine; ++i) {
+  auto advance = [&](int i) {
     ptx::cp_async_wait_group<kS - 2>();
     __syncwarp();
     load(i + kS - 1, next);  // into the stage that step i - 1 has read
     next = look_up(i + kS);
+  };
+  // Tile i, which has arrived. False, and nothing is changed, where l and O need references of
+  // their own (E4M3; the same for the whole warp), which they have in the instance kApart. That
+  // is in a loop of its own: in this one it cost every call 1 to 4%.
+  auto tile = [&](int i, auto instance) __attribute__((always_inline)) {
+    constexpr bool kApart = decltype(instance)::value;
     const uint32_t K = ring + (i % kS) * T::kStage, V = K + T::kBytes;
     const uint32_t k_at = K + k_lane, v_at = V + v_lane;
     const int key0 = tile_key(i);
@@ -387,7 +398,24 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
     // Weights against the running maximum; over the bound, the maximum is
     // raised and they are taken again.
     float p[kMT][kNT][4];
-    bool raise = false;
+    float vs_max = kF8 ? fmaxf(vs[0][0], vs[0][1]) : 0.f;
+    if (kF8) {
+#pragma unroll
+      for (int t = 1; t < kMT; ++t) vs_max = fmaxf(fmaxf(vs_max, vs[t][0]), vs[t][1]);
+    }
+    bool raise = kApart || vs_max > 0x1p80f;
+    // This lane's largest score of a row, and its largest with the value's scale.
+    auto tops = [&](int n, int j, float& top, float& top_v) {
+      top = top_v = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < kMT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float v = s[t][n][2 * h + j];
+          top = fmaxf(top, v);
+          if (kF8 && vs[t][h] > 0.f && vs[t][h] < INFINITY) top_v = fmaxf(top_v, v + __log2f(vs[t][h]));
+        }
+    };
 #pragma unroll
     for (int t = 0; t < kMT; ++t)
 #pragma unroll
@@ -424,30 +452,37 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
             raise = raise || !(p[t][n][x] <= 0x1p68f) ||
                     (v != -INFINITY && !(p[t][n][x] * vs[t][x / 2] <= 0x1p15f));
         }
-    if (__any_sync(0xffffffffu, raise)) {
+    if (!kApart && __any_sync(0xffffffffu, raise)) {
+      // The reference that each row asks for. E4M3: the largest weight times its value's scale
+      // becomes 2^7 (an infinite scale aside: the sum of weights does not see values), and no
+      // weight itself is above 2^60.
+      float up[kNT][2];
+      // l needs a reference of its own: fp32 may have lost weights that so large a scale makes
+      // count, or a lane's weights without their scales ask for more.
+      bool part = vs_max > 0x1p80f;
 #pragma unroll
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float top = m[n][j];
+          float top, top_v;
+          tops(n, j, top, top_v);
+          float u = top;
+          if (kF8) {
+            top_v -= 7.f, top -= 60.f;
+            part = part || top > fmaxf(top_v, m[n][j]);
+            u = fmaxf(top_v, top);
+          }
 #pragma unroll
-          for (int t = 0; t < kMT; ++t)
+          for (int x = 4; x < 32; x *= 2) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, x));
+          up[n][j] = fmaxf(m[n][j], u);
+        }
+      if (kF8 && __any_sync(0xffffffffu, part)) return false;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float v = s[t][n][2 * h + j];
-              // E4M3: the largest weight times its value's scale becomes 2^7 (an
-              // infinite scale aside: the sum of weights does not see values),
-              // and no weight itself is above 2^60
-              if (kF8)
-                v = fmaxf(vs[t][h] > 0.f && vs[t][h] < INFINITY ? v + __log2f(vs[t][h]) - 7.f
-                                                                : -INFINITY,
-                          v - 60.f);
-              top = fmaxf(top, v);
-            }
+      for (int n = 0; n < kNT; ++n)
 #pragma unroll
-          for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-          const float f = ptx::ex2(m[n][j] - top);
-          m[n][j] = top;
+        for (int j = 0; j < 2; ++j) {
+          const float f = ptx::ex2(m[n][j] - up[n][j]);
+          m[n][j] = up[n][j];
           l[n][j] *= f;
 #pragma unroll
           for (int d = 0; d < kDT; ++d) {
@@ -457,9 +492,47 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
 #pragma unroll
           for (int t = 0; t < kMT; ++t)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) p[t][n][2 * h + j] = ptx::ex2(s[t][n][2 * h + j] - top);
+            for (int h = 0; h < 2; ++h) p[t][n][2 * h + j] = ptx::ex2(s[t][n][2 * h + j] - m[n][j]);
         }
     }
+    if (kApart) {
+      // m follows the scores with their values' scales, l's reference (in shared memory) the
+      // scores alone.
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float top, top_v;
+          tops(n, j, top, top_v);
+#pragma unroll
+          for (int x = 4; x < 32; x *= 2) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            top_v = fmaxf(top_v, __shfl_xor_sync(0xffffffffu, top_v, x));
+          }
+          float& kept = l_ref[8 * n + 2 * quad + j];
+          const float was = kept, ref = top > was + 8.f ? top : was;
+          __syncwarp();
+          if (oct == 0) kept = ref;
+          l[n][j] *= ptx::ex2(was - ref);
+          const float up = top_v > m[n][j] + 15.f ? top_v - 7.f : m[n][j], f = ptx::ex2(m[n][j] - up);
+          m[n][j] = up;
+#pragma unroll
+          for (int d = 0; d < kDT; ++d) {
+            o[n][d][j] *= f;
+            o[n][d][2 + j] *= f;
+          }
+#pragma unroll
+          for (int t = 0; t < kMT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float v = s[t][n][2 * h + j];
+              l[n][j] += ptx::ex2(v - ref);
+              // 0 for a key that is not seen, whatever its scale
+              p[t][n][2 * h + j] = v == -INFINITY ? 0.f : ptx::ex2(v + __log2f(vs[t][h]) - up);
+            }
+        }
+    }
+    if (!kApart) {
 #pragma unroll
     for (int t = 0; t < kMT; ++t)
 #pragma unroll
@@ -469,6 +542,7 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
           l[n][x % 2] += p[t][n][x];
           if (kF8 && p[t][n][x] > 0.f) p[t][n][x] *= vs[t][x / 2];
         }
+    }
 
     // A key that some rows see and others do not may hold values that are not
     // finite, and 0 times those is not 0: such a tile goes element by element.
@@ -521,7 +595,7 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
                 }
             }
         __syncwarp();
-        continue;
+        return true;
       }
     }
 
@@ -568,6 +642,25 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
       }
     }
     __syncwarp();  // every lane has read this stage
+    return true;
+  };
+  int i = 0;
+  for (; i < mine; ++i) {
+    advance(i);
+    if (!tile(i, std::false_type{})) break;
+  }
+  const bool apart = kF8 && i < mine;
+  if (apart) {
+#pragma unroll
+    for (int n = 0; n < kNT; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (oct == 0) l_ref[8 * n + 2 * quad + j] = m[n][j];
+    __syncwarp();
+    for (bool here = true; i < mine; ++i, here = false) {
+      if (!here) advance(i);
+      tile(i, std::true_type{});
+    }
   }
   ptx::cp_async_wait_all();
 
@@ -581,6 +674,7 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
       if (oct == 0) {
         stat[warp * kRows + 8 * n + 2 * quad + j] = m[n][j];
         stat[(kWarps + warp) * kRows + 8 * n + 2 * quad + j] = l[n][j];
+        if (kF8 && !apart) l_ref[8 * n + 2 * quad + j] = m[n][j];
       }
     }
   __syncthreads();
@@ -599,12 +693,16 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
       for (int w = 1; w < kWarps; ++w) top = fmaxf(top, stat[w * kRows + r]);
       const float f = ptx::ex2(m[n][j] - top);
       if (warp == 0 && oct == 0) {
-        float sum = 0.f;
+        const float* refs = stat + (kF8 ? 2 * kWarps * kRows : 0) + r;
+        float sum = 0.f, ref = refs[0];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) ref = fmaxf(ref, refs[w * kRows]);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
-          sum += stat[(kWarps + w) * kRows + r] * ptx::ex2(stat[w * kRows + r] - top);
-        joined[r] = top;
+          sum += stat[(kWarps + w) * kRows + r] * ptx::ex2(refs[w * kRows] - ref);
+        joined[r] = ref;
         joined[kRows + r] = sum;
+        if (kF8) joined[2 * kRows + r] = top;
       }
 #pragma unroll
       for (int d = 0; d < kDT; ++d)
@@ -614,7 +712,7 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
               o[n][d][2 * h + j] * f;
     }
   __syncthreads();
-  finish<kRows, kDim, kWarps, kThreads, L::kOwnInbox, __nv_bfloat16>(
+  finish<kRows, kDim, kWarps, kThreads, L::kOwnInbox, __nv_bfloat16, kF8>(
       prm, it, reinterpret_cast<float*>(smem), kS * T::kStage / 4, kLd, joined, inbox);
 }
 

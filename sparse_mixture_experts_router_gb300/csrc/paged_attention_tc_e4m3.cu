@@ -12,12 +12,13 @@
 // that meets the code is
 //   2^s v / 2^M = 2^(s + log2 v - M),
 // a fused multiply-add whose factor and addend are constants of 32 keys. (Where pages
-// do not hold whole groups of 32, and once a scale outside 2^-40 .. 2^40 has come by, whose
-// weights could leave fp32's range, it is 2^(s - M) times v.) M is the running reference of a
+// do not hold whole groups of 32 it is 2^(s - M) times v.) M is the running reference of a
 // row: when it is raised, the largest weight becomes 2^7, and it stands until one
 // passes 2^15, so that fp16 holds weights to 2^-11 of themselves down to 2^-21 of
 // the largest and none is off by more than 2^-32 of it. The sum of weights
-// is taken without v (the group's sum times 1 / v); no weight without v passes 2^68.
+// is taken without v (the group's sum times 1 / v), relative to 2^M too: scales of 2^-40 ..
+// 2^40 leave all of that in fp32's range. Once another has come by, the sum has a reference
+// of its own, which follows the scores without v, and a weight takes two exponentials.
 //
 // A block has the SM and runs two streams of tiles, each with its S and O in Tensor
 // Memory, four warps of softmax and a warp that issues its products, so that one's
@@ -67,13 +68,14 @@ struct Layout {
   static constexpr int kTile = kHalves * kHalf;  // 128 rows of Q, K or V
   static constexpr int kK = 2 * kTile, kV = 4 * kTile, kRing = 6 * kTile;
   static constexpr int kLd = kDim + 4;           // floats a row of a stream's O, to be joined
-  static constexpr int kInbox = ((int)sizeof(Inbox<kRows, kDim>) + 1023) / 1024 * 1024;
+  static constexpr int kInbox = ((int)sizeof(Inbox<kRows, kDim, true>) + 1023) / 1024 * 1024;
   static constexpr int kTiles = kRing > kInbox ? kRing : kInbox;
   static_assert(kTileRows * kLd * 4 <= kRing - kK, "a stream's O fits over K and V");
   static constexpr int kBars = 256;
-  static constexpr int kScales = 4 * 4 * kKeys * 4;  // of four tiles: of keys; of values, their log2 and inverse
+  // of four tiles: of keys; of values, their log2 and inverse
+  static constexpr int kScales = 4 * 4 * kKeys * 4;
   static constexpr int kLines = kEdgeKeys * (2 * kDim + 16);
-  static constexpr int kJoin = kTileRows * 8;
+  static constexpr int kJoin = kTileRows * (16 + 8);
   static constexpr int kAll = 1024 + kTiles + kBars + kScales + kLines + kJoin;
 };
 
@@ -84,6 +86,7 @@ struct Bars {
   uint64_t s_full[2], p_full[2], pv_done[2], drained[2];
   uint32_t tmem;
   int abort_flag;
+  int far_tile;  // the first of the block's tiles with a value's scale outside 2^-40 .. 2^40
 };
 static_assert(sizeof(Bars) <= 256, "");
 
@@ -180,7 +183,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_e4m3_kernel(const __grid_const
   Bars& bars = *reinterpret_cast<Bars*>(smem + L::kTiles);
   float* scales = reinterpret_cast<float*>(smem + L::kTiles + L::kBars);
   uint8_t* lines = reinterpret_cast<uint8_t*>(scales) + L::kScales;
-  float2* of_odd = reinterpret_cast<float2*>(lines + L::kLines);  // the odd stream's (M, sum) of a row
+  float4* of_odd = reinterpret_cast<float4*>(lines + L::kLines);  // the odd stream's (M, sum, the sum's reference) of a row
+  float* sum_refs = reinterpret_cast<float*>(of_odd + kTileRows);  // of the streams' rows, where that is not M
   const AttnArgs& a = prm.a;
   const moe_attn_config& c = a.c;
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
@@ -212,6 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_e4m3_kernel(const __grid_const
       ptx::mbar_init(ptx::smem_addr(&bars.drained[i]), 1);
     }
     bars.abort_flag = 0;
+    bars.far_tile = 0x7fffffff;
     ptx::fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -313,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_e4m3_kernel(const __grid_const
     // A score's factor with its key's scale: never 0 (a query of zeros, a page of zeros), by
     // which -inf would be NaN; products are below 2^33, so the least normal number is 0 to them.
     auto by = [&](float key_scale) { return fmaxf(factor * key_scale, FLT_MIN); };
-    bool wide = false;  // scales outside 2^-40 .. 2^40 have come by
+    sum_refs[threadIdx.x] = -INFINITY;  // not in use
     // of the stream's first tile's columns, from .. to - 1 are keys that the row sees
     int from = max(first, seen.lo_min) - key0 - tile_of(st, 0) * kKeys;
     int to = min(pos, seen.hi_max) + 1 - key0 - tile_of(st, 0) * kKeys;
@@ -322,89 +327,136 @@ __global__ void __launch_bounds__(kThreads, 1) tc_e4m3_kernel(const __grid_const
         ptx::tc_fence_after();
         const float* fk = scales + (tile_of(st, t) & 3) * 4 * kKeys;
         const float *fv = fk + kKeys, *ev = fv + kKeys, *iv = ev + kKeys;
-        const bool edge = __any_sync(0xffffffffu, from > 0 || to < kKeys);
-        uint32_t w[kGroups][32];
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) ptx::tmem_ld32(s_at + kGroup * g, w[g]);
-        // the largest score, and the largest with its value's scale
-        float top = -INFINITY, top_v = -INFINITY;
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          tmem_ready(w[g]);
-          if (edge) {
-#pragma unroll
-            for (int x = 0; x < kGroup; ++x)
-              if (kGroup * g + x < from || kGroup * g + x >= to) w[g][x] = 0xff800000u;  // -inf
-          }
-          if (kUniform) {
-            float u[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int x = 0; x < 32; ++x) u[x % 4] = fmaxf(u[x % 4], __uint_as_float(w[g][x]));
-            const float v = fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])) * by(fk[g]), e = ev[g];
-            top = fmaxf(top, v);
-            top_v = fmaxf(top_v, v + e);
-            wide = wide || !(fabsf(e) <= 40.f);
-          } else {
-#pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              const float u = __uint_as_float(w[g][x]) * by(fk[kGroup * g + x]);
-              top = fmaxf(top, u);
-              top_v = fmaxf(top_v, u + ev[kGroup * g + x]);
-            }
-          }
-        }
-        const bool raise = top_v > m + 15.f || top > m + 68.f;
-        if (__any_sync(0xffffffffu, raise)) {
-          const float up = raise ? fmaxf(top_v - 7.f, top - 60.f) : m, f = ptx::ex2(m - up);
-          m = up;
-          l *= f;
-          if (t > 0) {  // O is still while P of this tile is not there
+        auto scale_o = [&](float f) {  // O is still while P of this tile is not there
 #pragma unroll 1
-            for (int x = 0; x < kDim; x += 16) {
-              uint32_t o[16];
-              ptx::tmem_ld16(o_at + x, o);
-              ptx::tmem_ld_wait();
+          for (int x = 0; x < kDim; x += 16) {
+            uint32_t o[16];
+            ptx::tmem_ld16(o_at + x, o);
+            ptx::tmem_ld_wait();
 #pragma unroll
-              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-              ptx::tmem_st16(o_at + x, o);
+            for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+            ptx::tmem_st16(o_at + x, o);
+          }
+        };
+        if (__builtin_expect(tile_of(st, t) >= *const_cast<volatile int*>(&bars.far_tile), 0)) {
+          // A scale outside 2^-40 .. 2^40 has come by, in this tile or before (either stream's).
+          float top = -INFINITY, top_v = -INFINITY;
+          uint32_t s[32];
+          auto score = [&](int g, int x) {
+            const bool seen_here = kGroup * g + x >= from && kGroup * g + x < to;
+            return seen_here ? __uint_as_float(s[x]) * by(fk[kUniform ? g : kGroup * g + x]) : -INFINITY;
+          };
+#pragma unroll 1
+          for (int g = 0; g < kGroups; ++g) {
+            ptx::tmem_ld32(s_at + kGroup * g, s);
+            tmem_ready(s);
+#pragma unroll
+            for (int x = 0; x < kGroup; ++x) {
+              const float v = score(g, x);
+              top = fmaxf(top, v);
+              top_v = fmaxf(top_v, v + ev[kUniform ? g : kGroup * g + x]);
             }
           }
-        }
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          uint64_t sum[2] = {0, 0};
-          uint32_t p[16];
-          if (kUniform && !wide) {
-            const float f1 = by(fk[g]), a1 = ev[g] - m;
-            const uint64_t f2 = ptx::f32x2(f1, f1), a2 = ptx::f32x2(a1, a1);
-#pragma unroll
-            for (int y = 0; y < 16; ++y) {
-              const uint64_t v = ptx::fma_f32x2((uint64_t)w[g][2 * y + 1] << 32 | w[g][2 * y], f2, a2);
-              const float lo = ptx::ex2(ptx::f32x2_lo(v)), hi = ptx::ex2(ptx::f32x2_hi(v));
-              sum[y % 2] = ptx::add_f32x2(sum[y % 2], ptx::f32x2(lo, hi));
-              p[y] = pack_f16(lo, hi);
-            }
-            sum[0] = ptx::add_f32x2(sum[0], sum[1]);
-            l = fmaf(ptx::f32x2_lo(sum[0]) + ptx::f32x2_hi(sum[0]), iv[g], l);
-          } else {
-#pragma unroll
-            for (int y = 0; y < 16; ++y) {
-              const int k = kUniform ? g : kGroup * g + 2 * y, k1 = kUniform ? g : k + 1;
-              const float lo = ptx::ex2(fmaf(__uint_as_float(w[g][2 * y]), by(fk[k]), -m));
-              const float hi = ptx::ex2(fmaf(__uint_as_float(w[g][2 * y + 1]), by(fk[k1]), -m));
-              sum[y % 2] = ptx::add_f32x2(sum[y % 2], ptx::f32x2(lo, hi));
-              p[y] = pack_f16(lo * fv[k], hi * fv[k1]);
-            }
-            sum[0] = ptx::add_f32x2(sum[0], sum[1]);
-            l += ptx::f32x2_lo(sum[0]) + ptx::f32x2_hi(sum[0]);
+          const float was = sum_refs[threadIdx.x] == -INFINITY ? m : sum_refs[threadIdx.x];
+          const float ref = top > was + 8.f ? top : was;
+          sum_refs[threadIdx.x] = ref;
+          l *= ptx::ex2(was - ref);
+          const bool raise = top_v > m + 15.f;
+          if (__any_sync(0xffffffffu, raise)) {
+            const float up = raise ? top_v - 7.f : m, f = ptx::ex2(m - up);
+            m = up;
+            if (t > 0) scale_o(f);
           }
-          ptx::tmem_st16(s_at + 16 * g, p);  // over scores, which are in registers
+#pragma unroll 1
+          for (int g = 0; g < kGroups; ++g) {
+            uint32_t p[16];
+            ptx::tmem_ld32(s_at + kGroup * g, s);
+            tmem_ready(s);
+            auto weight = [&](int x) {
+              const float v = score(g, x);
+              l += ptx::ex2(v - ref);
+              // 0 for a key that is not seen, whatever its scale
+              return v == -INFINITY ? 0.f : ptx::ex2(v + (ev[kUniform ? g : kGroup * g + x] - m));
+            };
+#pragma unroll
+            for (int y = 0; y < 16; ++y) {
+              const float lo = weight(2 * y);
+              p[y] = pack_f16(lo, weight(2 * y + 1));
+            }
+            ptx::tmem_st16(s_at + 16 * g, p);  // over scores of this group or of one before
+          }
+        } else {
+          const bool edge = __any_sync(0xffffffffu, from > 0 || to < kKeys);
+          uint32_t w[kGroups][32];
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) ptx::tmem_ld32(s_at + kGroup * g, w[g]);
+          // the largest score with its value's scale (without it, it is at most 40 more)
+          float top_v = -INFINITY;
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) {
+            tmem_ready(w[g]);
+            if (edge) {
+#pragma unroll
+              for (int x = 0; x < kGroup; ++x)
+                if (kGroup * g + x < from || kGroup * g + x >= to) w[g][x] = 0xff800000u;  // -inf
+            }
+            if (kUniform) {
+              float u[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int x = 0; x < 32; ++x) u[x % 4] = fmaxf(u[x % 4], __uint_as_float(w[g][x]));
+              top_v = fmaxf(top_v, fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])) * by(fk[g]) + ev[g]);
+            } else {
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                top_v = fmaxf(top_v, __uint_as_float(w[g][x]) * by(fk[kGroup * g + x]) + ev[kGroup * g + x]);
+            }
+          }
+          const bool raise = top_v > m + 15.f;
+          if (__any_sync(0xffffffffu, raise)) {
+            const float up = raise ? top_v - 7.f : m, f = ptx::ex2(m - up);
+            m = up;
+            l *= f;
+            if (t > 0) scale_o(f);
+          }
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) {
+            uint64_t sum[2] = {0, 0};
+            uint32_t p[16];
+            if (kUniform) {
+              const float f1 = by(fk[g]), a1 = ev[g] - m;
+              const uint64_t f2 = ptx::f32x2(f1, f1), a2 = ptx::f32x2(a1, a1);
+#pragma unroll
+              for (int y = 0; y < 16; ++y) {
+                const uint64_t v = ptx::fma_f32x2((uint64_t)w[g][2 * y + 1] << 32 | w[g][2 * y], f2, a2);
+                const float lo = ptx::ex2(ptx::f32x2_lo(v)), hi = ptx::ex2(ptx::f32x2_hi(v));
+                sum[y % 2] = ptx::add_f32x2(sum[y % 2], ptx::f32x2(lo, hi));
+                p[y] = pack_f16(lo, hi);
+              }
+              sum[0] = ptx::add_f32x2(sum[0], sum[1]);
+              l = fmaf(ptx::f32x2_lo(sum[0]) + ptx::f32x2_hi(sum[0]), iv[g], l);
+            } else {
+#pragma unroll
+              for (int y = 0; y < 16; ++y) {
+                const int k = kGroup * g + 2 * y, k1 = k + 1;
+                const float lo = ptx::ex2(fmaf(__uint_as_float(w[g][2 * y]), by(fk[k]), -m));
+                const float hi = ptx::ex2(fmaf(__uint_as_float(w[g][2 * y + 1]), by(fk[k1]), -m));
+                sum[y % 2] = ptx::add_f32x2(sum[y % 2], ptx::f32x2(lo, hi));
+                p[y] = pack_f16(lo * fv[k], hi * fv[k1]);
+              }
+              sum[0] = ptx::add_f32x2(sum[0], sum[1]);
+              l += ptx::f32x2_lo(sum[0]) + ptx::f32x2_hi(sum[0]);
+            }
+            ptx::tmem_st16(s_at + 16 * g, p);  // over scores, which are in registers
+          }
         }
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
       }
       ptx::mbar_arrive(ptx::smem_addr(&bars.p_full[st]));
     }
+
+    float l_ref = sum_refs[threadIdx.x];
+    if (l_ref == -INFINITY) l_ref = m;
 
     // ---- the keys that only some rows see, where a value is NaN ----
     const bool go = my_tiles == 0 || warp_wait(bars.pv_done[st], my_tiles - 1);
@@ -453,11 +505,17 @@ __global__ void __launch_bounds__(kThreads, 1) tc_e4m3_kernel(const __grid_const
               dot = fmaf(qx.x, kx.x, fmaf(qx.y, kx.y, dot));
             }
           }
-          // weight and O relative to the largest of both, in fp32
+          // weight (with its value's scale) and O relative to the largest of both, in fp32; the
+          // sum to its own
           const float s = dot * (factor * line_scale[2 * (e - e0)]), vs = line_scale[2 * (e - e0) + 1];
-          const float up = see && s > m ? s : m, f = ptx::ex2(m - up), p = see ? ptx::ex2(s - up) : 0.f;
+          const bool usual = vs > 0.f && vs < INFINITY;
+          const float sv = usual ? s + __log2f(vs) : s;
+          const float up = see && sv > m ? sv : m, f = ptx::ex2(m - up);
+          const float p = see ? ptx::ex2(sv - up) * (usual ? 1.f : vs) : 0.f;
           m = up;
-          l = l * f + p;
+          const float ref = see && s > l_ref ? s : l_ref;
+          l = l * ptx::ex2(l_ref - ref) + (see ? ptx::ex2(s - ref) : 0.f);
+          l_ref = ref;
           for (int x = 0; x < kDim; x += 32) {
             uint32_t o[32];
             ptx::tmem_ld32(o_at + x, o);
@@ -466,8 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_e4m3_kernel(const __grid_const
             for (int y = 0; y < 32; y += 2) {
               const float2 v = unpack_f16(codes_f16(*reinterpret_cast<const uint16_t*>(line + kDim + x + y)));
               const float o0 = __uint_as_float(o[y]) * f, o1 = __uint_as_float(o[y + 1]) * f;
-              o[y] = __float_as_uint(see ? fmaf(p * vs, v.x, o0) : o0);
-              o[y + 1] = __float_as_uint(see ? fmaf(p * vs, v.y, o1) : o1);
+              o[y] = __float_as_uint(see ? fmaf(p, v.x, o0) : o0);
+              o[y + 1] = __float_as_uint(see ? fmaf(p, v.y, o1) : o1);
             }
             tmem_st32(o_at + x, o);
           }
@@ -484,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_e4m3_kernel(const __grid_const
       // the odd stream leaves its O to the even one
       softmax_sync();  // both streams' products are done
       if (st == 1) {
-        of_odd[row_in] = make_float2(m, l);
+        of_odd[row_in] = make_float4(m, l, l_ref, 0.f);
         if (active && any) {
 #pragma unroll 1
           for (int x = 0; x < kDim; x += 32) {
@@ -499,12 +557,13 @@ __global__ void __launch_bounds__(kThreads, 1) tc_e4m3_kernel(const __grid_const
       }
       softmax_sync();
       if (st == 0) {
-        const float2 odd = of_odd[row_in];
-        const float up = fmaxf(m, odd.x);
+        const float4 odd = of_odd[row_in];
+        const float up = fmaxf(m, odd.x), ref = fmaxf(l_ref, odd.z);
         scale_o = ptx::ex2(m - up);
         scale_odd = ptx::ex2(odd.x - up);
         m = up;
-        l = l * scale_o + odd.y * scale_odd;
+        l = l * ptx::ex2(l_ref - ref) + odd.y * ptx::ex2(odd.z - ref);
+        l_ref = ref;
       }
     }
     const bool odd_any = !by_rows && tiles_of(1) > 0;
@@ -531,8 +590,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_e4m3_kernel(const __grid_const
 #pragma unroll
             for (int y = 0; y < 32; y += 4)
               if (x + y < c.head_dim)
-                write_row<__nv_bfloat16>(prm, it, row, (x + y) / 4, make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]),
-                                         m, l);
+                write_row<__nv_bfloat16, true>(prm, it, row, (x + y) / 4,
+                                               make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]), l_ref, l, m);
           }
         }
       }
@@ -540,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_e4m3_kernel(const __grid_const
       __syncthreads();
     } else {
       // O leaves Tensor Memory before every block's tiles are free for what the others send.
-      auto* inbox = reinterpret_cast<Inbox<kRows, kDim>*>(smem);
+      auto* inbox = reinterpret_cast<Inbox<kRows, kDim, true>*>(smem);
       float o[kDim / 32][32];
       if (writes) {
 #pragma unroll
@@ -551,8 +610,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_e4m3_kernel(const __grid_const
       ptx::cluster_sync();
       const int slice = div(prm.by_parts, it.rows * vecs + prm.parts - 1);
       if (writes && row < it.rows) {
-        for (int b = 0; b < prm.parts; ++b)
-          ptx::st_cluster_v2(ptx::mapa_shared(ptx::smem_addr(&inbox->ml[it.part][row]), b), m, l);
+        for (int b = 0; b < prm.parts; ++b) {
+          ptx::st_cluster_v2(ptx::mapa_shared(ptx::smem_addr(&inbox->ml[it.part][row]), b), l_ref, l);
+          ptx::st_cluster(ptx::mapa_shared(ptx::smem_addr(&inbox->ref[it.part][row]), b), m);
+        }
         int i = row * vecs, to_block = i / slice;
 #pragma unroll
         for (int x = 0; x < kDim; x += 4) {
@@ -567,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_e4m3_kernel(const __grid_const
       __syncwarp();
       ptx::cluster_sync();
       __syncthreads();
-      join_slices<kRows, kDim, 32 * kSoftmaxWarps, __nv_bfloat16>(prm, it, inbox);
+      join_slices<kRows, kDim, 32 * kSoftmaxWarps, __nv_bfloat16, true>(prm, it, inbox);
     }
   } else if (warp >= kMmaWarp) {
     fewer_registers<kMmaRegs>();
@@ -739,7 +800,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_e4m3_kernel(const __grid_const
         const float ks = now.in ? now.ks : 1.f, vs = now.in ? now.vs : 1.f;
         fk[k] = ks;
         fk[kKeys + k] = vs;
-        fk[2 * kKeys + k] = __log2f(vs);
+        const float log_vs = __log2f(vs);
+        fk[2 * kKeys + k] = log_vs;
+        if (!(fabsf(log_vs) <= 40.f)) atomicMin(&bars.far_tile, i);
         if (kUniform) fk[3 * kKeys + k] = __frcp_rn(vs);
       }
       ptx::mbar_arrive(ptx::smem_addr(&bars.k_full[slot]));

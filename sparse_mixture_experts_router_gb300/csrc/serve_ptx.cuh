@@ -112,6 +112,9 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 // Writes to the shared memory of a CTA of the cluster (shared::cluster address).
+__device__ __forceinline__ void st_cluster(uint32_t addr, float x) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
+}
 __device__ __forceinline__ void st_cluster_v2(uint32_t addr, float x, float y) {
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
 }
