@@ -8,7 +8,8 @@ pool of pages: a prompt is computed and kept once, its samples share its pages.
                          drafted) -> moe_pages_update -> qkv -> ... -> logits
 
 without a host synchronisation between the calls. The cache holds E4M3 codes under one scale
-a page and head; tokens that a sample has had are penalised. Weights are random; run it as
+a page and head; tokens that a sample has had are penalised. A sample that the pool has no
+room for appends nothing, and stops or waits for the next step. Weights are random; run it as
 
     python examples/sample_prompts.py
 """
@@ -27,10 +28,11 @@ def ints(x):
 
 
 class Samples:
-    """`samples` sequences for each of `prompts` (lists of tokens), with room for `steps` tokens."""
+    """`samples` sequences for each of `prompts` (lists of tokens), with room for `steps` tokens, or in
+    a pool of so many `pages`."""
 
     def __init__(self, prompts, samples, steps, d_model=256, heads=8, kv_heads=2, dim=64, experts=8, top_k=2, d_ff=512, vocab=512,
-                 page=32, temperature=1.0, frequency=0.5, repetition=1.1, seed=0):
+                 page=32, temperature=1.0, frequency=0.5, repetition=1.1, seed=0, pages=None):
         self.prompts, self.S, self.V = prompts, samples, vocab
         self.B = B = len(prompts) * samples
         self.heads, self.kv_heads, self.dim, self.d_model = heads, kv_heads, dim, d_model
@@ -49,12 +51,13 @@ class Samples:
         # the pool: the prompts' pages, and each sample's own
         longest = max(len(p) for p in prompts) + steps + 1
         columns = -(-longest // page)
-        self.pages = sum(-(-len(p) // page) for p in prompts) + B * (-(-(steps + 1) // page) + 2)
+        self.pages = pages or sum(-(-len(p) // page) for p in prompts) + B * (-(-(steps + 1) // page) + 2)
         self.k_cache, self.v_cache = (torch.zeros((self.pages, page, kv_heads, dim), dtype=torch.uint8, device="cuda") for _ in range(2))
         self.k_scale, self.v_scale = (torch.zeros((self.pages, kv_heads), device="cuda") for _ in range(2))
         self.tables = [torch.zeros((B, columns), dtype=torch.int32, device="cuda") for _ in range(2)]
         self.refs = torch.zeros(self.pages, dtype=torch.int32, device="cuda")
         self.length = torch.zeros(B, dtype=torch.int32, device="cuda")  # tokens there is room for
+        self.live = torch.ones(B, dtype=torch.bool, device="cuda")  # samples that go on
         self.ws, self.columns, self.page = {}, columns, page
         self.layers = dict(d_model=d_model, n_experts=experts, top_k=top_k, d_ff=d_ff)
 
@@ -91,6 +94,16 @@ class Samples:
                              self.k_scale, self.v_scale, self.workspace("pages", cfg, "pages"))
         self.tables, self.length = [new, old], need
 
+    def grow(self, parent, kept):
+        """Room for one more token behind `kept` of each sample that goes on. A refused one keeps what it
+        has (its granted length is `kept`): a token written all the same would go over the last one it
+        has, in a page that others may hold. The first refused one does not fit, and stops; those behind
+        it are refused with it, and ask again with the next step."""
+        self.update(parent, kept, kept + self.live.int())
+        self.room = self.live & (self.length > kept)
+        refused = self.live & ~self.room
+        self.live = self.live & ~(refused & (refused.cumsum(0) == 1))
+
     def block(self, name, tokens, cu, length, most):
         """The block's output rows of new tokens, whose keys and values go into the pages."""
         T, wide = tokens.numel(), (self.heads + 2 * self.kv_heads) * self.dim
@@ -120,8 +133,9 @@ class Samples:
         x = self.block("prompts", ints([t for p in self.prompts for t in p]), ints(cu), self.length, max(first))
         ends = ints([cu[i * self.S + 1] - 1 for i in range(len(self.prompts))]).long().repeat_interleave(self.S)
         parent = ints([b // self.S * self.S for b in range(self.B)])
-        kept = self.n_prompt.clone()
-        self.update(parent, kept, kept + 1)
+        kept = self.length[parent.long()]
+        self.live = kept > 0  # a prompt that found no room has none
+        self.grow(parent, kept)
         return (x[ends] @ self.w_out.t()).float()
 
     def draw(self, logits):
@@ -136,16 +150,18 @@ class Samples:
         return tokens
 
     def generate(self, steps):
-        """[B][steps] tokens."""
+        """[B][steps] tokens, -1 where a sample had no room."""
         logits, out = self.start(), []
         for _ in range(steps):
-            tokens = self.draw(logits)
+            tokens = torch.where(self.room, self.draw(logits), -1)
             out.append(tokens)
             # self.length counts the token just drawn: it goes behind what is cached
-            self.history.scatter_(1, self.length.long()[:, None] - 1, tokens[:, None])
-            x = self.block("step", tokens, self.one_each, self.length, 1)
-            logits = (x @ self.w_out.t()).float()
-            self.update(None, self.length, self.length + 1)
+            at = (self.length.long()[:, None] - 1).clamp(min=0)
+            self.history.scatter_(1, at, torch.where(self.room[:, None], tokens[:, None], self.history.gather(1, at)))
+            # length 0: a token without a slot is not written (and recorded by the append)
+            x = self.block("step", tokens, self.one_each, torch.where(self.room, self.length, 0), 1)
+            logits = torch.where(self.room[:, None], (x @ self.w_out.t()).float(), logits)
+            self.grow(None, self.length)
         return torch.stack(out, 1)
 
     def status(self):
@@ -161,10 +177,11 @@ def main():
     prompts = [[(7 * i + 3 * t) % 512 for t in range(40 + 25 * i)] for i in range(a.prompts)]
     s = Samples(prompts, a.samples, a.steps)
     out = s.generate(a.steps)
-    assert not any(s.status().values()), s.status()
+    stopped = int((~s.live).sum())
+    assert stopped or not any(s.status().values()), s.status()
     held = int((s.refs > 0).sum())
     alone = sum(-(-int(n) // s.page) for n in s.length.tolist())
-    print(f"{out.numel()} tokens of {s.B} samples; {held} pages held, {alone} if none were shared")
+    print(f"{out.numel()} tokens of {s.B} samples; {held} pages held, {alone} if none were shared; {stopped} stopped for want of room")
     print("first samples:", *out[:2, :12].tolist(), sep="\n  ")
 
 

@@ -841,6 +841,11 @@ MOE_API int moe_logits_probs(const moe_logits_config* cfg, const void* logits,
  * in the order of its entries. When they run out, sequences whose wants, added up in
  * order, pass the number of free pages get none: granted[b] = kept[b] where need[b]
  * is granted otherwise (a page given up by copy on write is free in the next call).
+ * The sum counts those refused before: behind the first refused sequence every one is,
+ * also one that wants no page for its need. This is no error and leaves the status
+ * word alone: a caller that goes on without looking (no host synchronisation) gives
+ * a refused sequence a kv_len of 0 in the append, where its tokens are then without a slot
+ * (recorded there, and not written); at granted[b] they would go over kept ones.
  *
  *  parent     [device] [B] int32, -1 (no tokens) .. B-1, or NULL: b.
  *  len        [device] [B] int32: tokens held, in the tables as they are.
