@@ -10,8 +10,8 @@
 // So the new tokens of one page have to meet before any of them is written: an
 // item is a (sequence, page) that the call touches. Sequence b's items start at
 // floor(cu_new[b] / page_size) + 2 b, which leaves each sequence at least as many
-// as n tokens can touch (1 + ceil((n - 1) / page_size)); with one new token a
-// sequence, at b. A block takes an item, or some heads of it: a warp a row (several
+// as n tokens can touch (1 + ceil((n - 1) / page_size)); where no sequence has more
+// than one new token, item b is sequence b's. A block takes an item, or some heads of it: a warp a row (several
 // a row where there are few), so that a row's sines are computed once for all its
 // heads, a group of lanes a head. It goes over the rows twice, for the maxima (and the
 // queries, which are done then) and to write keys and values; a warp with one row
@@ -62,15 +62,19 @@ struct PageItem {
 };
 // The item of index i (false: none), found by a whole block.
 template <int kThreads>
-__device__ __forceinline__ bool page_item(const AttnArgs& a, const FastDiv& by_page, int per_seq,
-                                          int index, int lane, PageItem& it) {
+__device__ __forceinline__ bool page_item(const AttnArgs& a, const FastDiv& by_page, int index, int lane,
+                                          PageItem& it) {
   const moe_attn_config& c = a.c;
-  auto start_of = [&](int cu, int b) { return div(by_page, clamp_int(cu, 0, c.n_tokens)) + per_seq * b; };
+  auto start_of = [&](int cu, int b) {
+    return c.max_new == 1 ? b : div(by_page, clamp_int(cu, 0, c.n_tokens)) + 2 * b;
+  };
   auto start = [&](int b) { return start_of(__ldg(a.cu_new + b), b); };
   // the first sequence whose items end after index: counted in one round trip where the
   // threads hold the list, else found in steps of 32 comparisons
   int lo = 0;
-  if (c.n_seqs <= kThreads) {
+  if (c.max_new == 1) {
+    lo = index;
+  } else if (c.n_seqs <= kThreads) {
     const int t = threadIdx.x;
     lo = __syncthreads_count(t < c.n_seqs && start(t + 1) <= index);
   } else {
@@ -103,7 +107,7 @@ __device__ __forceinline__ bool page_item(const AttnArgs& a, const FastDiv& by_p
 template <int kWarps, int kUnits>
 __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
     rope_append_page_kernel(const AttnArgs a, const __grid_constant__ RopeTable rope,
-                            const FastDiv by_page, int lane_bits, int per_seq) {
+                            const FastDiv by_page, int lane_bits) {
   using T = __nv_bfloat16;
   constexpr int kThreads = 32 * kWarps;
   __shared__ float2 turns[kWarps][kMaxPairs + kMaxPairs / 8];  // (cos, sin) of a row's pairs, padded
@@ -127,7 +131,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
     return;
   }
   PageItem it;
-  if (!page_item<kThreads>(a, by_page, per_seq, (int)blockIdx.x - 1, lane, it)) return;
+  if (!page_item<kThreads>(a, by_page, (int)blockIdx.x - 1, lane, it)) return;
 
   // This block's heads: j * G + y of the keys, of the values and of the queries.
   const int y = blockIdx.y, G = gridDim.y;
@@ -365,8 +369,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
 cudaError_t launch_rope_append_page(const AttnArgs& a, const RopeTable& rope, int lane_bits,
                                     cudaStream_t s) {
   const moe_attn_config& c = a.c;
-  const int per_seq = c.max_new == 1 ? 1 : 2;
-  const long long items = c.n_tokens / c.page_size + (long long)per_seq * c.n_seqs;
+  const long long items = c.max_new == 1 ? c.n_seqs : c.n_tokens / c.page_size + 2LL * c.n_seqs;
   // Prompts, whose items have a row for each of 16 warps: a block an item, with four heads
   // in flight (two: 67 us for 59, 8197 tokens). Else blocks of 8 warps with two (four: 12.6
   // us for 11.2, 225 tokens of 64 sequences), and an item's heads over several
@@ -381,10 +384,8 @@ cudaError_t launch_rope_append_page(const AttnArgs& a, const RopeTable& rope, in
     split *= 2;
   const FastDiv by_page = fast_div((uint32_t)c.page_size);
   const dim3 grid((unsigned)items + 1, (unsigned)split), block((unsigned)(32 * warps));
-  return wide ? launch_pdl(rope_append_page_kernel<16, 4>, grid, block, 0, s, 1, a, rope, by_page, lane_bits,
-                           per_seq)
-              : launch_pdl(rope_append_page_kernel<8, 2>, grid, block, 0, s, 1, a, rope, by_page, lane_bits,
-                           per_seq);
+  return wide ? launch_pdl(rope_append_page_kernel<16, 4>, grid, block, 0, s, 1, a, rope, by_page, lane_bits)
+              : launch_pdl(rope_append_page_kernel<8, 2>, grid, block, 0, s, 1, a, rope, by_page, lane_bits);
 }
 
 }  // namespace moe
