@@ -429,7 +429,9 @@ def moe_pages_compact(cfg, length, block_table, refs, table_out, refs_out, page_
 
 def moe_pages_copy(cfg, src, dst, n_src_pages, k_from, v_from, k_from_scale, v_from_scale, k_cache,
                    v_cache, k_scale, v_scale, ws, stream=None):
-    """Copies pages src[i] (of n_src_pages) to pages dst[i]."""
+    """Copies pages src[i] (of n_src_pages) to pages dst[i]; the lists are equally long."""
+    if src.numel() != dst.numel():
+        _check("moe_pages_copy", MOE_ERR_INVALID_ARG)
     _check("moe_pages_copy", lib().moe_pages_copy(
         ctypes.byref(cfg), src.numel(), _ptr(src), _ptr(dst), n_src_pages, _ptr(k_from),
         _ptr(v_from), _ptr(k_from_scale), _ptr(v_from_scale), _ptr(k_cache), _ptr(v_cache),
