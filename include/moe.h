@@ -783,7 +783,8 @@ MOE_API int moe_verify_drafts(const moe_verify_config* cfg, const void* p, const
  *  temperature [device] [B] fp32, or NULL: 1. >= 0, finite.
  *  p          [device] [T][V] cfg->out_dtype out, p_stride between rows; may be
  *             logits if dtypes and strides are equal. cfg->out_logits: x times
- *             1 / temperature (x itself for 0) and no softmax.
+ *             1 / temperature (at most fp32's largest number; x itself for 0) and no
+ *             softmax.
  *  ws         [device] moe_logits_workspace_size(cfg) bytes.
  * MOE_ERR_DEVICE_CHECK: cu_new as above; cu_history or cu_bias not ascending from 0
  * to n_history or n_bias; n_prompt outside the history's length; a token (of the

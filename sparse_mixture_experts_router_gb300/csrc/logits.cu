@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, kHeld > 16 ? 2 : 4)
       const int v0 = v_begin + t * kTileVecs;
       if (t > 0) load(v0), load_mask(v0);
       take(v0);
-      write(v0, inv_t);
+      write(v0, fminf(inv_t, FLT_MAX));  // a subnormal temperature's inverse is infinite, by which 0 is NaN
     }
     ptx::cluster_wait();
     return;

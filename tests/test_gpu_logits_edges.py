@@ -31,3 +31,20 @@ def test_rows_in_place_leave_what_is_between_them(dtype):
     assert moe.moe_stream_status(ws) == 0
     assert np.array_equal(p[:, :45].double().cpu().numpy(), want)
     assert torch.equal(p[:, 45:].cpu(), r.logits[:, 45:].to(TORCH[dtype]))
+
+
+def test_logits_out_over_the_least_temperatures():
+    """1 / temperature is infinite in fp32 from 2^-128 down: 0 stays 0, others become large or infinite
+    with their sign, by fp32's largest number."""
+    x = torch.tensor([0.0, -0.0, 1e-10, -1e-10, 1.0, -1.0, 3.0, -3.0, float("-inf"), float("inf")])
+    top = float(torch.finfo(torch.float32).max)
+    for temp in (2.0 ** -149, 1e-40, 2.0 ** -129):
+        cfg = moe.logits_config(n_seqs=1, n_tokens=1, vocab=x.numel(), out_logits=True)
+        ws = moe.workspace(cfg, "logits")
+        p = torch.empty((1, x.numel()), device="cuda")
+        cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+        t = torch.tensor([temp], device="cuda")
+        moe.moe_logits_probs(cfg, x[None].cuda(), cu, *[None] * 12, t, p, ws)
+        assert moe.moe_stream_status(ws) == 0
+        want = (x.double() * min(1 / temp, top)).float()
+        assert torch.allclose(p[0].cpu(), want, rtol=2.0 ** -23, atol=0.0), (temp, p)
