@@ -398,13 +398,8 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
     // Weights against the running maximum; over the bound, the maximum is
     // raised and they are taken again.
     float p[kMT][kNT][4];
-    float vs_max = kF8 ? fmaxf(vs[0][0], vs[0][1]) : 0.f;
-    if (kF8) {
-#pragma unroll
-      for (int t = 1; t < kMT; ++t) vs_max = fmaxf(fmaxf(vs_max, vs[t][0]), vs[t][1]);
-    }
-    bool raise = kApart || vs_max > 0x1p80f;
-    // This lane's largest score of a row, and its largest with the value's scale.
+    // This lane's largest score of a row, and its largest with the value's scale (an infinite
+    // scale aside: the sum of weights does not see values).
     auto tops = [&](int n, int j, float& top, float& top_v) {
       top = top_v = -INFINITY;
 #pragma unroll
@@ -437,7 +432,31 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
             if (key > seen.x || key < seen.y) s[t][n][x] = -INFINITY;
           }
         }
+      if (kF8) {  // a key that no row sees has a scale of 0 here
+#pragma unroll
+        for (int t = 0; t < kMT; ++t)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int key = key0 + 16 * t + T::key_of(8 * h + oct);
+            if (key > rg.hi_max || key < rg.lo_min) vs[t][h] = 1.f;
+          }
+      }
     }
+    // Scales for which l and O can share a reference: where weights are up to 2^15 with them, they
+    // are up to 2^68 without, and none that fp32 has flushed to 0 would be above 2^-46 with them.
+    // (By their bits, which order positive numbers and leave a NaN above them.)
+    uint32_t least = __float_as_uint(1.f), most = least;
+    if (kF8) {
+#pragma unroll
+      for (int t = 0; t < kMT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          least = min(least, __float_as_uint(vs[t][h]));
+          most = max(most, __float_as_uint(vs[t][h]));
+        }
+    }
+    const bool far = least < (127u - 53u) << 23 || most > (127u + 80u) << 23;
+    bool raise = kApart || far;
 #pragma unroll
     for (int t = 0; t < kMT; ++t)
 #pragma unroll
@@ -449,40 +468,23 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
           if (!kF8)
             raise = raise || v > m[n][x % 2] + 8.f;
           else  // 0 * vs may be a NaN of a key that is not seen
-            raise = raise || !(p[t][n][x] <= 0x1p68f) ||
-                    (v != -INFINITY && !(p[t][n][x] * vs[t][x / 2] <= 0x1p15f));
+            raise = raise || (v != -INFINITY && !(p[t][n][x] * vs[t][x / 2] <= 0x1p15f));
         }
     if (!kApart && __any_sync(0xffffffffu, raise)) {
-      // The reference that each row asks for. E4M3: the largest weight times its value's scale
-      // becomes 2^7 (an infinite scale aside: the sum of weights does not see values), and no
-      // weight itself is above 2^60.
-      float up[kNT][2];
-      // l needs a reference of its own: fp32 may have lost weights that so large a scale makes
-      // count, or a lane's weights without their scales ask for more.
-      bool part = vs_max > 0x1p80f;
+      if (kF8 && __any_sync(0xffffffffu, far)) return false;
 #pragma unroll
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
+          // E4M3: the largest weight times its value's scale becomes 2^7.
           float top, top_v;
           tops(n, j, top, top_v);
-          float u = top;
-          if (kF8) {
-            top_v -= 7.f, top -= 60.f;
-            part = part || top > fmaxf(top_v, m[n][j]);
-            u = fmaxf(top_v, top);
-          }
+          float up = kF8 ? top_v - 7.f : top;
 #pragma unroll
-          for (int x = 4; x < 32; x *= 2) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, x));
-          up[n][j] = fmaxf(m[n][j], u);
-        }
-      if (kF8 && __any_sync(0xffffffffu, part)) return false;
-#pragma unroll
-      for (int n = 0; n < kNT; ++n)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float f = ptx::ex2(m[n][j] - up[n][j]);
-          m[n][j] = up[n][j];
+          for (int x = 4; x < 32; x *= 2) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, x));
+          up = fmaxf(m[n][j], up);
+          const float f = ptx::ex2(m[n][j] - up);
+          m[n][j] = up;
           l[n][j] *= f;
 #pragma unroll
           for (int d = 0; d < kDT; ++d) {
@@ -492,7 +494,7 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
 #pragma unroll
           for (int t = 0; t < kMT; ++t)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) p[t][n][2 * h + j] = ptx::ex2(s[t][n][2 * h + j] - m[n][j]);
+            for (int h = 0; h < 2; ++h) p[t][n][2 * h + j] = ptx::ex2(s[t][n][2 * h + j] - up);
         }
     }
     if (kApart) {
