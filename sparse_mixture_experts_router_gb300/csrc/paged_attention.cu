@@ -27,8 +27,11 @@ namespace {
 //   2 of 20000, D 128                         89 and  52    90 and  98
 constexpr int kTcRows = 48;
 // The same of an E4M3 cache with a scale a page. us of the warp-level kernel and of the
-// tcgen05 kernel (32 sequences of 100 to 12000 keys, 8 key-value heads, 8 new tokens, D 128,
-// pages of 64): 64 rows 314 and 314, 80: 380 and 319, 96: 446 and 322, 128: 572 and 330.
+// tcgen05 kernel (32 sequences of 100 to 12000 keys, 8 key-value heads, 8 new tokens, D 128):
+//             48 rows       64            80            128
+//   pages of 64  245 and 267   304 and 269   358 and 272   532 and 286
+//   pages of 16  255 and 337   315 and 340   369 and 348   547 and 366
+// (64 rows were level in both kernels' first form, and with pages of 64 no longer are.)
 constexpr int kTcRowsE4m3 = 64;
 
 // Rows whose keys were cut into splits: one warp a row. kRef: E4M3 caches.
@@ -104,7 +107,8 @@ Plan plan_of(const moe_attn_config& c) {
   // 20 rows: 147 us in one block, 138 in two; E4M3, 28 rows: 282 and 206; fp32,
   // 16 rows: 42.6 and 37.3.
   // The tcgen05 kernels take all that they have lanes of Tensor Memory for: 128,
-  // of an E4M3 cache 256 in two streams.
+  // of an E4M3 cache 256 in two streams (as one item and as two of up to 128, the calls
+  // above: 136 rows 365 and 427 us, 192: 378 and 437, 256: 398 and 460).
   p.row_blocks = ceil_div(units, p.tc ? (f8 ? 16 : 8) : f32 && c.head_dim <= 128 ? 3 : 2);
   p.nt = ceil_div(units, p.row_blocks);
   p.items = (long long)c.n_seqs * c.n_kv_heads * p.row_blocks;

@@ -327,7 +327,9 @@ __global__ void __launch_bounds__(warps_of(kDim) * 32, blocks_per_sm(kDim))
   };
   // Tile i, which has arrived. False, and nothing is changed, where l and O need references of
   // their own (E4M3; the same for the whole warp), which they have in the instance kApart. That
-  // is in a loop of its own: in this one it cost every call 1 to 4%.
+  // is in a loop of its own and asked for by the scales: in this loop, and asked for by weights
+  // that grow too large, it cost every call 1 to 4%, so 40 rows 257 us for 244 (32 sequences of
+  // 100 to 12000 keys, heads of 128).
   auto tile = [&](int i, auto instance) __attribute__((always_inline)) {
     constexpr bool kApart = decltype(instance)::value;
     const uint32_t K = ring + (i % kS) * T::kStage, V = K + T::kBytes;

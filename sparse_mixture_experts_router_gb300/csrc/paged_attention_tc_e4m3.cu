@@ -33,13 +33,17 @@
 // not 0), those keys are left out of the products and added at the end, row by row.
 //
 // 4 sequences of 200 to 1024 new tokens over 1500 to 4000 keys, 32/8 heads of 128, pages of
-// 64: 184 to 205 us, 480 to 530 TFLOP/s, 0.26 to 0.28 of the measured dense rate (578 us in the
-// warp-level kernel's blocks of 16 rows). Bound by latency: of a stream's tile about 2800
-// cycles are softmax (a warp alone on its scheduler issues every 5 to 6 cycles, and has 128
-// scores to load, compare, exponentiate, round and store), 530 Q K^T and 1000 P V, and two streams
-// overlap so far that the tensor pipe is busy 27% of the time. One stream and 16 warps took
+// 64: 150 to 203 us as the lengths fall, 184 to 195 and 500 to 530 TFLOP/s, 0.27 to 0.28 of the
+// measured dense rate, for the mean of them (578 us in the warp-level kernel's blocks of 16 rows).
+// Pages that do not hold whole groups of 32 keys: 216 to 298 us, as each key has its own lookup
+// and each score its own factors. Bound by latency: of a stream's tile about 2800
+// cycles were softmax when the first took 205 (a warp alone on its scheduler issues every 5 to 6
+// cycles, and has 128 scores to load, compare, exponentiate, round and store), 530 Q K^T and 1000
+// P V, and two streams overlap so far that the tensor pipe is busy 29% of the time; and items of
+// unequal length, one an SM, leave a last wave that few of them fill. One stream and 16 warps took
 // 243 us, two threads a row with two blocks an SM 253 (spills); with 8 warps that widen, 40
-// rows of 32 sequences took 292 us for 264.
+// rows of 32 sequences took 292 us for 264. Far scales in the tile's one path, and not in one
+// of their own, cost 3 to 8%.
 #include <cfloat>
 
 #include "paged_attention.cuh"
